@@ -9,7 +9,8 @@ Names follow the C ABI:
   nf4_build_codebook, nf4_build_int4_codebook, nf4_build_fp4_codebook, nf4_quantize,
   nf4_double_quant, nf4_double_quant_int8, nf4_dequant, nf4_dequant_single, qlora_linear_fwd,
   qlora_linear_fwd_static, qlora_linear_bwd, qlora_swiglu_fwd, qlora_swiglu_bwd, qlora_gated_fwd, qlora_gated_bwd,
-  qlora_multi_fwd.
+  qlora_multi_fwd, nf4_int8_quantize, nf4_int8_dequant, qlora_int8_linear_fwd, qlora_int8_linear_bwd,
+  qlora_norm_fwd, qlora_norm_bwd.
 """
 from __future__ import annotations
 
@@ -36,6 +37,8 @@ EXPORTS = (
     "qlora_linear_workspace_size", "qlora_linear_route", "qlora_linear_fwd", "qlora_linear_fwd_static", "qlora_linear_bwd",
     "qlora_swiglu_fwd", "qlora_swiglu_bwd", "qlora_gated_workspace_size", "qlora_gated_fwd", "qlora_gated_bwd",
     "qlora_multi_workspace_size", "qlora_multi_fwd",
+    "nf4_int8_quantize", "nf4_int8_dequant", "qlora_int8_linear_workspace_size", "qlora_int8_linear_fwd",
+    "qlora_int8_linear_bwd", "qlora_norm_fwd", "qlora_norm_workspace_size", "qlora_norm_bwd",
     "nf4_set_gemm_timing_events", "nf4_gemm_timing_count",
 )
 
@@ -61,6 +64,29 @@ class _WeightDesc(ctypes.Structure):
     ]
 
 
+class _Int8Desc(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+    ]
+
+
+class _NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("w_pre", ctypes.c_void_p),
+        ("w_post", ctypes.c_void_p),
+        ("gate", ctypes.c_void_p),
+        ("gate_tokens", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("alpha", ctypes.c_float),
+        ("beta", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("resid_type", ctypes.c_int32),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m bit_nf4_quantized_codebook_amd.build` "
@@ -74,7 +100,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
     i = ctypes.c_int
-    W = ctypes.POINTER(_WeightDesc)
+    W, Q, D = ctypes.POINTER(_WeightDesc), ctypes.POINTER(_Int8Desc), ctypes.POINTER(_NormDesc)
     sigs = {
         "nf4_status_string": (ctypes.c_char_p, [i]),
         "nf4_last_error": (ctypes.c_char_p, []),
@@ -103,6 +129,14 @@ def _load():
         "qlora_swiglu_bwd": (i, [P, P, P, P, P, i64, P]),
         "qlora_multi_workspace_size": (sz, [i32, P, i64, i64, i32]),
         "qlora_multi_fwd": (i, [i32, P, P, P, P, ctypes.c_float, i64, i32, P, P, P, sz, P]),
+        "nf4_int8_quantize": (i, [P, i32, i64, i64, P, P, P]),
+        "nf4_int8_dequant": (i, [Q, P, P]),
+        "qlora_int8_linear_workspace_size": (sz, [i64, i64, i64, i32]),
+        "qlora_int8_linear_fwd": (i, [Q, P, P, P, P, P, ctypes.c_float, i64, i32, P, P, P, sz, P]),
+        "qlora_int8_linear_bwd": (i, [Q, P, P, P, P, P, ctypes.c_float, i64, i32, P, P, P, ctypes.c_uint32, P, sz, P]),
+        "qlora_norm_fwd": (i, [D, P, P, i64, P, P, P, P, P]),
+        "qlora_norm_workspace_size": (sz, [i64, i64]),
+        "qlora_norm_bwd": (i, [D, P, P, P, P, i64, P, P, P, P, P, P, sz, P]),
         "nf4_set_gemm_timing_events": (i, [P, P, P, i32]),
         "nf4_gemm_timing_count": (i32, []),
     }
@@ -484,6 +518,267 @@ def qlora_swiglu_bwd(dh, g, u):
     _check(lib.qlora_swiglu_bwd(_ptr(dh), _ptr(g), _ptr(u), _ptr(dg), _ptr(du), g.numel(),
                                 _stream(g.device)), "qlora_swiglu_bwd")
     return dg, du
+
+
+# ------------------------------------------------------------------------------------------
+# Int8: rows with one constant each, and the linear layer on them
+# ------------------------------------------------------------------------------------------
+
+def _at(t):
+    """Address of a tensor that may be None (NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+def _expect(t, dtype, shape, dev, name):
+    """t: a contiguous tensor of this type and shape on dev (the call's device)."""
+    _need(t, dtype, name)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's first tensor on {dev}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {shape}")
+    return t
+
+
+def _out(t, dtype, shape, dev, name):
+    """An output given by the caller, checked, or a new one."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    return _expect(t, dtype, shape, dev, name)
+
+
+def _launch(name, dev, *args):
+    """lib.name(*args, stream) on the device's current stream, with that device current."""
+    cuda = _torch().cuda
+    if cuda.current_device() == dev.index:
+        status = getattr(lib, name)(*args, cuda.current_stream(dev).cuda_stream)
+    else:
+        with cuda.device(dev):
+            status = getattr(lib, name)(*args, cuda.current_stream(dev).cuda_stream)
+    _check(status, name)
+
+
+def nf4_int8_quantize(X, codes=None, scales=None):
+    """Rows of a bf16 or float32 device tensor [rows, cols] to 8-bit integers with one constant per
+    row: returns (codes int8 [rows, cols], scales float32 [rows])."""
+    torch = _torch()
+    f32 = getattr(X, "dtype", None) == torch.float32
+    _need(X, torch.float32 if f32 else torch.bfloat16, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [rows, cols]")
+    rows, cols = X.shape
+    codes = _out(codes, torch.int8, (rows, cols), X.device, "codes")
+    scales = _out(scales, torch.float32, (rows,), X.device, "scales")
+    _launch("nf4_int8_quantize", X.device, X.data_ptr(), int(f32), rows, cols, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+class Int8Weight:
+    """A frozen weight [rows = N_out, cols = K_in] in 8-bit integers, one constant per output channel."""
+
+    def __init__(self, codes, scales):
+        torch = _torch()
+        _need(codes, torch.int8, "codes")
+        if codes.dim() != 2:
+            raise ValueError("codes must be [rows, cols]")
+        _expect(scales, torch.float32, (codes.shape[0],), codes.device, "scales")
+        self.codes, self.scales = codes, scales
+
+    @classmethod
+    def from_float(cls, W):
+        """Quantize a float32 or bf16 [rows, cols] device tensor."""
+        return cls(*nf4_int8_quantize(W.contiguous()))
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def descriptor(self) -> _Int8Desc:
+        rows, cols = self.codes.shape
+        return _Int8Desc(self.codes.data_ptr(), self.scales.data_ptr(), rows, cols)
+
+
+def nf4_int8_dequant(w: Int8Weight):
+    """bf16(scale * code), [rows, cols]: the weight that the backward's gradient runs through."""
+    torch = _torch()
+    out = torch.empty((w.rows, w.cols), dtype=torch.bfloat16, device=w.device)
+    _launch("nf4_int8_dequant", w.device, ctypes.byref(w.descriptor()), out.data_ptr())
+    return out
+
+
+def qlora_int8_linear_workspace_size(M: int, N: int, K: int, r: int) -> int:
+    return int(lib.qlora_int8_linear_workspace_size(M, N, K, r))
+
+
+def _int8_adapter(L1, L2, N, K, dev):
+    """The adapter's rank (0: none)."""
+    if L1 is None and L2 is None:
+        return 0
+    torch = _torch()
+    _need(L1, torch.bfloat16, "L1")
+    r = L1.shape[-1]
+    _expect(L1, torch.bfloat16, (K, r), dev, "L1")
+    _expect(L2, torch.bfloat16, (r, N), dev, "L2")
+    return r
+
+
+def qlora_int8_linear_fwd(w: Int8Weight, X, L1=None, L2=None, scale: float = 1.0, keep_T: bool = True, Xq=None,
+                          Y=None, workspace=None, T=None):
+    """Y = xs ws (Xq Wq^T) + scale (X L1) L2, X quantized per token to 8-bit integers.  Returns (Y, T) with
+    T = X L1 (or None).  L1, L2: both or neither.  Xq: X's (codes, scales) where they are there already
+    (nf4_int8_quantize, qlora_norm_fwd); X may then be None if there is no adapter."""
+    torch = _torch()
+    bf16, N, K, dev = torch.bfloat16, w.rows, w.cols, w.device
+    r = _int8_adapter(L1, L2, N, K, dev)
+    M = (X if X is not None else Xq[0]).shape[0]
+    if X is not None:
+        _expect(X, bf16, (M, K), dev, "X")
+    q = qs = None
+    if Xq is not None:
+        q, qs = _expect(Xq[0], torch.int8, (M, K), dev, "Xq[0]"), _expect(Xq[1], torch.float32, (M,), dev, "Xq[1]")
+    Y = _out(Y, bf16, (M, N), dev, "Y")
+    if not r:
+        if T is not None:
+            raise ValueError("T without an adapter")
+    elif T is not None or keep_T:
+        T = _out(T, bf16, (M, r), dev, "T")
+    wsb = lib.qlora_int8_linear_workspace_size(M, N, K, r)
+    ws = _workspace(wsb, dev, workspace)
+    _launch("qlora_int8_linear_fwd", dev, ctypes.byref(w.descriptor()), _at(X), _at(q), _at(qs), _at(L1), _at(L2),
+            scale, M, r, Y.data_ptr(), _at(T), ws.data_ptr(), wsb)
+    return Y, T
+
+
+def qlora_int8_linear_bwd(w: Int8Weight, dY, X=None, L1=None, L2=None, T=None, scale: float = 1.0,
+                          need_dX: bool = True, dX=None, accumulate: bool = False, workspace=None, dL1=None, dL2=None):
+    """Returns (dX or None, dL1, dL2) for the layer above (dL1 and dL2 None without an adapter); the
+    gradient of X runs through nf4_int8_dequant(w)."""
+    torch = _torch()
+    bf16, N, K, dev = torch.bfloat16, w.rows, w.cols, w.device
+    r = _int8_adapter(L1, L2, N, K, dev)
+    _need(dY, bf16, "dY")
+    M = dY.shape[0]
+    _expect(dY, bf16, (M, N), dev, "dY")
+    if r:
+        _expect(X, bf16, (M, K), dev, "X")
+        if T is not None:
+            _expect(T, bf16, (M, r), dev, "T")
+        dL1 = _out(dL1, bf16, (K, r), dev, "dL1")
+        dL2 = _out(dL2, bf16, (r, N), dev, "dL2")
+    elif T is not None or dL1 is not None or dL2 is not None:
+        raise ValueError("T, dL1 or dL2 without an adapter")
+    if accumulate and need_dX and dX is None:
+        raise ValueError("accumulate needs dX")
+    dX = _out(dX, bf16, (M, K), dev, "dX") if need_dX else None
+    wsb = lib.qlora_int8_linear_workspace_size(M, N, K, r)
+    ws = _workspace(wsb, dev, workspace)
+    _launch("qlora_int8_linear_bwd", dev, ctypes.byref(w.descriptor()), dY.data_ptr(), _at(X) if r else None, _at(L1),
+            _at(L2), _at(T), scale, M, r, _at(dX), _at(dL1), _at(dL2), QLORA_DX_ACCUMULATE if accumulate else 0,
+            ws.data_ptr(), wsb)
+    return dX, dL1, dL2
+
+
+# ------------------------------------------------------------------------------------------
+# Norm glue between blocks
+# ------------------------------------------------------------------------------------------
+
+@dataclass
+class QLoRANorm:
+    """What stands between two blocks of a decoder layer: the norm after a block (w_post), its gate, the
+    residual sum with its scales and the norm before the next block (w_pre).  Weights bf16 [C], each
+    optional; gate bf16 [ceil(M / gate_tokens), C], one row for every gate_tokens consecutive tokens."""
+    w_pre: object = None
+    w_post: object = None
+    gate: object = None
+    gate_tokens: int = 0
+    alpha: float = 1.0
+    beta: float = 1.0
+    eps: float = 1e-6
+
+    def _descriptor(self, R, B, name):
+        """Checks R, B and the weights against each other; returns (descriptor, M, C)."""
+        torch = _torch()
+        f32 = getattr(R, "dtype", None) == torch.float32
+        _need(R, torch.float32 if f32 else torch.bfloat16, name)
+        if R.dim() != 2:
+            raise ValueError(f"{name} must be [M, C]")
+        M, C = R.shape
+        bf16, dev = torch.bfloat16, R.device
+        if B is not None:
+            _expect(B, bf16, (M, C), dev, "B")
+        if self.w_pre is not None:
+            _expect(self.w_pre, bf16, (C,), dev, "w_pre")
+        if self.w_post is not None:
+            _expect(self.w_post, bf16, (C,), dev, "w_post")
+        if self.gate is not None:
+            if self.gate_tokens < 1:
+                raise ValueError("gate_tokens must be >= 1 with a gate")
+            _expect(self.gate, bf16, (-(-M // self.gate_tokens), C), dev, "gate")
+        return _NormDesc(_at(self.w_pre), _at(self.w_post), _at(self.gate), self.gate_tokens, C, self.alpha,
+                         self.beta, self.eps, int(f32)), M, C
+
+
+def qlora_norm_fwd(norm: QLoRANorm, R, B=None, quantize: bool = False, R_out=None, H=None):
+    """R' = alpha R + beta gate * norm(B; w_post) and H = norm(R'; w_pre), R and R' bf16 or float32.
+    Returns (R', H); R' is None without B, H without w_pre.  quantize: also H's (codes, scales), for
+    qlora_int8_linear_fwd's Xq, as a third value.  R_out may be R itself."""
+    torch = _torch()
+    d, M, C = norm._descriptor(R, B, "R")
+    dev, q = R.device, None
+    if B is not None:
+        R_out = _out(R_out, R.dtype, (M, C), dev, "R_out")
+    elif R_out is not None:
+        raise ValueError("R_out without B")
+    if norm.w_pre is not None:
+        H = _out(H, torch.bfloat16, (M, C), dev, "H")
+    elif H is not None or quantize:
+        raise ValueError("H or quantize without w_pre")
+    if quantize:
+        q = (torch.empty((M, C), dtype=torch.int8, device=dev), torch.empty((M,), dtype=torch.float32, device=dev))
+    _launch("qlora_norm_fwd", dev, ctypes.byref(d), R.data_ptr(), _at(B), M, _at(R_out), _at(H),
+            _at(q[0]) if q else None, _at(q[1]) if q else None)
+    return (R_out, H, q) if quantize else (R_out, H)
+
+
+def qlora_norm_workspace_size(M: int, C: int) -> int:
+    return int(lib.qlora_norm_workspace_size(M, C))
+
+
+def qlora_norm_bwd(norm: QLoRANorm, R_out, B=None, dR_out=None, dH=None, need_weights: bool = True, dR=None, dB=None,
+                   workspace=None):
+    """Backward of qlora_norm_fwd, with R_out as it returned it (R itself where there was no B).
+    Returns (dR, dB, grads): grads holds dw_pre, dw_post and dgate of the weights that norm has (empty
+    with need_weights false).  dR_out None counts as zero.  dR may be dR_out itself, dB may be dH or B."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    d, M, C = norm._descriptor(R_out, B, "R_out")
+    dev = R_out.device
+    if dR_out is not None:
+        _expect(dR_out, R_out.dtype, (M, C), dev, "dR_out")
+    if dH is not None:
+        _expect(dH, bf16, (M, C), dev, "dH")
+    dR = _out(dR, R_out.dtype, (M, C), dev, "dR")
+    if B is not None:
+        dB = _out(dB, bf16, (M, C), dev, "dB")
+    elif dB is not None:
+        raise ValueError("dB without B")
+    grads = {}
+    if need_weights:
+        for name, w in (("dw_pre", norm.w_pre), ("dw_post", norm.w_post), ("dgate", norm.gate)):
+            if w is not None:
+                grads[name] = torch.empty_like(w)
+    wsb = lib.qlora_norm_workspace_size(M, C)
+    ws = _workspace(wsb, dev, workspace)
+    _launch("qlora_norm_bwd", dev, ctypes.byref(d), R_out.data_ptr(), _at(B), _at(dR_out), _at(dH), M, dR.data_ptr(),
+            _at(dB), _at(grads.get("dw_pre")), _at(grads.get("dw_post")), _at(grads.get("dgate")), ws.data_ptr(), wsb)
+    return dR, dB, grads
 
 
 class GemmTimer:

@@ -993,3 +993,301 @@ int qlora_swiglu_bwd(const uint16_t *dh, const uint16_t *g, const uint16_t *u, u
     return NF4_OK;
 }
 
+
+// ---------------------------------------------------------------------------------------------
+// Int8: rows with one constant each, and the linear layer on them
+// ---------------------------------------------------------------------------------------------
+namespace {
+int check_int8_weight(const nf4_int8_weight *w) {
+    if (!w) return fail(NF4_ERR_NULL, "weight descriptor is NULL");
+    if (!w->codes || !w->scales) return fail(NF4_ERR_NULL, "weight descriptor has a NULL pointer");
+    if (w->rows <= 0 || w->cols <= 0) return fail(NF4_ERR_SHAPE, "weight rows and cols must be > 0");
+    if (w->cols % 64) return fail(NF4_ERR_UNSUPPORTED, "weight cols (K) must be a multiple of 64");
+    if (w->rows % 8) return fail(NF4_ERR_UNSUPPORTED, "weight rows (N) must be a multiple of 8");
+    if (w->cols > NF4_INT8_MAX_COLS) return fail(NF4_ERR_UNSUPPORTED, "weight cols (K) exceed NF4_INT8_MAX_COLS");
+    if (!aligned16(w->codes)) return fail(NF4_ERR_ALIGN, "weight codes must be 16-byte aligned");
+    if ((uintptr_t)w->scales & 3u) return fail(NF4_ERR_ALIGN, "weight scales must be 4-byte aligned");
+    return NF4_OK;
+}
+
+nf4k::Int8View view_of(const nf4_int8_weight *w) { return nf4k::Int8View{w->codes, w->scales, w->rows, w->cols}; }
+
+struct Int8Plan {
+    int ksT, ksdT, msL2, msL1;
+    nf4k::SplitPlan kb;            // split of the backward's dX product
+    size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_P, off_Wd, off_Pg, total;
+};
+
+// One layout for both directions: the forward uses Xq, xs, sT and P, the backward T, dT, P, Wd and Pg.
+Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
+    Int8Plan p;
+    const int64_t mt = (M + kTile - 1) / kTile, rt = (r + kTile - 1) / kTile;
+    p.ksT = p.ksdT = p.msL2 = p.msL1 = 1;
+    size_t pmax = 0;
+    if (r) {
+        p.ksT = nf4k::choose_split(mt * rt, (K + kTile - 1) / kTile);
+        p.ksdT = nf4k::choose_split(mt * rt, (N + kTile - 1) / kTile);
+        p.msL2 = nf4k::choose_split(rt * ((N + kTile - 1) / kTile), mt);
+        p.msL1 = nf4k::choose_split(((K + kTile - 1) / kTile) * rt, mt);
+        pmax = (size_t)(p.ksT > p.ksdT ? p.ksT : p.ksdT) * M * r;
+        const size_t ptn = (size_t)p.msL2 * r * N + (size_t)p.msL1 * K * r;
+        pmax = pmax > ptn ? pmax : ptn;
+    }
+    const int64_t tiles = (M + kGemmTile - 1) / kGemmTile * ((K + kGemmTile - 1) / kGemmTile);
+    p.kb = nf4k::gemm_split(tiles, (N + kTile - 1) / kTile, kSplitQuantum);
+    size_t off = 0;
+    p.off_Xq = off;  off += round256((size_t)M * K);
+    p.off_xs = off;  off += round256((size_t)M * 4);
+    p.off_T = off;   off += round256((size_t)M * r * 2);
+    p.off_sT = off;  off += round256((size_t)M * r * 2);
+    p.off_dT = off;  off += round256((size_t)M * r * 2);
+    p.off_P = off;   off += round256(pmax * 4);
+    p.off_Wd = off;  off += round256((size_t)N * K * 2);
+    p.off_Pg = off;  off += round256(p.kb.ksplit > 1 ? (size_t)p.kb.ksplit * M * K * 4 : 0);
+    p.total = off;
+    return p;
+}
+
+int check_int8_linear_args(const nf4_int8_weight *w, int64_t M, int32_t r, float scale) {
+    const int rc = check_int8_weight(w);
+    if (rc) return rc;
+    if (M <= 0) return fail(NF4_ERR_SHAPE, "M must be >= 1");
+    if (r < 0 || r > 128) return fail(NF4_ERR_UNSUPPORTED, "r must be in [0, 128]");
+    if (r % 8) return fail(NF4_ERR_UNSUPPORTED, "r must be a multiple of 8");
+    if (!std::isfinite(scale)) return fail(NF4_ERR_ARG, "scale must be finite");
+    // kernels address each operand with 32-bit byte offsets
+    const int64_t lim = (int64_t)1 << 31;
+    if (M >= lim || w->rows >= lim || w->rows * w->cols >= lim || M * w->cols * 2 >= lim || M * w->rows * 2 >= lim)
+        return fail(NF4_ERR_UNSUPPORTED, "an operand exceeds 2 GiB");
+    return NF4_OK;
+}
+}  // namespace
+
+int nf4_int8_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols, int8_t *codes, float *scales,
+                      void *stream) {
+    if (x_type != NF4_ROWS_BF16 && x_type != NF4_ROWS_F32)
+        return fail(NF4_ERR_ARG, "x_type must be NF4_ROWS_BF16 or NF4_ROWS_F32");
+    if (rows < 0) return fail(NF4_ERR_SHAPE, "rows must be >= 0");
+    if (cols < 8) return fail(NF4_ERR_SHAPE, "cols must be >= 8");
+    if (cols % 8) return fail(NF4_ERR_UNSUPPORTED, "cols must be a multiple of 8");
+    if (cols > NF4_INT8_MAX_COLS) return fail(NF4_ERR_UNSUPPORTED, "cols exceed NF4_INT8_MAX_COLS");
+    if (rows == 0) return NF4_OK;
+    if (!x || !codes || !scales) return fail(NF4_ERR_NULL, "x, codes and scales must be non-NULL");
+    if (!aligned16(x) || !aligned16(codes)) return fail(NF4_ERR_ALIGN, "x and codes must be 16-byte aligned");
+    if ((uintptr_t)scales & 3u) return fail(NF4_ERR_ALIGN, "scales must be 4-byte aligned");
+    NF4_CHECK_HIP(nf4k::launch_int8_rows(x, x_type == NF4_ROWS_F32, rows, cols, codes, scales,
+                                         reinterpret_cast<hipStream_t>(stream)),
+                  "int8 quantize");
+    return NF4_OK;
+}
+
+int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream) {
+    const int rc = check_int8_weight(w);
+    if (rc) return rc;
+    if (w->rows >= ((int64_t)1 << 40) / w->cols) return fail(NF4_ERR_UNSUPPORTED, "the weight exceeds 2^40 elements");
+    if (!out_bf16) return fail(NF4_ERR_NULL, "out_bf16 is NULL");
+    if (!aligned16(out_bf16)) return fail(NF4_ERR_ALIGN, "out_bf16 must be 16-byte aligned");
+    NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/false, out_bf16, reinterpret_cast<hipStream_t>(stream)),
+                  "int8 dequant");
+    return NF4_OK;
+}
+
+size_t qlora_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r) {
+    const int64_t lim = (int64_t)1 << 31;      // beyond: shapes that the calls refuse
+    if (M <= 0 || N <= 0 || K <= 0 || r < 0 || M >= lim || N >= lim || K >= lim) return 0;
+    return make_int8_plan(M, N, K, r).total;
+}
+
+int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int8_t *Xq, const float *xs,
+                          const uint16_t *L1, const uint16_t *L2, float scale, int64_t M, int32_t r, uint16_t *Y,
+                          uint16_t *T_out, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_int8_linear_args(w, M, r, scale);
+    if (rc) return rc;
+    if (!Xq != !xs) return fail(NF4_ERR_NULL, "Xq and xs must be given together");
+    if (!Y || (!X && (!Xq || r))) return fail(NF4_ERR_NULL, "Y, and X (or Xq and xs where r is 0), must be non-NULL");
+    if (r && (!L1 || !L2)) return fail(NF4_ERR_NULL, "L1 and L2 must be non-NULL");
+    if (!r && (L1 || L2 || T_out)) return fail(NF4_ERR_ARG, "r is 0: L1, L2 and T_out must be NULL");
+    for (const void *q : {(const void *)X, (const void *)Xq, (const void *)L1, (const void *)L2, (const void *)Y,
+                          (const void *)T_out})
+        if (q && !aligned16(q)) return fail(NF4_ERR_ALIGN, "activations and adapters must be 16-byte aligned");
+    if ((uintptr_t)xs & 3u) return fail(NF4_ERR_ALIGN, "xs must be 4-byte aligned");
+    const int64_t N = w->rows, K = w->cols;
+    const Int8Plan p = make_int8_plan(M, N, K, r);
+    if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "int8 linear workspace too small");
+    if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (!Xq) {
+        int8_t *q = ws_at<int8_t>(workspace, p.off_Xq);
+        float *qs = ws_at<float>(workspace, p.off_xs);
+        NF4_CHECK_HIP(nf4k::launch_int8_rows(X, false, M, K, q, qs, s), "int8 quantize (fwd)");
+        Xq = q;
+        xs = qs;
+    }
+    uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT);
+    if (r) {
+        float *P = ws_at<float>(workspace, p.off_P);
+        NF4_CHECK_HIP(nf4k::launch_skinny_nt(X, L1, /*b_rows_k=*/true, P, M, r, K, p.ksT, s), "T = X L1");
+        const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
+        NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "T reduce");
+    }
+    NF4_CHECK_HIP(nf4k::launch_int8_gemm(nf4k::Int8Product{Xq, w->codes, xs, w->scales, sT, L2, M, N, K, r, Y}, s),
+                  "int8 GEMM (fwd)");
+    return NF4_OK;
+}
+
+int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const uint16_t *X, const uint16_t *L1,
+                          const uint16_t *L2, const uint16_t *T, float scale, int64_t M, int32_t r, uint16_t *dX,
+                          uint16_t *dL1, uint16_t *dL2, uint32_t flags, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    int rc = check_int8_linear_args(w, M, r, scale);
+    if (rc) return rc;
+    if (flags & ~QLORA_DX_ACCUMULATE) return fail(NF4_ERR_ARG, "unknown flags");
+    if (!dY) return fail(NF4_ERR_NULL, "dY must be non-NULL");
+    if (r && (!X || !L1 || !L2 || !dL1 || !dL2)) return fail(NF4_ERR_NULL, "X, L1, L2, dL1 and dL2 must be non-NULL");
+    if (!r && (L1 || L2 || T || dL1 || dL2)) return fail(NF4_ERR_ARG, "r is 0: L1, L2, T, dL1 and dL2 must be NULL");
+    if (!r && !dX) return fail(NF4_ERR_NULL, "dX must be non-NULL where r is 0");
+    for (const void *q : {(const void *)dY, (const void *)X, (const void *)L1, (const void *)L2, (const void *)T,
+                          (const void *)dX, (const void *)dL1, (const void *)dL2})
+        if (q && !aligned16(q)) return fail(NF4_ERR_ALIGN, "activations, adapters and gradients must be 16-byte aligned");
+    const int64_t N = w->rows, K = w->cols;
+    const Int8Plan p = make_int8_plan(M, N, K, r);
+    if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "int8 linear workspace too small");
+    if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    uint16_t *dT = ws_at<uint16_t>(workspace, p.off_dT);
+    if (r) {
+        float *P = ws_at<float>(workspace, p.off_P);
+        const uint16_t *Tuse = T;
+        if (!Tuse) {
+            uint16_t *Tb = ws_at<uint16_t>(workspace, p.off_T);
+            NF4_CHECK_HIP(nf4k::launch_skinny_nt(X, L1, /*b_rows_k=*/true, P, M, r, K, p.ksT, s), "T = X L1");
+            const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, Tb, 0.0f, nullptr};
+            NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "T reduce");
+            Tuse = Tb;
+        }
+        NF4_CHECK_HIP(nf4k::launch_skinny_nt(dY, L2, /*b_rows_k=*/false, P, M, r, N, p.ksdT, s), "dT = dY L2^T");
+        const nf4k::Reduction red_dT{P, p.ksdT, M * r, scale, dT, 0.0f, nullptr};
+        NF4_CHECK_HIP(nf4k::launch_reduce_partials(red_dT, nullptr, s), "dT reduce");
+        // both adapters' gradients in one launch, their partials side by side
+        float *P1 = P + (size_t)p.msL2 * r * N;
+        const bool direct = p.msL2 == 1 && p.msL1 == 1;
+        nf4k::TnProduct tn_dL2{Tuse, dY, P, r, N, p.msL2};
+        nf4k::TnProduct tn_dL1{X, dT, P1, K, r, p.msL1};
+        if (direct) {
+            tn_dL2.out = dL2; tn_dL2.scale = scale;
+            tn_dL1.out = dL1; tn_dL1.scale = 1.0f;
+        }
+        NF4_CHECK_HIP(nf4k::launch_skinny_tn(tn_dL2, &tn_dL1, M, s), "dL2 = T^T dY, dL1 = X^T dT");
+        if (!direct) {
+            const nf4k::Reduction red_dL2{P, p.msL2, (int64_t)r * N, scale, dL2, 0.0f, nullptr};
+            const nf4k::Reduction red_dL1{P1, p.msL1, K * (int64_t)r, 1.0f, dL1, 0.0f, nullptr};
+            NF4_CHECK_HIP(nf4k::launch_reduce_partials(red_dL2, &red_dL1, s), "dL2, dL1 reduce");
+        }
+    }
+    if (!dX) return NF4_OK;
+    // the weight in bf16, transposed, then the bf16 product with the adapter's steps
+    uint16_t *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
+    NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, s), "int8 expansion");
+    const bool acc = (flags & QLORA_DX_ACCUMULATE) != 0;
+    float *Pg = ws_at<float>(workspace, p.off_Pg);
+    NF4_CHECK_HIP(nf4k::launch_gemm_bf16_bwd(dY, WdT, dT, L1, r, M, N, K, dX, acc,
+                                             nf4k::SplitK{p.kb.ksplit, p.kb.per, Pg}, s),
+                  "bf16 GEMM (int8 bwd)");
+    if (p.kb.ksplit > 1) {
+        nf4k::Reduction red{Pg, p.kb.ksplit, M * K, 1.0f, dX, 0.0f, nullptr};
+        red.accum = acc;
+        NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "split product reduce");
+    }
+    return NF4_OK;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Norm glue between blocks
+// ---------------------------------------------------------------------------------------------
+namespace {
+int check_norm(const qlora_norm *p, const void *B, int64_t M) {
+    if (!p) return fail(NF4_ERR_NULL, "norm descriptor is NULL");
+    if (M <= 0) return fail(NF4_ERR_SHAPE, "M must be >= 1");
+    if (p->cols < 8) return fail(NF4_ERR_SHAPE, "cols must be >= 8");
+    if (p->cols % 8) return fail(NF4_ERR_UNSUPPORTED, "cols must be a multiple of 8");
+    if (p->cols > 16384) return fail(NF4_ERR_UNSUPPORTED, "cols must be at most 16384");
+    if (M > ((int64_t)1 << 46) / p->cols) return fail(NF4_ERR_UNSUPPORTED, "M * cols exceeds 2^46");
+    if (p->resid_type != NF4_ROWS_BF16 && p->resid_type != NF4_ROWS_F32)
+        return fail(NF4_ERR_ARG, "resid_type must be NF4_ROWS_BF16 or NF4_ROWS_F32");
+    if (!std::isfinite(p->alpha) || !std::isfinite(p->beta)) return fail(NF4_ERR_ARG, "alpha and beta must be finite");
+    if (!(p->eps > 0.0f) || !std::isfinite(p->eps)) return fail(NF4_ERR_ARG, "eps must be positive and finite");
+    if (!B && (p->w_post || p->gate || p->alpha != 1.0f || p->beta != 1.0f))
+        return fail(NF4_ERR_ARG, "without B: w_post and gate must be NULL, alpha and beta 1");
+    if (!B && !p->w_pre) return fail(NF4_ERR_NULL, "without B, w_pre must be non-NULL");
+    if (p->gate && p->gate_tokens < 1) return fail(NF4_ERR_SHAPE, "gate_tokens must be >= 1 with a gate");
+    for (const void *q : {(const void *)p->w_pre, (const void *)p->w_post, (const void *)p->gate})
+        if (q && !aligned16(q)) return fail(NF4_ERR_ALIGN, "norm weights and gate must be 16-byte aligned");
+    return NF4_OK;
+}
+nf4k::NormArgs norm_args(const qlora_norm *p, const void *R, const uint16_t *B, int64_t M) {
+    nf4k::NormArgs a{};
+    a.w_pre = p->w_pre; a.w_post = p->w_post; a.gate = p->gate;
+    a.gate_tokens = p->gate_tokens;
+    a.M = M;
+    a.C = (int32_t)p->cols;
+    a.alpha = p->alpha; a.beta = p->beta; a.eps = p->eps;
+    a.f32 = p->resid_type == NF4_ROWS_F32;
+    a.R = R;
+    a.B = B;
+    return a;
+}
+}  // namespace
+
+int qlora_norm_fwd(const qlora_norm *p, const void *R, const uint16_t *B, int64_t M, void *R_out, uint16_t *H,
+                   int8_t *Hq, float *Hs, void *stream) {
+    const int rc = check_norm(p, B, M);
+    if (rc) return rc;
+    if (!R) return fail(NF4_ERR_NULL, "R is NULL");
+    if (!B != !R_out) return fail(NF4_ERR_NULL, "R_out is written exactly when B is given");
+    if (!p->w_pre != !H) return fail(NF4_ERR_NULL, "H is written exactly when w_pre is given");
+    if (!Hq != !Hs) return fail(NF4_ERR_NULL, "Hq and Hs must be given together");
+    if (Hq && !H) return fail(NF4_ERR_NULL, "Hq needs H");
+    for (const void *q : {R, (const void *)B, (const void *)R_out, (const void *)H, (const void *)Hq})
+        if (q && !aligned16(q)) return fail(NF4_ERR_ALIGN, "norm buffers must be 16-byte aligned");
+    if ((uintptr_t)Hs & 3u) return fail(NF4_ERR_ALIGN, "Hs must be 4-byte aligned");
+    nf4k::NormArgs a = norm_args(p, R, B, M);
+    a.R_out = R_out;
+    a.H = H;
+    a.Hq = Hq;
+    a.Hs = Hs;
+    NF4_CHECK_HIP(nf4k::launch_norm_fwd(a, reinterpret_cast<hipStream_t>(stream)), "norm fwd");
+    return NF4_OK;
+}
+
+size_t qlora_norm_workspace_size(int64_t M, int64_t C) {
+    if (M <= 0 || C <= 0 || C > 16384) return 0;
+    return nf4k::norm_bwd_ws(M, C);
+}
+
+int qlora_norm_bwd(const qlora_norm *p, const void *R_out, const uint16_t *B, const void *dR_out, const uint16_t *dH,
+                   int64_t M, void *dR, uint16_t *dB, uint16_t *dw_pre, uint16_t *dw_post, uint16_t *dgate,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+    const int rc = check_norm(p, B, M);
+    if (rc) return rc;
+    if (!R_out || !dR) return fail(NF4_ERR_NULL, "R_out and dR must be non-NULL");
+    if (!p->w_pre != !dH) return fail(NF4_ERR_NULL, "dH is read exactly when w_pre is given");
+    if (!dR_out && !dH) return fail(NF4_ERR_NULL, "dR_out or dH must be non-NULL");
+    if (!B != !dB) return fail(NF4_ERR_NULL, "dB is written exactly when B is given");
+    if ((dw_pre && !p->w_pre) || (dw_post && !p->w_post) || (dgate && !p->gate))
+        return fail(NF4_ERR_ARG, "a gradient was asked for of a weight or gate that is NULL");
+    for (const void *q : {R_out, (const void *)B, dR_out, (const void *)dH, (const void *)dR, (const void *)dB,
+                          (const void *)dw_pre, (const void *)dw_post, (const void *)dgate})
+        if (q && !aligned16(q)) return fail(NF4_ERR_ALIGN, "norm buffers must be 16-byte aligned");
+    if (!workspace || workspace_bytes < nf4k::norm_bwd_ws(M, p->cols))
+        return fail(NF4_ERR_WORKSPACE, "norm workspace too small");
+    if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
+    nf4k::NormArgs a = norm_args(p, R_out, B, M);
+    a.dR_out = dR_out;
+    a.dH = dH;
+    a.dR = dR;
+    a.dB = dB;
+    a.dw_pre = dw_pre; a.dw_post = dw_post; a.dgate = dgate;
+    a.P = ws_at<float>(workspace, 0);
+    NF4_CHECK_HIP(nf4k::launch_norm_bwd(a, reinterpret_cast<hipStream_t>(stream)), "norm bwd");
+    return NF4_OK;
+}

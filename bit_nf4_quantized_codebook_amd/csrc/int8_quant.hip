@@ -1,0 +1,131 @@
+// Row-wise 8-bit integer quantization and the bf16 expansion of an Int8 weight (gfx950).
+//
+// Page: "QLoRA: Efficient Finetuning of Quantized LLMs" study notes (gitcode.csdn.net),
+// section 3.1 eq. (1) (absmax Int8, here one constant per row) and eq. (2).
+
+#include "common.h"
+#include "int8.h"
+#include "launch.h"
+
+namespace nf4k {
+
+namespace {
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void *x, int64_t i8, float f[8]) {
+    if (F32) {
+        typedef float f32v4 __attribute__((ext_vector_type(4)));
+        const f32v4 a = reinterpret_cast<const f32v4 *>(x)[2 * i8], b = reinterpret_cast<const f32v4 *>(x)[2 * i8 + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+    } else {
+        unpack8_bf16(reinterpret_cast<const u32x4 *>(x)[i8], f);
+    }
+}
+
+// One workgroup per row, the row read twice.
+template <bool F32>
+__global__ __launch_bounds__(256) void int8_rows_kernel(const void *__restrict__ x, int64_t cols,
+                                                        int8_t *__restrict__ codes, float *__restrict__ scales) {
+    __shared__ uint32_t red[4];
+    const int64_t row = blockIdx.x, c8 = cols >> 3;
+    const int tid = threadIdx.x;
+    uint32_t m = 0;
+    for (int64_t i = tid; i < c8; i += 256) {
+        float f[8];
+        load8<F32>(x, row * c8 + i, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+    }
+    m = wave_max(m);
+    if ((tid & 63) == 0) red[tid >> 6] = m;
+    __syncthreads();
+    m = max(max(red[0], red[1]), max(red[2], red[3]));
+    const RowCode rc = row_code(m);
+    if (tid == 0) scales[row] = rc.scale;
+    for (int64_t i = tid; i < c8; i += 256) {
+        float f[8];
+        load8<F32>(x, row * c8 + i, f);
+        reinterpret_cast<uint2 *>(codes)[row * c8 + i] = codes8(f, rc);
+    }
+}
+
+__device__ __forceinline__ float sext8(uint32_t w, int i) { return (float)((int32_t)(w << (24 - 8 * i)) >> 24); }
+
+// out[n, k] = bf16(scales[n] * codes[n, k]), 8 elements per thread and step
+__global__ __launch_bounds__(256) void int8_expand_rows_kernel(const int8_t *__restrict__ codes,
+                                                               const float *__restrict__ scales, int64_t rows,
+                                                               int64_t cols, uint16_t *__restrict__ out) {
+    const int64_t c8 = cols >> 3, n8 = rows * c8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
+        const uint2 v = reinterpret_cast<const uint2 *>(codes)[i];
+        const float s = scales[i / c8];
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = s * sext8(v.x, k);
+            f[4 + k] = s * sext8(v.y, k);
+        }
+        reinterpret_cast<u32x4 *>(out)[i] = pack8_bf16(f);
+    }
+}
+
+// out[k, n] = bf16(scales[n] * codes[n, k]): one 64 x 64 tile per workgroup, turned through LDS
+constexpr int ET = 64;
+__global__ __launch_bounds__(256) void int8_expand_transposed_kernel(const int8_t *__restrict__ codes,
+                                                                     const float *__restrict__ scales, int64_t N,
+                                                                     int64_t K, uint16_t *__restrict__ out) {
+    __shared__ uint16_t tile[ET][ET + 8];
+    const int64_t ntn = (N + ET - 1) / ET;
+    const int64_t n0 = ((int64_t)blockIdx.x % ntn) * ET, k0 = ((int64_t)blockIdx.x / ntn) * ET;
+    const int t = threadIdx.x, row = t >> 2, q = t & 3;
+    if (n0 + row < N) {
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(codes + (n0 + row) * K + k0 + 16 * q);
+        const float s = scales[n0 + row];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) tile[16 * q + i][row] = (uint16_t)f32_to_bf16(s * sext8(v[i >> 2], i & 3));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t n = n0 + 16 * q + 8 * h;      // N % 8 == 0: a group of 8 is inside or outside
+        if (n < N)
+            *reinterpret_cast<u32x4 *>(out + (k0 + row) * N + n) = *reinterpret_cast<const u32x4 *>(&tile[row][16 * q + 8 * h]);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_int8_rows(const void *x, bool f32, int64_t rows, int64_t cols, int8_t *codes, float *scales,
+                            hipStream_t stream) {
+    for (int64_t r0 = 0; r0 < rows; r0 += kMaxRowGrid) {
+        const int64_t n = rows - r0 < kMaxRowGrid ? rows - r0 : kMaxRowGrid;
+        const char *xr = reinterpret_cast<const char *>(x) + r0 * cols * (f32 ? 4 : 2);
+        if (f32)
+            hipLaunchKernelGGL(int8_rows_kernel<true>, dim3((unsigned)n), dim3(256), 0, stream, xr, cols,
+                               codes + r0 * cols, scales + r0);
+        else
+            hipLaunchKernelGGL(int8_rows_kernel<false>, dim3((unsigned)n), dim3(256), 0, stream, xr, cols,
+                               codes + r0 * cols, scales + r0);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, hipStream_t stream) {
+    if (!transposed) {
+        int64_t grid = ((w.rows * w.cols >> 3) + 255) / 256;
+        if (grid > 256 * 64) grid = 256 * 64;
+        hipLaunchKernelGGL(int8_expand_rows_kernel, dim3((unsigned)grid), dim3(256), 0, stream, w.codes, w.scales,
+                           w.rows, w.cols, out);
+    } else {
+        const int64_t tiles = ((w.rows + ET - 1) / ET) * (w.cols / ET);
+        hipLaunchKernelGGL(int8_expand_transposed_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, w.codes,
+                           w.scales, w.rows, w.cols, out);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace nf4k

@@ -148,6 +148,55 @@ hipError_t launch_reduce_partials(const Reduction &a, const Reduction *b, hipStr
 struct RedProb;
 RedProb red_prob(const Reduction &r, uint32_t &nblocks);
 
+// A launch counts its threads in 32 bits: kernels with a workgroup of up to 1024 threads per row take
+// at most this many rows per launch, and their launchers go on with the next rows.
+constexpr int64_t kMaxRowGrid = (int64_t)1 << 21;
+
+// ---- Int8: one constant per row (eq. (1)) ----
+struct Int8View {
+    const int8_t *codes;
+    const float *scales;
+    int64_t rows, cols;
+};
+hipError_t launch_int8_rows(const void *x, bool f32, int64_t rows, int64_t cols, int8_t *codes, float *scales,
+                            hipStream_t stream);
+// bf16(scale * code), as [rows, cols] or transposed [cols, rows] (cols a multiple of 64, rows of 8)
+hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, hipStream_t stream);
+// Y = xs ws (Xq Wq^T) + sT L2 (r = 0: no adapter)
+struct Int8Product {
+    const int8_t *Xq, *Wq;
+    const float *xs, *ws;
+    const uint16_t *sT, *L2;
+    int64_t M, N, K;
+    int32_t r;
+    uint16_t *Y;
+};
+hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream);
+
+// ---- norm glue between blocks ----
+struct NormArgs {
+    const uint16_t *w_pre, *w_post, *gate;
+    int64_t gate_tokens, M;
+    int32_t C;
+    float alpha, beta, eps;
+    bool f32;
+    const void *R;           // forward: R; backward: R'
+    const uint16_t *B;
+    void *R_out;
+    uint16_t *H;
+    int8_t *Hq;
+    float *Hs;
+    const void *dR_out;
+    const uint16_t *dH;
+    void *dR;
+    uint16_t *dB, *dw_pre, *dw_post, *dgate;
+    float *P;                // backward: partial sums of the weights' and gate's gradients
+    int64_t m0;              // forward: first row of the launch
+};
+hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream);
+size_t norm_bwd_ws(int64_t M, int64_t C);
+hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream);
+
 // Optional per-thread timing events recorded on the launch stream right before and after each
 // instrumented launch (see nf4.h).
 void timing_before(hipStream_t stream, int kind);

@@ -318,6 +318,115 @@ int qlora_swiglu_bwd(const uint16_t *dh, const uint16_t *g, const uint16_t *u, u
                      uint16_t *du, int64_t n, void *stream);
 
 /*
+ * 8-bit integers with one constant per row -- section 3.1 eq. (1), X^Int8 = round(127/absmax X), with
+ * a constant for each token (rows of an activation) or each output channel (rows of a weight).
+ *   x:      device [rows, cols], row-major: bf16 (x_type NF4_ROWS_BF16) or float32 (NF4_ROWS_F32).
+ *   rows:   >= 0 (0 is a no-op).  cols: a multiple of 8, 8 .. NF4_INT8_MAX_COLS.
+ *   codes:  device int8 [rows, cols];  scales: device float32 [rows].
+ * Per row: a = max |x|; scale = fp32(a / 127); code = the integer nearest to the real quotient
+ * x / scale (ties to even, decided exactly, not on a rounded quotient), clamped to [-127, 127]; all 0
+ * when scale == 0.  A row with an infinity or a NaN gets scale NaN and codes 0, so that whatever is
+ * computed from it is NaN and the other rows are untouched.
+ * x and codes must be 16-byte aligned, scales 4-byte aligned.
+ */
+enum { NF4_ROWS_BF16 = 0, NF4_ROWS_F32 = 1 };
+#define NF4_INT8_MAX_COLS 131008   /* cols * 128 * 128 stays below 2^31: the products' sums are exact */
+int nf4_int8_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols, int8_t *codes, float *scales,
+                      void *stream);
+
+/* One frozen weight in 8-bit integers with a constant per output channel (nf4_int8_quantize of the
+ * float32 weight).  Device pointers. */
+typedef struct nf4_int8_weight {
+    const int8_t *codes;          /* [rows, cols], 16-byte aligned; codes of any value, -128 included */
+    const float *scales;          /* [rows] */
+    int64_t rows;                 /* N_out, a multiple of 8 */
+    int64_t cols;                 /* K_in, a multiple of 64, at most NF4_INT8_MAX_COLS */
+} nf4_int8_weight;
+
+/*
+ * Dequantization to BF16 -- section 3.1 eq. (2): out[n, k] = bf16_RNE(fp32(scales[n] * codes[n, k])).
+ *   out_bf16: device uint16 [rows, cols], 16-byte aligned.
+ */
+int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream);
+
+/*
+ * Int8 QLoRA linear forward -- eq. (3) and (5) with eq. (1)'s integers for the storage and for the
+ * product: activations quantized per token, weights per output channel, exact int32 sums:
+ *   T = X L1;   Y[m, n] = xs[m] ws[n] sum_k Xq[m, k] Wq[n, k] + s (T L2)[m, n]
+ *   X:    [M, K] bf16.  Xq, xs: its codes int8 [M, K] and constants float32 [M] (from
+ *         nf4_int8_quantize or qlora_norm_fwd), or both NULL: quantized here, into the workspace.
+ *   L1: [K, r] bf16, L2: [r, N] bf16, r a multiple of 8 in [8, 128]; or r = 0 without an adapter
+ *         (L1, L2, T_out NULL; X may then be NULL where Xq is given).
+ *   Y: [M, N] bf16.  T_out: optional [M, r] bf16 (unscaled), as qlora_linear_fwd's.
+ *   scale: s, finite.  M >= 1.  Each operand below 2 GiB, as in qlora_linear_fwd.
+ *   workspace: >= qlora_int8_linear_workspace_size(M, N, K, r) bytes (forward and backward), 16-byte
+ *         aligned; calls that may overlap need a workspace each.
+ * Y is rounded to bf16 once.  Rows of X with non-finite values give rows of NaN in Y and leave the
+ * other rows as they are.
+ */
+size_t qlora_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r);
+int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int8_t *Xq, const float *xs,
+                          const uint16_t *L1, const uint16_t *L2, float scale, int64_t M, int32_t r, uint16_t *Y,
+                          uint16_t *T_out, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Int8 QLoRA linear backward -- section 3.5: gradients for the adapters and for X only, through the
+ * weight in BF16 (W' = nf4_int8_dequant); the rounding of X to its codes counts as the identity.
+ *   dT = s dY L2^T;  dX = dY W' + dT L1^T;  dL1 = X^T dT;  dL2 = s T^T dY
+ * Arguments, flags (QLORA_DX_ACCUMULATE) and outputs as qlora_linear_bwd; r = 0 without an adapter
+ * (X, L1, L2, T, dL1 and dL2 NULL, dX required).
+ */
+int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const uint16_t *X, const uint16_t *L1,
+                          const uint16_t *L2, const uint16_t *T, float scale, int64_t M, int32_t r, uint16_t *dX,
+                          uint16_t *dL1, uint16_t *dL2, uint32_t flags, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * Norm glue between two blocks of a decoder layer (not a step of the method): the norm after a
+ * block, its gate, the residual sum with its scales, and the norm before the next block, in one pass.
+ *   n[m]  = w_post * B[m] / sqrt(mean(B[m]^2) + eps)     (w_post NULL: n = B)
+ *   R'[m] = alpha R[m] + beta gate[m / gate_tokens] * n[m]       (gate NULL: 1)
+ *   H[m]  = w_pre * R'[m] / sqrt(mean(R'[m]^2) + eps)
+ * in float32 per row; H is taken from R' before R' is rounded to its type.  Mean squares have to
+ * stay within float32's range (values up to about 1e18).
+ */
+typedef struct qlora_norm {
+    const uint16_t *w_pre;        /* [cols] bf16, or NULL: no norm before the next block (no H) */
+    const uint16_t *w_post;       /* [cols] bf16, or NULL: no norm after the block */
+    const uint16_t *gate;         /* [ceil(M / gate_tokens), cols] bf16, or NULL: no gate */
+    int64_t gate_tokens;          /* consecutive tokens that share a gate row (with a gate: >= 1) */
+    int64_t cols;                 /* C, a multiple of 8, 8 .. 16384 */
+    float alpha, beta;            /* scales of the residual and of the block's output, finite */
+    float eps;                    /* > 0, finite */
+    int32_t resid_type;           /* R, R', dR, dR': NF4_ROWS_BF16 or NF4_ROWS_F32 */
+} qlora_norm;
+
+/*
+ * Forward.  R: [M, C]; B: [M, C] bf16, or NULL: only the norm before a block, H = norm(R) (then
+ * w_post, gate and R_out are NULL and alpha = beta = 1).  R_out: [M, C], required with B (it may be R
+ * itself).  H: [M, C] bf16, with w_pre.  Hq, Hs: optional, with H: its codes and constants, equal to
+ * nf4_int8_quantize's of H bit for bit, for qlora_int8_linear_fwd.  M >= 1.  No workspace.
+ */
+int qlora_norm_fwd(const qlora_norm *p, const void *R, const uint16_t *B, int64_t M, void *R_out, uint16_t *H,
+                   int8_t *Hq, float *Hs, void *stream);
+
+/*
+ * Backward of the same, with R_out as the forward wrote it (R itself where B was NULL); the root mean
+ * squares are recomputed.  With xh = R' / rms(R'), bh = B / rms(B):
+ *   t = dR' + (w_pre dH - xh mean(w_pre dH xh)) / rms(R');  dR = alpha t;  dw_pre = sum_m dH xh
+ *   u = beta gate t;  dgate = beta sum_m t n (over the tokens of a gate row);
+ *   dB = (w_post u - bh mean(w_post u bh)) / rms(B);  dw_post = sum_m u bh    (w_post NULL: dB = u)
+ *   dR_out: [M, C], or NULL: zero; dH: [M, C] bf16, given exactly when w_pre is; at least one of both.
+ *   dR: [M, C] of the residual's type (it may be dR_out itself).  dB: [M, C] bf16, required with B (it
+ *   may be dH or B itself).  dw_pre, dw_post: [C] bf16, dgate: like gate, each NULL: not computed.
+ *   workspace: >= qlora_norm_workspace_size(M, C) bytes, 16-byte aligned.
+ */
+size_t qlora_norm_workspace_size(int64_t M, int64_t C);
+int qlora_norm_bwd(const qlora_norm *p, const void *R_out, const uint16_t *B, const void *dR_out, const uint16_t *dH,
+                   int64_t M, void *dR, uint16_t *dB, uint16_t *dw_pre, uint16_t *dw_post, uint16_t *dgate,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Timing instrumentation (not part of the method).  While set on the calling thread, the library
  * records begin[i] and end[i] (hipEvent_t handles created by the caller) on the launch stream
  * immediately before and after the i-th subsequent launch of an instrumented kernel -- the

@@ -24,6 +24,9 @@ Quantized LLMs" study notes, gitcode.csdn.net/6a0046f754b52172bc72e356, unless n
 * ``backward``      -- section 3.5: gradients for the adapters only, through the BF16 weight.
 * ``swiglu_*``      -- not a step of the method: the gated MLP that the LLaMA-shaped workloads
                        wrap around three such linears.
+* ``int8_*``        -- section 3.1 eq. (1) with one constant per row (token or output channel) and
+                       the product of two such matrices.
+* ``norm_*``        -- not a step of the method: the norms, gate and residual sum between blocks.
 
 The bit-exact steps (codebook, quantize, double quant, dequant, bf16 and E4M3 rounding) are plain
 C in ``nf4_oracle.c``, built with gcc ``-O2 -ffp-contract=off``.  The linear-layer algebra is
@@ -391,6 +394,85 @@ def swiglu_bwd(dh, g, u):
     du = dh * g * sg
     dg = dh * u * sg * (1.0 + g * (1.0 - sg))
     return dg, du
+
+
+# ------------------------------------------------------------------------------------------
+# Int8 rows (eq. (1), one constant per row) and the norm glue between blocks
+# ------------------------------------------------------------------------------------------
+
+def int8_rows(x):
+    """(codes int8, scales float32) of each row: scale = fp32(max|x| / 127), code = the integer nearest
+    to the quotient x / scale, ties to even.  The float64 quotient decides as the real one does: x and
+    scale have 24 bits, so a quotient that is no half-integer is at least 2^-32 away from one.
+    Non-finite rows: scale NaN, codes 0."""
+    x = _f64(x)
+    fine = np.isfinite(x).all(axis=1)
+    x = np.where(fine[:, None], x, 0.0)
+    scales = (np.abs(x).max(axis=1) / 127.0).astype(np.float32)
+    step = np.where(scales > 0, scales, np.float32(np.inf)).astype(np.float64)
+    codes = np.clip(np.rint(x / step[:, None]), -127, 127).astype(np.int8)
+    return codes, np.where(fine, scales, np.float32(np.nan))
+
+
+def int8_weight_bf16(codes, scales) -> np.ndarray:
+    """bf16 bits of scale * code (one float32 product per element)."""
+    p = np.asarray(scales, np.float32)[:, None] * np.asarray(codes).astype(np.float32)
+    return bf16_rne(p).reshape(p.shape)
+
+
+def int8_product(Xq, xs, Wq, ws) -> np.ndarray:
+    """xs ws (Xq Wq^T): the integer sums exact (int64), the constants applied in float64."""
+    acc = np.asarray(Xq).astype(np.int64) @ np.asarray(Wq).astype(np.int64).T
+    return acc.astype(np.float64) * _f64(xs)[:, None] * _f64(ws)[None, :]
+
+
+def _gate_rows(gate, gate_tokens, M, C):
+    return np.ones((M, C)) if gate is None else _f64(gate)[np.arange(M) // gate_tokens]
+
+
+def norm_fwd(R, B=None, w_pre=None, w_post=None, gate=None, gate_tokens=0, alpha=1.0, beta=1.0, eps=1e-6):
+    """R' = alpha R + beta gate * n, n = w_post B / rms(B) (or B); H = w_pre R' / rms(R')."""
+    R = _f64(R)
+    rms = lambda x: np.sqrt((x * x).mean(axis=1, keepdims=True) + eps)  # noqa: E731
+    if B is not None:
+        B = _f64(B)
+        n = B if w_post is None else _f64(w_post) * B / rms(B)
+        R = alpha * R + beta * _gate_rows(gate, gate_tokens, *B.shape) * n
+    return R, None if w_pre is None else _f64(w_pre) * R / rms(R)
+
+
+def norm_bwd(R_out, B=None, dR_out=None, dH=None, w_pre=None, w_post=None, gate=None, gate_tokens=0, alpha=1.0,
+             beta=1.0, eps=1e-6):
+    """Gradients at R' = R_out, row by row: each norm's Jacobian is formed and applied (no fused form)."""
+    R = _f64(R_out)
+    M, C = R.shape
+    t = np.zeros((M, C)) if dR_out is None else _f64(dR_out).copy()
+
+    def through(x, w, dy):
+        """(dx, dw) of y = w x / rms(x) for one row: dy_i/dx_j = w_i (delta_ij / q - x_i x_j / (C q^3))."""
+        q = np.sqrt((x * x).mean() + eps)
+        jac = w[:, None] * (np.eye(C) / q - np.outer(x, x) / (C * q ** 3))
+        return jac.T @ dy, dy * x / q
+
+    out = {}
+    if w_pre is not None:
+        rows = [through(R[m], _f64(w_pre), _f64(dH)[m]) for m in range(M)]
+        t += np.stack([r[0] for r in rows])
+        out["dw_pre"] = np.sum([r[1] for r in rows], axis=0)
+    if B is None:
+        return {**out, "dR": t}
+    B = _f64(B)
+    out["dR"] = alpha * t
+    g = _gate_rows(gate, gate_tokens, M, C)
+    n, _ = (B, None) if w_post is None else norm_fwd(B, w_pre=w_post, eps=eps)[::-1]
+    if gate is not None:
+        out["dgate"] = np.zeros(_f64(gate).shape)
+        np.add.at(out["dgate"], np.arange(M) // gate_tokens, beta * t * n)
+    u = beta * g * t
+    if w_post is None:
+        return {**out, "dB": u}
+    rows = [through(B[m], _f64(w_post), u[m]) for m in range(M)]
+    return {**out, "dB": np.stack([r[0] for r in rows]), "dw_post": np.sum([r[1] for r in rows], axis=0)}
 
 
 # ------------------------------------------------------------------------------------------

@@ -1,0 +1,370 @@
+"""GPU parity of the Int8 rows and the Int8 linear layer against the oracle (exact codes, float64
+products), element by element.
+
+Tolerances, from the roundings on the way (u = 2^-24, a float32 step's half; h = 2^-8, a bf16 one's):
+  Y: one bf16 rounding (h |Y|); the integer sum is exact, its conversion and the two constants round
+     3 u of its size; s T is rounded to bf16 (h of each of the adapter's r products) and summed in
+     float32 as T is: a sum of n float32 terms is off by at most n u of the sum of their sizes.
+  dX: the products are bf16 x bf16, exact in float32: (N + r + 16) u of the sizes' sum, h |dX|, and
+     dT's bf16 rounding, h of the adapter's products; likewise dL1, dL2 (sums over the tokens).
+"""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import bit_nf4_quantized_codebook_amd as nf4  # noqa: E402
+
+DEV = torch.device("cuda:0")
+U, H = 2.0 ** -24, 2.0 ** -8
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+def bf16(a):
+    """(device bf16 tensor, its values in float64)"""
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).bfloat16()
+    return t.to(DEV), t.double().numpy()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def within(name, got, ref, tol):
+    got = f64(got)
+    assert got.shape == ref.shape, name
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], ref[bad][:4], tol[bad][:4])
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ---- rows to codes ----
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 8), (3, 64), (5, 1000), (2, 2056), (130, 512), (7, 4096), (3, 8200), (2, 16384),
+                                       (2, 28672), (1, 131008)])
+def test_quantize_rows_bit_exact(rows, cols, f32):
+    x = synth.normal_f32(100 + rows + cols, (rows, cols), 1.0)
+    x[0, cols // 2] = -37.5
+    xd = dev(x) if f32 else bf16(x)[0]
+    codes, scales = nf4.nf4_int8_quantize(xd)
+    rc, rs = oracle.int8_rows(f64(xd))
+    assert np.array_equal(codes.cpu().numpy(), rc)
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+
+
+def _border_rows():
+    """Rows where the code is decided next to a border: half-integer quotients (the constant a power of
+    two), the floats just beside them, tiny and huge constants, denormals, zeros, signed zeros."""
+    rng = np.random.default_rng(9)
+    rows = []
+    for scale in (0.5, 1.0, 2.0 ** -20, 2.0 ** 90, 2.0 ** -110, 2.0 ** -130):
+        k = rng.integers(-126, 127, 256)
+        v = (k + 0.5).astype(np.float32)
+        v[::3] = np.nextafter(v[::3], np.float32(np.inf))
+        v[1::3] = np.nextafter(v[1::3], np.float32(-np.inf))
+        v[0] = 127.0
+        rows.append((v * np.float32(scale)).astype(np.float32))
+    for a in (0.7, 1.3e-20, 3.3e38, 1e-37, 2e-40, 1e-44):        # quotients beside k + 1/2 with a ragged constant
+        s = np.float32(a / 127.0)
+        v = ((rng.integers(-126, 127, 256) + 0.5) * float(s)).astype(np.float32)
+        v[::3] = np.nextafter(v[::3], np.float32(np.inf))
+        v[1::3] = np.nextafter(v[1::3], np.float32(-np.inf))
+        v[0] = a
+        rows.append(v)
+    rows += [np.zeros(256, np.float32), np.full(256, -0.0, np.float32), np.full(256, 1e-45, np.float32),
+             np.full(256, np.float32(3.4028235e38), np.float32)]
+    return np.stack(rows)
+
+
+def test_quantize_rows_next_to_borders():
+    x = _border_rows()
+    codes, scales = nf4.nf4_int8_quantize(dev(x))
+    rc, rs = oracle.int8_rows(x)
+    for i in range(len(x)):
+        assert np.array_equal(codes[i].cpu().numpy(), rc[i]), (i, x[i][codes[i].cpu().numpy() != rc[i]])
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), rs.view(np.uint32))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_quantize_rows_not_finite(bad):
+    x = synth.normal_f32(11, (4, 520), 1.0)
+    x[2, 519] = bad
+    for xd in (dev(x), bf16(x)[0]):
+        codes, scales = nf4.nf4_int8_quantize(xd)
+        clean = xd.clone()
+        clean[2] = 0
+        c2, s2 = nf4.nf4_int8_quantize(clean)
+        assert same(codes, c2) and torch.isnan(scales[2])
+        assert same(scales[[0, 1, 3]], s2[[0, 1, 3]])
+
+
+def test_quantize_no_rows():
+    codes, scales = nf4.nf4_int8_quantize(torch.empty((0, 64), device=DEV))
+    assert codes.shape == (0, 64) and scales.shape == (0,)
+
+
+@pytest.mark.parametrize("N,K", [(8, 64), (200, 320), (1032, 576)])
+def test_dequant_bit_exact(N, K):
+    w = nf4.Int8Weight.from_float(dev(synth.normal_f32(12, (N, K), 0.02)))
+    ref = oracle.int8_weight_bf16(w.codes.cpu().numpy(), w.scales.cpu().numpy())
+    assert np.array_equal(nf4.nf4_int8_dequant(w).view(torch.int16).cpu().numpy().view(np.uint16), ref)
+
+
+# ---- the linear layer ----
+
+class Lin:
+    def __init__(self, seed, N, K, r):
+        self.w = nf4.Int8Weight.from_float(dev(synth.heavy_tail_f32(seed, seed + 1, (N, K), 0.02, 0.2, 0.01)))
+        self.Wq, self.ws = self.w.codes.cpu().numpy(), self.w.scales.cpu().numpy()
+        self.L1 = self.L2 = self.l1 = self.l2 = None
+        if r:
+            self.L1, self.l1 = bf16(synth.normal_f32(seed + 2, (K, r), 1.0 / r))
+            self.L2, self.l2 = bf16(synth.normal_f32(seed + 3, (r, N), 0.05))
+
+
+def check_fwd(lin, X, s, Y, T, Xq=None):
+    x = f64(X)
+    codes, scales = oracle.int8_rows(x) if Xq is None else Xq
+    ref = oracle.int8_product(codes, scales, lin.Wq, lin.ws)
+    tol = 3 * U * np.abs(ref)
+    K = x.shape[1]
+    if lin.l1 is not None:
+        t = x @ lin.l1
+        t_tol = (K + 70) * U * (np.abs(x) @ np.abs(lin.l1))
+        if T is not None:
+            within("T", T, t, H * np.abs(t) + 1.01 * t_tol)
+        r = lin.l1.shape[1]
+        lora = np.abs(s) * (np.abs(t) @ np.abs(lin.l2))
+        tol = tol + abs(s) * (t_tol @ np.abs(lin.l2)) * 1.01 + (H + (r + 8) * U) * 1.01 * lora + 2 * U * np.abs(ref)
+        ref = ref + s * (t @ lin.l2)
+    within("Y", Y, ref, H * (np.abs(ref) + tol) + tol)
+
+
+FWD = [  # M, N, K, r
+    (1, 8, 64, 0), (1, 8, 64, 8), (1, 256, 256, 16), (2, 520, 1024, 8), (3, 1032, 4096, 64), (4, 264, 8192, 128),
+    (5, 4096, 320, 24), (8, 512, 1088, 64), (9, 72, 128, 8), (16, 2056, 2048, 40), (17, 264, 512, 0), (31, 1000, 704, 16),
+    (33, 328, 1600, 64), (63, 600, 640, 8), (64, 512, 4096, 128), (65, 256, 256, 16), (100, 264, 192, 72),
+    (128, 1040, 1024, 64), (255, 304, 576, 0), (257, 520, 320, 128), (300, 768, 2752, 64), (515, 1032, 512, 8),
+    (1024, 256, 1024, 64), (1100, 520, 448, 16),
+]
+
+
+@pytest.mark.parametrize("M,N,K,r", FWD)
+def test_linear_forward(M, N, K, r):
+    print(f"int8 forward M={M} N={N} K={K} r={r}", flush=True)
+    lin = Lin(2000 + M + N, N, K, r)
+    X, _ = bf16(synth.heavy_tail_f32(2001 + M, 2002 + K, (M, K), 1.0, 20.0, 0.01))
+    s = 16.0 / r if r else 1.0
+    Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, s)
+    assert (T is None) == (r == 0)
+    check_fwd(lin, X, s, Y, T)
+    # the codes given beforehand: the same bits
+    Y2, T2 = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, s, Xq=nf4.nf4_int8_quantize(X))
+    assert same(Y, Y2) and (T is None or same(T, T2))
+    if not r:
+        Y3, _ = nf4.qlora_int8_linear_fwd(lin.w, None, Xq=nf4.nf4_int8_quantize(X))
+        assert same(Y, Y3)
+    else:
+        Y4, T4 = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, s, keep_T=False)
+        assert T4 is None and same(Y, Y4)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1, 264, 512, 8), (6, 136, 320, 0), (40, 264, 512, 16), (300, 264, 576, 8)])
+def test_linear_forward_extreme_codes(M, N, K, r):
+    """Every code -128 or 127 (sums at the integer range's end of this K), codes given by the caller."""
+    lin = Lin(2300 + M, N, K, r)
+    rng = np.random.default_rng(M)
+    lin.Wq = np.where(rng.random((N, K)) < 0.9, -128, 127).astype(np.int8)
+    lin.w = nf4.Int8Weight(dev(lin.Wq), lin.w.scales)
+    X, _ = bf16(synth.normal_f32(2301, (M, K), 1.0))
+    xq = np.where(rng.random((M, K)) < 0.9, -128, 127).astype(np.int8)
+    xs = rng.random(M).astype(np.float32)
+    Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, Xq=(dev(xq), dev(xs)))
+    check_fwd(lin, X, 0.5, Y, T, (xq, xs))
+
+
+def test_linear_forward_longest_reduction():
+    """K at its limit with every product 128 * 128: the sum is 65504 * 2^15, just inside int32."""
+    for M in (1, 3, 20, 70):
+        K, N = 131008, 8
+        w = nf4.Int8Weight(torch.full((N, K), -128, dtype=torch.int8, device=DEV), torch.ones(N, device=DEV))
+        Xq = (torch.full((M, K), -128, dtype=torch.int8, device=DEV), torch.ones(M, device=DEV))
+        Y, _ = nf4.qlora_int8_linear_fwd(w, None, Xq=Xq)
+        assert (Y.double() == torch.tensor(131008.0 * 16384).bfloat16().double()).all(), M
+
+
+@pytest.mark.parametrize("M", [1, 5, 30, 200])
+def test_linear_forward_rows_that_are_not_finite_or_zero(M):
+    N, K, r = 264, 512, 8
+    lin = Lin(2400, N, K, r)
+    x = synth.normal_f32(2401, (M + 2, K), 1.0)
+    X, _ = bf16(x)
+    Y, _ = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+    Xb = X.clone()
+    Xb[M // 2, 3] = float("nan")
+    Xb[M, K - 1] = float("inf")
+    Xb[M + 1] = 0
+    Yb, _ = nf4.qlora_int8_linear_fwd(lin.w, Xb, lin.L1, lin.L2, 0.5)
+    assert torch.isnan(Yb[M // 2]).all() and torch.isnan(Yb[M]).all() and (Yb[M + 1] == 0).all()
+    keep = [m for m in range(M) if m != M // 2]
+    assert same(Yb[keep], Y[keep])
+
+
+def test_linear_forward_leaves_the_rest_alone():
+    """Outputs inside larger buffers: what stands before and after them stays."""
+    for M, N, K, r in ((1, 72, 128, 8), (13, 72, 128, 8), (70, 264, 192, 16), (257, 520, 128, 8)):
+        lin = Lin(2500, N, K, r)
+        X, _ = bf16(synth.normal_f32(2501, (M, K), 1.0))
+        buf = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+        tb = torch.full((M + 2, r), 7.0, dtype=torch.bfloat16, device=DEV)
+        Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, Y=buf[1:M + 1], T=tb[1:M + 1])
+        check_fwd(lin, X, 0.5, Y, T)
+        for b in (buf, tb):
+            assert (b[0] == 7).all() and (b[M + 1] == 7).all()
+
+
+BWD = [(1, 8, 64, 8), (1, 264, 512, 0), (5, 520, 320, 16), (16, 264, 1088, 64), (37, 1032, 576, 128), (64, 512, 256, 8),
+       (100, 264, 704, 24), (300, 776, 1024, 64), (1024, 256, 512, 16), (1100, 520, 448, 0)]
+
+
+@pytest.mark.parametrize("M,N,K,r", BWD)
+def test_linear_backward(M, N, K, r):
+    print(f"int8 backward M={M} N={N} K={K} r={r}", flush=True)
+    lin = Lin(3000 + M + N, N, K, r)
+    Wb = oracle.bf16_to_f32(oracle.int8_weight_bf16(lin.Wq, lin.ws)).astype(np.float64)
+    dY, dy = bf16(synth.normal_f32(3001 + M, (M, N), 1.0))
+    s = 16.0 / r if r else 1.0
+    size = np.abs(dy) @ np.abs(Wb)
+    if not r:
+        dX, dL1, dL2 = nf4.qlora_int8_linear_bwd(lin.w, dY)
+        assert dL1 is None and dL2 is None
+        ref = dy @ Wb
+        within("dX", dX, ref, H * np.abs(ref) + 1.01 * (N + 16) * U * size)
+        return
+    X, x = bf16(synth.normal_f32(3002 + M, (M, K), 1.0))
+    T, t = bf16(x @ lin.l1)
+    dX, dL1, dL2 = nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, T, s)
+    dt = s * (dy @ lin.l2.T)
+    dt_size = abs(s) * (np.abs(dy) @ np.abs(lin.l2.T))
+    dt_tol = H * np.abs(dt) + 1.01 * (N + 70) * U * dt_size
+    ref = dy @ Wb + dt @ lin.l1.T
+    tol = 1.01 * (N + r + 16) * U * (size + np.abs(dt) @ np.abs(lin.l1.T)) + dt_tol @ np.abs(lin.l1.T)
+    within("dX", dX, ref, H * (np.abs(ref) + tol) + tol)
+    ref = x.T @ dt
+    tol = 1.01 * (M + 70) * U * (np.abs(x).T @ np.abs(dt)) + np.abs(x).T @ dt_tol
+    within("dL1", dL1, ref, H * (np.abs(ref) + tol) + tol)
+    ref = s * (t.T @ dy)
+    tol = 1.01 * (M + 70) * U * abs(s) * (np.abs(t).T @ np.abs(dy))
+    within("dL2", dL2, ref, H * (np.abs(ref) + tol) + tol)
+    # T left out: computed again, to bf16 of the same sums (their order may differ by a rounding)
+    again = nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, None, s)
+    assert same(again[0], dX) and same(again[1], dL1)
+    t_tol = 2 * H * np.abs(t) + 1.01 * (K + 70) * U * (np.abs(x) @ np.abs(lin.l1))
+    tol = tol + abs(s) * (t_tol.T @ np.abs(dy))
+    within("dL2 (T again)", again[2], ref, H * (np.abs(ref) + tol) + tol)
+    # without dX; and added to what is there (the sum in float32, one rounding)
+    none, dL1b, dL2b = nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, T, s, need_dX=False)
+    assert none is None and same(dL1b, dL1) and same(dL2b, dL2)
+    base, bv = bf16(synth.normal_f32(3003, (M, K), 3.0))
+    acc, _, _ = nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, T, s, dX=base, accumulate=True)
+    ref = dy @ Wb + dt @ lin.l1.T + bv
+    tol = 1.01 * (N + r + 17) * U * (size + np.abs(dt) @ np.abs(lin.l1.T) + np.abs(bv)) + dt_tol @ np.abs(lin.l1.T)
+    within("dX accumulated", acc, ref, H * (np.abs(ref) + tol) + tol)
+
+
+def test_linear_repeats_bit_for_bit_and_with_a_dirty_workspace():
+    for M, N, K, r in ((1, 1032, 4096, 64), (20, 520, 2048, 16), (200, 520, 4096, 64), (1100, 520, 1024, 8)):
+        lin = Lin(4000, N, K, r)
+        X, _ = bf16(synth.normal_f32(4001, (M, K), 1.0))
+        dY, _ = bf16(synth.normal_f32(4002, (M, N), 1.0))
+        n = nf4.qlora_int8_linear_workspace_size(M, N, K, r)
+        first = None
+        for fill in (0, 0x7F, 0xFF):
+            ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+            Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, workspace=ws)
+            ws.fill_(fill)
+            out = (Y, T) + nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, T, 0.5, workspace=ws)
+            first = first or out
+            assert all(same(a, b) for a, b in zip(first, out)), (M, fill)
+
+
+def test_linear_on_a_side_stream_and_two_at_once():
+    M, N, K, r = 12, 520, 2048, 16
+    lin = Lin(4100, N, K, r)
+    X, _ = bf16(synth.normal_f32(4101, (M, K), 1.0))
+    ref, _ = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                got.append(nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)[0])
+    torch.cuda.synchronize()
+    assert all(same(ref, y) for y in got)
+
+
+@pytest.mark.parametrize("M", [1, 16, 300, 1100])
+def test_linear_step_captured_and_replayed(M):
+    N, K, r = 520, 1024, 16
+    lin = Lin(4200, N, K, r)
+    X, _ = bf16(synth.normal_f32(4201, (M, K), 1.0))
+    dY, _ = bf16(synth.normal_f32(4202, (M, N), 1.0))
+
+    def step():
+        Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+        return (Y, T) + nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, T, 0.5)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step()
+    for rep in range(3):
+        X.copy_(bf16(synth.normal_f32(4210 + rep, (M, K), 1.0))[0])
+        dY.copy_(bf16(synth.normal_f32(4220 + rep, (M, N), 1.0))[0])
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(outs, step())), rep
+        torch.cuda.synchronize()
+
+
+def test_binding_refusals():
+    lin = Lin(4300, 64, 128, 8)
+    X, _ = bf16(np.ones((4, 128)))
+    for bad in (lambda: nf4.qlora_int8_linear_fwd(lin.w, X.t().contiguous(), lin.L1, lin.L2),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2[:, :56].contiguous()),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X[:, ::2]),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X, T=X),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X, Y=X),
+                lambda: nf4.qlora_int8_linear_bwd(lin.w, X[:, :64].contiguous(), accumulate=True),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)),
+                lambda: nf4.Int8Weight(lin.w.codes, lin.w.scales[:8])):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: nf4.qlora_int8_linear_fwd(lin.w, X.float()), lambda: nf4.nf4_int8_quantize(X.half()),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, None), lambda: nf4.Int8Weight(lin.w.codes.int(), None)):
+        with pytest.raises(TypeError):
+            bad()
+    with pytest.raises(nf4.NF4Error):
+        nf4.qlora_int8_linear_fwd(lin.w, X[:0])
+    with pytest.raises(nf4.NF4Error):
+        nf4.nf4_int8_quantize(torch.zeros((2, 12), device=DEV))
