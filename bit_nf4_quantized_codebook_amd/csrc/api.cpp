@@ -1014,11 +1014,12 @@ nf4k::Int8View view_of(const nf4_int8_weight *w) { return nf4k::Int8View{w->code
 
 struct Int8Plan {
     int ksT, ksdT, msL2, msL1;
-    nf4k::SplitPlan kb;            // split of the backward's dX product
-    size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_P, off_Wd, off_Pg, total;
+    nf4k::SplitPlan kf, kb;        // split of the forward's product and of the backward's dX product
+    size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_L2T, off_P, off_Wd, off_Pg, total;
 };
 
-// One layout for both directions: the forward uses Xq, xs, sT and P, the backward T, dT, P, Wd and Pg.
+// One layout for both directions: the forward uses Xq, xs, sT, L2T, P and Pg, the backward T, dT, P, Wd
+// and Pg.
 Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     Int8Plan p;
     const int64_t mt = (M + kTile - 1) / kTile, rt = (r + kTile - 1) / kTile;
@@ -1035,15 +1036,19 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     }
     const int64_t tiles = (M + kGemmTile - 1) / kGemmTile * ((K + kGemmTile - 1) / kGemmTile);
     p.kb = nf4k::gemm_split(tiles, (N + kTile - 1) / kTile, kSplitQuantum);
+    p.kf = nf4k::int8_gemm_split(M, N, K);
+    size_t pg = p.kb.ksplit > 1 ? (size_t)p.kb.ksplit * M * K : 0;
+    if (p.kf.ksplit > 1 && (size_t)p.kf.ksplit * M * N > pg) pg = (size_t)p.kf.ksplit * M * N;
     size_t off = 0;
     p.off_Xq = off;  off += round256((size_t)M * K);
     p.off_xs = off;  off += round256((size_t)M * 4);
     p.off_T = off;   off += round256((size_t)M * r * 2);
     p.off_sT = off;  off += round256((size_t)M * r * 2);
     p.off_dT = off;  off += round256((size_t)M * r * 2);
+    p.off_L2T = off; off += round256((size_t)N * r * 2);
     p.off_P = off;   off += round256(pmax * 4);
     p.off_Wd = off;  off += round256((size_t)N * K * 2);
-    p.off_Pg = off;  off += round256(p.kb.ksplit > 1 ? (size_t)p.kb.ksplit * M * K * 4 : 0);
+    p.off_Pg = off;  off += round256(pg * 4);
     p.total = off;
     return p;
 }
@@ -1116,22 +1121,34 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
     if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "int8 linear workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    // T's partials; then one launch for X's codes, T's sum and L2's transpose; then the product
+    nf4k::Int8Prep prep{};
+    prep.M = M; prep.K = K; prep.N = N; prep.r = r;
     if (!Xq) {
-        int8_t *q = ws_at<int8_t>(workspace, p.off_Xq);
-        float *qs = ws_at<float>(workspace, p.off_xs);
-        NF4_CHECK_HIP(nf4k::launch_int8_rows(X, false, M, K, q, qs, s), "int8 quantize (fwd)");
-        Xq = q;
-        xs = qs;
+        prep.X = X;
+        prep.Xq = ws_at<int8_t>(workspace, p.off_Xq);
+        prep.xs = ws_at<float>(workspace, p.off_xs);
+        Xq = prep.Xq;
+        xs = prep.xs;
     }
-    uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT);
+    uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT), *L2T = ws_at<uint16_t>(workspace, p.off_L2T);
+    float *P = ws_at<float>(workspace, p.off_P);
+    const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
     if (r) {
-        float *P = ws_at<float>(workspace, p.off_P);
         NF4_CHECK_HIP(nf4k::launch_skinny_nt(X, L1, /*b_rows_k=*/true, P, M, r, K, p.ksT, s), "T = X L1");
-        const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
-        NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "T reduce");
+        prep.Tred = &red;
+        prep.L2 = L2;
+        prep.L2T = L2T;
     }
-    NF4_CHECK_HIP(nf4k::launch_int8_gemm(nf4k::Int8Product{Xq, w->codes, xs, w->scales, sT, L2, M, N, K, r, Y}, s),
+    NF4_CHECK_HIP(nf4k::launch_int8_prep(prep, s), "int8 quantize + T reduce + L2 transpose");
+    float *Pg = ws_at<float>(workspace, p.off_Pg);
+    NF4_CHECK_HIP(nf4k::launch_int8_gemm(nf4k::Int8Product{Xq, w->codes, xs, w->scales, sT, L2T, M, N, K, r, Y,
+                                                           p.kf.ksplit, (int32_t)p.kf.per, Pg}, s),
                   "int8 GEMM (fwd)");
+    if (p.kf.ksplit > 1) {
+        const nf4k::Reduction sum{Pg, p.kf.ksplit, M * N, 1.0f, Y, 0.0f, nullptr};
+        NF4_CHECK_HIP(nf4k::launch_reduce_partials(sum, nullptr, s), "split product reduce");
+    }
     return NF4_OK;
 }
 

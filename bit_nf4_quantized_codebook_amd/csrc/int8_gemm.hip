@@ -1,10 +1,29 @@
-// Int8 product of the Int8 QLoRA linear forward (gfx950):
+// Int8 product of the Int8 QLoRA linear forward from 65 tokens (gfx950):
 //   Y[m, n] = xs[m] ws[n] sum_k Xq[m, k] Wq[n, k] + (sT L2)[m, n]
 //
 // Page: "QLoRA: Efficient Finetuning of Quantized LLMs" study notes (gitcode.csdn.net), section 3.1
 // eq. (1) (8-bit integers), section 3.5 eq. (5), section 4 eq. (3).
 //
-// Block tile 64 x 64, reduction step 64, four waves of 32 x 32 with v_mfma_i32_32x32x32_i8.
+// The integer sums are exact in any order (K * 2^14 < 2^31), so only the epilogue rounds: the sum to
+// float32, times the two constants, plus the adapter's product, once to bf16.
+//
+// Block tile 256 x 256 outputs, reduction step 128 (128-byte LDS rows), 4 waves in 2 x 2, each
+// 128 x 128 with v_mfma_i32_32x32x32_i8 (16 tiles, 256 int32 accumulators): a 32 x 32 x 32 int8 MFMA
+// takes the operand bytes and the cycles of a 32 x 32 x 16 bf16 one, so the loop moves the same bytes
+// per cycle as the bf16 GEMM's and does twice its products.  Both operands go straight from global
+// memory to LDS (buffer_load ... lds), two 32 KB stages each, 16-byte chunks XOR-swizzled by
+// (row / 2) so that the fragment reads are free of bank conflicts.  After the last step the
+// accumulators are turned to float32 tile by tile and the adapter's r/64 steps run on them with
+// v_mfma_f32_32x32x16_bf16, whose output layout is the same.  (All 16 tiles turned first and then
+// multiplied, the kernel spilled 70 registers.)
+//
+// Bound by the MFMA loop: the whole forward call (codes of X, T, this product) takes 355 us at 2048
+// tokens through a 22016 x 8192 weight with r = 64 (2.1 POPS) and 89 us at 4096 through 4096 x 4096;
+// a 64 x 64 tile with one LDS stage took 1667 and 420 us.
+//
+// Few output tiles (fewer than half the CUs): the reduction is split over up to 16 workgroups per
+// tile, each writing a scaled float32 partial tile (the last also the adapter's product), summed
+// afterwards in a fixed order.
 
 #include "common.h"
 #include "dqtile.h"
@@ -15,57 +34,268 @@ namespace nf4k {
 
 namespace {
 
-constexpr int BT = 64;
-constexpr int PITCH = BT + 16;     // bytes of a padded LDS row
+constexpr int TM = 256, TN = 256;
+constexpr int TKB = 128;                    // bytes of a reduction step: 128 codes, or 64 bf16 of the adapter
+constexpr int STAGE = TM * TKB;             // 32 KB per operand stage
 
-__global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Product g) {
-    __shared__ __align__(16) uint8_t As[BT * PITCH];
-    __shared__ __align__(16) uint8_t Bs[BT * PITCH];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave >> 1, wn = wave & 1, r32 = lane & 31, hh = lane >> 5;
-    const int64_t m0 = (int64_t)blockIdx.y * BT, n0 = (int64_t)blockIdx.x * BT;
+__global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
+    // one LDS object per stage: a fragment read of one stage provably never aliases the
+    // direct-to-LDS loads in flight into the other
+    __shared__ __align__(16) uint8_t As0[STAGE];
+    __shared__ __align__(16) uint8_t As1[STAGE];
+    __shared__ __align__(16) uint8_t Bs0[STAGE];
+    __shared__ __align__(16) uint8_t Bs1[STAGE];
+    __shared__ __align__(16) float xs_l[TM];
+    __shared__ float ws_l[TN];
+    typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave >> 1, wn = wave & 1;
+    const int r32 = lane & 31, hh = lane >> 5;
+
+    const int ntm = (int)((g.M + TM - 1) / TM);
+    const int ntn = (int)((g.N + TN - 1) / TN);
+    const int ntiles = ntm * ntn;
+    const int split = (int)(blockIdx.x / (uint32_t)ntiles);
+    int tm, tn;
+    tile_coords_grouped<4>(ntm, ntn, (int)blockIdx.x - split * ntiles, tm, tn);
+    const int64_t m0 = (int64_t)tm * TM;
+    const int64_t n0 = (int64_t)tn * TN;
+    // this workgroup's reduction steps: kb .. kb + steps - 1
+    const int all_steps = (int)((g.K + TKB - 1) / TKB);
+    const int kb = split * g.split_per;
+    const int steps = min(all_steps - kb, g.split_per);
+    const int ext_steps = split == g.ksplit - 1 ? (g.r + 63) / 64 : 0;
+
+    // tile-relative descriptors: rows past M (or N) read zeros
     const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.Xq + m0 * g.K, (g.M - m0) * g.K);
     const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.Wq + n0 * g.K, (g.N - n0) * g.K);
-    const int row = tid >> 2, q = tid & 3;
-    i32x16 acc = {};
-    for (int64_t k0 = 0; k0 < g.K; k0 += BT) {
-        const uint32_t off = (uint32_t)(row * g.K + k0 + 16 * q);
-        const u32x4 a = bload16(rA, off), b = bload16(rB, off);
-        __syncthreads();
-        *reinterpret_cast<u32x4 *>(As + row * PITCH + 16 * q) = a;
-        *reinterpret_cast<u32x4 *>(Bs + row * PITCH + 16 * q) = b;
-        __syncthreads();
+
+    // Loads: instruction q of wave w writes stage rows 8u .. 8u+7 (u = 8w + q); lane l takes row
+    // 8u + l/8 and physical chunk l%8, which holds logical chunk (l%8) ^ ((row/2)%8); (row/2)%8 =
+    // (4q + l/16)%8, so the lane's chunk depends only on the parity of q.
+    int a_col[2];
+    uint32_t voff[2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const i32x4 fa = *reinterpret_cast<const i32x4 *>(As + (wm * 32 + r32) * PITCH + s * 32 + hh * 16);
-            const i32x4 fb = *reinterpret_cast<const i32x4 *>(Bs + (wn * 32 + r32) * PITCH + s * 32 + hh * 16);
-            acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa, fb, acc, 0, 0, 0);
-        }
+    for (int q = 0; q < 2; ++q) {
+        const int row = 8 * (8 * wave + q) + (lane >> 3);
+        a_col[q] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+        voff[q] = (uint32_t)((lane >> 3) * g.K + a_col[q]);
     }
-    const int64_t n = n0 + wn * 32 + r32;
-    if (n >= g.N) return;
-    const float ws = g.ws[n];
+    const uint32_t wave_off = (uint32_t)(64 * wave * g.K);
+    const uint32_t row8_off = (uint32_t)(8 * g.K);
+    // Codes at or past the end of the split (the ragged last step, the steps past the end) read
+    // zeros; the whole offset sits in the lane offset, so rows past the operand's end are out of
+    // range for the descriptor's bound check.
+    const int kend = (int)min(g.K, (int64_t)(kb + steps) * TKB);
+    auto load = [&](__amdgpu_buffer_rsrc_t r, int step, uint8_t *st, int q0 = 0, int q1 = 8) {
+        lds_u8 *dst = (lds_u8 *)st + wave * 8192;
+        const int k0 = (kb + step) * TKB, rem = kend - k0;
+        const uint32_t base = wave_off + (uint32_t)k0;
+        const uint32_t v0 = a_col[0] < rem ? voff[0] + base : 0x80000000u;
+        const uint32_t v1 = a_col[1] < rem ? voff[1] + base : 0x80000000u;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int64_t m = m0 + wm * 32 + (v >> 2) * 8 + hh * 4 + (v & 3);
-        if (m >= g.M) continue;
-        float y = ((float)acc[v] * g.xs[m]) * ws;
-        float l = 0.0f;
-        for (int j = 0; j < g.r; ++j)
-            l = __builtin_fmaf(bf16_to_f32(g.sT[m * g.r + j]), bf16_to_f32(g.L2[(int64_t)j * g.N + n]), l);
-        g.Y[m * g.N + n] = (uint16_t)f32_to_bf16(y + l);
+        for (int q = 0; q < 8; ++q) {
+            if (q < q0 || q >= q1) continue;
+            const uint32_t v = ((q & 1) ? v1 : v0) + (uint32_t)q * row8_off;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(dst + q * 1024), 16, v, 0, 0, 0);
+        }
+    };
+
+    i32x16 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+
+    // fragment of sub-step s (32 bytes of the row): lane (r32, hh) takes its 16-byte chunk 2 s + hh
+    uint32_t lds_off[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) lds_off[s] = (uint32_t)(r32 * 128 + (((2 * s + hh) ^ ((r32 >> 1) & 7)) * 16));
+    struct Frags {
+        i32x4 a[4], b[4];
+    };
+    auto read = [&](const uint8_t *Ast, const uint8_t *Bst, int s, Frags &f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f.a[i] = *reinterpret_cast<const i32x4 *>(Ast + lds_off[s] + (wm * 128 + 32 * i) * 128);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f.b[j] = *reinterpret_cast<const i32x4 *>(Bst + lds_off[s] + (wn * 128 + 32 * j) * 128);
+    };
+    auto mma = [&](const Frags &f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+    };
+    // The schedule is the bf16 GEMM's: fragment reads one sub-step ahead of the MFMAs, each of the
+    // first 8 MFMAs of a sub-step followed by one read, and in a sub-step that carries loads every
+    // second MFMA by one direct-to-LDS load.
+    auto interleave = [&](int nvmem) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                             // 1 MFMA
+            if (k < 8) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                  // 1 DS read
+            if ((k & 1) && (k >> 1) < nvmem) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // 1 VMEM
+        }
+    };
+    // One step computes stage (Ac, Bc) while step + 1 lands in (An, Bn).  The workgroup barrier sits
+    // between sub-steps 2 and 3: by then every wave has its sub-step 3 fragments in registers, so
+    // after it stage c is free for the loads of step + 2, and stage n is complete.
+    Frags f0, f1;
+    auto step_body = [&](int step, uint8_t *Ac, uint8_t *Bc, uint8_t *An, uint8_t *Bn) {
+#pragma unroll
+        for (int s = 0; s < 3; ++s) {
+            Frags &cur = (s & 1) ? f1 : f0;
+            Frags &nxt = (s & 1) ? f0 : f1;
+            if (s == 0) {
+                load(rA, step + 1, An, 4, 8);
+                load(rB, step + 1, Bn, 4, 8);
+            }
+            read(Ac, Bc, s + 1, nxt);
+            mma(cur);
+            interleave(s == 0 ? 8 : 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // step + 1 landed (this wave's loads) and this wave's fragment reads of stage c are done
+        __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (0 << 8));
+        __syncthreads();
+        read(An, Bn, 0, f0);
+        load(rA, step + 2, Ac, 0, 4);
+        load(rB, step + 2, Bc, 0, 4);
+        mma(f1);
+        interleave(8);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    load(rA, 0, As0);
+    load(rB, 0, Bs0);
+    load(rA, 1, As1, 0, 4);
+    load(rB, 1, Bs1, 0, 4);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    read(As0, Bs0, 0, f0);
+    int step = 0;
+    for (; step + 1 < steps; step += 2) {
+        step_body(step, As0, Bs0, As1, Bs1);
+        step_body(step + 1, As1, Bs1, As0, Bs0);
+    }
+    if (step < steps) step_body(step, As0, Bs0, As1, Bs1);   // odd count: the last one
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+
+    // lane indices for the code after the main loop, recomputed (mbcnt) rather than kept live
+    // across it
+    const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    const int r32_e = lane_e & 31, hh_e = lane_e >> 5;
+    const int tid_e = wave * 64 + lane_e;
+
+    // ---- epilogue operands into LDS: the tile's constants, and the adapter's steps (r <= 128: at most
+    // two), sT rows in the A stages and L2^T rows in the B stages, zero padded past r ----
+    if (tid_e < TM) {
+        xs_l[tid_e] = m0 + tid_e < g.M ? g.xs[m0 + tid_e] : 0.0f;
+        ws_l[tid_e] = n0 + tid_e < g.N ? g.ws[n0 + tid_e] : 0.0f;
+    }
+    if (ext_steps > 0) {
+        const __amdgpu_buffer_rsrc_t rAe = make_rsrc(g.sT + m0 * g.r, (g.M - m0) * (int64_t)g.r * 2);
+        const __amdgpu_buffer_rsrc_t rBe = make_rsrc(g.L2T + n0 * g.r, (g.N - n0) * (int64_t)g.r * 2);
+        auto load_ext = [&](int e, uint8_t *Ast, uint8_t *Bst) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int row = 8 * (8 * wave + q) + (lane_e >> 3);
+                const int jj = e * 64 + (a_col[q & 1] >> 1);
+                const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0x80000000u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rAe, (lds_void *)((lds_u8 *)Ast + wave * 8192 + q * 1024), 16, off, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rBe, (lds_void *)((lds_u8 *)Bst + wave * 8192 + q * 1024), 16, off, 0, 0, 0);
+            }
+        };
+        load_ext(0, As0, Bs0);
+        if (ext_steps > 1) load_ext(1, As1, Bs1);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+
+    // ---- one 32 x 32 tile after the other: the sum to float32 times both constants, the adapter's
+    // MFMAs on it, the store.  Lane (r32, hh) of tile (i, j) holds column wn*128 + 32 j + r32 and rows
+    // wm*128 + 32 i + 8 (v/4) + 4 hh + v%4; rows past M fall outside the descriptors. ----
+    const bool part = g.ksplit > 1;
+    const uint32_t row_bytes = (uint32_t)(g.N * (part ? 4 : 2));
+    const __amdgpu_buffer_rsrc_t rC =
+        part ? make_rsrc(g.P + (int64_t)split * g.M * g.N + m0 * g.N, (g.M - m0) * g.N * 4)
+             : make_rsrc(g.Y + m0 * g.N, (g.M - m0) * g.N * 2);
+    const uint32_t lane_off = (uint32_t)((wm * 128 + hh_e * 4) * row_bytes) + (uint32_t)((n0 + wn * 128 + r32_e) * (part ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f32x4 x[4];
+#pragma unroll
+        for (int v4 = 0; v4 < 4; ++v4)
+            x[v4] = *reinterpret_cast<const f32x4 *>(xs_l + wm * 128 + i * 32 + v4 * 8 + hh_e * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float w = ws_l[wn * 128 + j * 32 + r32_e];
+            f32x16 f;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) f[v] = ((float)acc[i][j][v] * x[v >> 2][v & 3]) * w;
+            auto adapter = [&](const uint8_t *Ast, const uint8_t *Bst) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t o = (uint32_t)(r32_e * 128 + (((2 * s + hh_e) ^ ((r32_e >> 1) & 7)) * 16));
+                    const bf16x8 fa = *reinterpret_cast<const bf16x8 *>(Ast + o + (wm * 128 + 32 * i) * 128);
+                    const bf16x8 fb = *reinterpret_cast<const bf16x8 *>(Bst + o + (wn * 128 + 32 * j) * 128);
+                    f = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, f, 0, 0, 0);
+                }
+            };
+            if (ext_steps > 0) adapter(As0, Bs0);
+            if (ext_steps > 1) adapter(As1, Bs1);
+            if (n0 + wn * 128 + j * 32 + r32_e >= g.N) continue;
+            if (part) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const uint32_t rows = (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3));
+                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[v]), rC, lane_off + j * 128, rows * row_bytes, 0);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < 16; v += 2) {
+                    const uint32_t rows = (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3));
+                    const uint32_t pk = pack_bf16x2(f[v], f[v + 1]);
+                    const uint32_t soff = rows * row_bytes;
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pk, rC, lane_off + j * 64, soff, 0);
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pk >> 16), rC, lane_off + j * 64, soff + row_bytes, 0);
+                }
+            }
+        }
     }
 }
 
 }  // namespace
 
 hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream) {
+    const int64_t tiles = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
+    const int64_t steps = (p.K + TKB - 1) / TKB;
+    Int8Product a = p;
+    if (a.ksplit <= 1) {
+        a.ksplit = 1;
+        a.split_per = (int32_t)steps;
+    } else if (!a.P || (int64_t)(a.ksplit - 1) * a.split_per >= steps || (int64_t)a.ksplit * a.split_per < steps) {
+        return hipErrorInvalidValue;     // every split non-empty, the partials somewhere to go
+    }
     timing_before(stream, 0);
-    hipLaunchKernelGGL(int8_gemm_kernel, dim3((unsigned)((p.N + BT - 1) / BT), (unsigned)((p.M + BT - 1) / BT)), dim3(256), 0,
-                       stream, p);
+    hipLaunchKernelGGL(int8_gemm_kernel, dim3((unsigned)(tiles * a.ksplit)), dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
+}
+
+// Reduction steps of 128 codes split as the bf16 products' are (fewer output tiles than half the CUs).
+SplitPlan int8_gemm_split(int64_t M, int64_t N, int64_t K) {
+    return gemm_split(((M + TM - 1) / TM) * ((N + TN - 1) / TN), (K + TKB - 1) / TKB, 4);
 }
 
 }  // namespace nf4k

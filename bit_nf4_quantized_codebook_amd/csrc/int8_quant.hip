@@ -6,6 +6,8 @@
 #include "common.h"
 #include "int8.h"
 #include "launch.h"
+#include "reduce.h"
+#include "transpose.h"
 
 namespace nf4k {
 
@@ -26,12 +28,12 @@ __device__ __forceinline__ void load8(const void *x, int64_t i8, float f[8]) {
     }
 }
 
-// One workgroup per row, the row read twice.
+// One row per workgroup of 256 threads, the row read twice.
 template <bool F32>
-__global__ __launch_bounds__(256) void int8_rows_kernel(const void *__restrict__ x, int64_t cols,
-                                                        int8_t *__restrict__ codes, float *__restrict__ scales) {
+__device__ __forceinline__ void int8_row(const void *__restrict__ x, int64_t row, int64_t cols, int8_t *__restrict__ codes,
+                                         float *__restrict__ scales) {
     __shared__ uint32_t red[4];
-    const int64_t row = blockIdx.x, c8 = cols >> 3;
+    const int64_t c8 = cols >> 3;
     const int tid = threadIdx.x;
     uint32_t m = 0;
     for (int64_t i = tid; i < c8; i += 256) {
@@ -51,6 +53,37 @@ __global__ __launch_bounds__(256) void int8_rows_kernel(const void *__restrict__
         load8<F32>(x, row * c8 + i, f);
         reinterpret_cast<uint2 *>(codes)[row * c8 + i] = codes8(f, rc);
     }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void int8_rows_kernel(const void *__restrict__ x, int64_t cols,
+                                                        int8_t *__restrict__ codes, float *__restrict__ scales) {
+    int8_row<F32>(x, blockIdx.x, cols, codes, scales);
+}
+
+// The short jobs first, so that they run alongside the rows instead of trailing them.
+struct PrepArgs {
+    const uint16_t *X;
+    int64_t K;
+    int8_t *Xq;
+    float *xs;
+    RedProb red;
+    const uint16_t *L2;
+    uint16_t *L2T;
+    int32_t r;
+    int64_t N;
+    uint32_t ntr, nred;
+};
+__global__ __launch_bounds__(256) void int8_prep_kernel(PrepArgs g) {
+    if (blockIdx.x < g.ntr) {
+        transpose_block(g.L2, g.L2T, g.r, g.N, blockIdx.x);
+        return;
+    }
+    if (blockIdx.x < g.ntr + g.nred) {
+        reduce_partials_block(g.red, blockIdx.x - g.ntr, g.nred);
+        return;
+    }
+    int8_row<false>(g.X, blockIdx.x - g.ntr - g.nred, g.K, g.Xq, g.xs);
 }
 
 __device__ __forceinline__ float sext8(uint32_t w, int i) { return (float)((int32_t)(w << (24 - 8 * i)) >> 24); }
@@ -111,6 +144,21 @@ hipError_t launch_int8_rows(const void *x, bool f32, int64_t rows, int64_t cols,
             hipLaunchKernelGGL(int8_rows_kernel<false>, dim3((unsigned)n), dim3(256), 0, stream, xr, cols,
                                codes + r0 * cols, scales + r0);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_prep(const Int8Prep &p, hipStream_t stream) {
+    PrepArgs a{};
+    a.X = p.X; a.K = p.K; a.Xq = p.Xq; a.xs = p.xs;
+    a.L2 = p.L2; a.L2T = p.L2T; a.r = p.r; a.N = p.N;
+    if (p.L2) a.ntr = transpose_blocks(p.r, p.N);
+    if (p.Tred) a.red = red_prob(*p.Tred, a.nred);
+    // X stays below 2 GiB with at least 64 columns: fewer than 2^24 rows, 2^32 threads
+    const int64_t rows = p.X ? p.M : 0;
+    const int64_t grid = (int64_t)a.ntr + a.nred + rows;
+    if (grid == 0) return hipSuccess;
+    if (grid >= (int64_t)1 << 24) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(int8_prep_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

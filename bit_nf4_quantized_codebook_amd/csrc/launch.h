@@ -162,15 +162,33 @@ hipError_t launch_int8_rows(const void *x, bool f32, int64_t rows, int64_t cols,
                             hipStream_t stream);
 // bf16(scale * code), as [rows, cols] or transposed [cols, rows] (cols a multiple of 64, rows of 8)
 hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, hipStream_t stream);
-// Y = xs ws (Xq Wq^T) + sT L2 (r = 0: no adapter)
+// What the product needs beforehand, as one launch: rows of X to codes (X non-null), T's pending
+// reduction (Tred non-null) and L2 [r, N] transposed into L2T [N, r] (L2 non-null).
+struct Int8Prep {
+    const uint16_t *X;
+    int64_t M, K;
+    int8_t *Xq;
+    float *xs;
+    const Reduction *Tred;
+    const uint16_t *L2;
+    uint16_t *L2T;
+    int32_t r;
+    int64_t N;
+};
+hipError_t launch_int8_prep(const Int8Prep &p, hipStream_t stream);
+// Y = xs ws (Xq Wq^T) + sT L2 (r = 0: no adapter).  ksplit > 1: split_per steps of 128 codes per
+// workgroup, float32 partials P [ksplit][M, N] for launch_reduce_partials instead of Y.
 struct Int8Product {
     const int8_t *Xq, *Wq;
     const float *xs, *ws;
-    const uint16_t *sT, *L2;
+    const uint16_t *sT, *L2T;
     int64_t M, N, K;
     int32_t r;
     uint16_t *Y;
+    int32_t ksplit, split_per;
+    float *P;
 };
+SplitPlan int8_gemm_split(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream);
 
 // ---- norm glue between blocks ----

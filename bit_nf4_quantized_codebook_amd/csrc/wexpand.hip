@@ -14,6 +14,7 @@
 #include "dqtile.h"
 #include "launch.h"
 #include "reduce.h"
+#include "transpose.h"
 
 namespace nf4k {
 
@@ -42,36 +43,6 @@ struct ExpandArgs {
     uint32_t ntr;
 };
 
-// One 64 x 64 tile of the small transpose per workgroup (L2 [r, N] -> [N, r] for the GEMM's LoRA
-// step, so that it loads like the backward's L1).  Thread t loads two 16-byte pieces of row t / 4
-// of the tile (columns 16 (t % 4) ..), and stores two 16-byte pieces of output row t / 4; r and
-// N are multiples of 8, so no piece straddles an edge.
-__device__ __forceinline__ void transpose_block(const ExpandArgs &g, int64_t blk) {
-    __shared__ uint16_t tt[64][64 + 8];
-    const int64_t ncb = (g.tr_n + 63) / 64;
-    const int64_t j0 = (blk / ncb) * 64, n0 = (blk % ncb) * 64;
-    const int t = threadIdx.x, row = t >> 2, c0 = (t & 3) * 16;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t j = j0 + row, n = n0 + c0 + 8 * h;
-        u32x4 v = {0u, 0u, 0u, 0u};
-        if (j < g.tr_r && n < g.tr_n) v = *reinterpret_cast<const u32x4 *>(g.tr_in + j * g.tr_n + n);
-        *reinterpret_cast<u32x4 *>(&tt[row][c0 + 8 * h]) = v;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t n = n0 + row, j = j0 + c0 + 8 * h;
-        if (n < g.tr_n && j < g.tr_r) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                w[k] = (uint32_t)tt[c0 + 8 * h + 2 * k][row] | ((uint32_t)tt[c0 + 8 * h + 2 * k + 1][row] << 16);
-            *reinterpret_cast<u32x4 *>(g.tr_out + n * g.tr_r + j) = u32x4{w[0], w[1], w[2], w[3]};
-        }
-    }
-}
-
 // Row layout: 8 lanes per block, one packed dword (8 weights) each, so a wave reads 256
 // contiguous packed bytes and writes 1 KB of contiguous bf16 per store.  The 8 lanes of a block
 // each build its table (the kernel is bound by HBM, not VALU).  Blocks run over the row-major
@@ -80,7 +51,7 @@ __device__ __forceinline__ void transpose_block(const ExpandArgs &g, int64_t blk
 // then overlap the expansion instead of trailing it), the nexp expansion workgroups after them.
 __global__ __launch_bounds__(256) void expand_rows_kernel(ExpandArgs g) {
     if (blockIdx.x < g.ntr) {
-        transpose_block(g, blockIdx.x);
+        transpose_block(g.tr_in, g.tr_out, g.tr_r, g.tr_n, blockIdx.x);
         return;
     }
     if (blockIdx.x < g.ntr + g.nred) {
@@ -175,7 +146,7 @@ hipError_t launch_expand_weight(const WeightView &w, bool transposed, uint16_t *
                                 int32_t tr_r, int64_t tr_n) {
     ExpandArgs a;
     a.tr_in = tr_in; a.tr_out = tr_out; a.tr_r = tr_r; a.tr_n = tr_n;
-    a.ntr = (!transposed && tr_in) ? (uint32_t)(((tr_r + 63) / 64) * ((tr_n + 63) / 64)) : 0u;
+    a.ntr = (!transposed && tr_in) ? transpose_blocks(tr_r, tr_n) : 0u;
     a.packed = w.packed; a.c2 = w.c2; a.c1 = w.c1; a.mean = w.mean; a.dq_int8 = w.dq_int8;
     a.out = out; a.N = w.rows; a.K = w.cols;
     for (int j = 0; j < 16; ++j) a.cb.v[j] = w.cb[j];
