@@ -1027,6 +1027,11 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     size_t pmax = 0;
     if (r) {
         p.ksT = nf4k::choose_split(mt * rt, (K + kTile - 1) / kTile);
+        if (M <= kGemvMaxM) {
+            // one tile of T: four reduction steps per workgroup (one batch of loads), up to 64
+            const int64_t ks4 = ((K + kTile - 1) / kTile + 3) / 4;
+            if (ks4 > p.ksT) p.ksT = (int)(ks4 < 64 ? ks4 : 64);
+        }
         p.ksdT = nf4k::choose_split(mt * rt, (N + kTile - 1) / kTile);
         p.msL2 = nf4k::choose_split(rt * ((N + kTile - 1) / kTile), mt);
         p.msL1 = nf4k::choose_split(((K + kTile - 1) / kTile) * rt, mt);
@@ -1036,7 +1041,7 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     }
     const int64_t tiles = (M + kGemmTile - 1) / kGemmTile * ((K + kGemmTile - 1) / kGemmTile);
     p.kb = nf4k::gemm_split(tiles, (N + kTile - 1) / kTile, kSplitQuantum);
-    p.kf = nf4k::int8_gemm_split(M, N, K);
+    p.kf = M <= kGemvMaxM ? nf4k::SplitPlan{1, 0} : nf4k::int8_gemm_split(M, N, K);
     size_t pg = p.kb.ksplit > 1 ? (size_t)p.kb.ksplit * M * K : 0;
     if (p.kf.ksplit > 1 && (size_t)p.kf.ksplit * M * N > pg) pg = (size_t)p.kf.ksplit * M * N;
     size_t off = 0;
@@ -1062,7 +1067,8 @@ int check_int8_linear_args(const nf4_int8_weight *w, int64_t M, int32_t r, float
     if (!std::isfinite(scale)) return fail(NF4_ERR_ARG, "scale must be finite");
     // kernels address each operand with 32-bit byte offsets
     const int64_t lim = (int64_t)1 << 31;
-    if (M >= lim || w->rows >= lim || w->rows * w->cols >= lim || M * w->cols * 2 >= lim || M * w->rows * 2 >= lim)
+    if (M >= lim || w->rows >= lim || w->rows * w->cols >= lim || M * w->cols * 2 >= lim || M * w->rows * 2 >= lim ||
+        w->rows * r * 2 >= lim)
         return fail(NF4_ERR_UNSUPPORTED, "an operand exceeds 2 GiB");
     return NF4_OK;
 }
@@ -1121,6 +1127,29 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
     if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "int8 linear workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if (M <= kGemvMaxM) {
+        int8_t *q = ws_at<int8_t>(workspace, p.off_Xq);
+        float *qs = ws_at<float>(workspace, p.off_xs), *P = ws_at<float>(workspace, p.off_P);
+        NF4_CHECK_HIP(nf4k::launch_int8_rows_t(X, L1, P, M, r, K, p.ksT, Xq ? nullptr : q, qs, s),
+                      "int8 quantize + T = X L1");
+        nf4k::Int8Gemv a{};
+        a.Xq = Xq ? Xq : q; a.xs = Xq ? xs : qs;
+        a.Wq = w->codes; a.ws = w->scales;
+        a.scale = scale;
+        a.L2 = L2;
+        a.M = M; a.N = N; a.K = K; a.r = r;
+        a.Y = Y;
+        if (r && (size_t)p.ksT * M * r * 4 <= kGemvTSumBytes) {
+            a.Tp = P; a.ksT = p.ksT; a.T_out = T_out;
+        } else if (r) {
+            uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT);
+            const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
+            NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "T reduce");
+            a.sT = sT;
+        }
+        NF4_CHECK_HIP(nf4k::launch_int8_gemv(a, s), "int8 GEMV (fwd)");
+        return NF4_OK;
+    }
     // T's partials; then one launch for X's codes, T's sum and L2's transpose; then the product
     nf4k::Int8Prep prep{};
     prep.M = M; prep.K = K; prep.N = N; prep.r = r;

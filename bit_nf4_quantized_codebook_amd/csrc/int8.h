@@ -89,4 +89,46 @@ __device__ __forceinline__ uint2 codes8(const float x[8], const RowCode &c) {
     return uint2{b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24)};
 }
 
+template <bool F32>
+__device__ __forceinline__ void load8(const void *x, int64_t i8, float f[8]) {
+    if (F32) {
+        typedef float f32v4 __attribute__((ext_vector_type(4)));
+        const f32v4 a = reinterpret_cast<const f32v4 *>(x)[2 * i8], b = reinterpret_cast<const f32v4 *>(x)[2 * i8 + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = a[i];
+            f[4 + i] = b[i];
+        }
+    } else {
+        unpack8_bf16(reinterpret_cast<const u32x4 *>(x)[i8], f);
+    }
+}
+
+// One row per workgroup of 256 threads, the row read twice.
+template <bool F32>
+__device__ __forceinline__ void int8_row(const void *__restrict__ x, int64_t row, int64_t cols, int8_t *__restrict__ codes,
+                                         float *__restrict__ scales) {
+    __shared__ uint32_t red[4];
+    const int64_t c8 = cols >> 3;
+    const int tid = threadIdx.x;
+    uint32_t m = 0;
+    for (int64_t i = tid; i < c8; i += 256) {
+        float f[8];
+        load8<F32>(x, row * c8 + i, f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+    }
+    m = wave_max(m);
+    if ((tid & 63) == 0) red[tid >> 6] = m;
+    __syncthreads();
+    m = max(max(red[0], red[1]), max(red[2], red[3]));
+    const RowCode rc = row_code(m);
+    if (tid == 0) scales[row] = rc.scale;
+    for (int64_t i = tid; i < c8; i += 256) {
+        float f[8];
+        load8<F32>(x, row * c8 + i, f);
+        reinterpret_cast<uint2 *>(codes)[row * c8 + i] = codes8(f, rc);
+    }
+}
+
 }  // namespace nf4k

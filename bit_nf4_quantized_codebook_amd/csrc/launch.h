@@ -191,6 +191,24 @@ struct Int8Product {
 SplitPlan int8_gemm_split(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream);
 
+// up to 64 tokens: X's codes (Xq non-null) and T's partials (nsplit of them; r = 0: none) in one launch,
+// then the product, which sums T's partials itself (Tp, ksT, writing T_out) or takes s T (sT)
+hipError_t launch_int8_rows_t(const uint16_t *X, const uint16_t *L1, float *P, int64_t M, int32_t r, int64_t K, int nsplit,
+                              int8_t *Xq, float *xs, hipStream_t stream);
+struct Int8Gemv {
+    const int8_t *Xq, *Wq;
+    const float *xs, *ws;
+    const float *Tp;
+    int32_t ksT;
+    float scale;
+    uint16_t *T_out;
+    const uint16_t *sT, *L2;
+    int64_t M, N, K;
+    int32_t r;
+    uint16_t *Y;
+};
+hipError_t launch_int8_gemv(const Int8Gemv &p, hipStream_t stream);
+
 // ---- norm glue between blocks ----
 struct NormArgs {
     const uint16_t *w_pre, *w_post, *gate;

@@ -152,6 +152,7 @@ def test_int8_linear_refusals():
         assert f(_w8(cols=96)) == EUNSUP and f(_w8(rows=12)) == EUNSUP and f(_w8(rows=0)) == ESHAPE
         assert f(_w8(rows=1 << 24, cols=128)) == EUNSUP and f(M=1 << 22) == EUNSUP and f(M=1 << 40) == EUNSUP
         assert f(_w8(rows=65536), M=1 << 14) == EUNSUP
+        assert f(_w8(rows=1 << 23, cols=64), M=1, r=128) == EUNSUP     # L2: 128 x 2^23 bf16 = 2 GiB
         assert f(L1=None) == ENULL and f(L2=None) == ENULL and f(X=None) == ENULL
         assert f(r=0) == EARG                                   # an adapter, but no rank
         assert f(X=MIS) == EALIGN and f(L1=MIS) == EALIGN and f(L2=MIS) == EALIGN and f(ws=MIS) == EALIGN
