@@ -167,9 +167,15 @@ def version() -> str:
 # torch plumbing (device memory and streams only)
 # ------------------------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(device=None):
@@ -530,13 +536,18 @@ def _at(t):
 
 
 def _expect(t, dtype, shape, dev, name):
-    """t: a contiguous tensor of this type and shape on dev (the call's device)."""
+    """t: a contiguous tensor of this type and shape on dev (the call's device).  The checks run in one
+    expression, and again one by one for the message where it fails: a decode call is a few
+    microseconds, and these are a third of its host time otherwise."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
     _need(t, dtype, name)
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call's first tensor on {dev}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {shape}")
-    return t
+    raise ValueError(f"shape mismatch: {name} is {tuple(t.shape)}, expected {shape}")
 
 
 def _out(t, dtype, shape, dev, name):
@@ -546,15 +557,24 @@ def _out(t, dtype, shape, dev, name):
     return _expect(t, dtype, shape, dev, name)
 
 
-def _launch(name, dev, *args):
-    """lib.name(*args, stream) on the device's current stream, with that device current."""
-    cuda = _torch().cuda
-    if cuda.current_device() == dev.index:
-        status = getattr(lib, name)(*args, cuda.current_stream(dev).cuda_stream)
+def _like(t, like, name):
+    """An output of another tensor's type and shape."""
+    return _torch().empty_like(like) if t is None else _expect(t, like.dtype, like.shape, like.device, name)
+
+
+def _launch(fn, name, dev, *args):
+    """fn(*args, stream) on the device's current stream, with that device current."""
+    torch = _torch()
+    index = dev.index
+    # the stream's handle alone: torch.cuda.current_stream builds a Python object around it each time
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream(index))
     else:
-        with cuda.device(dev):
-            status = getattr(lib, name)(*args, cuda.current_stream(dev).cuda_stream)
-    _check(status, name)
+        with torch.cuda.device(index):
+            status = fn(*args, stream(index))
+    if status != NF4_OK:
+        _check(status, name)
 
 
 def nf4_int8_quantize(X, codes=None, scales=None):
@@ -566,9 +586,10 @@ def nf4_int8_quantize(X, codes=None, scales=None):
     if X.dim() != 2:
         raise ValueError("X must be [rows, cols]")
     rows, cols = X.shape
-    codes = _out(codes, torch.int8, (rows, cols), X.device, "codes")
-    scales = _out(scales, torch.float32, (rows,), X.device, "scales")
-    _launch("nf4_int8_quantize", X.device, X.data_ptr(), int(f32), rows, cols, codes.data_ptr(), scales.data_ptr())
+    dev = X.device
+    codes = _out(codes, torch.int8, (rows, cols), dev, "codes")
+    scales = _out(scales, torch.float32, (rows,), dev, "scales")
+    _launch(lib.nf4_int8_quantize, "nf4_int8_quantize", dev, X.data_ptr(), int(f32), rows, cols, codes.data_ptr(), scales.data_ptr())
     return codes, scales
 
 
@@ -609,7 +630,7 @@ def nf4_int8_dequant(w: Int8Weight):
     """bf16(scale * code), [rows, cols]: the weight that the backward's gradient runs through."""
     torch = _torch()
     out = torch.empty((w.rows, w.cols), dtype=torch.bfloat16, device=w.device)
-    _launch("nf4_int8_dequant", w.device, ctypes.byref(w.descriptor()), out.data_ptr())
+    _launch(lib.nf4_int8_dequant, "nf4_int8_dequant", w.device, ctypes.byref(w.descriptor()), out.data_ptr())
     return out
 
 
@@ -651,7 +672,7 @@ def qlora_int8_linear_fwd(w: Int8Weight, X, L1=None, L2=None, scale: float = 1.0
         T = _out(T, bf16, (M, r), dev, "T")
     wsb = lib.qlora_int8_linear_workspace_size(M, N, K, r)
     ws = _workspace(wsb, dev, workspace)
-    _launch("qlora_int8_linear_fwd", dev, ctypes.byref(w.descriptor()), _at(X), _at(q), _at(qs), _at(L1), _at(L2),
+    _launch(lib.qlora_int8_linear_fwd, "qlora_int8_linear_fwd", dev, ctypes.byref(w.descriptor()), _at(X), _at(q), _at(qs), _at(L1), _at(L2),
             scale, M, r, Y.data_ptr(), _at(T), ws.data_ptr(), wsb)
     return Y, T
 
@@ -679,7 +700,7 @@ def qlora_int8_linear_bwd(w: Int8Weight, dY, X=None, L1=None, L2=None, T=None, s
     dX = _out(dX, bf16, (M, K), dev, "dX") if need_dX else None
     wsb = lib.qlora_int8_linear_workspace_size(M, N, K, r)
     ws = _workspace(wsb, dev, workspace)
-    _launch("qlora_int8_linear_bwd", dev, ctypes.byref(w.descriptor()), dY.data_ptr(), _at(X) if r else None, _at(L1),
+    _launch(lib.qlora_int8_linear_bwd, "qlora_int8_linear_bwd", dev, ctypes.byref(w.descriptor()), dY.data_ptr(), _at(X) if r else None, _at(L1),
             _at(L2), _at(T), scale, M, r, _at(dX), _at(dL1), _at(dL2), QLORA_DX_ACCUMULATE if accumulate else 0,
             ws.data_ptr(), wsb)
     return dX, dL1, dL2
@@ -709,20 +730,20 @@ class QLoRANorm:
         _need(R, torch.float32 if f32 else torch.bfloat16, name)
         if R.dim() != 2:
             raise ValueError(f"{name} must be [M, C]")
-        M, C = R.shape
+        M, C = shape = R.shape
         bf16, dev = torch.bfloat16, R.device
+        w_pre, w_post, gate = self.w_pre, self.w_post, self.gate
         if B is not None:
-            _expect(B, bf16, (M, C), dev, "B")
-        if self.w_pre is not None:
-            _expect(self.w_pre, bf16, (C,), dev, "w_pre")
-        if self.w_post is not None:
-            _expect(self.w_post, bf16, (C,), dev, "w_post")
-        if self.gate is not None:
+            _expect(B, bf16, shape, dev, "B")
+        if w_pre is not None:
+            w_pre = _expect(w_pre, bf16, (C,), dev, "w_pre").data_ptr()
+        if w_post is not None:
+            w_post = _expect(w_post, bf16, (C,), dev, "w_post").data_ptr()
+        if gate is not None:
             if self.gate_tokens < 1:
                 raise ValueError("gate_tokens must be >= 1 with a gate")
-            _expect(self.gate, bf16, (-(-M // self.gate_tokens), C), dev, "gate")
-        return _NormDesc(_at(self.w_pre), _at(self.w_post), _at(self.gate), self.gate_tokens, C, self.alpha,
-                         self.beta, self.eps, int(f32)), M, C
+            gate = _expect(gate, bf16, (-(-M // self.gate_tokens), C), dev, "gate").data_ptr()
+        return _NormDesc(w_pre, w_post, gate, self.gate_tokens, C, self.alpha, self.beta, self.eps, f32), M, C
 
 
 def qlora_norm_fwd(norm: QLoRANorm, R, B=None, quantize: bool = False, R_out=None, H=None):
@@ -730,19 +751,20 @@ def qlora_norm_fwd(norm: QLoRANorm, R, B=None, quantize: bool = False, R_out=Non
     Returns (R', H); R' is None without B, H without w_pre.  quantize: also H's (codes, scales), for
     qlora_int8_linear_fwd's Xq, as a third value.  R_out may be R itself."""
     torch = _torch()
+    bf16 = torch.bfloat16
     d, M, C = norm._descriptor(R, B, "R")
     dev, q = R.device, None
     if B is not None:
-        R_out = _out(R_out, R.dtype, (M, C), dev, "R_out")
+        R_out = _like(R_out, R, "R_out")
     elif R_out is not None:
         raise ValueError("R_out without B")
     if norm.w_pre is not None:
-        H = _out(H, torch.bfloat16, (M, C), dev, "H")
+        H = _like(H, R if B is None else B, "H") if R.dtype is bf16 or B is not None else _out(H, bf16, (M, C), dev, "H")
     elif H is not None or quantize:
         raise ValueError("H or quantize without w_pre")
     if quantize:
         q = (torch.empty((M, C), dtype=torch.int8, device=dev), torch.empty((M,), dtype=torch.float32, device=dev))
-    _launch("qlora_norm_fwd", dev, ctypes.byref(d), R.data_ptr(), _at(B), M, _at(R_out), _at(H),
+    _launch(lib.qlora_norm_fwd, "qlora_norm_fwd", dev, ctypes.byref(d), R.data_ptr(), _at(B), M, _at(R_out), _at(H),
             _at(q[0]) if q else None, _at(q[1]) if q else None)
     return (R_out, H, q) if quantize else (R_out, H)
 
@@ -764,9 +786,9 @@ def qlora_norm_bwd(norm: QLoRANorm, R_out, B=None, dR_out=None, dH=None, need_we
         _expect(dR_out, R_out.dtype, (M, C), dev, "dR_out")
     if dH is not None:
         _expect(dH, bf16, (M, C), dev, "dH")
-    dR = _out(dR, R_out.dtype, (M, C), dev, "dR")
+    dR = _like(dR, R_out, "dR")
     if B is not None:
-        dB = _out(dB, bf16, (M, C), dev, "dB")
+        dB = _like(dB, B, "dB")
     elif dB is not None:
         raise ValueError("dB without B")
     grads = {}
@@ -776,7 +798,7 @@ def qlora_norm_bwd(norm: QLoRANorm, R_out, B=None, dR_out=None, dH=None, need_we
                 grads[name] = torch.empty_like(w)
     wsb = lib.qlora_norm_workspace_size(M, C)
     ws = _workspace(wsb, dev, workspace)
-    _launch("qlora_norm_bwd", dev, ctypes.byref(d), R_out.data_ptr(), _at(B), _at(dR_out), _at(dH), M, dR.data_ptr(),
+    _launch(lib.qlora_norm_bwd, "qlora_norm_bwd", dev, ctypes.byref(d), R_out.data_ptr(), _at(B), _at(dR_out), _at(dH), M, dR.data_ptr(),
             _at(dB), _at(grads.get("dw_pre")), _at(grads.get("dw_post")), _at(grads.get("dgate")), ws.data_ptr(), wsb)
     return dR, dB, grads
 
