@@ -175,7 +175,7 @@ __global__ __launch_bounds__(256) void int8_rows_t_kernel(RowsT g) {
         skinny_nt_block<true>(g.X, g.L1, g.P, g.M, g.r, g.K, g.kchunk, 0, blockIdx.x % g.nty, blockIdx.x / g.nty);
         return;
     }
-    int8_row<false>(g.X, blockIdx.x - g.nt, g.K, g.Xq, g.xs);
+    int8_rows_block<false>(g.X, blockIdx.x - g.nt, g.M, g.K, g.Xq, g.xs);
 }
 
 template <int RG>
@@ -200,7 +200,7 @@ hipError_t launch_int8_rows_t(const uint16_t *X, const uint16_t *L1, float *P, i
         a.nty = (uint32_t)((r + ST - 1) / ST);
         a.nt = a.nty * (uint32_t)nsplit;
     }
-    const uint32_t rows = Xq ? (uint32_t)M : 0u;
+    const uint32_t rows = Xq ? (uint32_t)int8_rows_blocks(M, K) : 0u;
     if (a.nt + rows == 0) return hipSuccess;
     hipLaunchKernelGGL(int8_rows_t_kernel, dim3(a.nt + rows), dim3(256), 0, stream, a);
     return hipGetLastError();

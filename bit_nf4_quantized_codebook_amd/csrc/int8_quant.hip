@@ -14,15 +14,15 @@ namespace nf4k {
 namespace {
 
 template <bool F32>
-__global__ __launch_bounds__(256) void int8_rows_kernel(const void *__restrict__ x, int64_t cols,
+__global__ __launch_bounds__(256) void int8_rows_kernel(const void *__restrict__ x, int64_t rows, int64_t cols,
                                                         int8_t *__restrict__ codes, float *__restrict__ scales) {
-    int8_row<F32>(x, blockIdx.x, cols, codes, scales);
+    int8_rows_block<F32>(x, blockIdx.x, rows, cols, codes, scales);
 }
 
 // The short jobs first, so that they run alongside the rows instead of trailing them.
 struct PrepArgs {
     const uint16_t *X;
-    int64_t K;
+    int64_t M, K;
     int8_t *Xq;
     float *xs;
     RedProb red;
@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void int8_prep_kernel(PrepArgs g) {
         reduce_partials_block(g.red, blockIdx.x - g.ntr, g.nred);
         return;
     }
-    int8_row<false>(g.X, blockIdx.x - g.ntr - g.nred, g.K, g.Xq, g.xs);
+    int8_rows_block<false>(g.X, blockIdx.x - g.ntr - g.nred, g.M, g.K, g.Xq, g.xs);
 }
 
 __device__ __forceinline__ float sext8(uint32_t w, int i) { return (float)((int32_t)(w << (24 - 8 * i)) >> 24); }
@@ -95,25 +95,23 @@ hipError_t launch_int8_rows(const void *x, bool f32, int64_t rows, int64_t cols,
     for (int64_t r0 = 0; r0 < rows; r0 += kMaxRowGrid) {
         const int64_t n = rows - r0 < kMaxRowGrid ? rows - r0 : kMaxRowGrid;
         const char *xr = reinterpret_cast<const char *>(x) + r0 * cols * (f32 ? 4 : 2);
+        const dim3 grid((unsigned)int8_rows_blocks(n, cols));
         if (f32)
-            hipLaunchKernelGGL(int8_rows_kernel<true>, dim3((unsigned)n), dim3(256), 0, stream, xr, cols,
-                               codes + r0 * cols, scales + r0);
+            hipLaunchKernelGGL(int8_rows_kernel<true>, grid, dim3(256), 0, stream, xr, n, cols, codes + r0 * cols, scales + r0);
         else
-            hipLaunchKernelGGL(int8_rows_kernel<false>, dim3((unsigned)n), dim3(256), 0, stream, xr, cols,
-                               codes + r0 * cols, scales + r0);
+            hipLaunchKernelGGL(int8_rows_kernel<false>, grid, dim3(256), 0, stream, xr, n, cols, codes + r0 * cols, scales + r0);
     }
     return hipGetLastError();
 }
 
 hipError_t launch_int8_prep(const Int8Prep &p, hipStream_t stream) {
     PrepArgs a{};
-    a.X = p.X; a.K = p.K; a.Xq = p.Xq; a.xs = p.xs;
+    a.X = p.X; a.M = p.M; a.K = p.K; a.Xq = p.Xq; a.xs = p.xs;
     a.L2 = p.L2; a.L2T = p.L2T; a.r = p.r; a.N = p.N;
     if (p.L2) a.ntr = transpose_blocks(p.r, p.N);
     if (p.Tred) a.red = red_prob(*p.Tred, a.nred);
-    // X stays below 2 GiB with at least 64 columns: fewer than 2^24 rows, 2^32 threads
-    const int64_t rows = p.X ? p.M : 0;
-    const int64_t grid = (int64_t)a.ntr + a.nred + rows;
+    // X stays below 2 GiB with at least 64 columns: fewer than 2^24 rows, 2^30 threads
+    const int64_t grid = (int64_t)a.ntr + a.nred + (p.X ? int8_rows_blocks(p.M, p.K) : 0);
     if (grid == 0) return hipSuccess;
     if (grid >= (int64_t)1 << 24) return hipErrorInvalidValue;
     hipLaunchKernelGGL(int8_prep_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a);

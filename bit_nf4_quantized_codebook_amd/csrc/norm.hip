@@ -19,29 +19,31 @@ namespace {
 
 typedef float f32v4 __attribute__((ext_vector_type(4)));
 
+// The forward reads the residual past the caches (43.2 -> 39.2 us at 4096 x 4096 float32); in the
+// backward that cost 1.5 to 6 us a call, and its loads stay ordinary.
 template <bool F32>
 __device__ __forceinline__ void load_res(const void *x, int64_t e, float f[8]) {
-    if (F32) {
-        const f32v4 *p = reinterpret_cast<const f32v4 *>(reinterpret_cast<const float *>(x) + e);
-        const f32v4 a = p[0], b = p[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = a[i];
-            f[4 + i] = b[i];
-        }
-    } else {
-        unpack8_bf16(*reinterpret_cast<const u32x4 *>(reinterpret_cast<const uint16_t *>(x) + e), f);
-    }
+    Raw8<F32> r;
+    r.template load<true>(x, e);
+    r.floats(f);
 }
+// The large outputs are stored past the caches (nontemporal): they are written whole and far larger
+// than an L2, and a launch's end otherwise waits for their write-back (forward, 4096 x 4096 float32
+// residual: 46.2 -> 42.5 us a call; backward, 1001 x 8192: 37.9 -> 35.1 us).
 template <bool F32>
 __device__ __forceinline__ void store_res(void *x, int64_t e, const float f[8]) {
     if (F32) {
         f32v4 *p = reinterpret_cast<f32v4 *>(reinterpret_cast<float *>(x) + e);
-        p[0] = f32v4{f[0], f[1], f[2], f[3]};
-        p[1] = f32v4{f[4], f[5], f[6], f[7]};
+        __builtin_nontemporal_store(f32v4{f[0], f[1], f[2], f[3]}, p);
+        __builtin_nontemporal_store(f32v4{f[4], f[5], f[6], f[7]}, p + 1);
     } else {
-        *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(x) + e) = pack8_bf16(f);
+        __builtin_nontemporal_store(pack8_bf16(f), reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(x) + e));
     }
+}
+// partial sums: read again by the next launch
+__device__ __forceinline__ void store_sum(float *p, const float f[8]) {
+    reinterpret_cast<f32v4 *>(p)[0] = f32v4{f[0], f[1], f[2], f[3]};
+    reinterpret_cast<f32v4 *>(p)[1] = f32v4{f[4], f[5], f[6], f[7]};
 }
 __device__ __forceinline__ u32x4 load_p(const uint16_t *x, int64_t e) { return *reinterpret_cast<const u32x4 *>(x + e); }
 __device__ __forceinline__ void load_b16(const uint16_t *x, int64_t e, float f[8]) { unpack8_bf16(load_p(x, e), f); }
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs g) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) r[v][k] = r[v][k] * ir * w[k];
         const u32x4 h = pack8_bf16(r[v]);
-        *reinterpret_cast<u32x4 *>(g.H + row + c) = h;
+        __builtin_nontemporal_store(h, reinterpret_cast<u32x4 *>(g.H + row + c));
         unpack8_bf16(h, r[v]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) amax = max(amax, __float_as_uint(r[v][k]) & 0x7FFFFFFFu);
@@ -146,13 +148,16 @@ __global__ __launch_bounds__(NT) void norm_fwd_kernel(NormArgs g) {
 #pragma unroll
         for (int w = 0; w < NT / 64; ++w) amax = max(amax, redm[w]);
     }
-    const RowCode rc = row_code(amax);
+    const RowCode rc = row_code<false>(amax);
     if (tid == 0) g.Hs[m] = rc.scale;
+    by_mode(rc, [&](auto mode) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int c = (v * NT + tid) * 8;
-        if (in[v]) *reinterpret_cast<uint2 *>(g.Hq + row + c) = codes8(r[v], rc);
-    }
+        for (int v = 0; v < V; ++v) {
+            const int c = (v * NT + tid) * 8;
+            const uint2 o = codes8<decltype(mode)::value>(r[v], rc);
+            if (in[v]) *reinterpret_cast<uint2 *>(g.Hq + row + c) = o;
+        }
+    });
 }
 
 // How the backward's rows are cut into runs, one workgroup each.  Without a gate (or with one row of
@@ -167,11 +172,13 @@ struct NormRuns {
 };
 
 // The weights and the gate row stay in registers over a run, except with four pieces per thread: the
-// sums and the row take all 256 registers, and they are read again (from L2) for each row.
+// row takes the registers, the weights are read again (from L2) for each row, and the sums for dw_pre
+// and dw_post lie in LDS, every thread's own.
 template <int NT, int V, bool F32>
 __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
     constexpr bool HOLD = V < 4;
     __shared__ float red[4][3][NT / 64];
+    __shared__ f32v4 lsum[2][HOLD ? 1 : V * 2][HOLD ? 1 : NT];     // dw_pre's and dw_post's sums
     const int tid = threadIdx.x;
     const int64_t run = blockIdx.x;
     const float inv_c = 1.0f / (float)g.C;
@@ -187,7 +194,21 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
     const u32x4 none = {0u, 0u, 0u, 0u}, ones = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
     bool in[V];
     u32x4 hpre[HOLD ? V : 1], hpost[HOLD ? V : 1], hgate[HOLD ? V : 1];
-    float a_pre[V][8], a_post[V][8], a_gate[V][8];
+    float a_pre[HOLD ? V : 1][8], a_post[HOLD ? V : 1][8], a_gate[V][8];
+    // sum[which][v] += d
+    auto add = [&](int which, int v, const float d[8]) {
+        if (HOLD) {
+            float *a = which ? a_post[HOLD ? v : 0] : a_pre[HOLD ? v : 0];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[k] += d[k];
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                f32v4 &a = lsum[which][HOLD ? 0 : 2 * v + h][HOLD ? 0 : tid];
+                a += f32v4{d[4 * h], d[4 * h + 1], d[4 * h + 2], d[4 * h + 3]};
+            }
+        }
+    };
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = (v * NT + tid) * 8;
@@ -196,14 +217,19 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
             hpre[v] = in[v] && g.w_pre ? load_p(g.w_pre, c) : none;
             hpost[v] = in[v] && g.w_post ? load_p(g.w_post, c) : none;
             hgate[v] = ones;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a_pre[HOLD ? v : 0][k] = a_post[HOLD ? v : 0][k] = 0.0f;
+        } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) lsum[h & 1][HOLD ? 0 : 2 * v + (h >> 1)][HOLD ? 0 : tid] = f32v4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) a_pre[v][k] = a_post[v][k] = a_gate[v][k] = 0.0f;
+        for (int k = 0; k < 8; ++k) a_gate[v][k] = 0.0f;
     }
     int64_t grow = 0, next_gate = m0;         // the gate row, and the token at which it changes
     auto pre = [&](int v, float f[8]) {
         if (HOLD) unpack8_bf16(hpre[v], f);
-        else unpack8_bf16(g.w_pre ? load_p(g.w_pre, (v * NT + tid) * 8) : none, f);
+        else unpack8_bf16(g.w_pre && in[v] ? load_p(g.w_pre, (v * NT + tid) * 8) : none, f);
     };
     auto post = [&](int v, float f[8]) {
         if (HOLD) unpack8_bf16(hpost[v], f);
@@ -213,8 +239,36 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
         if (HOLD) unpack8_bf16(hgate[v], f);
         else unpack8_bf16(g.gate ? load_p(g.gate, grow * g.C + (v * NT + tid) * 8) : ones, f);
     };
+    // A row's four operands, loaded one row ahead where the registers allow it: the row's two sums over
+    // the workgroup then run under the next row's loads.
+    struct Row {
+        Raw8<F32> r[V], t[V];
+        u32x4 dh[V], b[V];
+    };
+    auto load = [&](int64_t m, Row &x) {
+        const int64_t row = m * g.C;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int64_t e = row + (v * NT + tid) * 8;
+            x.r[v].zero();
+            x.t[v].zero();
+            x.dh[v] = x.b[v] = none;
+            if (!in[v]) continue;
+            if (g.dH) {
+                x.r[v].load(g.R, e);
+                x.dh[v] = load_p(g.dH, e);
+            }
+            if (g.dR_out) x.t[v].load(g.dR_out, e);
+            if (g.B) x.b[v] = load_p(g.B, e);
+        }
+    };
+    constexpr bool AHEAD = V < 4;
+    Row cur, nxt;
+    if (AHEAD && m0 < m1) load(m0, cur);
     for (int64_t m = m0; m < m1; ++m) {
         const int64_t row = m * g.C;
+        if (AHEAD) load(m + 1 < m1 ? m + 1 : m, nxt);
+        else load(m, cur);
         if (g.gate && m == next_gate) {
             grow = m / q.T;
             next_gate = (grow + 1) * q.T;
@@ -229,21 +283,10 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int c = (v * NT + tid) * 8;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) r[v][k] = t[v][k] = 0.0f;
-            dh[v] = b[v] = none;
-            if (!in[v]) continue;
-            if (g.dH) {
-                load_res<F32>(g.R, row + c, r[v]);
-                dh[v] = load_p(g.dH, row + c);
-            }
-            if (g.dR_out) load_res<F32>(g.dR_out, row + c, t[v]);
-            if (g.B) b[v] = load_p(g.B, row + c);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (!in[v]) continue;
+            cur.r[v].floats(r[v]);
+            cur.t[v].floats(t[v]);
+            dh[v] = cur.dh[v];
+            b[v] = cur.b[v];
             float w[8], d[8], x[8];
             pre(v, w);
             unpack8_bf16(dh[v], d);
@@ -269,8 +312,10 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
             unpack8_bf16(dh[v], d);
             unpack8_bf16(b[v], x);
 #pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = d[k] * (r[v][k] * ir);
+            add(0, v, o);
+#pragma unroll
             for (int k = 0; k < 8; ++k) {
-                a_pre[v][k] = __builtin_fmaf(d[k], r[v][k] * ir, a_pre[v][k]);
                 t[v][k] += ir * w[k] * d[k] - k1 * r[v][k];
                 o[k] = g.alpha * t[v][k];
             }
@@ -283,9 +328,10 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
                 const float bh = x[k] * ib;
                 a_gate[v][k] = __builtin_fmaf(t[v][k], g.w_post ? bh * w[k] : bh, a_gate[v][k]);
                 t[v][k] *= g.beta * o[k];                                    // u
-                a_post[v][k] = __builtin_fmaf(t[v][k], bh, a_post[v][k]);
+                o[k] = t[v][k] * bh;
                 s2[0] = __builtin_fmaf(w[k] * t[v][k], x[k], s2[0]);
             }
+            if (g.w_post) add(1, v, o);
         }
         if (g.dB) {
             float k2 = 0.0f;
@@ -303,9 +349,10 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) t[v][k] = ib * w[k] * t[v][k] - k2 * x[k];
                 }
-                *reinterpret_cast<u32x4 *>(g.dB + row + (v * NT + tid) * 8) = pack8_bf16(t[v]);
+                __builtin_nontemporal_store(pack8_bf16(t[v]), reinterpret_cast<u32x4 *>(g.dB + row + (v * NT + tid) * 8));
             }
         }
+        if (AHEAD) cur = nxt;
         if (!q.cpg && g.dgate && (m + 1 == next_gate || m + 1 == g.M)) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -325,9 +372,18 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
     for (int v = 0; v < V; ++v) {
         const int c = (v * NT + tid) * 8;
         if (!in[v]) continue;
-        if (g.dw_pre) store_res<true>(g.P, run * g.C + c, a_pre[v]);
-        if (g.dw_post) store_res<true>(g.P, (q.n + run) * g.C + c, a_post[v]);
-        if (g.dgate && q.cpg) store_res<true>(g.P, (2 * q.n + run) * g.C + c, a_gate[v]);
+        if (HOLD) {
+            if (g.dw_pre) store_sum(g.P + run * g.C + c, a_pre[HOLD ? v : 0]);
+            if (g.dw_post) store_sum(g.P + (q.n + run) * g.C + c, a_post[HOLD ? v : 0]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (g.dw_pre) reinterpret_cast<f32v4 *>(g.P + run * g.C + c)[h] = lsum[0][HOLD ? 0 : 2 * v + h][HOLD ? 0 : tid];
+                if (g.dw_post)
+                    reinterpret_cast<f32v4 *>(g.P + (q.n + run) * g.C + c)[h] = lsum[1][HOLD ? 0 : 2 * v + h][HOLD ? 0 : tid];
+            }
+        }
+        if (g.dgate && q.cpg) store_sum(g.P + (2 * q.n + run) * g.C + c, a_gate[v]);
     }
 }
 
@@ -357,7 +413,15 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs g, NormRuns q, i
     }
     f32v4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < g.C)
-        for (int64_t i = sl; i < n; i += 16) acc += *reinterpret_cast<const f32v4 *>(P + i * g.C + c);
+        for (int64_t i = sl; i < n; i += 16 * 8) {       // eight loads in flight, added in order
+            f32v4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i + 16 * u < n) v[u] = *reinterpret_cast<const f32v4 *>(P + (i + 16 * u) * g.C + c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (i + 16 * u < n) acc += v[u];
+        }
     part[sl][lc] = acc;
     __syncthreads();
     if (sl == 0 && c < g.C) {
@@ -367,12 +431,21 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs g, NormRuns q, i
     }
 }
 
-constexpr int64_t kRuns = 1024;      // runs aimed at: four workgroups per CU
+// Runs aimed at: as many workgroups as the CUs hold at once (eight waves with two or more pieces per
+// thread, sixteen with one), but no fewer than eight rows each beyond the first 256, so that the
+// partials stay a small part of the traffic.
+int64_t norm_target(int64_t M, int64_t C) {
+    const int64_t per_cu = C <= 512 ? 16 : (C <= 1024 ? 8 : (C <= 2048 ? 4 : (C <= 4096 ? 2 : 1)));
+    const int64_t most = M / 8 > 256 ? M / 8 : 256;
+    const int64_t runs = 256 * per_cu < most ? 256 * per_cu : most;
+    return runs < M ? runs : M;
+}
 
-NormRuns norm_runs(int64_t M, int64_t gate_tokens) {
+NormRuns norm_runs(int64_t M, int64_t C, int64_t gate_tokens) {
     NormRuns q;
     q.T = gate_tokens > 0 && gate_tokens < M ? gate_tokens : M;
-    q.per = (M + kRuns - 1) / kRuns;
+    const int64_t runs = norm_target(M, C);
+    q.per = (M + runs - 1) / runs;
     const int64_t groups = (M + q.T - 1) / q.T;
     if (q.T >= q.per) {
         q.cpg = (q.T + q.per - 1) / q.per;
@@ -423,12 +496,11 @@ hipError_t launch_norm_fwd(const NormArgs &a, hipStream_t stream) {
 
 // Runs, whatever the gate: ceil(M / T) ceil(T / per) with T >= per is at most 2 M / per + 2.
 size_t norm_bwd_ws(int64_t M, int64_t C) {
-    const int64_t runs = 2 * (M < kRuns ? M : kRuns) + 2;
-    return (size_t)runs * 3 * C * 4;
+    return (size_t)(2 * norm_target(M, C) + 2) * 3 * C * 4;
 }
 
 hipError_t launch_norm_bwd(const NormArgs &a, hipStream_t stream) {
-    const NormRuns q = norm_runs(a.M, a.gate ? a.gate_tokens : 0);
+    const NormRuns q = norm_runs(a.M, a.C, a.gate ? a.gate_tokens : 0);
     if ((size_t)q.n * 3 * a.C * 4 > norm_bwd_ws(a.M, a.C)) return hipErrorInvalidValue;
     if (a.f32) bwd_any<true>(a, q, stream);
     else bwd_any<false>(a, q, stream);
