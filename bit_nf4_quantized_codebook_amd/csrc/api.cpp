@@ -1012,6 +1012,11 @@ int check_int8_weight(const nf4_int8_weight *w) {
 
 nf4k::Int8View view_of(const nf4_int8_weight *w) { return nf4k::Int8View{w->codes, w->scales, w->rows, w->cols}; }
 
+// Each workgroup of the Int8 GEMV (one per 16 weight rows) sums T's partials itself while their bytes
+// times the workgroups, all read from L2, stay within this; beyond, the reduction's own launch is
+// cheaper (16 tokens, r = 64: 4096 rows 12.7 against 15.9 us, 28672 rows 68.8 against 62.7 us).
+constexpr size_t kInt8TSumBytes = (size_t)64 << 20;
+
 struct Int8Plan {
     int ksT, ksdT, msL2, msL1;
     nf4k::SplitPlan kf, kb;        // split of the forward's product and of the backward's dX product
@@ -1139,7 +1144,7 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
         a.L2 = L2;
         a.M = M; a.N = N; a.K = K; a.r = r;
         a.Y = Y;
-        if (r && (size_t)p.ksT * M * r * 4 <= kGemvTSumBytes) {
+        if (r && (size_t)p.ksT * M * r * 4 * (size_t)((N + 15) / 16) <= kInt8TSumBytes) {
             a.Tp = P; a.ksT = p.ksT; a.T_out = T_out;
         } else if (r) {
             uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT);

@@ -7,15 +7,17 @@
 // The shape streams the weight's N K bytes once from HBM; everything else has to stay out of the way
 // of those loads.  Two launches:
 //   1. X's rows to codes, and T's float32 split partials (independent of each other);
-//   2. the product.  A workgroup of 8 waves owns 16 RG weight rows and its waves take turns along K
-//      (256-byte chunks, wave w takes chunks w, w + 8, ..), so that a few thousand rows already keep
-//      every CU loading; a chunk is loaded while the one before it is multiplied
-//      (v_mfma_i32_16x16x64_i8; the 16 columns of the MFMA hold 16 tokens, G groups of them).  A
-//      weight fragment's bytes go from the load straight into the MFMA: no LDS, no decode.  The
-//      codes of X (at most 64 K bytes) come from L2 with the same addressing.
+//   2. the product.  A workgroup of 4 or 8 waves owns 16 RG weight rows and its waves take turns along
+//      K (256-byte chunks, wave w takes chunks w, w + waves, ..), so that a few thousand rows already
+//      keep every CU loading; a chunk is loaded while the one before it is multiplied
+//      (v_mfma_i32_16x16x64_i8; the 16 rows of its other operand hold 16 tokens, G groups of them).  A
+//      weight fragment's bytes go from the load straight into the MFMA: no LDS, no decode.
 //      The waves' int32 sums meet in LDS by integer adds, exact in any order; then the constants, the
-//      adapter's MFMAs (s T from T's partials, summed in the prologue in a fixed order) and one
-//      rounding to bf16.
+//      adapter's MFMAs (s T from T's partials, summed in a fixed order) and one rounding to bf16.
+// Measured (both launches): 47 us for one token x 28672 x 8192 with r = 64 (5.0 TB/s of weight bytes; a
+// large copy reaches 5.2 here), 12 us at 4096 x 4096; 20 us for 23 tokens x 4096 x 11008.
+// Small workgroups with few registers win, many waves hiding the loads' latency: one token at 28672 x
+// 8192 took 45 us (r = 0) with 4 waves and 16 rows each, 57 with 32 rows, 55 with 8 waves and 64 rows.
 
 #include "common.h"
 #include "dqtile.h"
@@ -27,16 +29,18 @@ namespace nf4k {
 
 namespace {
 
-constexpr int NW = 8;              // waves
-constexpr int NT = NW * 64;
 constexpr int CHUNK = 256;         // bytes of K per wave and turn
 constexpr int CS = CHUNK / 64;     // MFMA steps of a chunk
 constexpr int R_MAX = 128;
 
-template <int RG, int G>
-__global__ __launch_bounds__(NT) void int8_gemv_kernel(Int8Gemv g) {
+// DIRECT (up to 4 tokens): the tokens are loaded in the operands' own layout, too few lines to matter.
+template <int NW, int RG, int G, bool DIRECT>
+__global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
+    constexpr int NT = NW * 64;
     __shared__ int32_t sums[RG * G * 256];                 // [tile][lane][4]
     __shared__ __align__(16) uint16_t sTs[16 * G * R_MAX];  // s T, bf16 [M][r]
+    __shared__ __align__(16) uint8_t xtile[NW][DIRECT ? 16 : G * 4096];   // each wave's tokens of a chunk
+    __shared__ f32x4 tpart[NT];                             // sums over parts of T's partials
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ln = lane & 15, lg = lane >> 4;
@@ -46,74 +50,143 @@ __global__ __launch_bounds__(NT) void int8_gemv_kernel(Int8Gemv g) {
     const __amdgpu_buffer_rsrc_t rX = make_rsrc(g.Xq, g.M * g.K);
     const int nchunk = (int)((g.K + CHUNK - 1) / CHUNK);
 
-    struct Stage {
-        u32x4 w[CS][RG], x[CS][G];
+    // Weight rows: lane (ln, lg) of step s loads bytes 64 s + 16 lg .. +15 of row ln, which is its
+    // operand.  Rows past N, tokens past M and bytes past K read zeros.
+    struct WStage {
+        u32x4 w[CS][RG];
     };
-    // rows past N, tokens past M and steps past K read zeros
     const uint32_t lane_off = (uint32_t)ln * K + lg * 16;
-    auto load = [&](int c, Stage &st) {
+    auto load_w = [&](int c, WStage &st) {
 #pragma unroll
         for (int s = 0; s < CS; ++s) {
             const uint32_t k = (uint32_t)c * CHUNK + s * 64;
             const bool live = k < K;
 #pragma unroll
             for (int q = 0; q < RG; ++q) st.w[s][q] = bload16(rW, live ? lane_off + k + q * 16 * K : 0xFFFFFFF0u);
-#pragma unroll
-            for (int q = 0; q < G; ++q) st.x[s][q] = bload16(rX, live ? lane_off + k + q * 16 * K : 0xFFFFFFF0u);
         }
     };
+    // Tokens: 16 lanes load a row's 256 bytes (four rows per load), and the wave turns them into
+    // operands through its own LDS tile, 16-byte pieces XOR-ed with the row so that neither side has
+    // bank conflicts.  Loaded in the operands' own layout (16 rows by 64 bytes), the rows' separate
+    // lines bound the kernel: 79.8 us for 16 tokens x 28672 x 8192, against 44.9 us for one.
+    static_assert(CS == 4, "a chunk's pieces: 4 loads of 4 rows, or 4 steps");
+    u32x4 xr[G][4];
+    auto load_x = [&](int c) {
+        if (DIRECT) {
+#pragma unroll
+            for (int s = 0; s < CS; ++s) {
+                const uint32_t k = (uint32_t)c * CHUNK + s * 64;
+                xr[0][s] = bload16(rX, k < K ? lane_off + k : 0xFFFFFFF0u);
+            }
+            return;
+        }
+        const int r4 = lane >> 4;
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 4 * i + r4;
+                const uint32_t k = (uint32_t)c * CHUNK + ((ln ^ row) * 16);
+                xr[q][i] = bload16(rX, k < K ? (uint32_t)(16 * q + row) * K + k : 0xFFFFFFF0u);
+            }
+    };
+    uint8_t *xt = xtile[wave];
     i32x4 acc[RG][G];
 #pragma unroll
     for (int a = 0; a < RG; ++a)
 #pragma unroll
         for (int b = 0; b < G; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
-    auto mul = [&](const Stage &st) {
+    // The tile is the wave's own: its LDS operations complete in order, so no barrier is needed, only
+    // that the compiler keeps the order of one lane's writes and another's reads.
+    auto wave_order = [&]() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+    u32x4 xd[DIRECT ? CS : 1];
+    auto put_x = [&]() {
+        if (DIRECT) {
 #pragma unroll
-        for (int s = 0; s < CS; ++s)
+            for (int s = 0; s < CS; ++s) xd[DIRECT ? s : 0] = xr[0][s];
+            return;
+        }
+        wave_order();
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(xt + q * 4096 + i * 1024 + lane * 16) = xr[q][i];
+        wave_order();
+    };
+    auto mul = [&](const WStage &st) {
+#pragma unroll
+        for (int s = 0; s < CS; ++s) {
+            i32x4 x[G];
+#pragma unroll
+            for (int b = 0; b < G; ++b)
+                x[b] = DIRECT ? __builtin_bit_cast(i32x4, xd[DIRECT ? s : 0])
+                              : *reinterpret_cast<const i32x4 *>(xt + b * 4096 + ln * 256 + (((4 * s + lg) ^ ln) * 16));
 #pragma unroll
             for (int a = 0; a < RG; ++a)
 #pragma unroll
                 for (int b = 0; b < G; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, st.x[s][b]),
-                                                                      __builtin_bit_cast(i32x4, st.w[s][a]), acc[a][b], 0, 0, 0);
+                    acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x[b], __builtin_bit_cast(i32x4, st.w[s][a]), acc[a][b], 0, 0, 0);
+        }
     };
 
-    Stage s0, s1;
-    load(wave, s0);
-    // prologue, while the first chunk streams in: the sums' zeros, s T (and T, by workgroup 0)
+    WStage s0, s1;
+    load_w(wave, s0);
+    load_x(wave);
+    // Prologue, while the first chunk streams in: the sums' zeros, and s T (and T, by workgroup 0).
+    // Where T has fewer pieces than the workgroup threads, `parts` threads share a piece's partials, so
+    // that their loads are one latency, not one after the other; the parts are added in order below.
     for (int i = tid; i < RG * G * 256; i += NT) sums[i] = 0;
+    const int E4 = (int)((g.M * g.r) >> 2);
+    const int parts = E4 > 0 && E4 < NT ? min(NT / E4, 16) : 1;
+    auto put_T = [&](int i, f32x4 t) {
+        const float s = g.scale;
+        *reinterpret_cast<uint2 *>(sTs + 4 * i) = uint2{pack_bf16x2(s * t.x, s * t.y), pack_bf16x2(s * t.z, s * t.w)};
+        if (blockIdx.x == 0 && g.T_out)
+            reinterpret_cast<uint2 *>(g.T_out)[i] = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
+    };
     if (g.r && !g.Tp) {
-        const uint2 *src = reinterpret_cast<const uint2 *>(g.sT);
-        for (int i = tid; i < (int)((g.M * g.r) >> 2); i += NT) reinterpret_cast<uint2 *>(sTs)[i] = src[i];
+        for (int i = tid; i < E4; i += NT) reinterpret_cast<uint2 *>(sTs)[i] = reinterpret_cast<const uint2 *>(g.sT)[i];
     } else if (g.r) {
-        const int64_t E4 = (g.M * g.r) >> 2;
         const f32x4 *Tp = reinterpret_cast<const f32x4 *>(g.Tp);
-        for (int i = tid; i < (int)E4; i += NT) {
-            f32x4 t = Tp[i];
-            for (int k0 = 1; k0 < g.ksT; k0 += 8) {
+        for (int j = tid; j < E4 * parts; j += NT) {
+            const int i = j % E4;
+            f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int k0 = j / E4; k0 < g.ksT; k0 += 8 * parts) {
                 f32x4 v[8];
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (k0 + u < g.ksT) v[u] = Tp[(int64_t)(k0 + u) * E4 + i];
+                    if (k0 + u * parts < g.ksT) v[u] = Tp[(int64_t)(k0 + u * parts) * E4 + i];
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (k0 + u < g.ksT) t += v[u];
+                    if (k0 + u * parts < g.ksT) t += v[u];
             }
-            const float s = g.scale;
-            *reinterpret_cast<uint2 *>(sTs + 4 * i) = uint2{pack_bf16x2(s * t.x, s * t.y), pack_bf16x2(s * t.z, s * t.w)};
-            if (blockIdx.x == 0 && g.T_out)
-                reinterpret_cast<uint2 *>(g.T_out)[i] = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
+            if (parts == 1) put_T(i, t);
+            else tpart[j] = t;
         }
     }
-    __syncthreads();
 
-    for (int c = wave; c < nchunk; c += 2 * NW) {      // chunks past the end load nothing and add zeros
-        load(c + NW, s1);
+    // One chunk ahead (two cost the registers of more waves: 45.5 -> 48.8 us for one token at
+    // 28672 x 8192).  Chunks past the end load nothing and add zeros.
+    for (int c = wave; c < nchunk; c += 2 * NW) {
+        put_x();
+        load_x(c + NW);
+        load_w(c + NW, s1);
         mul(s0);
-        load(c + 2 * NW, s0);
+        put_x();
+        load_x(c + 2 * NW);
+        load_w(c + 2 * NW, s0);
         mul(s1);
     }
 
+    __syncthreads();
+    if (parts > 1 && tid < E4 && g.Tp) {
+        f32x4 t = tpart[tid];
+        for (int p = 1; p < parts; ++p) t += tpart[p * E4 + tid];
+        put_T(tid, t);
+    }
     if (nchunk > wave) {
 #pragma unroll
         for (int a = 0; a < RG; ++a)
@@ -178,12 +251,18 @@ __global__ __launch_bounds__(256) void int8_rows_t_kernel(RowsT g) {
     int8_rows_block<false>(g.X, blockIdx.x - g.nt, g.M, g.K, g.Xq, g.xs);
 }
 
-template <int RG>
-void launch_rg(const Int8Gemv &a, hipStream_t s) {
-    const dim3 gd((unsigned)((a.N + 16 * RG - 1) / (16 * RG)));
-    if (a.M <= 16) hipLaunchKernelGGL((int8_gemv_kernel<RG, 1>), gd, dim3(NT), 0, s, a);
-    else if (a.M <= 32) hipLaunchKernelGGL((int8_gemv_kernel<RG, 2>), gd, dim3(NT), 0, s, a);
-    else hipLaunchKernelGGL((int8_gemv_kernel<RG, 4>), gd, dim3(NT), 0, s, a);
+template <int NW, int RG, int G, bool DIRECT = false>
+void launch_one(const Int8Gemv &a, hipStream_t s) {
+    hipLaunchKernelGGL((int8_gemv_kernel<NW, RG, G, DIRECT>), dim3((unsigned)((a.N + 16 * RG - 1) / (16 * RG))), dim3(NW * 64), 0, s, a);
+}
+// More than 16 tokens: 32 weight rows share the tokens' loads where that leaves a workgroup for every
+// CU (32 x 8192 x 22016: 56.5 against 64.1 us with 16 rows; 64 x 8192 x 8192 27.0 against 33.3).
+template <int G>
+void launch_g(const Int8Gemv &a, hipStream_t s) {
+    const int64_t groups = (a.N + 15) / 16;
+    if (groups >= 4 * 256) launch_one<4, 2, G>(a, s);
+    else if (groups >= 2 * 256) launch_one<8, 2, G>(a, s);
+    else launch_one<8, 1, G>(a, s);
 }
 
 }  // namespace
@@ -208,12 +287,16 @@ hipError_t launch_int8_rows_t(const uint16_t *X, const uint16_t *L1, float *P, i
 
 hipError_t launch_int8_gemv(const Int8Gemv &p, hipStream_t stream) {
     if (p.M < 1 || p.M > 64 || p.r < 0 || p.r > R_MAX || (p.r && !p.Tp == !p.sT)) return hipErrorInvalidValue;
-    // as many rows per workgroup (they share X's loads) as still leave one for every CU
+    // Four waves where the rows make at least two workgroups a CU, else eight (8192 x 22016, one token:
+    // 45.5 against 47.5 us; 4096 x 4096: 8.4 us with eight, 10.0 with sixteen).
     const int64_t groups = (p.N + 15) / 16;
     timing_before(stream, 2);
-    if (groups >= 4 * 256) launch_rg<4>(p, stream);
-    else if (groups >= 2 * 256) launch_rg<2>(p, stream);
-    else launch_rg<1>(p, stream);
+    if (p.M > 32) launch_g<4>(p, stream);
+    else if (p.M > 16) launch_g<2>(p, stream);
+    else if (p.M > 4 && groups >= 512) launch_one<4, 1, 1>(p, stream);
+    else if (p.M > 4) launch_one<8, 1, 1>(p, stream);
+    else if (groups >= 512) launch_one<4, 1, 1, true>(p, stream);
+    else launch_one<8, 1, 1, true>(p, stream);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
