@@ -1017,7 +1017,11 @@ nf4k::Int8View view_of(const nf4_int8_weight *w) { return nf4k::Int8View{w->code
 // cheaper (16 tokens, r = 64: 4096 rows 12.7 against 15.9 us, 28672 rows 68.8 against 62.7 us).
 constexpr size_t kInt8TSumBytes = (size_t)64 << 20;
 
+// From this many tokens on, the backward expands the weight to bf16 first
+constexpr int64_t kInt8ExpandMinM = 1024;
+
 struct Int8Plan {
+    bool expand;
     int ksT, ksdT, msL2, msL1;
     nf4k::SplitPlan kf, kb;        // split of the forward's product and of the backward's dX product
     size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_L2T, off_P, off_Wd, off_Pg, total;
@@ -1045,7 +1049,8 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
         pmax = pmax > ptn ? pmax : ptn;
     }
     const int64_t tiles = (M + kGemmTile - 1) / kGemmTile * ((K + kGemmTile - 1) / kGemmTile);
-    p.kb = nf4k::gemm_split(tiles, (N + kTile - 1) / kTile, kSplitQuantum);
+    p.expand = M >= kInt8ExpandMinM;
+    p.kb = p.expand ? nf4k::gemm_split(tiles, (N + kTile - 1) / kTile, kSplitQuantum) : nf4k::int8_bwd_split(M, N, K);
     p.kf = M <= kGemvMaxM ? nf4k::SplitPlan{1, 0} : nf4k::int8_gemm_split(M, N, K);
     size_t pg = p.kb.ksplit > 1 ? (size_t)p.kb.ksplit * M * K : 0;
     if (p.kf.ksplit > 1 && (size_t)p.kf.ksplit * M * N > pg) pg = (size_t)p.kf.ksplit * M * N;
@@ -1057,7 +1062,7 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     p.off_dT = off;  off += round256((size_t)M * r * 2);
     p.off_L2T = off; off += round256((size_t)N * r * 2);
     p.off_P = off;   off += round256(pmax * 4);
-    p.off_Wd = off;  off += round256((size_t)N * K * 2);
+    p.off_Wd = off;  off += p.expand ? round256((size_t)N * K * 2) : 0;
     p.off_Pg = off;  off += round256(pg * 4);
     p.total = off;
     return p;
@@ -1206,6 +1211,8 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     uint16_t *dT = ws_at<uint16_t>(workspace, p.off_dT);
+    nf4k::Reduction sums[3];
+    int nsum = 0;
     if (r) {
         float *P = ws_at<float>(workspace, p.off_P);
         const uint16_t *Tuse = T;
@@ -1230,25 +1237,34 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
         }
         NF4_CHECK_HIP(nf4k::launch_skinny_tn(tn_dL2, &tn_dL1, M, s), "dL2 = T^T dY, dL1 = X^T dT");
         if (!direct) {
-            const nf4k::Reduction red_dL2{P, p.msL2, (int64_t)r * N, scale, dL2, 0.0f, nullptr};
-            const nf4k::Reduction red_dL1{P1, p.msL1, K * (int64_t)r, 1.0f, dL1, 0.0f, nullptr};
-            NF4_CHECK_HIP(nf4k::launch_reduce_partials(red_dL2, &red_dL1, s), "dL2, dL1 reduce");
+            sums[nsum++] = nf4k::Reduction{P, p.msL2, (int64_t)r * N, scale, dL2, 0.0f, nullptr};
+            sums[nsum++] = nf4k::Reduction{P1, p.msL1, K * (int64_t)r, 1.0f, dL1, 0.0f, nullptr};
         }
     }
-    if (!dX) return NF4_OK;
-    // the weight in bf16, transposed, then the bf16 product with the adapter's steps
-    uint16_t *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
-    NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, s), "int8 expansion");
-    const bool acc = (flags & QLORA_DX_ACCUMULATE) != 0;
-    float *Pg = ws_at<float>(workspace, p.off_Pg);
-    NF4_CHECK_HIP(nf4k::launch_gemm_bf16_bwd(dY, WdT, dT, L1, r, M, N, K, dX, acc,
-                                             nf4k::SplitK{p.kb.ksplit, p.kb.per, Pg}, s),
-                  "bf16 GEMM (int8 bwd)");
-    if (p.kb.ksplit > 1) {
-        nf4k::Reduction red{Pg, p.kb.ksplit, M * K, 1.0f, dX, 0.0f, nullptr};
-        red.accum = acc;
-        NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "split product reduce");
+    if (dX) {
+        const bool acc = (flags & QLORA_DX_ACCUMULATE) != 0;
+        float *Pg = ws_at<float>(workspace, p.off_Pg);
+        if (p.expand) {
+            // the weight in bf16, transposed, then the bf16 product with the adapter's steps
+            uint16_t *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
+            NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, s), "int8 expansion");
+            NF4_CHECK_HIP(nf4k::launch_gemm_bf16_bwd(dY, WdT, dT, L1, r, M, N, K, dX, acc,
+                                                     nf4k::SplitK{p.kb.ksplit, p.kb.per, Pg}, s),
+                          "bf16 GEMM (int8 bwd)");
+        } else {
+            NF4_CHECK_HIP(nf4k::launch_int8_bwd(nf4k::Int8Bwd{dY, w->codes, w->scales, dT, L1, dX, M, N, K, r,
+                                                              acc ? 1u : 0u, p.kb.ksplit, (int32_t)p.kb.per, Pg}, s),
+                          "int8 GEMM (bwd)");
+        }
+        if (p.kb.ksplit > 1) {
+            sums[nsum] = nf4k::Reduction{Pg, p.kb.ksplit, M * K, 1.0f, dX, 0.0f, nullptr};
+            sums[nsum++].accum = acc;
+        }
     }
+    // every split product's sum in one launch
+    if (nsum)
+        NF4_CHECK_HIP(nf4k::launch_reduce_partials(sums[0], nsum > 1 ? &sums[1] : nullptr, s, nsum > 2 ? &sums[2] : nullptr),
+                      "dL2, dL1, dX reduce");
     return NF4_OK;
 }
 

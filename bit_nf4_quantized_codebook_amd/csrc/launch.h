@@ -209,6 +209,24 @@ struct Int8Gemv {
 };
 hipError_t launch_int8_gemv(const Int8Gemv &p, hipStream_t stream);
 
+// dX = dY W' + dT L1^T through the codes, without expanding the weight first; ksplit as Int8Product's
+// (steps of 64 weight rows), accumulate: dX is added to (with a split: by the reduction)
+struct Int8Bwd {
+    const uint16_t *dY;
+    const int8_t *Wq;
+    const float *ws;
+    const uint16_t *dT, *L1;
+    uint16_t *dX;
+    int64_t M, N, K;
+    int32_t r;
+    uint32_t accumulate;
+    int32_t ksplit, split_per;
+    float *P;
+};
+inline int64_t int8_bwd_tile(int64_t M) { return M <= 64 ? 64 : 128; }
+SplitPlan int8_bwd_split(int64_t M, int64_t N, int64_t K);
+hipError_t launch_int8_bwd(const Int8Bwd &p, hipStream_t stream);
+
 // ---- norm glue between blocks ----
 struct NormArgs {
     const uint16_t *w_pre, *w_post, *gate;
