@@ -6,8 +6,8 @@
 // eq. (2) (dequantization, here one constant per row), section 3.5 (the gradient to X runs through the
 // BF16 weight), section 4 eq. (3).
 //
-// Block tile TM x 256 outputs (TM 64 up to 64 tokens, else 128), reduction step 64, 4 waves, MFMA
-// v_mfma_f32_32x32x16_bf16.  dY goes straight from global memory to LDS, 16-byte chunks XOR-swizzled
+// Block tile TM x 256 outputs (TM 64 up to 64 tokens, else 128), reduction step 64, 8 waves in 2 x 4,
+// MFMA v_mfma_f32_32x32x16_bf16.  dY goes straight from global memory to LDS, 16-byte chunks XOR-swizzled
 // by (row / 2).  The weight's 64 x 256 codes of a step come through registers two steps ahead and are
 // turned to bf16 on the way to LDS, spread over the MFMA sub-steps: with u = code + 128 as an unsigned
 // byte, fma(u, ws, -128 ws) is ws * code rounded once (128 ws is exact), so a code costs one byte
@@ -28,25 +28,31 @@ namespace {
 
 constexpr int TN = 256;          // output columns per block tile
 constexpr int TK = 64;           // W rows per step
-constexpr int WL = 8;            // a thread's weight loads per step: 4 of codes, 4 of constants
-// s_waitcnt immediate: vmcnt <= WL (the weight loads issued after the dY loads may stay in flight),
-// expcnt unchecked, lgkmcnt = 0
-constexpr int kWaitA = WL | (7 << 4) | (0 << 8);
+constexpr int NT = 512;          // 8 waves
+constexpr int WL = 4;            // a thread's weight loads per step: 2 of codes, 2 of constants
+// The end of a step: at most VM of the wave's loads still in flight, its LDS operations done, then the
+// workgroup barrier.  (__syncthreads would wait for every direct-to-LDS load in flight, those of later
+// steps too.)
+template <int VM>
+__device__ __forceinline__ void step_end() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
+}
 constexpr int ROWB_RED = (TK + 8) * 2;     // adapter step's L1: [256 out][64 red]
 constexpr int ROWB_OUT = (TN + 16) * 2;    // weight step: [64 red][256 out]
 constexpr int B_STAGE = (TN * ROWB_RED > TK * ROWB_OUT) ? TN * ROWB_RED : TK * ROWB_OUT;
 
 template <int TM>
-__global__ __launch_bounds__(256, 1) void int8_bwd_kernel(Int8Bwd g) {
+__global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
     constexpr int A_STAGE = TM * TK * 2;
-    constexpr int WN_WAVES = TM == 64 ? 4 : 2;        // waves along the output columns
-    constexpr int WT_M = TM * WN_WAVES / 4;           // wave tile: WT_M x WT_N
-    constexpr int WT_N = TN / WN_WAVES;
+    constexpr int WN_WAVES = 4;                       // waves along the output columns, two along the rows
+    constexpr int WT_M = TM / 2, WT_N = TN / WN_WAVES;   // wave tile
     constexpr int IM = WT_M / 32, JN = WT_N / 32;
-    constexpr int QA = TM / 32;                       // dY loads (1 KB each) per wave and step
+    constexpr int QA = TM / 64;                       // dY loads (1 KB each) per wave and step
     // each stage its own LDS object: a read of one provably never aliases the loads into another
     __shared__ __align__(16) uint8_t As0[A_STAGE];
     __shared__ __align__(16) uint8_t As1[A_STAGE];
+    __shared__ __align__(16) uint8_t As2[A_STAGE];
+    __shared__ __align__(16) uint8_t As3[A_STAGE];
     __shared__ __align__(16) uint8_t Bs0[B_STAGE];
     __shared__ __align__(16) uint8_t Bs1[B_STAGE];
     typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -92,46 +98,43 @@ __global__ __launch_bounds__(256, 1) void int8_bwd_kernel(Int8Bwd g) {
             const uint32_t off = a_col[q] < rem ? a_voff[q] + (uint32_t)n0 * 2 : 0xFFFFFFF0u;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(dst + q * 1024), 16, off, 0, 0, 0);
         }
-        // what follows stays behind these loads: kWaitA counts on it
+        // what follows stays behind these loads: the waits count on the order
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // ---- W: thread -> rows tid/16 + 16 q (q < 4) of the step, columns 16 (tid%16) .. +15: 16 lanes
+    // ---- W: thread -> rows tid/16 + 32 q (q < 2) of the step, columns 16 (tid%16) .. +15: 16 lanes
     // read 256 contiguous bytes of a row ----
     const int w_row = tid >> 4, w_col = (tid & 15) * 16;
     struct WStage {
-        u32x4 w[4];
-        uint32_t s[4];
+        u32x4 w[2];
+        uint32_t s[2];
     };
     const bool col_in = o0 + w_col < g.K;                           // K % 64 == 0: all 16 or none
     auto load_W = [&](int step, WStage &st) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int64_t n = (int64_t)(kb + step) * TK + w_row + 16 * q;
+        for (int q = 0; q < 2; ++q) {
+            const int64_t n = (int64_t)(kb + step) * TK + w_row + 32 * q;
             const bool in = n < nend;
             st.w[q] = bload16(rW, in && col_in ? (uint32_t)(n * g.K + o0 + w_col) : 0xFFFFFFF0u);
             st.s[q] = bload4(rS, in ? (uint32_t)n * 4 : 0xFFFFFFF0u);
         }
     };
-    // row part q of a stage to bf16 (rows past the end: constant 0, so zeros)
-    auto write_B = [&](const WStage &st, uint8_t *Bst, int q) {
+    // part p (0..3) of a stage to bf16: eight codes of row p / 2 (rows past the end: constant 0, so zeros)
+    auto write_B = [&](const WStage &st, uint8_t *Bst, int p) {
+        const int q = p >> 1, h = p & 1;
         const float s = __uint_as_float(st.s[q]), off = -128.0f * s;
-        uint8_t *Bd = Bst + (w_row + 16 * q) * ROWB_OUT + w_col * 2;
+        uint32_t o[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t o[4];
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const uint32_t u = st.w[q][2 * h + d] ^ 0x80808080u;
-                const float f0 = __builtin_fmaf((float)(u & 0xFFu), s, off);
-                const float f1 = __builtin_fmaf((float)((u >> 8) & 0xFFu), s, off);
-                const float f2 = __builtin_fmaf((float)((u >> 16) & 0xFFu), s, off);
-                const float f3 = __builtin_fmaf((float)(u >> 24), s, off);
-                o[2 * d] = pack_bf16x2(f0, f1);
-                o[2 * d + 1] = pack_bf16x2(f2, f3);
-            }
-            *reinterpret_cast<u32x4 *>(Bd + 16 * h) = u32x4{o[0], o[1], o[2], o[3]};
+        for (int d = 0; d < 2; ++d) {
+            const uint32_t u = st.w[q][2 * h + d] ^ 0x80808080u;
+            const float f0 = __builtin_fmaf((float)(u & 0xFFu), s, off);
+            const float f1 = __builtin_fmaf((float)((u >> 8) & 0xFFu), s, off);
+            const float f2 = __builtin_fmaf((float)((u >> 16) & 0xFFu), s, off);
+            const float f3 = __builtin_fmaf((float)(u >> 24), s, off);
+            o[2 * d] = pack_bf16x2(f0, f1);
+            o[2 * d + 1] = pack_bf16x2(f2, f3);
         }
+        *reinterpret_cast<u32x4 *>(Bst + (w_row + 32 * q) * ROWB_OUT + w_col * 2 + 16 * h) = u32x4{o[0], o[1], o[2], o[3]};
     };
 
     f32x16 acc[IM][JN];
@@ -181,16 +184,16 @@ __global__ __launch_bounds__(256, 1) void int8_bwd_kernel(Int8Bwd g) {
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
     };
     // one sub-step: its MFMAs, the next sub-step's fragment reads, a quarter of the next step's
-    // conversion (about 44 VALU, 2 LDS writes) and of the weight loads, interleaved
+    // conversion, interleaved
     auto interleave = [&]() {
         constexpr int NM = IM * JN, ND = IM + 2 * JN;
 #pragma unroll
         for (int k = 0; k < NM; ++k) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // 1 MFMA
-            __builtin_amdgcn_sched_group_barrier(0x002, (48 + NM - 1) / NM, 0);     // VALU
-            if (k < (ND + 1) / 2) __builtin_amdgcn_sched_group_barrier(0x100, (NM >= 8) ? 2 : 3, 0);   // DS reads
-            if (k == NM / 2 || k == NM - 1) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);         // DS write
-            if (k < 2) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);           // VMEM
+            __builtin_amdgcn_sched_group_barrier(0x002, 24 / NM, 0);                // VALU
+            __builtin_amdgcn_sched_group_barrier(0x100, (ND + NM - 1) / NM, 0);     // DS reads
+            if (k == NM - 1) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);     // DS write
+            if (k == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);          // VMEM
         }
     };
     // compute stage (Ac, Bc); the weight registers `st` of the step after it go to Bn
@@ -209,36 +212,38 @@ __global__ __launch_bounds__(256, 1) void int8_bwd_kernel(Int8Bwd g) {
         }
     };
 
-    // ---- main loop: dY of step + 1 goes to LDS at the start of step, the codes of step + 2 to
-    // registers, those of step + 1 to bf16 in the other B stage during it ----
-    WStage R0, R1;
+    // ---- main loop: at step s the dY tile of step s + 3 is on its way to LDS and the codes of step
+    // s + 4 to registers, while those of step s + 1 become bf16 in the other B stage.  (With one step
+    // ahead, each step waited out the loads' latency: 1.3 us of them against 0.5 us of MFMAs.) ----
+    WStage R0, R1, R2, R3;
+    // Loads issued after dY of step s + 1 (step s - 2's weights, then two steps of both) may be in
+    // flight at the end of step s.
+    constexpr int kWaitVm = WL + 2 * (QA + WL);
+    auto step_do = [&](int step, const uint8_t *Ac, uint8_t *An, const uint8_t *Bc, uint8_t *Bn, const WStage &conv,
+                       WStage &fill) {
+        load_A(step + 3, An);
+        load_W(step + 4, fill);
+        half_step(Ac, Bc, Bn, conv);
+        step_end<kWaitVm>();                     // dY of step + 1 landed, this wave's LDS operations done
+    };
     load_A(0, As0);
     load_W(0, R0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) write_B(R0, Bs0, q);
+    load_A(1, As1);
     load_W(1, R1);
+    load_A(2, As2);
+    load_W(2, R2);
+    load_W(3, R3);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) write_B(R0, Bs0, p);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    int step = 0;
-    for (; step + 1 < steps; step += 2) {
-        load_A(step + 1, As1);
-        load_W(step + 2, R0);
-        half_step(As0, Bs0, Bs1, R1);
-        __builtin_amdgcn_s_waitcnt(kWaitA);      // dY of step + 1 landed, LDS writes done
-        __syncthreads();
-        load_A(step + 2, As0);
-        load_W(step + 3, R1);
-        half_step(As1, Bs1, Bs0, R0);            // zeros past the end
-        __builtin_amdgcn_s_waitcnt(kWaitA);
-        __syncthreads();
-    }
-    if (step < steps) {                          // odd count: the last step sits in stage 0
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            Frags f;
-            load_frags(As0, Bs0, s, f);
-            mma(f);
-        }
+    // whole groups of four steps: those past the end multiply zeros (leaving in mid-group made the
+    // compiler copy registers with loads in flight, and wait for them)
+    for (int step = 0; step < steps; step += 4) {
+        step_do(step, As0, As3, Bs0, Bs1, R1, R0);
+        step_do(step + 1, As1, As0, Bs1, Bs0, R2, R1);
+        step_do(step + 2, As2, As1, Bs0, Bs1, R3, R2);
+        step_do(step + 3, As3, As2, Bs1, Bs0, R0, R3);
     }
     __builtin_amdgcn_s_waitcnt(0);               // loads past the end still write their zeros
     __syncthreads();
@@ -249,11 +254,11 @@ __global__ __launch_bounds__(256, 1) void int8_bwd_kernel(Int8Bwd g) {
         const __amdgpu_buffer_rsrc_t rBe = make_rsrc(g.L1 + o0 * g.r, (g.K - o0) * (int64_t)g.r * 2);
         for (int e = 0; e < ext_steps; ++e) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int row = (tid >> 3) + 32 * q, chunk = tid & 7;
+            for (int q = 0; q < 4; ++q) {
+                const int row = (tid >> 3) + 64 * q, chunk = tid & 7;
                 const int jj = e * TK + chunk * 8;
                 const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0xFFFFFFF0u;
-                if (q < TM / 32)
+                if (q < TM / 64)
                     *reinterpret_cast<u32x4 *>(As0 + row * 128 + (chunk ^ ((row >> 1) & 7)) * 16) = bload16(rAe, off);
                 *reinterpret_cast<u32x4 *>(Bs0 + row * ROWB_RED + chunk * 16) = bload16(rBe, off);
             }
@@ -329,8 +334,8 @@ hipError_t launch_int8_bwd(const Int8Bwd &p, hipStream_t stream) {
     }
     const dim3 grid((unsigned)(tiles * a.ksplit));
     timing_before(stream, 1);
-    if (TM == 64) hipLaunchKernelGGL(int8_bwd_kernel<64>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(int8_bwd_kernel<128>, grid, dim3(256), 0, stream, a);
+    if (TM == 64) hipLaunchKernelGGL(int8_bwd_kernel<64>, grid, dim3(NT), 0, stream, a);
+    else hipLaunchKernelGGL(int8_bwd_kernel<128>, grid, dim3(NT), 0, stream, a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
