@@ -109,18 +109,18 @@ __device__ __forceinline__ uint2 codes8(const float x[8], const RowCode &c) {
                                      __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0C0C0400u), 0x05040100u);
     return uint2{o[0], o[1]};
 }
-// f(std::integral_constant-like mode) once, by the row's (uniform) mode
+// f(the mode as a constant) once, by the row's (uniform) mode
 template <int MODE>
-struct RowMode {
+struct IntConst {
     static constexpr int value = MODE;
 };
 template <class F>
 __device__ __forceinline__ void by_mode(const RowCode &c, F f) {
     const int mode = __builtin_amdgcn_readfirstlane(c.mode);
-    if (mode == ROW_PLAIN) f(RowMode<ROW_PLAIN>());
-    else if (mode == ROW_TIES) f(RowMode<ROW_TIES>());
-    else if (mode == ROW_TINY) f(RowMode<ROW_TINY>());
-    else f(RowMode<ROW_ZERO>());
+    if (mode == ROW_PLAIN) f(IntConst<ROW_PLAIN>());
+    else if (mode == ROW_TIES) f(IntConst<ROW_TIES>());
+    else if (mode == ROW_TINY) f(IntConst<ROW_TINY>());
+    else f(IntConst<ROW_ZERO>());
 }
 
 // ---- rows to codes ----

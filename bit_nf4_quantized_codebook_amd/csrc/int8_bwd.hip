@@ -38,7 +38,10 @@ __device__ __forceinline__ void step_end() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(VM) : "memory");
 }
 constexpr int ROWB_RED = (TK + 8) * 2;     // adapter step's L1: [256 out][64 red]
-constexpr int ROWB_OUT = (TN + 16) * 2;    // weight step: [64 red][256 out]
+// weight step: [64 red][256 out].  A row starts 16 banks after the one before, so that the transposing
+// reads of four rows by 32 columns touch each bank once; and the 16-byte pieces of columns 128 .. 255 are
+// swapped in pairs, so that 16 lanes writing every second piece of a row do too.
+constexpr int ROWB_OUT = (TN + 32) * 2;
 constexpr int B_STAGE = (TN * ROWB_RED > TK * ROWB_OUT) ? TN * ROWB_RED : TK * ROWB_OUT;
 
 template <int TM>
@@ -67,7 +70,7 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
     const int ntiles = ntm * ntn;
     const int split = (int)(blockIdx.x / (uint32_t)ntiles);
     int tm, tn;
-    tile_coords(ntm, ntn, (int)blockIdx.x - split * ntiles, tm, tn);
+    tile_coords_grouped<4>(ntm, ntn, (int)blockIdx.x - split * ntiles, tm, tn);
     const int64_t m0 = (int64_t)tm * TM;
     const int64_t o0 = (int64_t)tn * TN;
     // this workgroup's steps: kb .. kb + steps - 1
@@ -109,15 +112,22 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
         u32x4 w[2];
         uint32_t s[2];
     };
-    const bool col_in = o0 + w_col < g.K;                           // K % 64 == 0: all 16 or none
-    auto load_W = [&](int step, WStage &st) {
+    // The loads go out in step order, so row and offset are kept and moved on (a multiplication and a
+    // branch less per step).  Rows past the end and columns past K (all 16 of a thread, K % 64 == 0) read
+    // zeros; offsets stay below 2^32: N K < 2^31, and at most 8 steps of 64 K beyond.
+    const int w_end = o0 + w_col < g.K ? nend : 0;
+    int w_n = kb * TK + w_row;
+    uint32_t w_off = (uint32_t)((int64_t)w_n * g.K + o0 + w_col);
+    const uint32_t row32 = (uint32_t)(32 * g.K), row64 = (uint32_t)(64 * g.K);
+    auto load_W = [&](WStage &st) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int64_t n = (int64_t)(kb + step) * TK + w_row + 32 * q;
-            const bool in = n < nend;
-            st.w[q] = bload16(rW, in && col_in ? (uint32_t)(n * g.K + o0 + w_col) : 0xFFFFFFF0u);
-            st.s[q] = bload4(rS, in ? (uint32_t)n * 4 : 0xFFFFFFF0u);
+            const bool in = w_n + 32 * q < w_end;
+            st.w[q] = bload16(rW, in ? w_off + q * row32 : 0xFFFFFFF0u);
+            st.s[q] = bload4(rS, in ? (uint32_t)(w_n + 32 * q) * 4 : 0xFFFFFFF0u);
         }
+        w_n += TK;
+        w_off += row64;
     };
     // part p (0..3) of a stage to bf16: eight codes of row p / 2 (rows past the end: constant 0, so zeros)
     auto write_B = [&](const WStage &st, uint8_t *Bst, int p) {
@@ -134,7 +144,7 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
             o[2 * d] = pack_bf16x2(f0, f1);
             o[2 * d + 1] = pack_bf16x2(f2, f3);
         }
-        *reinterpret_cast<u32x4 *>(Bst + (w_row + 32 * q) * ROWB_OUT + w_col * 2 + 16 * h) = u32x4{o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<u32x4 *>(Bst + (w_row + 32 * q) * ROWB_OUT + w_col * 2 + 16 * (h ^ (w_col >> 7))) = u32x4{o[0], o[1], o[2], o[3]};
     };
 
     f32x16 acc[IM][JN];
@@ -157,7 +167,7 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
         const int i16 = lane & 15, half = (lane >> 4) & 1;
         const int col0 = wn * WT_N + j * 32 + half * 16;
         const int rowb = s * 16 + hh * 8 + (i16 >> 2);
-        const uint8_t *base = Bst + (col0 + 4 * (i16 & 3)) * 2;
+        const uint8_t *base = Bst + (col0 + ((4 * (i16 & 3)) ^ (col0 >> 7 << 3))) * 2;
         const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(base + rowb * ROWB_OUT));
         const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16 *)(base + (rowb + 4) * ROWB_OUT));
         const v8i16 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -183,67 +193,75 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
             for (int j = 0; j < JN; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
     };
-    // one sub-step: its MFMAs, the next sub-step's fragment reads, a quarter of the next step's
+    // one sub-step: its MFMAs, the next sub-step's fragment reads, and up to half of the next step's
     // conversion, interleaved
-    auto interleave = [&]() {
-        constexpr int NM = IM * JN, ND = IM + 2 * JN;
+    auto interleave = [&](auto parts) {
+        constexpr int NM = IM * JN, ND = IM + 2 * JN, dsw = decltype(parts)::value, valu = 24 * dsw;
 #pragma unroll
         for (int k = 0; k < NM; ++k) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                      // 1 MFMA
-            __builtin_amdgcn_sched_group_barrier(0x002, 24 / NM, 0);                // VALU
+            __builtin_amdgcn_sched_group_barrier(0x002, (valu + NM - 1) / NM, 0);   // VALU
             __builtin_amdgcn_sched_group_barrier(0x100, (ND + NM - 1) / NM, 0);     // DS reads
-            if (k == NM - 1) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);     // DS write
-            if (k == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);          // VMEM
-        }
-    };
-    // compute stage (Ac, Bc); the weight registers `st` of the step after it go to Bn
-    auto half_step = [&](const uint8_t *Ac, const uint8_t *Bc, uint8_t *Bn, const WStage &st) {
-        Frags f0, f1;
-        load_frags(Ac, Bc, 0, f0);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            Frags &cur = (s & 1) ? f1 : f0;
-            Frags &nxt = (s & 1) ? f0 : f1;
-            if (s < 3) load_frags(Ac, Bc, s + 1, nxt);
-            mma(cur);
-            write_B(st, Bn, s);
-            interleave();
-            __builtin_amdgcn_sched_barrier(0);
+            if (k >= NM - dsw) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);   // DS write
         }
     };
 
-    // ---- main loop: at step s the dY tile of step s + 3 is on its way to LDS and the codes of step
-    // s + 4 to registers, while those of step s + 1 become bf16 in the other B stage.  (With one step
-    // ahead, each step waited out the loads' latency: 1.3 us of them against 0.5 us of MFMAs.) ----
+    // ---- main loop.  Step s computes stage (Ac, Bc); its next stage's dY landed earlier, and the codes
+    // of step s + 1 (registers) become bf16 in Bn during sub-steps 0 to 2.  The barrier sits between
+    // sub-steps 2 and 3: by then every wave has its last fragments of the stage in registers and Bn is
+    // whole, so the first fragments of the next stage are read under sub-step 3's MFMAs.  After it, dY
+    // of step s + 4 starts into the stage's own LDS and the codes of step s + 4 into registers: three
+    // steps ahead, since with one each step waited out the loads' latency. ----
     WStage R0, R1, R2, R3;
-    // Loads issued after dY of step s + 1 (step s - 2's weights, then two steps of both) may be in
-    // flight at the end of step s.
+    Frags f0, f1;
+    // Loads issued after dY of step s + 1 that may still be in flight at step s's barrier: step s + 1's
+    // codes, then dY and codes of two more steps.
     constexpr int kWaitVm = WL + 2 * (QA + WL);
-    auto step_do = [&](int step, const uint8_t *Ac, uint8_t *An, const uint8_t *Bc, uint8_t *Bn, const WStage &conv,
+    auto step_do = [&](int step, uint8_t *Ac, const uint8_t *Bc, const uint8_t *An, uint8_t *Bn, const WStage &conv,
                        WStage &fill) {
-        load_A(step + 3, An);
-        load_W(step + 4, fill);
-        half_step(Ac, Bc, Bn, conv);
-        step_end<kWaitVm>();                     // dY of step + 1 landed, this wave's LDS operations done
+        load_frags(Ac, Bc, 1, f1);
+        mma(f0);
+        write_B(conv, Bn, 0);
+        write_B(conv, Bn, 1);
+        interleave(IntConst<2>());
+        __builtin_amdgcn_sched_barrier(0);
+        load_frags(Ac, Bc, 2, f0);
+        mma(f1);
+        write_B(conv, Bn, 2);
+        interleave(IntConst<1>());
+        __builtin_amdgcn_sched_barrier(0);
+        load_frags(Ac, Bc, 3, f1);
+        mma(f0);
+        write_B(conv, Bn, 3);
+        interleave(IntConst<1>());
+        __builtin_amdgcn_sched_barrier(0);
+        step_end<kWaitVm>();
+        load_A(step + 4, Ac);
+        load_W(fill);
+        load_frags(An, Bn, 0, f0);
+        mma(f1);
+        __builtin_amdgcn_sched_barrier(0);
     };
     load_A(0, As0);
-    load_W(0, R0);
+    load_W(R0);
     load_A(1, As1);
-    load_W(1, R1);
+    load_W(R1);
     load_A(2, As2);
-    load_W(2, R2);
-    load_W(3, R3);
+    load_W(R2);
+    load_A(3, As3);
+    load_W(R3);
 #pragma unroll
     for (int p = 0; p < 4; ++p) write_B(R0, Bs0, p);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
+    load_frags(As0, Bs0, 0, f0);
     // whole groups of four steps: those past the end multiply zeros (leaving in mid-group made the
     // compiler copy registers with loads in flight, and wait for them)
     for (int step = 0; step < steps; step += 4) {
-        step_do(step, As0, As3, Bs0, Bs1, R1, R0);
-        step_do(step + 1, As1, As0, Bs1, Bs0, R2, R1);
-        step_do(step + 2, As2, As1, Bs0, Bs1, R3, R2);
-        step_do(step + 3, As3, As2, Bs1, Bs0, R0, R3);
+        step_do(step, As0, Bs0, As1, Bs1, R1, R0);
+        step_do(step + 1, As1, Bs1, As2, Bs0, R2, R1);
+        step_do(step + 2, As2, Bs0, As3, Bs1, R3, R2);
+        step_do(step + 3, As3, Bs1, As0, Bs0, R0, R3);
     }
     __builtin_amdgcn_s_waitcnt(0);               // loads past the end still write their zeros
     __syncthreads();
