@@ -1017,8 +1017,30 @@ nf4k::Int8View view_of(const nf4_int8_weight *w) { return nf4k::Int8View{w->code
 // cheaper (16 tokens, r = 64: 4096 rows 12.7 against 15.9 us, 28672 rows 68.8 against 62.7 us).
 constexpr size_t kInt8TSumBytes = (size_t)64 << 20;
 
-// From this many tokens on, the backward expands the weight to bf16 first
-constexpr int64_t kInt8ExpandMinM = 1024;
+// Whether the backward's dX product expands the weight to bf16 first (256 x 256 tiles of the bf16 GEMM) or
+// converts the codes on the way (64 or 128 x 256 tiles): the smaller of the two times estimated from
+// what was measured, in us.
+//   - a reduction step of 64 takes about 1.05 in the converting kernel; in the bf16 GEMM 1.0 with up to
+//     half the CUs busy, rising to 1.6 with all of them (the clock falls under its MFMA load);
+//   - the expansion moves 3 bytes a weight at 4.2 TB/s;
+//   - a split's float32 partials cost their bytes at about 5 TB/s.
+// Measured with r = 64 (expanding / converting, the whole call): 333 x 11008 x 4096 99 / 69, 768 x 4096 x
+// 11008 122 / 157 (258 tiles of 128 rows on 256 CUs), 1024 x 4096 x 4096 84 / 70, 1500 x 11008 x 4096
+// 187 / 201, 2048 x 22016 x 8192 764 / 820, 4096 x 4096 x 4096 154 / 185.
+bool int8_expands(int64_t M, int64_t N, int64_t K) {
+    const int64_t steps = (N + kTile - 1) / kTile, ntn = (K + kGemmTile - 1) / kGemmTile;
+    auto rounds = [](int64_t wgs) { return (double)((wgs + 255) / 256); };
+    auto partials = [&](const nf4k::SplitPlan &s) { return s.ksplit > 1 ? (double)s.ksplit * M * K * 4 / 5e6 : 0.0; };
+    const nf4k::SplitPlan c = nf4k::int8_bwd_split(M, N, K);
+    const int64_t ct = (M + nf4k::int8_bwd_tile(M) - 1) / nf4k::int8_bwd_tile(M) * ntn * c.ksplit;
+    const int64_t et = (M + kGemmTile - 1) / kGemmTile * ntn;
+    const nf4k::SplitPlan e = nf4k::gemm_split(et, steps, kSplitQuantum);
+    const double convert = rounds(ct) * c.per * 1.05 + partials(c);
+    const double busy = et * e.ksplit >= 256 ? 1.0 : (double)(et * e.ksplit) / 256;
+    const double step = 1.0 + (busy > 0.5 ? 1.2 * (busy - 0.5) : 0.0);
+    const double expand = (double)N * K * 3 / 4.2e6 + rounds(et * e.ksplit) * e.per * step + partials(e);
+    return expand < convert;
+}
 
 struct Int8Plan {
     bool expand;
@@ -1049,7 +1071,7 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
         pmax = pmax > ptn ? pmax : ptn;
     }
     const int64_t tiles = (M + kGemmTile - 1) / kGemmTile * ((K + kGemmTile - 1) / kGemmTile);
-    p.expand = M >= kInt8ExpandMinM;
+    p.expand = int8_expands(M, N, K);
     p.kb = p.expand ? nf4k::gemm_split(tiles, (N + kTile - 1) / kTile, kSplitQuantum) : nf4k::int8_bwd_split(M, N, K);
     p.kf = M <= kGemvMaxM ? nf4k::SplitPlan{1, 0} : nf4k::int8_gemm_split(M, N, K);
     size_t pg = p.kb.ksplit > 1 ? (size_t)p.kb.ksplit * M * K : 0;

@@ -1,5 +1,5 @@
-// dX of the Int8 QLoRA linear backward at token counts where expanding the weight to bf16 first costs
-// more than it saves (gfx950):
+// dX of the Int8 QLoRA linear backward where expanding the weight to bf16 first would cost
+// more than it saves, as up to about a thousand tokens (gfx950):
 //   dX = dY . W' + dT . L1^T,   W'[n, k] = bf16(ws[n] Wq[n, k]),   reduction over the W rows n
 //
 // Page: "QLoRA: Efficient Finetuning of Quantized LLMs" study notes (gitcode.csdn.net), section 3.1
@@ -28,8 +28,6 @@ namespace {
 
 constexpr int TN = 256;          // output columns per block tile
 constexpr int TK = 64;           // W rows per step
-constexpr int NT = 512;          // 8 waves
-constexpr int WL = 4;            // a thread's weight loads per step: 2 of codes, 2 of constants
 // The end of a step: at most VM of the wave's loads still in flight, its LDS operations done, then the
 // workgroup barrier.  (__syncthreads would wait for every direct-to-LDS load in flight, those of later
 // steps too.)
@@ -44,13 +42,16 @@ constexpr int ROWB_RED = (TK + 8) * 2;     // adapter step's L1: [256 out][64 re
 constexpr int ROWB_OUT = (TN + 32) * 2;
 constexpr int B_STAGE = (TN * ROWB_RED > TK * ROWB_OUT) ? TN * ROWB_RED : TK * ROWB_OUT;
 
-template <int TM>
-__global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
+template <int TM, int NW>
+__global__ __launch_bounds__(NW * 64) void int8_bwd_kernel(Int8Bwd g) {
+    constexpr int NT = NW * 64;
+    constexpr int WR = NT / 16, WQ = TK / WR;         // weight rows per pass of the workgroup, passes per step
+    constexpr int WL = 2 * WQ;                        // a thread's weight loads per step: codes and constants
     constexpr int A_STAGE = TM * TK * 2;
-    constexpr int WN_WAVES = 4;                       // waves along the output columns, two along the rows
+    constexpr int WN_WAVES = NW / 2;                  // waves along the output columns, two along the rows
     constexpr int WT_M = TM / 2, WT_N = TN / WN_WAVES;   // wave tile
     constexpr int IM = WT_M / 32, JN = WT_N / 32;
-    constexpr int QA = TM / 64;                       // dY loads (1 KB each) per wave and step
+    constexpr int QA = TM / (8 * NW);                       // dY loads (1 KB each) per wave and step
     // each stage its own LDS object: a read of one provably never aliases the loads into another
     __shared__ __align__(16) uint8_t As0[A_STAGE];
     __shared__ __align__(16) uint8_t As1[A_STAGE];
@@ -105,12 +106,12 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // ---- W: thread -> rows tid/16 + 32 q (q < 2) of the step, columns 16 (tid%16) .. +15: 16 lanes
+    // ---- W: thread -> rows tid/16 + WR q of the step, columns 16 (tid%16) .. +15: 16 lanes
     // read 256 contiguous bytes of a row ----
     const int w_row = tid >> 4, w_col = (tid & 15) * 16;
     struct WStage {
-        u32x4 w[2];
-        uint32_t s[2];
+        u32x4 w[WQ];
+        uint32_t s[WQ];
     };
     // The loads go out in step order, so row and offset are kept and moved on (a multiplication and a
     // branch less per step).  Rows past the end and columns past K (all 16 of a thread, K % 64 == 0) read
@@ -118,18 +119,18 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
     const int w_end = o0 + w_col < g.K ? nend : 0;
     int w_n = kb * TK + w_row;
     uint32_t w_off = (uint32_t)((int64_t)w_n * g.K + o0 + w_col);
-    const uint32_t row32 = (uint32_t)(32 * g.K), row64 = (uint32_t)(64 * g.K);
+    const uint32_t rowq = (uint32_t)(WR * g.K), row64 = (uint32_t)(64 * g.K);
     auto load_W = [&](WStage &st) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const bool in = w_n + 32 * q < w_end;
-            st.w[q] = bload16(rW, in ? w_off + q * row32 : 0xFFFFFFF0u);
-            st.s[q] = bload4(rS, in ? (uint32_t)(w_n + 32 * q) * 4 : 0xFFFFFFF0u);
+        for (int q = 0; q < WQ; ++q) {
+            const bool in = w_n + WR * q < w_end;
+            st.w[q] = bload16(rW, in ? w_off + q * rowq : 0xFFFFFFF0u);
+            st.s[q] = bload4(rS, in ? (uint32_t)(w_n + WR * q) * 4 : 0xFFFFFFF0u);
         }
         w_n += TK;
         w_off += row64;
     };
-    // part p (0..3) of a stage to bf16: eight codes of row p / 2 (rows past the end: constant 0, so zeros)
+    // part p (0 .. 2 WQ - 1) of a stage to bf16: eight codes of row p / 2 (rows past the end: constant 0, so zeros)
     auto write_B = [&](const WStage &st, uint8_t *Bst, int p) {
         const int q = p >> 1, h = p & 1;
         const float s = __uint_as_float(st.s[q]), off = -128.0f * s;
@@ -144,7 +145,7 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
             o[2 * d] = pack_bf16x2(f0, f1);
             o[2 * d + 1] = pack_bf16x2(f2, f3);
         }
-        *reinterpret_cast<u32x4 *>(Bst + (w_row + 32 * q) * ROWB_OUT + w_col * 2 + 16 * (h ^ (w_col >> 7))) = u32x4{o[0], o[1], o[2], o[3]};
+        *reinterpret_cast<u32x4 *>(Bst + (w_row + WR * q) * ROWB_OUT + w_col * 2 + 16 * (h ^ (w_col >> 7))) = u32x4{o[0], o[1], o[2], o[3]};
     };
 
     f32x16 acc[IM][JN];
@@ -221,19 +222,21 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
                        WStage &fill) {
         load_frags(Ac, Bc, 1, f1);
         mma(f0);
-        write_B(conv, Bn, 0);
-        write_B(conv, Bn, 1);
-        interleave(IntConst<2>());
+#pragma unroll
+        for (int p = 0; p < WQ; ++p) write_B(conv, Bn, p);
+        interleave(IntConst<WQ>());
         __builtin_amdgcn_sched_barrier(0);
         load_frags(Ac, Bc, 2, f0);
         mma(f1);
-        write_B(conv, Bn, 2);
-        interleave(IntConst<1>());
+#pragma unroll
+        for (int p = WQ; p < WQ + WQ / 2; ++p) write_B(conv, Bn, p);
+        interleave(IntConst<WQ / 2>());
         __builtin_amdgcn_sched_barrier(0);
         load_frags(Ac, Bc, 3, f1);
         mma(f0);
-        write_B(conv, Bn, 3);
-        interleave(IntConst<1>());
+#pragma unroll
+        for (int p = WQ + WQ / 2; p < 2 * WQ; ++p) write_B(conv, Bn, p);
+        interleave(IntConst<WQ / 2>());
         __builtin_amdgcn_sched_barrier(0);
         step_end<kWaitVm>();
         load_A(step + 4, Ac);
@@ -251,7 +254,7 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
     load_A(3, As3);
     load_W(R3);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) write_B(R0, Bs0, p);
+    for (int p = 0; p < 2 * WQ; ++p) write_B(R0, Bs0, p);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
     load_frags(As0, Bs0, 0, f0);
@@ -272,11 +275,11 @@ __global__ __launch_bounds__(NT) void int8_bwd_kernel(Int8Bwd g) {
         const __amdgpu_buffer_rsrc_t rBe = make_rsrc(g.L1 + o0 * g.r, (g.K - o0) * (int64_t)g.r * 2);
         for (int e = 0; e < ext_steps; ++e) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int row = (tid >> 3) + 64 * q, chunk = tid & 7;
+            for (int q = 0; q < TN / (8 * NW); ++q) {
+                const int row = (tid >> 3) + 8 * NW * q, chunk = tid & 7;
                 const int jj = e * TK + chunk * 8;
                 const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0xFFFFFFF0u;
-                if (q < TM / 64)
+                if (row < TM)
                     *reinterpret_cast<u32x4 *>(As0 + row * 128 + (chunk ^ ((row >> 1) & 7)) * 16) = bload16(rAe, off);
                 *reinterpret_cast<u32x4 *>(Bs0 + row * ROWB_RED + chunk * 16) = bload16(rBe, off);
             }
@@ -352,8 +355,8 @@ hipError_t launch_int8_bwd(const Int8Bwd &p, hipStream_t stream) {
     }
     const dim3 grid((unsigned)(tiles * a.ksplit));
     timing_before(stream, 1);
-    if (TM == 64) hipLaunchKernelGGL(int8_bwd_kernel<64>, grid, dim3(NT), 0, stream, a);
-    else hipLaunchKernelGGL(int8_bwd_kernel<128>, grid, dim3(NT), 0, stream, a);
+    if (TM == 64) hipLaunchKernelGGL((int8_bwd_kernel<64, 8>), grid, dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL((int8_bwd_kernel<128, 8>), grid, dim3(512), 0, stream, a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
