@@ -1130,7 +1130,8 @@ int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream)
     if (w->rows >= ((int64_t)1 << 40) / w->cols) return fail(NF4_ERR_UNSUPPORTED, "the weight exceeds 2^40 elements");
     if (!out_bf16) return fail(NF4_ERR_NULL, "out_bf16 is NULL");
     if (!aligned16(out_bf16)) return fail(NF4_ERR_ALIGN, "out_bf16 must be 16-byte aligned");
-    NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/false, out_bf16, reinterpret_cast<hipStream_t>(stream)),
+    NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/false, out_bf16, nullptr,
+                                           reinterpret_cast<hipStream_t>(stream)),
                   "int8 dequant");
     return NF4_OK;
 }
@@ -1232,7 +1233,8 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
     if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "int8 linear workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    uint16_t *dT = ws_at<uint16_t>(workspace, p.off_dT);
+    uint16_t *dT = ws_at<uint16_t>(workspace, p.off_dT), *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
+    const bool expand = dX && p.expand;
     nf4k::Reduction sums[3];
     int nsum = 0;
     if (r) {
@@ -1247,7 +1249,12 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
         }
         NF4_CHECK_HIP(nf4k::launch_skinny_nt(dY, L2, /*b_rows_k=*/false, P, M, r, N, p.ksdT, s), "dT = dY L2^T");
         const nf4k::Reduction red_dT{P, p.ksdT, M * r, scale, dT, 0.0f, nullptr};
-        NF4_CHECK_HIP(nf4k::launch_reduce_partials(red_dT, nullptr, s), "dT reduce");
+        // the weight's expansion, where it is wanted, carries dT's sum
+        if (expand)
+            NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, &red_dT, s),
+                          "int8 expansion + dT reduce");
+        else
+            NF4_CHECK_HIP(nf4k::launch_reduce_partials(red_dT, nullptr, s), "dT reduce");
         // both adapters' gradients in one launch, their partials side by side
         float *P1 = P + (size_t)p.msL2 * r * N;
         const bool direct = p.msL2 == 1 && p.msL1 == 1;
@@ -1266,10 +1273,10 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
     if (dX) {
         const bool acc = (flags & QLORA_DX_ACCUMULATE) != 0;
         float *Pg = ws_at<float>(workspace, p.off_Pg);
-        if (p.expand) {
+        if (expand) {
             // the weight in bf16, transposed, then the bf16 product with the adapter's steps
-            uint16_t *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
-            NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, s), "int8 expansion");
+            if (!r)
+                NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, nullptr, s), "int8 expansion");
             NF4_CHECK_HIP(nf4k::launch_gemm_bf16_bwd(dY, WdT, dT, L1, r, M, N, K, dX, acc,
                                                      nf4k::SplitK{p.kb.ksplit, p.kb.per, Pg}, s),
                           "bf16 GEMM (int8 bwd)");

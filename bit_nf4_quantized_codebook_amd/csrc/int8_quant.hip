@@ -64,27 +64,55 @@ __global__ __launch_bounds__(256) void int8_expand_rows_kernel(const int8_t *__r
     }
 }
 
-// out[k, n] = bf16(scales[n] * codes[n, k]): one 64 x 64 tile per workgroup, turned through LDS
-constexpr int ET = 64;
-__global__ __launch_bounds__(256) void int8_expand_transposed_kernel(const int8_t *__restrict__ codes,
-                                                                     const float *__restrict__ scales, int64_t N,
-                                                                     int64_t K, uint16_t *__restrict__ out) {
-    __shared__ uint16_t tile[ET][ET + 8];
-    const int64_t ntn = (N + ET - 1) / ET;
-    const int64_t n0 = ((int64_t)blockIdx.x % ntn) * ET, k0 = ((int64_t)blockIdx.x / ntn) * ET;
-    const int t = threadIdx.x, row = t >> 2, q = t & 3;
-    if (n0 + row < N) {
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(codes + (n0 + row) * K + k0 + 16 * q);
-        const float s = scales[n0 + row];
+// out[k, n] = bf16(scales[n] * codes[n, k]), one tile of 128 weight rows by 128 columns per workgroup,
+// turned through LDS.  Thread t takes rows 2 p and 2 p + 1 (p = t / 4) of the tile and 32 columns from
+// 32 q (q = t % 4); it writes the bf16 pairs (row 2p, row 2p + 1) of each column into an LDS tile
+// [128 columns][64 pairs], and 16 lanes write each column's 128 rows out, 16 bytes each.  In the tile the
+// 16-byte group of four pairs is XOR-ed with 4 q, so that a wave's 16 pairs by 4 column ranges land on 64
+// banks.  N % 8 == 0 and K % 64 == 0: pairs, groups of 8 rows and ranges of 32 columns are whole.
+// Bound by HBM: 1 byte read and 2 written per weight.
+struct ExpandTArgs {
+    const int8_t *codes;
+    const float *scales;
+    int64_t N, K;
+    uint16_t *out;
+    RedProb red;             // nred workgroups more, the first of the launch: a pending reduction
+    uint32_t nred;
+};
+constexpr int ET = 128;
+__global__ __launch_bounds__(256) void int8_expand_transposed_kernel(ExpandTArgs g) {
+    __shared__ __align__(16) uint32_t tile[ET * (ET / 2)];
+    if (blockIdx.x < g.nred) {
+        reduce_partials_block(g.red, blockIdx.x, g.nred);
+        return;
+    }
+    const int64_t tb = blockIdx.x - g.nred, ntn = (g.N + ET - 1) / ET;
+    const int64_t n0 = (tb % ntn) * ET, k0 = (tb / ntn) * ET;
+    const int t = threadIdx.x;
+    {
+        const int p = t >> 2, q = t & 3;
+        const int64_t n = n0 + 2 * p, k = k0 + 32 * q;
+        if (n < g.N && k < g.K) {
+            const u32x4 *pa = reinterpret_cast<const u32x4 *>(g.codes + n * g.K + k);
+            const u32x4 *pb = reinterpret_cast<const u32x4 *>(g.codes + (n + 1) * g.K + k);
+            const u32x4 a[2] = {pa[0], pa[1]}, b[2] = {pb[0], pb[1]};
+            const float sa = g.scales[n], sb = g.scales[n + 1];
+            uint32_t *col = tile + (((p >> 2) ^ (4 * q)) * 4 + (p & 3));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) tile[16 * q + i][row] = (uint16_t)f32_to_bf16(s * sext8(v[i >> 2], i & 3));
+            for (int i = 0; i < 32; ++i)
+                col[(32 * q + i) * (ET / 2)] = pack_bf16x2(sa * sext8(a[i >> 4][(i >> 2) & 3], i & 3),
+                                                           sb * sext8(b[i >> 4][(i >> 2) & 3], i & 3));
+        }
     }
     __syncthreads();
+    const int c = t & 15, r16 = t >> 4;
+    const int64_t n = n0 + 8 * c;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t n = n0 + 16 * q + 8 * h;      // N % 8 == 0: a group of 8 is inside or outside
-        if (n < N)
-            *reinterpret_cast<u32x4 *>(out + (k0 + row) * N + n) = *reinterpret_cast<const u32x4 *>(&tile[row][16 * q + 8 * h]);
+    for (int it = 0; it < ET / 16; ++it) {
+        const int kk = r16 + 16 * it;
+        if (k0 + kk < g.K && n < g.N)
+            *reinterpret_cast<u32x4 *>(g.out + (k0 + kk) * g.N + n) =
+                *reinterpret_cast<const u32x4 *>(tile + kk * (ET / 2) + ((c ^ (4 * (kk >> 5))) * 4));
     }
 }
 
@@ -118,16 +146,19 @@ hipError_t launch_int8_prep(const Int8Prep &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, hipStream_t stream) {
+hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, const Reduction *red, hipStream_t stream) {
     if (!transposed) {
+        if (red) return hipErrorInvalidValue;
         int64_t grid = ((w.rows * w.cols >> 3) + 255) / 256;
         if (grid > 256 * 64) grid = 256 * 64;
         hipLaunchKernelGGL(int8_expand_rows_kernel, dim3((unsigned)grid), dim3(256), 0, stream, w.codes, w.scales,
                            w.rows, w.cols, out);
     } else {
-        const int64_t tiles = ((w.rows + ET - 1) / ET) * (w.cols / ET);
-        hipLaunchKernelGGL(int8_expand_transposed_kernel, dim3((unsigned)tiles), dim3(256), 0, stream, w.codes,
-                           w.scales, w.rows, w.cols, out);
+        ExpandTArgs a{};
+        a.codes = w.codes; a.scales = w.scales; a.N = w.rows; a.K = w.cols; a.out = out;
+        if (red) a.red = red_prob(*red, a.nred);
+        const int64_t tiles = ((w.rows + ET - 1) / ET) * ((w.cols + ET - 1) / ET);
+        hipLaunchKernelGGL(int8_expand_transposed_kernel, dim3((unsigned)tiles + a.nred), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }

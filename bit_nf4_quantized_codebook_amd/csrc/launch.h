@@ -160,8 +160,10 @@ struct Int8View {
 };
 hipError_t launch_int8_rows(const void *x, bool f32, int64_t rows, int64_t cols, int8_t *codes, float *scales,
                             hipStream_t stream);
-// bf16(scale * code), as [rows, cols] or transposed [cols, rows] (cols a multiple of 64, rows of 8)
-hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, hipStream_t stream);
+// bf16(scale * code), as [rows, cols] or transposed [cols, rows] (cols a multiple of 64, rows of 8); red
+// (optional, transposed only): a partials reduction carried by extra workgroups of the same launch
+hipError_t launch_int8_expand(const Int8View &w, bool transposed, uint16_t *out, const Reduction *red,
+                              hipStream_t stream);
 // What the product needs beforehand, as one launch: rows of X to codes (X non-null), T's pending
 // reduction (Tred non-null) and L2 [r, N] transposed into L2T [N, r] (L2 non-null).
 struct Int8Prep {
