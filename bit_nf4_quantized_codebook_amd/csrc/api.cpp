@@ -1005,6 +1005,7 @@ int check_int8_weight(const nf4_int8_weight *w) {
     if (w->cols % 64) return fail(NF4_ERR_UNSUPPORTED, "weight cols (K) must be a multiple of 64");
     if (w->rows % 8) return fail(NF4_ERR_UNSUPPORTED, "weight rows (N) must be a multiple of 8");
     if (w->cols > NF4_INT8_MAX_COLS) return fail(NF4_ERR_UNSUPPORTED, "weight cols (K) exceed NF4_INT8_MAX_COLS");
+    if (w->rows > NF4_INT8_MAX_ROWS) return fail(NF4_ERR_UNSUPPORTED, "weight rows (N) exceed NF4_INT8_MAX_ROWS");
     if (!aligned16(w->codes)) return fail(NF4_ERR_ALIGN, "weight codes must be 16-byte aligned");
     if ((uintptr_t)w->scales & 3u) return fail(NF4_ERR_ALIGN, "weight scales must be 4-byte aligned");
     return NF4_OK;
@@ -1099,8 +1100,7 @@ int check_int8_linear_args(const nf4_int8_weight *w, int64_t M, int32_t r, float
     if (!std::isfinite(scale)) return fail(NF4_ERR_ARG, "scale must be finite");
     // kernels address each operand with 32-bit byte offsets
     const int64_t lim = (int64_t)1 << 31;
-    if (M >= lim || w->rows >= lim || w->rows * w->cols >= lim || M * w->cols * 2 >= lim || M * w->rows * 2 >= lim ||
-        w->rows * r * 2 >= lim)
+    if (M >= lim || w->rows * w->cols >= lim || M * w->cols * 2 >= lim || M * w->rows * 2 >= lim)
         return fail(NF4_ERR_UNSUPPORTED, "an operand exceeds 2 GiB");
     return NF4_OK;
 }
@@ -1114,6 +1114,7 @@ int nf4_int8_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols,
     if (cols < 8) return fail(NF4_ERR_SHAPE, "cols must be >= 8");
     if (cols % 8) return fail(NF4_ERR_UNSUPPORTED, "cols must be a multiple of 8");
     if (cols > NF4_INT8_MAX_COLS) return fail(NF4_ERR_UNSUPPORTED, "cols exceed NF4_INT8_MAX_COLS");
+    if (rows > ((int64_t)1 << 46) / cols) return fail(NF4_ERR_UNSUPPORTED, "rows * cols exceeds 2^46");
     if (rows == 0) return NF4_OK;
     if (!x || !codes || !scales) return fail(NF4_ERR_NULL, "x, codes and scales must be non-NULL");
     if (!aligned16(x) || !aligned16(codes)) return fail(NF4_ERR_ALIGN, "x and codes must be 16-byte aligned");
@@ -1127,7 +1128,6 @@ int nf4_int8_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols,
 int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream) {
     const int rc = check_int8_weight(w);
     if (rc) return rc;
-    if (w->rows >= ((int64_t)1 << 40) / w->cols) return fail(NF4_ERR_UNSUPPORTED, "the weight exceeds 2^40 elements");
     if (!out_bf16) return fail(NF4_ERR_NULL, "out_bf16 is NULL");
     if (!aligned16(out_bf16)) return fail(NF4_ERR_ALIGN, "out_bf16 must be 16-byte aligned");
     NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/false, out_bf16, nullptr,
@@ -1138,7 +1138,7 @@ int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream)
 
 size_t qlora_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t r) {
     const int64_t lim = (int64_t)1 << 31;      // beyond: shapes that the calls refuse
-    if (M <= 0 || N <= 0 || K <= 0 || r < 0 || M >= lim || N >= lim || K >= lim) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || r < 0 || r > 128 || M >= lim || N > NF4_INT8_MAX_ROWS || K > NF4_INT8_MAX_COLS) return 0;
     return make_int8_plan(M, N, K, r).total;
 }
 

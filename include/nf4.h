@@ -321,7 +321,7 @@ int qlora_swiglu_bwd(const uint16_t *dh, const uint16_t *g, const uint16_t *u, u
  * 8-bit integers with one constant per row -- section 3.1 eq. (1), X^Int8 = round(127/absmax X), with
  * a constant for each token (rows of an activation) or each output channel (rows of a weight).
  *   x:      device [rows, cols], row-major: bf16 (x_type NF4_ROWS_BF16) or float32 (NF4_ROWS_F32).
- *   rows:   >= 0 (0 is a no-op).  cols: a multiple of 8, 8 .. NF4_INT8_MAX_COLS.
+ *   rows:   >= 0 (0 is a no-op).  cols: a multiple of 8, 8 .. NF4_INT8_MAX_COLS; rows * cols <= 2^46.
  *   codes:  device int8 [rows, cols];  scales: device float32 [rows].
  * Per row: a = max |x|; scale = fp32(a / 127); code = the integer nearest to the real quotient
  * x / scale (ties to even, decided exactly, not on a rounded quotient), clamped to [-127, 127]; all 0
@@ -331,6 +331,7 @@ int qlora_swiglu_bwd(const uint16_t *dh, const uint16_t *g, const uint16_t *u, u
  */
 enum { NF4_ROWS_BF16 = 0, NF4_ROWS_F32 = 1 };
 #define NF4_INT8_MAX_COLS 131008   /* cols * 128 * 128 stays below 2^31: the products' sums are exact */
+#define NF4_INT8_MAX_ROWS 2097144  /* a product's tile of 256 float32 rows this wide stays below 2 GiB */
 int nf4_int8_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols, int8_t *codes, float *scales,
                       void *stream);
 
@@ -339,7 +340,7 @@ int nf4_int8_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols,
 typedef struct nf4_int8_weight {
     const int8_t *codes;          /* [rows, cols], 16-byte aligned; codes of any value, -128 included */
     const float *scales;          /* [rows] */
-    int64_t rows;                 /* N_out, a multiple of 8 */
+    int64_t rows;                 /* N_out, a multiple of 8, at most NF4_INT8_MAX_ROWS */
     int64_t cols;                 /* K_in, a multiple of 64, at most NF4_INT8_MAX_COLS */
 } nf4_int8_weight;
 

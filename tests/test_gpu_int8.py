@@ -347,6 +347,58 @@ def test_linear_step_captured_and_replayed(M):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("rows,cols", [((1 << 21) + 5, 64), (1_100_003, 4096)])
+def test_quantize_more_rows_than_a_launch_takes_and_offsets_past_32_bits(rows, cols):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(rows)
+    X = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV).normal_(0, 1, generator=gen)
+    codes, scales = nf4.nf4_int8_quantize(X)
+    for part in (slice(0, 3), slice((1 << 20) - 2, (1 << 20) + 2), slice(rows - 5, rows)):
+        rc, rs = oracle.int8_rows(f64(X[part]))
+        assert np.array_equal(codes[part].cpu().numpy(), rc) and np.array_equal(scales[part].cpu().numpy(), rs)
+
+
+def test_linear_with_operands_just_below_2_gib():
+    """X of 2^31 - 8192 bytes; a weight of more rows than 2^20: the last rows and columns against the oracle."""
+    M, N, K, r = 262143, 64, 4096, 8
+    lin = Lin(4400, N, K, r)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(1)
+    X = torch.empty((M, K), dtype=torch.bfloat16, device=DEV).normal_(0, 1, generator=gen)
+    Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+    dX, dL1, dL2 = nf4.qlora_int8_linear_bwd(lin.w, Y, X, lin.L1, lin.L2, T, 0.5)
+    Wb = oracle.bf16_to_f32(oracle.int8_weight_bf16(lin.Wq, lin.ws)).astype(np.float64)
+    for part in (slice(0, 3), slice(M - 3, M)):
+        check_fwd(lin, X[part], 0.5, Y[part], T[part])
+        dy = f64(Y[part])
+        dt = 0.5 * (dy @ lin.l2.T)
+        ref = dy @ Wb + dt @ lin.l1.T
+        size = np.abs(dy) @ np.abs(Wb) + np.abs(dt) @ np.abs(lin.l1.T)
+        dt_tol = H * np.abs(dt) + 1.01 * (N + 70) * U * 0.5 * (np.abs(dy) @ np.abs(lin.l2.T))
+        tol = 1.01 * (N + r + 16) * U * size + dt_tol @ np.abs(lin.l1.T)
+        within("dX", dX[part], ref, H * (np.abs(ref) + tol) + tol)
+    del X, dX, Y, T
+    N, K = (1 << 20) + 8, 64
+    w = nf4.Int8Weight.from_float(torch.empty((N, K), device=DEV).normal_(0, 1, generator=gen))
+    for M in (1, 3, 20, 65):
+        X, x = bf16(synth.normal_f32(4401 + M, (M, K), 1.0))
+        Y, _ = nf4.qlora_int8_linear_fwd(w, X)
+        part = slice(N - 40, N)
+        ref = oracle.int8_product(*oracle.int8_rows(x), w.codes[part].cpu().numpy(), w.scales[part].cpu().numpy())
+        within("Y", Y[:, part], ref, H * np.abs(ref) * 1.01 + 3 * U * np.abs(ref))
+        dX, _, _ = nf4.qlora_int8_linear_bwd(w, Y)
+        # a sum of 2^20 terms: against float64 on the device (a product of two contiguous float64 matrices)
+        Wd = (w.codes.float() * w.scales[:, None]).bfloat16().double()
+        ref, size = torch.mm(Y.double(), Wd), torch.mm(Y.double().abs(), Wd.abs())
+        within("dX", dX, f64(ref), H * np.abs(f64(ref)) * 1.01 + 1.01 * (N + 16) * U * f64(size))
+
+
+def test_weight_tensors_cannot_be_replaced():
+    w = nf4.Int8Weight(torch.zeros((8, 64), dtype=torch.int8, device=DEV), torch.zeros(8, device=DEV))
+    with pytest.raises(AttributeError):
+        w.codes = w.codes[:4]
+
+
 def test_binding_refusals():
     lin = Lin(4300, 64, 128, 8)
     X, _ = bf16(np.ones((4, 128)))
@@ -357,6 +409,7 @@ def test_binding_refusals():
                 lambda: nf4.qlora_int8_linear_fwd(lin.w, X, Y=X),
                 lambda: nf4.qlora_int8_linear_bwd(lin.w, X[:, :64].contiguous(), accumulate=True),
                 lambda: nf4.qlora_int8_linear_fwd(lin.w, X, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)),
+                lambda: nf4.qlora_int8_linear_fwd(lin.w, X, workspace=torch.empty(1 << 20, dtype=torch.uint8)),
                 lambda: nf4.Int8Weight(lin.w.codes, lin.w.scales[:8])):
         with pytest.raises(ValueError):
             bad()

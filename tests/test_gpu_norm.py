@@ -243,6 +243,37 @@ def test_repeats_bit_for_bit_with_a_dirty_workspace():
             assert all(same(a, b) for a, b in zip(first, out)), (M, C, fill)
 
 
+@pytest.mark.parametrize("M,C,f32", [((1 << 21) + 9, 64, False), (600_005, 4096, False)])
+def test_more_rows_than_a_launch_takes_and_offsets_past_32_bits(M, C, f32):
+    """Rows do not know of each other: the last ones of a large call equal a small call's, bit for bit."""
+    gate, last = 7, 7 * 5 + M % 7
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(M)
+    n = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV).normal_(0, 1, generator=gen)  # noqa: E731
+    R, B, dR, dH = n(M, C), n(M, C), n(M, C), n(M, C)
+    norm = nf4.QLoRANorm(w_pre=n(C), w_post=n(C), gate=n(-(-M // gate), C), gate_tokens=gate, alpha=0.5)
+    tail = nf4.QLoRANorm(w_pre=norm.w_pre, w_post=norm.w_post, gate=norm.gate[(M - last) // gate:].contiguous(),
+                         gate_tokens=gate, alpha=0.5)
+    cut = lambda t: t[M - last:].contiguous()  # noqa: E731
+    Ro, Hh, (q, s) = nf4.qlora_norm_fwd(norm, R, B, quantize=True)
+    small = nf4.qlora_norm_fwd(tail, cut(R), cut(B), quantize=True)
+    assert same(cut(Ro), small[0]) and same(cut(Hh), small[1]) and same(cut(q), small[2][0]) and same(cut(s), small[2][1])
+    q2, s2 = nf4.nf4_int8_quantize(Hh)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    got_dR, got_dB, g = nf4.qlora_norm_bwd(norm, Ro, B, dR, dH)
+    small_dR, small_dB, gs = nf4.qlora_norm_bwd(tail, small[0], cut(B), cut(dR), cut(dH))
+    assert same(cut(got_dR), small_dR) and same(cut(got_dB), small_dB)
+    # The two calls cut a gate row's tokens into runs differently, so its seven float32 terms are added in
+    # another order: the sums differ by at most 2 * 6 u of the terms' sizes, and each is rounded to bf16
+    # (h).  The terms' sizes from dR = alpha t (its own rounding, h, is the factor 1.01).
+    b = f64(cut(B))
+    n_size = np.abs(f64(norm.w_post) * b) / np.sqrt((b ** 2).mean(1, keepdims=True) + norm.eps)
+    size = np.zeros(gs["dgate"].shape)
+    np.add.at(size, np.arange(last) // gate, 1.01 * np.abs(f64(small_dR)) / 0.5 * n_size)
+    ref = f64(gs["dgate"])
+    within("dgate", g["dgate"][(M - last) // gate:], ref, 2 * H * 1.01 * np.abs(ref) + 12 * U * size)
+
+
 def test_gradients_against_differences():
     """The whole junction through the kernels in float32 residuals: a small step of one input moves the
     loss by its gradient.  The loss sums R' (float32) only, so that no bf16 output hides the step."""

@@ -1,6 +1,7 @@
 """Int8 linear and norm glue on the host: the oracle's own pins (exact rational quotients, finite
 differences, brute-force sums) and every refusal of the entry points, before any HIP call."""
 import ctypes
+import os
 from fractions import Fraction
 
 import numpy as np
@@ -11,6 +12,7 @@ import oracle
 nf4 = pytest.importorskip("bit_nf4_quantized_codebook_amd")
 lib = nf4.lib
 
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "nf4.h")
 OK, ENULL, ESHAPE, EALIGN, EUNSUP, EWS, EHIP, EARG = 0, -1, -2, -3, -4, -5, -6, -7
 FAKE = ctypes.c_void_p(0x100000)          # aligned, never dereferenced on these paths
 MIS = ctypes.c_void_p(0x100004)
@@ -110,7 +112,7 @@ def test_int8_quantize_refusals():
         x, t, rows, cols, codes, scales, None)
     assert call(t=2) == EARG and call(t=-1) == EARG
     assert call(rows=-1) == ESHAPE and call(cols=0) == ESHAPE
-    assert call(cols=63) == EUNSUP and call(cols=131016) == EUNSUP
+    assert call(cols=63) == EUNSUP and call(cols=131016) == EUNSUP and call(rows=1 << 41) == EUNSUP
     assert call(x=None, rows=0, codes=None, scales=None) == OK
     assert call(x=None) == ENULL and call(codes=None) == ENULL and call(scales=None) == ENULL
     assert call(x=MIS) == EALIGN and call(codes=MIS) == EALIGN and call(scales=ODD) == EALIGN
@@ -118,6 +120,13 @@ def test_int8_quantize_refusals():
 
 def _w8(rows=256, cols=256, codes=0x100000, scales=0x100000):
     return nf4._Int8Desc(codes, scales, rows, cols)
+
+
+def test_limits_match_the_header():
+    text = open(HEADER).read()
+    assert "#define NF4_INT8_MAX_COLS 131008 " in text and "#define NF4_INT8_MAX_ROWS 2097144 " in text
+    assert 131008 * 128 * 128 < 2 ** 31 <= (131008 + 64) * 128 * 128
+    assert 256 * 2097144 * 4 < 2 ** 31 <= 256 * (2097144 + 8) * 4
 
 
 def test_int8_weight_refusals():
@@ -134,7 +143,8 @@ def test_int8_linear_refusals():
     M, r = 8, 8
     wsb = lib.qlora_int8_linear_workspace_size(M, 256, 256, r)
     assert wsb > 0 and lib.qlora_int8_linear_workspace_size(0, 256, 256, r) == 0
-    assert lib.qlora_int8_linear_workspace_size(M, 256, 256, -8) == 0
+    for bad in ((M, 256, 256, -8), (M, 256, 256, 136), (1 << 31, 256, 256, r), (M, 1 << 21, 256, r), (M, 256, 1 << 17, r)):
+        assert lib.qlora_int8_linear_workspace_size(*bad) == 0
 
     def fwd(d=None, X=FAKE, Xq=None, xs=None, L1=FAKE, L2=FAKE, s=1.0, M=M, r=r, Y=FAKE, T=None, ws=FAKE, n=wsb):
         return lib.qlora_int8_linear_fwd(ctypes.byref(d or _w8()), X, Xq, xs, L1, L2, s, M, r, Y, T, ws, n, None)
@@ -152,7 +162,7 @@ def test_int8_linear_refusals():
         assert f(_w8(cols=96)) == EUNSUP and f(_w8(rows=12)) == EUNSUP and f(_w8(rows=0)) == ESHAPE
         assert f(_w8(rows=1 << 24, cols=128)) == EUNSUP and f(M=1 << 22) == EUNSUP and f(M=1 << 40) == EUNSUP
         assert f(_w8(rows=65536), M=1 << 14) == EUNSUP
-        assert f(_w8(rows=1 << 23, cols=64), M=1, r=128) == EUNSUP     # L2: 128 x 2^23 bf16 = 2 GiB
+        assert f(_w8(rows=1 << 21, cols=64), M=1) == EUNSUP            # a tile row offset would pass 32 bits
         assert f(L1=None) == ENULL and f(L2=None) == ENULL and f(X=None) == ENULL
         assert f(r=0) == EARG                                   # an adapter, but no rank
         assert f(X=MIS) == EALIGN and f(L1=MIS) == EALIGN and f(L2=MIS) == EALIGN and f(ws=MIS) == EALIGN
