@@ -1047,11 +1047,11 @@ struct Int8Plan {
     bool expand;
     int ksT, ksdT, msL2, msL1;
     nf4k::SplitPlan kf, kb;        // split of the forward's product and of the backward's dX product
-    size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_L2T, off_P, off_Wd, off_Pg, total;
+    size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_dTlo, off_L2T, off_P, off_Wd, off_Pg, total;
 };
 
-// One layout for both directions: the forward uses Xq, xs, sT, L2T, P and Pg, the backward T, dT, P, Wd
-// and Pg.
+// One layout for both directions: the forward uses Xq, xs, sT, L2T, P and Pg, the backward T, dT, dTlo,
+// P, Wd and Pg.
 Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     Int8Plan p;
     const int64_t mt = (M + kTile - 1) / kTile, rt = (r + kTile - 1) / kTile;
@@ -1083,6 +1083,7 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     p.off_T = off;   off += round256((size_t)M * r * 2);
     p.off_sT = off;  off += round256((size_t)M * r * 2);
     p.off_dT = off;  off += round256((size_t)M * r * 2);
+    p.off_dTlo = off; off += round256((size_t)M * r * 2);
     p.off_L2T = off; off += round256((size_t)N * r * 2);
     p.off_P = off;   off += round256(pmax * 4);
     p.off_Wd = off;  off += p.expand ? round256((size_t)N * K * 2) : 0;
@@ -1248,7 +1249,10 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
             Tuse = Tb;
         }
         NF4_CHECK_HIP(nf4k::launch_skinny_nt(dY, L2, /*b_rows_k=*/false, P, M, r, N, p.ksdT, s), "dT = dY L2^T");
-        const nf4k::Reduction red_dT{P, p.ksdT, M * r, scale, dT, 0.0f, nullptr};
+        // dL1 = X^T dT takes dT in two bf16 halves: dT's rounding alone would cost dL1 as much as its own
+        uint16_t *dTlo = ws_at<uint16_t>(workspace, p.off_dTlo);
+        nf4k::Reduction red_dT{P, p.ksdT, M * r, scale, dT, 0.0f, dTlo};
+        red_dT.resid = true;
         // the weight's expansion, where it is wanted, carries dT's sum
         if (expand)
             NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, &red_dT, s),
@@ -1260,6 +1264,7 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
         const bool direct = p.msL2 == 1 && p.msL1 == 1;
         nf4k::TnProduct tn_dL2{Tuse, dY, P, r, N, p.msL2};
         nf4k::TnProduct tn_dL1{X, dT, P1, K, r, p.msL1};
+        tn_dL1.Vlo = dTlo;
         if (direct) {
             tn_dL2.out = dL2; tn_dL2.scale = scale;
             tn_dL1.out = dL1; tn_dL1.scale = 1.0f;

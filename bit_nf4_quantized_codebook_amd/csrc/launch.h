@@ -127,6 +127,8 @@ struct TnProduct {
     // what the reduction of the one partial would write, and P unused
     uint16_t *out = nullptr;
     float scale = 1.0f;
+    // V's second half, V + Vlo held as two bf16 values (16 significant bits): P += U^T Vlo
+    const uint16_t *Vlo = nullptr;
 };
 hipError_t launch_skinny_tn(const TnProduct &a, const TnProduct *b, int64_t M, hipStream_t stream);
 // out = bf16(s1 * sum of the nsplit partials), out2 (optional) = bf16(s2 * same); partial k of
@@ -142,6 +144,7 @@ struct Reduction {
     uint16_t *out2;
     int64_t stride = 0;
     bool accum = false;
+    bool resid = false;     // out2 = bf16(s1 * sum - out): out + out2 holds the sum to 16 bits
 };
 hipError_t launch_reduce_partials(const Reduction &a, const Reduction *b, hipStream_t stream,
                                   const Reduction *c = nullptr);

@@ -44,13 +44,18 @@ struct TnProb {
     float scale;
     int64_t Pn, Qn, mchunk;
     int32_t tx, ty;
+    const uint16_t *Vlo;
 };
 struct TnGroup {
     TnProb p[2];
     int64_t M;
     uint32_t nb0;
 };
+// LO: a product may have its V as two bf16 halves; the second goes through the same loads, tile and MFMAs
+// beside the first, so that U is still read once.
+template <bool LO>
 __global__ __launch_bounds__(256) void skinny_tn_kernel(TnGroup grp) {
+    __shared__ __align__(16) uint8_t Ls[LO ? NSTAGE_TN : 1][LO ? ST * ROWB : 16];
     __shared__ __align__(16) uint8_t Us[NSTAGE_TN][ST * ROWB];
     __shared__ __align__(16) uint8_t Vs[NSTAGE_TN][ST * ROWB];
     const int second = blockIdx.x >= grp.nb0;
@@ -74,7 +79,9 @@ __global__ __launch_bounds__(256) void skinny_tn_kernel(TnGroup grp) {
     const int trow = tid >> 3, tch = tid & 7;
     const bool pok = p0 + tch * 8 < Pn, qok = q0 + tch * 8 < Qn;
 
-    auto load = [&](int step, TileLoad &a, TileLoad &b) {
+    const bool lo = LO && pr.Vlo;
+    const __amdgpu_buffer_rsrc_t rL = make_rsrc(lo ? pr.Vlo : V, lo ? M * Qn * 2 : 0);
+    auto load = [&](int step, TileLoad &a, TileLoad &b, TileLoad &c) {
         const int64_t mm = mbeg + (int64_t)step * ST;
         const bool live = step < nsteps;
 #pragma unroll
@@ -83,24 +90,26 @@ __global__ __launch_bounds__(256) void skinny_tn_kernel(TnGroup grp) {
             const bool ok = live && gm < mend;
             a.v[h] = bload16(rU, (ok && pok) ? (uint32_t)((gm * Pn + p0 + tch * 8) * 2) : 0xFFFFFFF0u);
             b.v[h] = bload16(rV, (ok && qok) ? (uint32_t)((gm * Qn + q0 + tch * 8) * 2) : 0xFFFFFFF0u);
+            if (LO) c.v[h] = bload16(rL, (ok && qok && lo) ? (uint32_t)((gm * Qn + q0 + tch * 8) * 2) : 0xFFFFFFF0u);
         }
     };
-    auto store = [&](int slot, const TileLoad &a, const TileLoad &b) {
+    auto store = [&](int slot, const TileLoad &a, const TileLoad &b, const TileLoad &c) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = trow + 32 * h;
+            if (LO && lo) *reinterpret_cast<u32x4 *>(&Ls[LO ? slot : 0][LO ? row * ROWB + tch * 16 : 0]) = c.v[h];
             *reinterpret_cast<u32x4 *>(&Us[slot][row * ROWB + tch * 16]) = a.v[h];
             *reinterpret_cast<u32x4 *>(&Vs[slot][row * ROWB + tch * 16]) = b.v[h];
         }
     };
 
     f32x16 acc = {};
-    TileLoad la[NSTAGE_TN], lb[NSTAGE_TN];
+    TileLoad la[NSTAGE_TN], lb[NSTAGE_TN], lc[NSTAGE_TN];
     for (int g0 = 0; g0 < nsteps; g0 += NSTAGE_TN) {
 #pragma unroll
-        for (int u = 0; u < NSTAGE_TN; ++u) load(g0 + u, la[u], lb[u]);
+        for (int u = 0; u < NSTAGE_TN; ++u) load(g0 + u, la[u], lb[u], lc[u]);
 #pragma unroll
-        for (int u = 0; u < NSTAGE_TN; ++u) store(u, la[u], lb[u]);
+        for (int u = 0; u < NSTAGE_TN; ++u) store(u, la[u], lb[u], lc[u]);
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < NSTAGE_TN; ++u) {
@@ -109,6 +118,10 @@ __global__ __launch_bounds__(256) void skinny_tn_kernel(TnGroup grp) {
                 const bf16x8 fa = frag_tr(Us[u], wm * 32, s, lane);
                 const bf16x8 fb = frag_tr(Vs[u], wn * 32, s, lane);
                 acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, acc, 0, 0, 0);
+                if (LO && lo) {
+                    const bf16x8 fl = frag_tr(Ls[LO ? u : 0], wn * 32, s, lane);
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fl, acc, 0, 0, 0);
+                }
             }
         }
         __syncthreads();
@@ -175,6 +188,7 @@ TnProb tn_prob(const TnProduct &t, int64_t M, uint32_t &nblocks) {
     p.U = t.U; p.V = t.V; p.P = t.P; p.Pn = t.Pn; p.Qn = t.Qn; p.mchunk = per * ST;
     p.out = t.nsplit == 1 ? t.out : nullptr;
     p.scale = t.scale;
+    p.Vlo = t.Vlo;
     p.tx = (int32_t)((t.Pn + ST - 1) / ST);
     p.ty = (int32_t)((t.Qn + ST - 1) / ST);
     nblocks = (uint32_t)p.tx * (uint32_t)p.ty * (uint32_t)t.nsplit;
@@ -187,6 +201,7 @@ RedProb red_prob(const Reduction &r, uint32_t &nblocks) {
     p.P = r.P; p.n = r.n; p.out = r.out; p.out2 = r.out2; p.s1 = r.s1; p.s2 = r.s2; p.nsplit = r.nsplit;
     p.stride = r.stride ? r.stride : r.n;
     p.accum = r.accum ? 1u : 0u;
+    p.resid = r.resid ? 1u : 0u;
     nblocks = reduce_blocks(r.n);
     return p;
 }
@@ -211,7 +226,10 @@ hipError_t launch_skinny_tn(const TnProduct &a, const TnProduct *b, int64_t M, h
     g.p[1] = b ? tn_prob(*b, M, n1) : g.p[0];
     g.M = M;
     g.nb0 = n0;
-    hipLaunchKernelGGL(skinny_tn_kernel, dim3(n0 + (b ? n1 : 0u)), dim3(256), 0, stream, g);
+    if (a.Vlo || (b && b->Vlo))
+        hipLaunchKernelGGL(skinny_tn_kernel<true>, dim3(n0 + (b ? n1 : 0u)), dim3(256), 0, stream, g);
+    else
+        hipLaunchKernelGGL(skinny_tn_kernel<false>, dim3(n0 + (b ? n1 : 0u)), dim3(256), 0, stream, g);
     return hipGetLastError();
 }
 

@@ -2,7 +2,7 @@
 // launch (one to three reductions) and, at large token counts, extra workgroups of the weight
 // expansion launch.
 //   out[i] = bf16(s1 * sum_k P[k stride + i]) (k ascending); out2 (optional) = bf16(s2 * the same
-//   sum); with accum, out[i] = bf16(s1 * sum + out[i]) (the product added to what out holds).
+//   sum), or with resid the rest that out's rounding left; with accum, out[i] = bf16(s1 * sum + out[i]) (the product added to what out holds).
 // Four elements per thread (n and stride are multiples of 4 for every caller: r % 8 == 0, and the
 // split GEMMs' output widths are multiples of 8).
 #pragma once
@@ -18,6 +18,7 @@ struct RedProb {
     float s1, s2;
     int32_t nsplit;
     uint32_t accum;
+    uint32_t resid;      // out2 = bf16(s1 * sum - out): what out's rounding left
 };
 
 // workgroup `blk` of `nblk` workgroups (256 threads) covering one reduction
@@ -52,7 +53,15 @@ __device__ __forceinline__ void reduce_partials_block(const RedProb &pr, int64_t
             uint2 o = {pack_bf16x2(s1 * acc.x, s1 * acc.y), pack_bf16x2(s1 * acc.z, s1 * acc.w)};
             reinterpret_cast<uint2 *>(out)[i] = o;
         }
-        if (out2) {
+        if (out2 && pr.resid) {
+            float f[4] = {s1 * acc.x, s1 * acc.y, s1 * acc.z, s1 * acc.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float hi = bf16_to_f32(f32_to_bf16(f[k]));
+                f[k] = __builtin_isfinite(hi) ? f[k] - hi : 0.0f;
+            }
+            reinterpret_cast<uint2 *>(out2)[i] = uint2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+        } else if (out2) {
             uint2 o = {pack_bf16x2(s2 * acc.x, s2 * acc.y), pack_bf16x2(s2 * acc.z, s2 * acc.w)};
             reinterpret_cast<uint2 *>(out2)[i] = o;
         }

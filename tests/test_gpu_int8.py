@@ -6,7 +6,8 @@ Tolerances, from the roundings on the way (u = 2^-24, a float32 step's half; h =
      3 u of its size; s T is rounded to bf16 (h of each of the adapter's r products) and summed in
      float32 as T is: a sum of n float32 terms is off by at most n u of the sum of their sizes.
   dX: the products are bf16 x bf16, exact in float32: (N + r + 16) u of the sizes' sum, h |dX|, and
-     dT's bf16 rounding, h of the adapter's products; likewise dL1, dL2 (sums over the tokens).
+     dT's bf16 rounding, h of the adapter's products; likewise dL2 (a sum over the tokens), and dL1,
+     which takes dT in two bf16 halves, h^2.
 """
 import numpy as np
 import pytest
@@ -265,7 +266,9 @@ def test_linear_backward(M, N, K, r):
     tol = 1.01 * (N + r + 16) * U * (size + np.abs(dt) @ np.abs(lin.l1.T)) + dt_tol @ np.abs(lin.l1.T)
     within("dX", dX, ref, H * (np.abs(ref) + tol) + tol)
     ref = x.T @ dt
-    tol = 1.01 * (M + 70) * U * (np.abs(x).T @ np.abs(dt)) + np.abs(x).T @ dt_tol
+    # dL1 takes dT as two bf16 values: H of a rest that is at most H of it
+    rest = H * H * np.abs(dt) + 1.01 * (N + 70) * U * dt_size
+    tol = 1.01 * (2 * M + 70) * U * (np.abs(x).T @ np.abs(dt)) + np.abs(x).T @ rest
     within("dL1", dL1, ref, H * (np.abs(ref) + tol) + tol)
     ref = s * (t.T @ dy)
     tol = 1.01 * (M + 70) * U * abs(s) * (np.abs(t).T @ np.abs(dy))
