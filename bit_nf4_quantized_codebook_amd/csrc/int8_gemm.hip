@@ -17,9 +17,10 @@
 // v_mfma_f32_32x32x16_bf16, whose output layout is the same.  (All 16 tiles turned first and then
 // multiplied, the kernel spilled 70 registers.)
 //
-// Bound by the MFMA loop: the whole forward call (codes of X, T, this product) takes 355 us at 2048
-// tokens through a 22016 x 8192 weight with r = 64 (2.1 POPS) and 89 us at 4096 through 4096 x 4096;
-// a 64 x 64 tile with one LDS stage took 1667 and 420 us.
+// Bound by the MFMA loop at the clock its power allows: 62.5 us at 4096 x 4096 x 4096 with r = 64 (2.2
+// POPS; a library int8 product of 8192 x 8192 x 8192 reaches 2.33 here) and 325 us at 2048 tokens x 22016 x
+// 8192 (2.3 POPS).  The whole forward call (codes of X, T, this product) takes 84 and 346 us; a 64 x 64
+// tile with one LDS stage took 420 and 1667 us.
 //
 // Few output tiles (fewer than half the CUs): the reduction is split over up to 16 workgroups per
 // tile, each writing a scaled float32 partial tile (the last also the adapter's product), summed

@@ -15,7 +15,8 @@
 //      The waves' int32 sums meet in LDS by integer adds, exact in any order; then the constants, the
 //      adapter's MFMAs (s T from T's partials, summed in a fixed order) and one rounding to bf16.
 // Measured (both launches): 47 us for one token x 28672 x 8192 with r = 64 (5.0 TB/s of weight bytes; a
-// large copy reaches 5.2 here), 12 us at 4096 x 4096; 20 us for 23 tokens x 4096 x 11008.
+// large copy reaches 5.2 here), 12 us at 4096 x 4096; 20 us for 23 tokens x 4096 x 11008 (16.5 where the
+// weight stays in the 256 MB cache).  Bound by HBM at large weights, by the two launches at small ones.
 // Small workgroups with few registers win, many waves hiding the loads' latency: one token at 28672 x
 // 8192 took 45 us (r = 0) with 4 waves and 16 rows each, 57 with 32 rows, 55 with 8 waves and 64 rows.
 

