@@ -306,7 +306,9 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
         block_sum<NT, 3>(s, red, par);
         const float ir = 1.0f / sqrtf(s[0] * inv_c + g.eps);
         const float ib = g.w_post ? 1.0f / sqrtf(s[2] * inv_c + g.eps) : 1.0f;
-        const float k1 = ir * ir * ir * (s[1] * inv_c);
+        // t = ir (w dH - xh mean(w dH xh)): no power of ir by itself, which would overflow where eps and
+        // the row are tiny (and, times a sum of zero, give NaN)
+        const float k1 = ir * (s[1] * inv_c);
         float s2[1] = {0.0f};
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -316,11 +318,14 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
             unpack8_bf16(dh[v], d);
             unpack8_bf16(b[v], x);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = d[k] * (r[v][k] * ir);
+            for (int k = 0; k < 8; ++k) {
+                const float xh = r[v][k] * ir;
+                o[k] = d[k] * xh;
+                t[v][k] += ir * (w[k] * d[k] - k1 * xh);
+            }
             add(0, v, o);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                t[v][k] += ir * w[k] * d[k] - k1 * r[v][k];
                 o[k] = g.alpha * t[v][k];
             }
             store_res<F32>(g.dR, row + (v * NT + tid) * 8, o);
@@ -341,7 +346,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
             float k2 = 0.0f;
             if (g.w_post) {
                 block_sum<NT, 1>(s2, red, par + 1);
-                k2 = ib * ib * ib * (s2[0] * inv_c);
+                k2 = ib * (s2[0] * inv_c);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -351,7 +356,7 @@ __global__ __launch_bounds__(NT) void norm_bwd_kernel(NormArgs g, NormRuns q) {
                     post(v, w);
                     unpack8_bf16(b[v], x);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) t[v][k] = ib * w[k] * t[v][k] - k2 * x[k];
+                    for (int k = 0; k < 8; ++k) t[v][k] = ib * (w[k] * t[v][k] - k2 * (x[k] * ib));
                 }
                 __builtin_nontemporal_store(pack8_bf16(t[v]), reinterpret_cast<u32x4 *>(g.dB + row + (v * NT + tid) * 8));
             }

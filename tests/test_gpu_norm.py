@@ -196,6 +196,20 @@ def test_rows_of_zeros_and_not_finite():
         assert same(dR[m], grads[0][m]) and same(dB[m], grads[1][m])
 
 
+@pytest.mark.parametrize("pre,f32", [(True, True), (True, False), (False, True)])
+@pytest.mark.parametrize("C", [520, 8200])
+def test_tiny_rows_and_eps(C, pre, f32):
+    """eps 1e-30, a row of zeros and one of about 1e-14: 1 / rms is up to 1e15 and its cube past float32."""
+    c = Case(4, C, pre=pre, gate=2, f32=f32, seed=11)
+    c.norm.eps = 1e-30
+    c.R[0] = 0
+    c.B[0] = 0
+    c.R[2] *= 1e-14
+    c.B[2] *= 1e-14
+    c.check_fwd()
+    c.check_bwd()
+
+
 @pytest.mark.parametrize("C", [8, 512, 520, 2048, 4096, 8200, 16384])
 @pytest.mark.parametrize("block", [False, True])
 def test_codes_equal_those_of_h(C, block):
