@@ -9,10 +9,9 @@
 // Block tile TM x 256 outputs (TM 64 up to 64 tokens, else 128), reduction step 64, 8 waves in 2 x 4,
 // MFMA v_mfma_f32_32x32x16_bf16.  dY goes straight from global memory to LDS, 16-byte chunks XOR-swizzled
 // by (row / 2).  The weight's 64 x 256 codes of a step come through registers four steps ahead and are
-// turned to bf16 on the way to LDS, spread over the MFMA sub-steps: with u = code + 128 as an unsigned
-// byte, fma(u, ws, -128 ws) is ws * code rounded once (128 ws is exact), so a code costs one byte
-// conversion, one fma and half a packed conversion.  The W rows are the reduction, so fragments are
-// read with ds_read_b64_tr_b16.  The adapter is r/64 more steps.
+// turned to bf16 on the way to LDS, spread over the MFMA sub-steps: a code costs one conversion of a
+// signed byte (v_cvt_f32_i32 with a byte select), one multiplication and half a packed conversion.  The
+// W rows are the reduction, so fragments are read with ds_read_b64_tr_b16.  The adapter is r/64 more steps.
 //
 // Bound by no one unit: over a large product the MFMAs are busy 47 % of the CUs' cycles and LDS 59 %
 // (counters, 1023 x 22016 x 8192).  Measured, the whole backward with r = 16: 67 us at 333 tokens x 11008 x
@@ -138,15 +137,15 @@ __global__ __launch_bounds__(NW * 64) void int8_bwd_kernel(Int8Bwd g) {
     // part p (0 .. 2 WQ - 1) of a stage to bf16: eight codes of row p / 2 (rows past the end: constant 0, so zeros)
     auto write_B = [&](const WStage &st, uint8_t *Bst, int p) {
         const int q = p >> 1, h = p & 1;
-        const float s = __uint_as_float(st.s[q]), off = -128.0f * s;
+        const float s = __uint_as_float(st.s[q]);
         uint32_t o[4];
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
-            const uint32_t u = st.w[q][2 * h + d] ^ 0x80808080u;
-            const float f0 = __builtin_fmaf((float)(u & 0xFFu), s, off);
-            const float f1 = __builtin_fmaf((float)((u >> 8) & 0xFFu), s, off);
-            const float f2 = __builtin_fmaf((float)((u >> 16) & 0xFFu), s, off);
-            const float f3 = __builtin_fmaf((float)(u >> 24), s, off);
+            const int32_t u = (int32_t)st.w[q][2 * h + d];
+            const float f0 = (float)(int8_t)u * s;
+            const float f1 = (float)(int8_t)(u >> 8) * s;
+            const float f2 = (float)(int8_t)(u >> 16) * s;
+            const float f3 = (float)(u >> 24) * s;
             o[2 * d] = pack_bf16x2(f0, f1);
             o[2 * d + 1] = pack_bf16x2(f2, f3);
         }

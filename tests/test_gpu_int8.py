@@ -289,6 +289,22 @@ def test_linear_backward(M, N, K, r):
     within("dX accumulated", acc, ref, H * (np.abs(ref) + tol) + tol)
 
 
+@pytest.mark.parametrize("M", [3, 300, 4096])
+def test_linear_backward_with_the_largest_constants(M):
+    """Constants next to FLT_MAX / 127: a weight's value fits bf16, 128 constants do not fit float32."""
+    N, K = 512, 512
+    codes = np.random.default_rng(31).integers(-127, 128, (N, K)).astype(np.int8)
+    scales = np.linspace(2.6e36, 2.66e36, N).astype(np.float32)
+    w = nf4.Int8Weight(dev(codes), dev(scales))
+    Wb = oracle.bf16_to_f32(oracle.int8_weight_bf16(codes, scales)).astype(np.float64)
+    assert np.isfinite(Wb).all()
+    dY, dy = bf16(synth.normal_f32(3100 + M, (M, N), 1e-10))
+    dX, _, _ = nf4.qlora_int8_linear_bwd(w, dY)
+    ref = dy @ Wb
+    tol = 1.01 * (N + 16) * U * (np.abs(dy) @ np.abs(Wb))
+    within("dX", dX, ref, H * (np.abs(ref) + tol) + tol)
+
+
 def test_linear_repeats_bit_for_bit_and_with_a_dirty_workspace():
     for M, N, K, r in ((1, 1032, 4096, 64), (20, 520, 2048, 16), (200, 520, 4096, 64), (1100, 520, 1024, 8)):
         lin = Lin(4000, N, K, r)
