@@ -670,6 +670,8 @@ def qlora_int8_linear_fwd(w: Int8Weight, X, L1=None, L2=None, scale: float = 1.0
     torch = _torch()
     bf16, N, K, dev = torch.bfloat16, w.rows, w.cols, w.device
     r = _int8_adapter(L1, L2, N, K, dev)
+    if X is None and (Xq is None or r):
+        raise ValueError("X is missing: without it, Xq has to be given and no adapter")
     M = (X if X is not None else Xq[0]).shape[0]
     if X is not None:
         _expect(X, bf16, (M, K), dev, "X")

@@ -198,7 +198,7 @@ __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
     }
     __syncthreads();
 
-    // wave w finishes tiles w, w + 8, ..: lane (ln, lg) holds weight row n and tokens 16 b + 4 lg + v
+    // wave w finishes tiles w, w + NW, ..: lane (ln, lg) holds weight row n and tokens 16 b + 4 lg + v
     const __amdgpu_buffer_rsrc_t rL2 = make_rsrc(g.L2, (int64_t)g.r * g.N * 2);
     for (int t = wave; t < RG * G; t += NW) {
         const int a = t / G, b = t % G;

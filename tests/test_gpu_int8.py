@@ -440,3 +440,13 @@ def test_binding_refusals():
         nf4.qlora_int8_linear_fwd(lin.w, X[:0])
     with pytest.raises(nf4.NF4Error):
         nf4.nf4_int8_quantize(torch.zeros((2, 12), device=DEV))
+
+
+def test_binding_refuses_a_missing_x():
+    lin = Lin(4400, 64, 128, 8)
+    X, _ = bf16(np.ones((4, 128)))
+    Xq = nf4.nf4_int8_quantize(X)
+    for bad in (lambda: nf4.qlora_int8_linear_fwd(lin.w, None), lambda: nf4.qlora_int8_linear_fwd(lin.w, None, lin.L1, lin.L2, Xq=Xq)):
+        with pytest.raises(ValueError):
+            bad()
+    assert same(nf4.qlora_int8_linear_fwd(lin.w, None, Xq=Xq)[0], nf4.qlora_int8_linear_fwd(lin.w, X)[0])
