@@ -1204,14 +1204,10 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
         prep.L2T = L2T;
     }
     NF4_CHECK_HIP(nf4k::launch_int8_prep(prep, s), "int8 quantize + T reduce + L2 transpose");
-    float *Pg = ws_at<float>(workspace, p.off_Pg);
+    int32_t *Pg = ws_at<int32_t>(workspace, p.off_Pg);
     NF4_CHECK_HIP(nf4k::launch_int8_gemm(nf4k::Int8Product{Xq, w->codes, xs, w->scales, sT, L2T, M, N, K, r, Y,
                                                            p.kf.ksplit, (int32_t)p.kf.per, Pg}, s),
                   "int8 GEMM (fwd)");
-    if (p.kf.ksplit > 1) {
-        const nf4k::Reduction sum{Pg, p.kf.ksplit, M * N, 1.0f, Y, 0.0f, nullptr};
-        NF4_CHECK_HIP(nf4k::launch_reduce_partials(sum, nullptr, s), "split product reduce");
-    }
     return NF4_OK;
 }
 

@@ -23,8 +23,8 @@
 // tile with one LDS stage took 420 and 1667 us.
 //
 // Few output tiles (fewer than half the CUs): the reduction is split over up to 16 workgroups per
-// tile, each writing a scaled float32 partial tile (the last also the adapter's product), summed
-// afterwards in a fixed order.
+// tile, each writing its int32 sums; a second launch adds them, still exact, and has the epilogue.  So
+// without an adapter a token's Y is the same bits whatever the batch it comes in.
 
 #include "common.h"
 #include "dqtile.h"
@@ -68,7 +68,8 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
     const int all_steps = (int)((g.K + TKB - 1) / TKB);
     const int kb = split * g.split_per;
     const int steps = min(all_steps - kb, g.split_per);
-    const int ext_steps = split == g.ksplit - 1 ? (g.r + 63) / 64 : 0;
+    const bool part = g.ksplit > 1;
+    const int ext_steps = part ? 0 : (g.r + 63) / 64;
 
     // tile-relative descriptors: rows past M (or N) read zeros
     const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.Xq + m0 * g.K, (g.M - m0) * g.K);
@@ -189,13 +190,32 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
     }
     if (step < steps) step_body(step, As0, Bs0, As1, Bs1);   // odd count: the last one
     __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+    if (!part) __syncthreads();
 
     // lane indices for the code after the main loop, recomputed (mbcnt) rather than kept live
     // across it
     const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     const int r32_e = lane_e & 31, hh_e = lane_e >> 5;
     const int tid_e = wave * 64 + lane_e;
+
+    // lane (r32, hh) of tile (i, j) holds column wn*128 + 32 j + r32 and rows wm*128 + 32 i + 8 (v/4) + 4 hh +
+    // v%4; rows past M fall outside the descriptors
+    const uint32_t row_bytes = (uint32_t)(g.N * (part ? 4 : 2));
+    const uint32_t lane_off = (uint32_t)((wm * 128 + hh_e * 4) * row_bytes) + (uint32_t)((n0 + wn * 128 + r32_e) * (part ? 4 : 2));
+    if (part) {
+        const __amdgpu_buffer_rsrc_t rP = make_rsrc(g.P + (int64_t)split * g.M * g.N + m0 * g.N, (g.M - m0) * g.N * 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (n0 + wn * 128 + j * 32 + r32_e >= g.N) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    __builtin_amdgcn_raw_buffer_store_b32((uint32_t)acc[i][j][v], rP, lane_off + j * 128,
+                                                          (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3)) * row_bytes, 0);
+        }
+        return;
+    }
 
     // ---- epilogue operands into LDS: the tile's constants, and the adapter's steps (r <= 128: at most
     // two), sT rows in the A stages and L2^T rows in the B stages, zero padded past r ----
@@ -223,14 +243,8 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
     __syncthreads();
 
     // ---- one 32 x 32 tile after the other: the sum to float32 times both constants, the adapter's
-    // MFMAs on it, the store.  Lane (r32, hh) of tile (i, j) holds column wn*128 + 32 j + r32 and rows
-    // wm*128 + 32 i + 8 (v/4) + 4 hh + v%4; rows past M fall outside the descriptors. ----
-    const bool part = g.ksplit > 1;
-    const uint32_t row_bytes = (uint32_t)(g.N * (part ? 4 : 2));
-    const __amdgpu_buffer_rsrc_t rC =
-        part ? make_rsrc(g.P + (int64_t)split * g.M * g.N + m0 * g.N, (g.M - m0) * g.N * 4)
-             : make_rsrc(g.Y + m0 * g.N, (g.M - m0) * g.N * 2);
-    const uint32_t lane_off = (uint32_t)((wm * 128 + hh_e * 4) * row_bytes) + (uint32_t)((n0 + wn * 128 + r32_e) * (part ? 4 : 2));
+    // MFMAs on it, the store ----
+    const __amdgpu_buffer_rsrc_t rC = make_rsrc(g.Y + m0 * g.N, (g.M - m0) * g.N * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         f32x4 x[4];
@@ -255,24 +269,106 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
             if (ext_steps > 0) adapter(As0, Bs0);
             if (ext_steps > 1) adapter(As1, Bs1);
             if (n0 + wn * 128 + j * 32 + r32_e >= g.N) continue;
-            if (part) {
 #pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const uint32_t rows = (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3));
-                    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f[v]), rC, lane_off + j * 128, rows * row_bytes, 0);
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < 16; v += 2) {
-                    const uint32_t rows = (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3));
-                    const uint32_t pk = pack_bf16x2(f[v], f[v + 1]);
-                    const uint32_t soff = rows * row_bytes;
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pk, rC, lane_off + j * 64, soff, 0);
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pk >> 16), rC, lane_off + j * 64, soff + row_bytes, 0);
-                }
+            for (int v = 0; v < 16; v += 2) {
+                const uint32_t rows = (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3));
+                const uint32_t pk = pack_bf16x2(f[v], f[v + 1]);
+                const uint32_t soff = rows * row_bytes;
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pk, rC, lane_off + j * 64, soff, 0);
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pk >> 16), rC, lane_off + j * 64, soff + row_bytes, 0);
             }
         }
     }
+}
+
+// The splits' sums and the epilogue of a split product.  A wave takes G groups of 16 tokens by 16 weight
+// rows: lane (ln, lg) holds token ln and rows 4 lg .. +3, 16 bytes of each partial, which is the output
+// layout of v_mfma_f32_16x16x32_bf16 with L2^T's rows as the first operand and s T's as the second, so
+// the adapter's RS steps of 32 go straight onto the scaled sums.  A workgroup's four waves lie along the
+// weight rows (256 contiguous bytes per token) and share s T's rows through LDS: read by each wave for
+// itself, their 16 rows per load made the whole call 82 instead of 75 us at 2048 x 4096 x 4096, r = 64.
+// Against float32 partials with the adapter's product in the last split's, which are not exact: 65 x
+// 4096 x 4096 with r = 64 31 -> 26 us, 2048 x 4096 x 4096 73 -> 75 us (63 both without an adapter).
+template <int G, int RS>
+__global__ __launch_bounds__(256) void int8_sum_kernel(Int8Product g) {
+    const int lane = threadIdx.x & 63, ln = lane & 15, lg = lane >> 4;
+    const int64_t nb = (g.N + 63) / 64;
+    const int64_t m0 = (int64_t)(blockIdx.x / (uint32_t)nb) * (16 * G) + ln;
+    const int64_t n0 = (int64_t)(blockIdx.x % (uint32_t)nb) * 64 + (threadIdx.x >> 6) * 16, n = n0 + 4 * lg;
+    const bool nin = n < g.N;                     // N % 8 == 0: the four rows are inside or outside
+    const u32x4 none = {0u, 0u, 0u, 0u};
+    u32x4 a[RS ? RS : 1];
+#pragma unroll
+    for (int s = 0; s < RS; ++s) {
+        const int j = 32 * s + 8 * lg;            // r % 8 == 0: a group of 8 is inside or outside
+        a[s] = j < g.r && n0 + ln < g.N ? *reinterpret_cast<const u32x4 *>(g.L2T + (n0 + ln) * g.r + j) : none;
+    }
+    float w[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) w[v] = nin ? g.ws[n + v] : 0.0f;
+    const int64_t plane = g.M * g.N / 4;
+    constexpr int KU = 8 / G;                     // partials' loads in flight per group
+    i32x4 sum[G];
+    const i32x4 *p[G];
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+        sum[q] = i32x4{0, 0, 0, 0};
+        const int64_t m = m0 + 16 * q;
+        p[q] = reinterpret_cast<const i32x4 *>(g.P + (nin && m < g.M ? m * g.N + n : 0));
+    }
+    // the tokens' s T rows, shared by the four waves
+    constexpr int ROW = RS * 64 + 16;             // bytes, padded: 16 rows' pieces lie on 64 different banks
+    __shared__ __align__(16) uint8_t st[RS ? 16 * G * ROW : 16];
+    if (RS > 0) {
+        const int64_t mt = m0 - ln;
+#pragma unroll
+        for (int i = 0; i < (G * RS + 3) / 4; ++i) {
+            const int c = (int)threadIdx.x + 256 * i, row = c / (RS ? 4 * RS : 1), j = c % (RS ? 4 * RS : 1) * 8;
+            if (row < 16 * G)
+                *reinterpret_cast<u32x4 *>(st + row * ROW + j * 2) =
+                    j < g.r && mt + row < g.M ? *reinterpret_cast<const u32x4 *>(g.sT + (mt + row) * g.r + j) : none;
+        }
+    }
+    for (int k0 = 0; k0 < g.ksplit; k0 += KU) {
+        i32x4 v[G][KU];
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+#pragma unroll
+            for (int q = 0; q < G; ++q)
+                if (k0 + u < g.ksplit) v[q][u] = p[q][(k0 + u) * plane];
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+#pragma unroll
+            for (int q = 0; q < G; ++q)
+                if (k0 + u < g.ksplit) sum[q] += v[q][u];
+    }
+    if (RS > 0) __syncthreads();
+#pragma unroll
+    for (int q = 0; q < G; ++q) {
+        const int64_t m = m0 + 16 * q;
+        const bool in = nin && m < g.M;
+        const float x = m < g.M ? g.xs[m] : 0.0f;
+        f32x4 f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) f[v] = ((float)sum[q][v] * x) * w[v];
+#pragma unroll
+        for (int s = 0; s < RS; ++s) {
+            const bf16x8 b = *reinterpret_cast<const bf16x8 *>(st + (16 * q + ln) * ROW + (32 * s + 8 * lg) * 2);
+            f = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[s]), b, f, 0, 0, 0);
+        }
+        if (in) *reinterpret_cast<uint2 *>(g.Y + m * g.N + n) = uint2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+    }
+}
+
+// Two groups of tokens a wave where one would make more than sixteen workgroups a CU: with one and with two,
+// 2048 x 4096 x 4096 with r = 64 81.1 and 79.4 us, 1000 x 4096 x 4096 59.4 and 59.9, 300 x 4096 x 11008
+// 53.8 and 57.
+template <int RS>
+void launch_sum(const Int8Product &a, hipStream_t s) {
+    const int64_t nb = (a.N + 63) / 64, m16 = (a.M + 15) / 16;
+    // a split product has at most 128 tiles: at most 8192 workgroups
+    if (m16 * nb > 4096) hipLaunchKernelGGL((int8_sum_kernel<2, RS>), dim3((unsigned)((m16 + 1) / 2 * nb)), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((int8_sum_kernel<1, RS>), dim3((unsigned)(m16 * nb)), dim3(256), 0, s, a);
 }
 
 }  // namespace
@@ -291,7 +387,11 @@ hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream) {
     hipLaunchKernelGGL(int8_gemm_kernel, dim3((unsigned)(tiles * a.ksplit)), dim3(256), 0, stream, a);
     const hipError_t e = hipGetLastError();
     timing_after(stream);
-    return e;
+    if (e != hipSuccess || a.ksplit == 1) return e;
+    if (a.r == 0) launch_sum<0>(a, stream);
+    else if (a.r <= 64) launch_sum<2>(a, stream);
+    else launch_sum<4>(a, stream);
+    return hipGetLastError();
 }
 
 // Reduction steps of 128 codes split as the bf16 products' are (fewer output tiles than half the CUs).

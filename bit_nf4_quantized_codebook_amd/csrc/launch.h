@@ -182,7 +182,7 @@ struct Int8Prep {
 };
 hipError_t launch_int8_prep(const Int8Prep &p, hipStream_t stream);
 // Y = xs ws (Xq Wq^T) + sT L2 (r = 0: no adapter).  ksplit > 1: split_per steps of 128 codes per
-// workgroup, float32 partials P [ksplit][M, N] for launch_reduce_partials instead of Y.
+// workgroup, int32 partials in P [ksplit][M, N] and a second launch that sums them.
 struct Int8Product {
     const int8_t *Xq, *Wq;
     const float *xs, *ws;
@@ -191,7 +191,7 @@ struct Int8Product {
     int32_t r;
     uint16_t *Y;
     int32_t ksplit, split_per;
-    float *P;
+    int32_t *P;
 };
 SplitPlan int8_gemm_split(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream);

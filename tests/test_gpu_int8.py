@@ -225,6 +225,26 @@ def test_linear_forward_rows_that_are_not_finite_or_zero(M):
     assert same(Yb[keep], Y[keep])
 
 
+@pytest.mark.parametrize("size", [1e-30, 1e30])
+@pytest.mark.parametrize("M,r", [(2, 0), (40, 16), (300, 0), (80, 64)])
+def test_linear_forward_small_and_large_values(M, r, size):
+    N, K = 264, 1024
+    lin = Lin(2950, N, K, r)
+    X, _ = bf16(np.clip(synth.normal_f32(2951, (M, K), size), -1e31, 1e31))
+    Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+    check_fwd(lin, X, 0.5, Y, T)
+
+
+def test_linear_forward_is_the_same_bits_in_any_batch():
+    """Without an adapter the integer sums are exact whatever kernel or split computes them."""
+    N, K = 520, 4096
+    lin = Lin(2970, N, K, 0)
+    X, _ = bf16(synth.normal_f32(2971, (700, K), 1.0))
+    Y, _ = nf4.qlora_int8_linear_fwd(lin.w, X)
+    for M in (1, 5, 17, 40, 64, 65, 200, 257, 513):
+        assert same(nf4.qlora_int8_linear_fwd(lin.w, X[:M])[0], Y[:M]), M
+
+
 def test_linear_forward_leaves_the_rest_alone():
     """Outputs inside larger buffers: what stands before and after them stays."""
     for M, N, K, r in ((1, 72, 128, 8), (13, 72, 128, 8), (70, 264, 192, 16), (257, 520, 128, 8)):
