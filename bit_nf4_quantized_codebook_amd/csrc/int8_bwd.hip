@@ -14,7 +14,7 @@
 // W rows are the reduction, so fragments are read with ds_read_b64_tr_b16.  The adapter is r/64 more steps.
 //
 // Bound by no one unit: over a large product the MFMAs are busy 47 % of the CUs' cycles and LDS 59 %
-// (counters, 1023 x 22016 x 8192).  Measured, the whole backward with r = 16: 67 us at 333 tokens x 11008 x
+// (counters, 1023 x 22016 x 8192).  Measured, the whole backward with r = 16: 66 us at 333 tokens x 11008 x
 // 4096 (this kernel 47), 99 with the weight expanded first.  Four waves of 64 x 128 instead of eight of
 // 64 x 64 measured 2 to 6 % slower.
 //
