@@ -225,6 +225,17 @@ def test_linear_forward_rows_that_are_not_finite_or_zero(M):
     assert same(Yb[keep], Y[keep])
 
 
+# split products of every form of the sum: ranks up to 64 and beyond, few and many output groups
+@pytest.mark.parametrize("M,N,K,r", [(65, 72, 4096, 8), (130, 520, 1088, 72), (90, 264, 2048, 128), (1041, 4104, 1024, 0),
+                                     (1041, 4104, 1024, 24), (1041, 4104, 1024, 104)])
+def test_linear_forward_split(M, N, K, r):
+    print(f"int8 forward split M={M} N={N} K={K} r={r}", flush=True)
+    lin = Lin(2900 + M + r, N, K, r)
+    X, _ = bf16(synth.normal_f32(2901 + M, (M, K), 1.0))
+    Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+    check_fwd(lin, X, 0.5, Y, T)
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e30])
 @pytest.mark.parametrize("M,r", [(2, 0), (40, 16), (300, 0), (80, 64)])
 def test_linear_forward_small_and_large_values(M, r, size):
