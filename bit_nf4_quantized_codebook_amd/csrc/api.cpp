@@ -1047,10 +1047,10 @@ struct Int8Plan {
     bool expand;
     int ksT, ksdT, msL2, msL1;
     nf4k::SplitPlan kf, kb;        // split of the forward's product and of the backward's dX product
-    size_t off_Xq, off_xs, off_T, off_sT, off_dT, off_dTlo, off_L2T, off_P, off_Wd, off_Pg, total;
+    size_t off_Xq, off_xs, off_T, off_sT, off_sTlo, off_dT, off_dTlo, off_L2T, off_P, off_Wd, off_Pg, total;
 };
 
-// One layout for both directions: the forward uses Xq, xs, sT, L2T, P and Pg, the backward T, dT, dTlo,
+// One layout for both directions: the forward uses Xq, xs, sT, sTlo, L2T, P and Pg, the backward T, dT, dTlo,
 // P, Wd and Pg.
 Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     Int8Plan p;
@@ -1082,6 +1082,7 @@ Int8Plan make_int8_plan(int64_t M, int64_t N, int64_t K, int32_t r) {
     p.off_xs = off;  off += round256((size_t)M * 4);
     p.off_T = off;   off += round256((size_t)M * r * 2);
     p.off_sT = off;  off += round256((size_t)M * r * 2);
+    p.off_sTlo = off; off += round256((size_t)M * r * 2);
     p.off_dT = off;  off += round256((size_t)M * r * 2);
     p.off_dTlo = off; off += round256((size_t)M * r * 2);
     p.off_L2T = off; off += round256((size_t)N * r * 2);
@@ -1176,10 +1177,11 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
         if (r && (size_t)p.ksT * M * r * 4 * (size_t)((N + 15) / 16) <= kInt8TSumBytes) {
             a.Tp = P; a.ksT = p.ksT; a.T_out = T_out;
         } else if (r) {
-            uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT);
-            const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
+            uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT), *sTlo = ws_at<uint16_t>(workspace, p.off_sTlo);
+            nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
+            red.lo2 = sTlo;
             NF4_CHECK_HIP(nf4k::launch_reduce_partials(red, nullptr, s), "T reduce");
-            a.sT = sT;
+            a.sT = sT; a.sTlo = sTlo;
         }
         NF4_CHECK_HIP(nf4k::launch_int8_gemv(a, s), "int8 GEMV (fwd)");
         return NF4_OK;
@@ -1194,9 +1196,11 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
         Xq = prep.Xq;
         xs = prep.xs;
     }
-    uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT), *L2T = ws_at<uint16_t>(workspace, p.off_L2T);
+    uint16_t *sT = ws_at<uint16_t>(workspace, p.off_sT), *sTlo = ws_at<uint16_t>(workspace, p.off_sTlo);
+    uint16_t *L2T = ws_at<uint16_t>(workspace, p.off_L2T);
     float *P = ws_at<float>(workspace, p.off_P);
-    const nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
+    nf4k::Reduction red{P, p.ksT, M * r, 1.0f, T_out, scale, sT};
+    red.lo2 = sTlo;
     if (r) {
         NF4_CHECK_HIP(nf4k::launch_skinny_nt(X, L1, /*b_rows_k=*/true, P, M, r, K, p.ksT, s), "T = X L1");
         prep.Tred = &red;
@@ -1205,7 +1209,7 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
     }
     NF4_CHECK_HIP(nf4k::launch_int8_prep(prep, s), "int8 quantize + T reduce + L2 transpose");
     int32_t *Pg = ws_at<int32_t>(workspace, p.off_Pg);
-    NF4_CHECK_HIP(nf4k::launch_int8_gemm(nf4k::Int8Product{Xq, w->codes, xs, w->scales, sT, L2T, M, N, K, r, Y,
+    NF4_CHECK_HIP(nf4k::launch_int8_gemm(nf4k::Int8Product{Xq, w->codes, xs, w->scales, sT, sTlo, L2T, M, N, K, r, Y,
                                                            p.kf.ksplit, (int32_t)p.kf.per, Pg}, s),
                   "int8 GEMM (fwd)");
     return NF4_OK;
@@ -1247,8 +1251,8 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
         NF4_CHECK_HIP(nf4k::launch_skinny_nt(dY, L2, /*b_rows_k=*/false, P, M, r, N, p.ksdT, s), "dT = dY L2^T");
         // dL1 = X^T dT takes dT in two bf16 halves: dT's rounding alone would cost dL1 as much as its own
         uint16_t *dTlo = ws_at<uint16_t>(workspace, p.off_dTlo);
-        nf4k::Reduction red_dT{P, p.ksdT, M * r, scale, dT, 0.0f, dTlo};
-        red_dT.resid = true;
+        nf4k::Reduction red_dT{P, p.ksdT, M * r, 0.0f, nullptr, scale, dT};
+        red_dT.lo2 = dTlo;
         // the weight's expansion, where it is wanted, carries dT's sum
         if (expand)
             NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, &red_dT, s),

@@ -35,6 +35,20 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
+// f as two bf16 values each, hi + lo: 16 significant bits, so a float32 sum that enters another
+// product loses 2^-16 of itself and not 2^-8.  Where hi is not finite, lo is zero (their sum is hi).
+__device__ __forceinline__ void split_bf16x4(const float f[4], uint2 &hi, uint2 &lo) {
+    hi = uint2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+    float d[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t w = k < 2 ? hi.x : hi.y;
+        const float h = __uint_as_float((k & 1) ? w & 0xFFFF0000u : w << 16);
+        d[k] = __builtin_isfinite(h) ? f[k] - h : 0.0f;
+    }
+    lo = uint2{pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3])};
+}
+
 // OCP FP8 E4M3 -> float (exact; codes 0x7F/0xFF are NaN and never produced here).
 // Branch-free: |v| = (8 [e > 0] + m) * 2^(max(e, 1) - 10), which covers subnormals (e = 0).
 __device__ __forceinline__ float e4m3_to_f32(uint32_t c) {

@@ -1,5 +1,5 @@
 // Int8 product of the Int8 QLoRA linear forward from 65 tokens (gfx950):
-//   Y[m, n] = xs[m] ws[n] sum_k Xq[m, k] Wq[n, k] + (sT L2)[m, n]
+//   Y[m, n] = xs[m] ws[n] sum_k Xq[m, k] Wq[n, k] + ((sT + sTlo) L2)[m, n]
 //
 // Page: "QLoRA: Efficient Finetuning of Quantized LLMs" study notes (gitcode.csdn.net), section 3.1
 // eq. (1) (8-bit integers), section 3.5 eq. (5), section 4 eq. (3).
@@ -13,9 +13,12 @@
 // per cycle as the bf16 GEMM's and does twice its products.  Both operands go straight from global
 // memory to LDS (buffer_load ... lds), two 32 KB stages each, 16-byte chunks XOR-swizzled by
 // (row / 2) so that the fragment reads are free of bank conflicts.  After the last step the
-// accumulators are turned to float32 tile by tile and the adapter's r/64 steps run on them with
+// accumulators are turned to float32 four tiles at a time and the adapter's r/64 steps run on them with
 // v_mfma_f32_32x32x16_bf16, whose output layout is the same.  (All 16 tiles turned first and then
-// multiplied, the kernel spilled 70 registers.)
+// multiplied, the kernel spilled 70 registers.)  s T comes as two bf16 halves, each with its own MFMAs: one
+// half alone would lose as much of the adapter's term as Y's own rounding.  (Tile by tile, with the
+// fragments read again for each, the second halves cost 3.3 us at 4096 x 4096 x 4096, r = 64; as it is,
+// 0.5.)
 //
 // Bound by the MFMA loop at the clock its power allows: 62.5 us at 4096 x 4096 x 4096 with r = 64 (2.2
 // POPS; a library int8 product of 8192 x 8192 x 8192 reaches 2.33 here) and 325 us at 2048 tokens x 22016 x
@@ -218,61 +221,94 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
     }
 
     // ---- epilogue operands into LDS: the tile's constants, and the adapter's steps (r <= 128: at most
-    // two), sT rows in the A stages and L2^T rows in the B stages, zero padded past r ----
+    // two), zero padded past r: sT's rows in stage As0, sTlo's in As1, L2^T's rows of step e in Bs0 or Bs1.
+    // With two steps an A stage holds both steps of half the tile's rows (64 of each wave row's 128), and
+    // is loaded again for the other half ----
+    const bool two = ext_steps > 1;
+    const __amdgpu_buffer_rsrc_t rAe = make_rsrc(g.sT + m0 * g.r, ext_steps ? (g.M - m0) * (int64_t)g.r * 2 : 0);
+    const __amdgpu_buffer_rsrc_t rAl = make_rsrc(g.sTlo + m0 * g.r, ext_steps ? (g.M - m0) * (int64_t)g.r * 2 : 0);
+    // a_col of the main loop, in elements
+    auto ext_col = [&](int q) { return ((lane_e & 7) ^ ((4 * q + (lane_e >> 4)) & 7)) * 8; };
+    auto load_ext_A = [&](int half) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int r8 = 8 * q + (lane_e >> 3);
+            const int row = two ? (wave & 1) * 128 + 64 * half + r8 : 64 * wave + r8;
+            const int jj = (two ? (wave >> 1) * 64 : 0) + ext_col(q);
+            const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0x80000000u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rAe, (lds_void *)((lds_u8 *)As0 + wave * 8192 + q * 1024), 16, off, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rAl, (lds_void *)((lds_u8 *)As1 + wave * 8192 + q * 1024), 16, off, 0, 0, 0);
+        }
+    };
     if (tid_e < TM) {
         xs_l[tid_e] = m0 + tid_e < g.M ? g.xs[m0 + tid_e] : 0.0f;
         ws_l[tid_e] = n0 + tid_e < g.N ? g.ws[n0 + tid_e] : 0.0f;
     }
     if (ext_steps > 0) {
-        const __amdgpu_buffer_rsrc_t rAe = make_rsrc(g.sT + m0 * g.r, (g.M - m0) * (int64_t)g.r * 2);
         const __amdgpu_buffer_rsrc_t rBe = make_rsrc(g.L2T + n0 * g.r, (g.N - n0) * (int64_t)g.r * 2);
-        auto load_ext = [&](int e, uint8_t *Ast, uint8_t *Bst) {
+        auto load_ext_B = [&](int e, uint8_t *Bst) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const int row = 8 * (8 * wave + q) + (lane_e >> 3);
-                const int jj = e * 64 + (a_col[q & 1] >> 1);
+                const int jj = e * 64 + ext_col(q);
                 const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0x80000000u;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rAe, (lds_void *)((lds_u8 *)Ast + wave * 8192 + q * 1024), 16, off, 0, 0, 0);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rBe, (lds_void *)((lds_u8 *)Bst + wave * 8192 + q * 1024), 16, off, 0, 0, 0);
             }
         };
-        load_ext(0, As0, Bs0);
-        if (ext_steps > 1) load_ext(1, As1, Bs1);
+        load_ext_A(0);
+        load_ext_B(0, Bs0);
+        if (two) load_ext_B(1, Bs1);
     }
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 
-    // ---- one 32 x 32 tile after the other: the sum to float32 times both constants, the adapter's
-    // MFMAs on it, the store ----
+    // ---- four 32 x 32 tiles side by side at a time: the sums to float32 times both constants, the
+    // adapter's MFMAs on them, the stores ----
     const __amdgpu_buffer_rsrc_t rC = make_rsrc(g.Y + m0 * g.N, (g.M - m0) * g.N * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if (i == 2 && two) {
+            __syncthreads();
+            load_ext_A(1);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+        }
         f32x4 x[4];
 #pragma unroll
         for (int v4 = 0; v4 < 4; ++v4)
             x[v4] = *reinterpret_cast<const f32x4 *>(xs_l + wm * 128 + i * 32 + v4 * 8 + hh_e * 4);
+        f32x16 f[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float w = ws_l[wn * 128 + j * 32 + r32_e];
-            f32x16 f;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) f[v] = ((float)acc[i][j][v] * x[v >> 2][v & 3]) * w;
-            auto adapter = [&](const uint8_t *Ast, const uint8_t *Bst) {
+            for (int v = 0; v < 16; ++v) f[j][v] = ((float)acc[i][j][v] * x[v >> 2][v & 3]) * w;
+        }
+#pragma unroll 1
+        for (int e = 0; e < ext_steps; ++e) {
+            const int row = two ? 128 * e + wm * 64 + 32 * (i & 1) : wm * 128 + 32 * i;
+            const uint8_t *Bst = (e ? Bs1 : Bs0) + wn * 128 * 128;
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t o = (uint32_t)(r32_e * 128 + (((2 * s + hh_e) ^ ((r32_e >> 1) & 7)) * 16));
-                    const bf16x8 fa = *reinterpret_cast<const bf16x8 *>(Ast + o + (wm * 128 + 32 * i) * 128);
-                    const bf16x8 fb = *reinterpret_cast<const bf16x8 *>(Bst + o + (wn * 128 + 32 * j) * 128);
-                    f = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb, f, 0, 0, 0);
-                }
-            };
-            if (ext_steps > 0) adapter(As0, Bs0);
-            if (ext_steps > 1) adapter(As1, Bs1);
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t o = (uint32_t)(r32_e * 128 + (((2 * s + hh_e) ^ ((r32_e >> 1) & 7)) * 16));
+                const bf16x8 fa = *reinterpret_cast<const bf16x8 *>(As0 + o + row * 128);
+                const bf16x8 fl = *reinterpret_cast<const bf16x8 *>(As1 + o + row * 128);
+                bf16x8 fb[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fb[j] = *reinterpret_cast<const bf16x8 *>(Bst + o + 32 * j * 128);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[j], f[j], 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fl, fb[j], f[j], 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             if (n0 + wn * 128 + j * 32 + r32_e >= g.N) continue;
 #pragma unroll
             for (int v = 0; v < 16; v += 2) {
                 const uint32_t rows = (uint32_t)(i * 32 + (v >> 2) * 8 + (v & 3));
-                const uint32_t pk = pack_bf16x2(f[v], f[v + 1]);
+                const uint32_t pk = pack_bf16x2(f[j][v], f[j][v + 1]);
                 const uint32_t soff = rows * row_bytes;
                 __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pk, rC, lane_off + j * 64, soff, 0);
                 __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(pk >> 16), rC, lane_off + j * 64, soff + row_bytes, 0);
@@ -284,9 +320,10 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_kernel(Int8Product g) {
 // The splits' sums and the epilogue of a split product.  A wave takes G groups of 16 tokens by 16 weight
 // rows: lane (ln, lg) holds token ln and rows 4 lg .. +3, 16 bytes of each partial, which is the output
 // layout of v_mfma_f32_16x16x32_bf16 with L2^T's rows as the first operand and s T's as the second, so
-// the adapter's RS steps of 32 go straight onto the scaled sums.  A workgroup's four waves lie along the
-// weight rows (256 contiguous bytes per token) and share s T's rows through LDS: read by each wave for
-// itself, their 16 rows per load made the whole call 82 instead of 75 us at 2048 x 4096 x 4096, r = 64.
+// the adapter's RS steps of 32 go straight onto the scaled sums, for each of s T's two halves.  A
+// workgroup's four waves lie along the weight rows (256 contiguous bytes per token) and share s T's rows
+// through LDS: read by each wave for itself, their 16 rows per load made the whole call 82 instead of
+// 75 us at 2048 x 4096 x 4096, r = 64.
 // Against float32 partials with the adapter's product in the last split's, which are not exact: 65 x
 // 4096 x 4096 with r = 64 31 -> 26 us, 2048 x 4096 x 4096 73 -> 75 us (63 both without an adapter).
 template <int G, int RS>
@@ -316,17 +353,22 @@ __global__ __launch_bounds__(256) void int8_sum_kernel(Int8Product g) {
         const int64_t m = m0 + 16 * q;
         p[q] = reinterpret_cast<const i32x4 *>(g.P + (nin && m < g.M ? m * g.N + n : 0));
     }
-    // the tokens' s T rows, shared by the four waves
+    // the tokens' s T rows, shared by the four waves: the first halves, then the second
     constexpr int ROW = RS * 64 + 16;             // bytes, padded: 16 rows' pieces lie on 64 different banks
-    __shared__ __align__(16) uint8_t st[RS ? 16 * G * ROW : 16];
+    constexpr int HALF = 16 * G * ROW;
+    __shared__ __align__(16) uint8_t st[RS ? 2 * HALF : 16];
     if (RS > 0) {
         const int64_t mt = m0 - ln;
 #pragma unroll
         for (int i = 0; i < (G * RS + 3) / 4; ++i) {
             const int c = (int)threadIdx.x + 256 * i, row = c / (RS ? 4 * RS : 1), j = c % (RS ? 4 * RS : 1) * 8;
-            if (row < 16 * G)
+            const bool live = j < g.r && mt + row < g.M;
+            if (row < 16 * G) {
                 *reinterpret_cast<u32x4 *>(st + row * ROW + j * 2) =
-                    j < g.r && mt + row < g.M ? *reinterpret_cast<const u32x4 *>(g.sT + (mt + row) * g.r + j) : none;
+                    live ? *reinterpret_cast<const u32x4 *>(g.sT + (mt + row) * g.r + j) : none;
+                *reinterpret_cast<u32x4 *>(st + HALF + row * ROW + j * 2) =
+                    live ? *reinterpret_cast<const u32x4 *>(g.sTlo + (mt + row) * g.r + j) : none;
+            }
         }
     }
     for (int k0 = 0; k0 < g.ksplit; k0 += KU) {
@@ -353,8 +395,11 @@ __global__ __launch_bounds__(256) void int8_sum_kernel(Int8Product g) {
         for (int v = 0; v < 4; ++v) f[v] = ((float)sum[q][v] * x) * w[v];
 #pragma unroll
         for (int s = 0; s < RS; ++s) {
-            const bf16x8 b = *reinterpret_cast<const bf16x8 *>(st + (16 * q + ln) * ROW + (32 * s + 8 * lg) * 2);
-            f = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[s]), b, f, 0, 0, 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bf16x8 b = *reinterpret_cast<const bf16x8 *>(st + h * HALF + (16 * q + ln) * ROW + (32 * s + 8 * lg) * 2);
+                f = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a[s]), b, f, 0, 0, 0);
+            }
         }
         if (in) *reinterpret_cast<uint2 *>(g.Y + m * g.N + n) = uint2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
     }

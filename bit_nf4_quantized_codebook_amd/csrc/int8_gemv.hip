@@ -12,8 +12,9 @@
 //      keep every CU loading; a chunk is loaded while the one before it is multiplied
 //      (v_mfma_i32_16x16x64_i8; the 16 rows of its other operand hold 16 tokens, G groups of them).  A
 //      weight fragment's bytes go from the load straight into the MFMA: no LDS, no decode.
-//      The waves' int32 sums meet in LDS by integer adds, exact in any order; then the constants, the
-//      adapter's MFMAs (s T from T's partials, summed in a fixed order) and one rounding to bf16.
+//      The waves' int32 sums meet in LDS, exact in any order; then the constants, the
+//      adapter's MFMAs (s T from T's partials, summed in a fixed order and held in two bf16 halves) and
+//      one rounding to bf16.
 // Measured (both launches): 47 us for one token x 28672 x 8192 with r = 64 (5.0 TB/s of weight bytes; a
 // large copy reaches 5.2 here), 12 us at 4096 x 4096; 20 us for 23 tokens x 4096 x 11008 (16.5 where the
 // weight stays in the 256 MB cache).  Bound by HBM at large weights, by the two launches at small ones.
@@ -38,10 +39,17 @@ constexpr int R_MAX = 128;
 template <int NW, int RG, int G, bool DIRECT>
 __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
     constexpr int NT = NW * 64;
-    __shared__ int32_t sums[RG * G * 256];                 // [tile][lane][4]
-    __shared__ __align__(16) uint16_t sTs[16 * G * R_MAX];  // s T, bf16 [M][r]
-    __shared__ __align__(16) uint8_t xtile[NW][DIRECT ? 16 : G * 4096];   // each wave's tokens of a chunk
-    __shared__ f32x4 tpart[NT];                             // sums over parts of T's partials
+    // A wave's tokens of a chunk, and after the last its int32 sums [tile][4][lane]; with the tokens in
+    // registers, the sums of all waves.
+    constexpr int XW = G * 4096, SUMS = RG * G * 256;
+    static_assert(SUMS * 4 <= XW, "a wave's sums fit where its tokens were");
+    __shared__ __align__(16) uint8_t xtile[DIRECT ? SUMS * 4 : NW * XW];
+    // s T as two bf16 halves, [2][M][r], and, where parts > 1 (below: 4 M r bytes of halves are then less
+    // than 16 NT), sums over parts of T's partials
+    constexpr int ST_MAX = 2 * 16 * G * R_MAX * 2, TPART = NT * 16;
+    __shared__ __align__(16) uint8_t st[ST_MAX > 2 * TPART ? ST_MAX : 2 * TPART];
+    uint16_t *sTs = reinterpret_cast<uint16_t *>(st);
+    f32x4 *tpart = reinterpret_cast<f32x4 *>(st + TPART);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int ln = lane & 15, lg = lane >> 4;
@@ -91,7 +99,7 @@ __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
                 xr[q][i] = bload16(rX, k < K ? (uint32_t)(16 * q + row) * K + k : 0xFFFFFFF0u);
             }
     };
-    uint8_t *xt = xtile[wave];
+    uint8_t *xt = xtile + (DIRECT ? 0 : wave * XW);
     i32x4 acc[RG][G];
 #pragma unroll
     for (int a = 0; a < RG; ++a)
@@ -139,17 +147,22 @@ __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
     // Prologue, while the first chunk streams in: the sums' zeros, and s T (and T, by workgroup 0).
     // Where T has fewer pieces than the workgroup threads, `parts` threads share a piece's partials, so
     // that their loads are one latency, not one after the other; the parts are added in order below.
-    for (int i = tid; i < RG * G * 256; i += NT) sums[i] = 0;
+    int32_t *sums = reinterpret_cast<int32_t *>(xt);
+    if (DIRECT)
+        for (int i = tid; i < SUMS; i += NT) sums[i] = 0;
     const int E4 = (int)((g.M * g.r) >> 2);
     const int parts = E4 > 0 && E4 < NT ? min(NT / E4, 16) : 1;
     auto put_T = [&](int i, f32x4 t) {
-        const float s = g.scale;
-        *reinterpret_cast<uint2 *>(sTs + 4 * i) = uint2{pack_bf16x2(s * t.x, s * t.y), pack_bf16x2(s * t.z, s * t.w)};
+        const float f[4] = {g.scale * t.x, g.scale * t.y, g.scale * t.z, g.scale * t.w};
+        split_bf16x4(f, reinterpret_cast<uint2 *>(sTs)[i], reinterpret_cast<uint2 *>(sTs)[E4 + i]);
         if (blockIdx.x == 0 && g.T_out)
             reinterpret_cast<uint2 *>(g.T_out)[i] = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
     };
     if (g.r && !g.Tp) {
-        for (int i = tid; i < E4; i += NT) reinterpret_cast<uint2 *>(sTs)[i] = reinterpret_cast<const uint2 *>(g.sT)[i];
+        for (int i = tid; i < E4; i += NT) {
+            reinterpret_cast<uint2 *>(sTs)[i] = reinterpret_cast<const uint2 *>(g.sT)[i];
+            reinterpret_cast<uint2 *>(sTs)[E4 + i] = reinterpret_cast<const uint2 *>(g.sTlo)[i];
+        }
     } else if (g.r) {
         const f32x4 *Tp = reinterpret_cast<const f32x4 *>(g.Tp);
         for (int j = tid; j < E4 * parts; j += NT) {
@@ -182,20 +195,25 @@ __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
         mul(s1);
     }
 
+    auto put_sum = [&](auto put) {
+#pragma unroll
+        for (int a = 0; a < RG; ++a)
+#pragma unroll
+            for (int b = 0; b < G; ++b)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) put(&sums[(a * G + b) * 256 + v * 64 + lane], acc[a][b][v]);
+    };
+    if (!DIRECT) {
+        wave_order();
+        put_sum([](int32_t *s, int32_t x) { *s = x; });
+    }
     __syncthreads();
     if (parts > 1 && tid < E4 && g.Tp) {
         f32x4 t = tpart[tid];
         for (int p = 1; p < parts; ++p) t += tpart[p * E4 + tid];
         put_T(tid, t);
     }
-    if (nchunk > wave) {
-#pragma unroll
-        for (int a = 0; a < RG; ++a)
-#pragma unroll
-            for (int b = 0; b < G; ++b)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) atomicAdd(&sums[(a * G + b) * 256 + v * 64 + lane], acc[a][b][v]);
-    }
+    if (DIRECT && nchunk > wave) put_sum([](int32_t *s, int32_t x) { atomicAdd(s, x); });
     __syncthreads();
 
     // wave w finishes tiles w, w + NW, ..: lane (ln, lg) holds weight row n and tokens 16 b + 4 lg + v
@@ -217,9 +235,12 @@ __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
                 bw[i] = (lo & 0xFFFFu) | (hi << 16);
             }
             const int64_t m = 16 * b + ln;
-            const u32x4 av = (m < g.M && jj < g.r) ? *reinterpret_cast<const u32x4 *>(sTs + m * g.r + jj) : u32x4{0u, 0u, 0u, 0u};
-            lora = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av),
-                                                           __builtin_bit_cast(bf16x8, u32x4{bw[0], bw[1], bw[2], bw[3]}), lora, 0, 0, 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 av = (m < g.M && jj < g.r) ? *reinterpret_cast<const u32x4 *>(sTs + (h * g.M + m) * g.r + jj) : u32x4{0u, 0u, 0u, 0u};
+                lora = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av),
+                                                               __builtin_bit_cast(bf16x8, u32x4{bw[0], bw[1], bw[2], bw[3]}), lora, 0, 0, 0);
+            }
         }
         if (n >= g.N) continue;
         const float w = g.ws[n];
@@ -227,7 +248,11 @@ __global__ __launch_bounds__(NW * 64) void int8_gemv_kernel(Int8Gemv g) {
         for (int v = 0; v < 4; ++v) {
             const int64_t m = 16 * b + 4 * lg + v;
             if (m < g.M) {
-                const float y = ((float)sums[t * 256 + v * 64 + lane] * g.xs[m]) * w + lora[v];
+                int32_t sum = 0;
+#pragma unroll
+                for (int u = 0; u < (DIRECT ? 1 : NW); ++u)
+                    sum += reinterpret_cast<const int32_t *>(xtile + u * XW)[t * 256 + v * 64 + lane];
+                const float y = ((float)sum * g.xs[m]) * w + lora[v];
                 g.Y[m * g.N + n] = (uint16_t)f32_to_bf16(y);
             }
         }
@@ -287,7 +312,7 @@ hipError_t launch_int8_rows_t(const uint16_t *X, const uint16_t *L1, float *P, i
 }
 
 hipError_t launch_int8_gemv(const Int8Gemv &p, hipStream_t stream) {
-    if (p.M < 1 || p.M > 64 || p.r < 0 || p.r > R_MAX || (p.r && !p.Tp == !p.sT)) return hipErrorInvalidValue;
+    if (p.M < 1 || p.M > 64 || p.r < 0 || p.r > R_MAX || (p.r && !p.Tp == !p.sT) || !p.sT != !p.sTlo) return hipErrorInvalidValue;
     // Four waves where the rows make at least two workgroups a CU, else eight (8192 x 22016, one token:
     // 45.5 against 47.5 us; 4096 x 4096: 8.4 us with eight, 10.0 with sixteen).
     const int64_t groups = (p.N + 15) / 16;

@@ -144,7 +144,7 @@ struct Reduction {
     uint16_t *out2;
     int64_t stride = 0;
     bool accum = false;
-    bool resid = false;     // out2 = bf16(s1 * sum - out): out + out2 holds the sum to 16 bits
+    uint16_t *lo2 = nullptr;     // bf16(s2 * sum - out2): out2 + lo2 holds s2 * sum to 16 bits
 };
 hipError_t launch_reduce_partials(const Reduction &a, const Reduction *b, hipStream_t stream,
                                   const Reduction *c = nullptr);
@@ -181,12 +181,12 @@ struct Int8Prep {
     int64_t N;
 };
 hipError_t launch_int8_prep(const Int8Prep &p, hipStream_t stream);
-// Y = xs ws (Xq Wq^T) + sT L2 (r = 0: no adapter).  ksplit > 1: split_per steps of 128 codes per
+// Y = xs ws (Xq Wq^T) + (sT + sTlo) L2 (r = 0: no adapter).  ksplit > 1: split_per steps of 128 codes per
 // workgroup, int32 partials in P [ksplit][M, N] and a second launch that sums them.
 struct Int8Product {
     const int8_t *Xq, *Wq;
     const float *xs, *ws;
-    const uint16_t *sT, *L2T;
+    const uint16_t *sT, *sTlo, *L2T;
     int64_t M, N, K;
     int32_t r;
     uint16_t *Y;
@@ -197,7 +197,7 @@ SplitPlan int8_gemm_split(int64_t M, int64_t N, int64_t K);
 hipError_t launch_int8_gemm(const Int8Product &p, hipStream_t stream);
 
 // up to 64 tokens: X's codes (Xq non-null) and T's partials (nsplit of them; r = 0: none) in one launch,
-// then the product, which sums T's partials itself (Tp, ksT, writing T_out) or takes s T (sT)
+// then the product, which sums T's partials itself (Tp, ksT, writing T_out) or takes s T (sT + sTlo)
 hipError_t launch_int8_rows_t(const uint16_t *X, const uint16_t *L1, float *P, int64_t M, int32_t r, int64_t K, int nsplit,
                               int8_t *Xq, float *xs, hipStream_t stream);
 struct Int8Gemv {
@@ -207,7 +207,7 @@ struct Int8Gemv {
     int32_t ksT;
     float scale;
     uint16_t *T_out;
-    const uint16_t *sT, *L2;
+    const uint16_t *sT, *sTlo, *L2;
     int64_t M, N, K;
     int32_t r;
     uint16_t *Y;

@@ -211,7 +211,7 @@ RedProb red_prob(const Reduction &r, uint32_t &nblocks) {
     p.P = r.P; p.n = r.n; p.out = r.out; p.out2 = r.out2; p.s1 = r.s1; p.s2 = r.s2; p.nsplit = r.nsplit;
     p.stride = r.stride ? r.stride : r.n;
     p.accum = r.accum ? 1u : 0u;
-    p.resid = r.resid ? 1u : 0u;
+    p.lo2 = r.lo2;
     nblocks = reduce_blocks(r.n);
     return p;
 }

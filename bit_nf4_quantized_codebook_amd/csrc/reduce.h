@@ -1,8 +1,9 @@
 // Fixed-order sum of split-reduction partials, shared by the launches that carry it: its own
 // launch (one to three reductions) and, at large token counts, extra workgroups of the weight
 // expansion launch.
-//   out[i] = bf16(s1 * sum_k P[k stride + i]) (k ascending); out2 (optional) = bf16(s2 * the same
-//   sum), or with resid the rest that out's rounding left; with accum, out[i] = bf16(s1 * sum + out[i]) (the product added to what out holds).
+//   out[i] = bf16(s1 * sum_k P[k stride + i]) (k ascending), or with accum bf16(s1 * sum + out[i])
+//   (the product added to what out holds); out2 (optional) = bf16(s2 * the same sum), and lo2
+//   (optional, with out2) the rest that out2's rounding left.
 // Four elements per thread (n and stride are multiples of 4 for every caller: r % 8 == 0, and the
 // split GEMMs' output widths are multiples of 8).
 #pragma once
@@ -14,11 +15,10 @@ namespace nf4k {
 struct RedProb {
     const float *P;
     int64_t n, stride;
-    uint16_t *out, *out2;
+    uint16_t *out, *out2, *lo2;
     float s1, s2;
     int32_t nsplit;
     uint32_t accum;
-    uint32_t resid;      // out2 = bf16(s1 * sum - out): what out's rounding left
 };
 
 // workgroup `blk` of `nblk` workgroups (256 threads) covering one reduction
@@ -27,6 +27,7 @@ __device__ __forceinline__ void reduce_partials_block(const RedProb &pr, int64_t
     const float *__restrict__ P = pr.P;
     uint16_t *__restrict__ out = pr.out;
     uint16_t *__restrict__ out2 = pr.out2;
+    uint16_t *__restrict__ lo2 = pr.lo2;
     const int64_t n = pr.n, stride = pr.stride;
     const int nsplit = pr.nsplit;
     const float s1 = pr.s1, s2 = pr.s2;
@@ -53,14 +54,12 @@ __device__ __forceinline__ void reduce_partials_block(const RedProb &pr, int64_t
             uint2 o = {pack_bf16x2(s1 * acc.x, s1 * acc.y), pack_bf16x2(s1 * acc.z, s1 * acc.w)};
             reinterpret_cast<uint2 *>(out)[i] = o;
         }
-        if (out2 && pr.resid) {
-            float f[4] = {s1 * acc.x, s1 * acc.y, s1 * acc.z, s1 * acc.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float hi = bf16_to_f32(f32_to_bf16(f[k]));
-                f[k] = __builtin_isfinite(hi) ? f[k] - hi : 0.0f;
-            }
-            reinterpret_cast<uint2 *>(out2)[i] = uint2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
+        if (out2 && lo2) {
+            const float f[4] = {s2 * acc.x, s2 * acc.y, s2 * acc.z, s2 * acc.w};
+            uint2 hi, lo;
+            split_bf16x4(f, hi, lo);
+            reinterpret_cast<uint2 *>(out2)[i] = hi;
+            reinterpret_cast<uint2 *>(lo2)[i] = lo;
         } else if (out2) {
             uint2 o = {pack_bf16x2(s2 * acc.x, s2 * acc.y), pack_bf16x2(s2 * acc.z, s2 * acc.w)};
             reinterpret_cast<uint2 *>(out2)[i] = o;

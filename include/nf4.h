@@ -362,7 +362,8 @@ int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream)
  *   scale: s, finite.  M >= 1.  Each operand below 2 GiB, as in qlora_linear_fwd.
  *   workspace: >= qlora_int8_linear_workspace_size(M, N, K, r) bytes (forward and backward), 16-byte
  *         aligned; calls that may overlap need a workspace each.
- * Y is rounded to bf16 once; the integer sum times xs[m] has to stay within float32's range (values of X up
+ * s T enters its product with L2 as two bf16 halves (16 significant bits), and Y is rounded to bf16 once; the
+ * integer sum times xs[m] has to stay within float32's range (values of X up
  * to 1e31 always do).  Rows of X with non-finite values give rows of NaN in Y and leave the
  * other rows as they are.
  */

@@ -481,3 +481,31 @@ def test_binding_refuses_a_missing_x():
         with pytest.raises(ValueError):
             bad()
     assert same(nf4.qlora_int8_linear_fwd(lin.w, None, Xq=Xq)[0], nf4.qlora_int8_linear_fwd(lin.w, X)[0])
+
+
+# every form of the forward: GEMV with 1, 2 and 4 groups of tokens, loads of its own and through LDS, 4 and 8
+# waves; the product whole, with one and two adapter steps; the split product's sum
+ADAPTER = [(1, 264, 512, 8), (3, 520, 1024, 128), (12, 520, 320, 64), (16, 264, 2048, 16), (29, 264, 512, 40),
+           (40, 264, 576, 128), (64, 520, 1024, 72), (3, 8200, 320, 8), (9, 8200, 320, 24), (20, 8200, 320, 16),
+           (40, 8200, 320, 72), (50, 16392, 192, 8), (100, 264, 192, 64), (257, 520, 320, 16), (100, 264, 192, 72),
+           (600, 520, 320, 128), (65, 72, 4096, 8), (130, 520, 1088, 72), (1041, 4104, 1024, 24)]
+
+
+@pytest.mark.parametrize("M,N,K,r", ADAPTER)
+def test_linear_forward_adapter_alone(M, N, K, r):
+    """A weight of zeros: Y is the adapter's term, rounded once.  s T enters it as two bf16 halves: the second
+    is off by at most h of a rest that is at most h of s T, so the term by h^2 of its products' sizes; its 2 r
+    products are summed in float32, and T as in check_fwd."""
+    print(f"int8 forward, adapter alone M={M} N={N} K={K} r={r}", flush=True)
+    w = nf4.Int8Weight(torch.zeros((N, K), dtype=torch.int8, device=DEV), torch.ones(N, device=DEV))
+    L1, l1 = bf16(synth.normal_f32(5000 + K, (K, r), 1.0 / r))
+    L2, l2 = bf16(synth.normal_f32(5001 + N, (r, N), 0.05))
+    X, x = bf16(synth.normal_f32(5002 + M, (M, K), 1.0))
+    s = 0.75
+    Y, T = nf4.qlora_int8_linear_fwd(w, X, L1, L2, s)
+    t = x @ l1
+    t_tol = 1.01 * (K + 70) * U * (np.abs(x) @ np.abs(l1))
+    within("T", T, t, H * (np.abs(t) + t_tol) + t_tol)
+    ref = s * (t @ l2)
+    tol = s * (t_tol @ np.abs(l2)) + 1.01 * (H * H + (2 * r + 16) * U) * s * (np.abs(t) @ np.abs(l2))
+    within("Y", Y, ref, H * (np.abs(ref) + tol) + tol)
