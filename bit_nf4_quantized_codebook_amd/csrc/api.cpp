@@ -1234,7 +1234,8 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
     if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "int8 linear workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    uint16_t *dT = ws_at<uint16_t>(workspace, p.off_dT), *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
+    uint16_t *dT = ws_at<uint16_t>(workspace, p.off_dT), *dTlo = ws_at<uint16_t>(workspace, p.off_dTlo);
+    uint16_t *WdT = ws_at<uint16_t>(workspace, p.off_Wd);
     const bool expand = dX && p.expand;
     nf4k::Reduction sums[3];
     int nsum = 0;
@@ -1249,8 +1250,7 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
             Tuse = Tb;
         }
         NF4_CHECK_HIP(nf4k::launch_skinny_nt(dY, L2, /*b_rows_k=*/false, P, M, r, N, p.ksdT, s), "dT = dY L2^T");
-        // dL1 = X^T dT takes dT in two bf16 halves: dT's rounding alone would cost dL1 as much as its own
-        uint16_t *dTlo = ws_at<uint16_t>(workspace, p.off_dTlo);
+        // dX and dL1 = X^T dT take dT in two bf16 halves: the rounding to one would cost them as much as their own
         nf4k::Reduction red_dT{P, p.ksdT, M * r, 0.0f, nullptr, scale, dT};
         red_dT.lo2 = dTlo;
         // the weight's expansion, where it is wanted, carries dT's sum
@@ -1283,10 +1283,10 @@ int qlora_int8_linear_bwd(const nf4_int8_weight *w, const uint16_t *dY, const ui
             if (!r)
                 NF4_CHECK_HIP(nf4k::launch_int8_expand(view_of(w), /*transposed=*/true, WdT, nullptr, s), "int8 expansion");
             NF4_CHECK_HIP(nf4k::launch_gemm_bf16_bwd(dY, WdT, dT, L1, r, M, N, K, dX, acc,
-                                                     nf4k::SplitK{p.kb.ksplit, p.kb.per, Pg}, s),
+                                                     nf4k::SplitK{p.kb.ksplit, p.kb.per, Pg}, s, r ? dTlo : nullptr),
                           "bf16 GEMM (int8 bwd)");
         } else {
-            NF4_CHECK_HIP(nf4k::launch_int8_bwd(nf4k::Int8Bwd{dY, w->codes, w->scales, dT, L1, dX, M, N, K, r,
+            NF4_CHECK_HIP(nf4k::launch_int8_bwd(nf4k::Int8Bwd{dY, w->codes, w->scales, dT, dTlo, L1, dX, M, N, K, r,
                                                               acc ? 1u : 0u, p.kb.ksplit, (int32_t)p.kb.per, Pg}, s),
                           "int8 GEMM (bwd)");
         }

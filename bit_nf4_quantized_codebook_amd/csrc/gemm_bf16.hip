@@ -50,6 +50,7 @@ struct GemmArgs {
     int64_t M, Nout, Kred;
     int32_t r;
     uint32_t accumulate;
+    // LO: Ae's second half, Ae + Ae2 held as two bf16 values.
     // two-segment backward: A2 = dU, B2 = deq(W_up)^T, Ae2 = dT_up, Be2 = L1_up (A, B, Ae, Be: gate's);
     // Kred is one segment's length
     const uint16_t *Ae2;
@@ -72,7 +73,7 @@ struct GemmArgs {
     float *P;
 };
 
-template <bool BWD, bool DUAL>
+template <bool BWD, bool DUAL, bool LO = false>
 __device__ __forceinline__ void gemm_body(const GemmArgs &g) {
     // one LDS object per stage: a fragment read of one stage provably never aliases the
     // direct-to-LDS loads in flight into the other
@@ -275,7 +276,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs &g) {
     }
 
     // ---- LoRA extension: r/64 more steps (zero padded past r) ----
-    //   A tile: Ae rows m0.., columns j (same swizzled layout, straight to LDS), in As0
+    //   A tile: Ae rows m0.., columns j (same swizzled layout, straight to LDS), in As0; LO: its second
+    //           half in As1, multiplied with the same B
     //   B tile: Be = L2^T (forward; transposed by the expansion launch) or L1 (backward) [Nout, r]:
     //           rows n, columns j -> swizzled layout in Bs0, straight to LDS, row reads
     if (ext_steps > 0) {
@@ -283,8 +285,8 @@ __device__ __forceinline__ void gemm_body(const GemmArgs &g) {
         const __amdgpu_buffer_rsrc_t rBe = make_rsrc(Be_t + cn0 * g.r, (cN - cn0) * (int64_t)g.r * 2);
         typedef __attribute__((address_space(3))) uint8_t lds_u8;
         // two segments: the up adapter's steps follow the gate's
-        const __amdgpu_buffer_rsrc_t rAeU = make_rsrc(DUAL ? g.Ae2 + m0 * g.r : g.Ae,
-                                                      DUAL ? (g.M - m0) * (int64_t)g.r * 2 : 0);
+        const __amdgpu_buffer_rsrc_t rAeU = make_rsrc(DUAL || LO ? g.Ae2 + m0 * g.r : g.Ae,
+                                                      DUAL || LO ? (g.M - m0) * (int64_t)g.r * 2 : 0);
         const __amdgpu_buffer_rsrc_t rBeU = make_rsrc(DUAL ? g.Be2 + n0 * g.r : g.Be,
                                                       DUAL ? (g.Nout - n0) * (int64_t)g.r * 2 : 0);
         for (int e = 0; e < (DUAL ? 2 : 1) * ext_steps; ++e) {
@@ -299,6 +301,9 @@ __device__ __forceinline__ void gemm_body(const GemmArgs &g) {
                 const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0x80000000u;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void *)((lds_u8 *)As0 + wave * 8192 + q * 1024),
                                                          16, off, 0, 0, 0);
+                if (LO)
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rAeU, (lds_void *)((lds_u8 *)As1 + wave * 8192 + q * 1024),
+                                                             16, off, 0, 0, 0);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void *)((lds_u8 *)Bs0 + wave * 8192 + q * 1024),
                                                          16, off, 0, 0, 0);
             }
@@ -314,6 +319,12 @@ __device__ __forceinline__ void gemm_body(const GemmArgs &g) {
                 for (int j = 0; j < 4; ++j)
                     f.b[j] = *reinterpret_cast<const bf16x8 *>(Bs0 + lds_off[s] + (wn * 128 + 32 * j) * 128);
                 mma(f);
+                if (LO) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f.a[i] = *reinterpret_cast<const bf16x8 *>(As1 + lds_off[s] + (wm * 128 + 32 * i) * 128);
+                    mma(f);
+                }
             }
             __syncthreads();
         }
@@ -386,11 +397,15 @@ __global__ __launch_bounds__(NTHREADS, 1) void gemm_bf16_kernel(GemmArgs g) {
     gemm_body<BWD, false>(g);
 }
 
+__global__ __launch_bounds__(NTHREADS, 1) void gemm_bf16_lo_kernel(GemmArgs g) {
+    gemm_body<true, false, true>(g);
+}
+
 __global__ __launch_bounds__(NTHREADS, 1) void gemm_bf16_dual_kernel(GemmArgs g) {
     gemm_body<true, true>(g);
 }
 
-template <bool BWD>
+template <bool BWD, bool LO = false>
 hipError_t launch_impl(GemmArgs &a, const SplitK &sk, hipStream_t stream) {
     const int ntm = (int)((a.M + TM - 1) / TM);
     const int ntn = (int)((a.Nout + TN - 1) / TN);
@@ -401,7 +416,9 @@ hipError_t launch_impl(GemmArgs &a, const SplitK &sk, hipStream_t stream) {
     if (a.ksplit > 1 && (!sk.P || (int64_t)(a.ksplit - 1) * sk.per >= steps || (int64_t)a.ksplit * sk.per < steps))
         return hipErrorInvalidValue;
     timing_before(stream, BWD ? 1 : 0);
-    hipLaunchKernelGGL(gemm_bf16_kernel<BWD>, dim3(ntm * ntn * a.ksplit), dim3(NTHREADS), 0, stream, a);
+    const dim3 grid(ntm * ntn * a.ksplit);
+    if (LO) hipLaunchKernelGGL(gemm_bf16_lo_kernel, grid, dim3(NTHREADS), 0, stream, a);
+    else hipLaunchKernelGGL(gemm_bf16_kernel<BWD>, grid, dim3(NTHREADS), 0, stream, a);
     hipError_t e = hipGetLastError();
     timing_after(stream);
     return e;
@@ -456,11 +473,12 @@ hipError_t launch_gemm_bf16_bwd_dual(const uint16_t *dG, const uint16_t *WdTg, c
 
 hipError_t launch_gemm_bf16_bwd(const uint16_t *dY, const uint16_t *WdT, const uint16_t *dT, const uint16_t *L1,
                                 int32_t r, int64_t M, int64_t N, int64_t K, uint16_t *dX, bool accumulate,
-                                const SplitK &sk, hipStream_t stream) {
+                                const SplitK &sk, hipStream_t stream, const uint16_t *dTlo) {
     GemmArgs a{};
     a.A = dY; a.B = WdT; a.Ae = dT; a.Be = L1; a.C = dX;
     a.M = M; a.Nout = K; a.Kred = N; a.r = r; a.accumulate = accumulate ? 1u : 0u;
-    return launch_impl<true>(a, sk, stream);
+    a.Ae2 = dTlo;
+    return dTlo ? launch_impl<true, true>(a, sk, stream) : launch_impl<true>(a, sk, stream);
 }
 
 }  // namespace nf4k

@@ -1,6 +1,6 @@
 // dX of the Int8 QLoRA linear backward where expanding the weight to bf16 first would cost
 // more than it saves, as up to about a thousand tokens (gfx950):
-//   dX = dY . W' + dT . L1^T,   W'[n, k] = bf16(ws[n] Wq[n, k]),   reduction over the W rows n
+//   dX = dY . W' + (dT + dTlo) . L1^T,   W'[n, k] = bf16(ws[n] Wq[n, k]),   reduction over the W rows n
 //
 // Page: "QLoRA: Efficient Finetuning of Quantized LLMs" study notes (gitcode.csdn.net), section 3.1
 // eq. (2) (dequantization, here one constant per row), section 3.5 (the gradient to X runs through the
@@ -11,7 +11,8 @@
 // by (row / 2).  The weight's 64 x 256 codes of a step come through registers four steps ahead and are
 // turned to bf16 on the way to LDS, spread over the MFMA sub-steps: a code costs one conversion of a
 // signed byte (v_cvt_f32_i32 with a byte select), one multiplication and half a packed conversion.  The
-// W rows are the reduction, so fragments are read with ds_read_b64_tr_b16.  The adapter is r/64 more steps.
+// W rows are the reduction, so fragments are read with ds_read_b64_tr_b16.  The adapter is r/64 more steps, with dT
+// in two bf16 halves: one alone would lose as much of the adapter's term as dX's own rounding.
 //
 // Bound by no one unit: over a large product the MFMAs are busy 47 % of the CUs' cycles and LDS 59 %
 // (counters, 1023 x 22016 x 8192).  Measured, the whole backward with r = 16: 66 us at 333 tokens x 11008 x
@@ -273,9 +274,10 @@ __global__ __launch_bounds__(NW * 64) void int8_bwd_kernel(Int8Bwd g) {
     __builtin_amdgcn_s_waitcnt(0);               // loads past the end still write their zeros
     __syncthreads();
 
-    // ---- adapter: r/64 more steps (zero padded past r) ----
+    // ---- adapter: r/64 more steps (zero padded past r), dT's first halves in As0, its second in As1 ----
     if (ext_steps > 0) {
         const __amdgpu_buffer_rsrc_t rAe = make_rsrc(g.dT + m0 * g.r, (g.M - m0) * (int64_t)g.r * 2);
+        const __amdgpu_buffer_rsrc_t rAl = make_rsrc(g.dTlo + m0 * g.r, (g.M - m0) * (int64_t)g.r * 2);
         const __amdgpu_buffer_rsrc_t rBe = make_rsrc(g.L1 + o0 * g.r, (g.K - o0) * (int64_t)g.r * 2);
         for (int e = 0; e < ext_steps; ++e) {
 #pragma unroll
@@ -283,8 +285,11 @@ __global__ __launch_bounds__(NW * 64) void int8_bwd_kernel(Int8Bwd g) {
                 const int row = (tid >> 3) + 8 * NW * q, chunk = tid & 7;
                 const int jj = e * TK + chunk * 8;
                 const uint32_t off = jj < g.r ? (uint32_t)((row * (int64_t)g.r + jj) * 2) : 0xFFFFFFF0u;
-                if (row < TM)
-                    *reinterpret_cast<u32x4 *>(As0 + row * 128 + (chunk ^ ((row >> 1) & 7)) * 16) = bload16(rAe, off);
+                if (row < TM) {
+                    const int at = row * 128 + (chunk ^ ((row >> 1) & 7)) * 16;
+                    *reinterpret_cast<u32x4 *>(As0 + at) = bload16(rAe, off);
+                    *reinterpret_cast<u32x4 *>(As1 + at) = bload16(rAl, off);
+                }
                 *reinterpret_cast<u32x4 *>(Bs0 + row * ROWB_RED + chunk * 16) = bload16(rBe, off);
             }
             __syncthreads();
@@ -295,6 +300,9 @@ __global__ __launch_bounds__(NW * 64) void int8_bwd_kernel(Int8Bwd g) {
                 for (int i = 0; i < IM; ++i) f.a[i] = frag_A(As0, s, i);
 #pragma unroll
                 for (int j = 0; j < JN; ++j) f.b[j] = frag_rowread(Bs0, s, j);
+                mma(f);
+#pragma unroll
+                for (int i = 0; i < IM; ++i) f.a[i] = frag_A(As1, s, i);
                 mma(f);
             }
             __syncthreads();

@@ -104,10 +104,11 @@ hipError_t launch_gemm_bf16_bwd_dual(const uint16_t *dG, const uint16_t *WdTg, c
                                     const uint16_t *dU, const uint16_t *WdTu, const uint16_t *dTu, const uint16_t *L1u,
                                     int32_t r, int64_t M, int64_t F, int64_t K, uint16_t *dX, bool accumulate,
                                     hipStream_t stream);
-// with sk.ksplit > 1, accumulate is the reduction's (the kernel writes partials)
+// with sk.ksplit > 1, accumulate is the reduction's (the kernel writes partials); dTlo (optional): dT's second
+// half, dT + dTlo held as two bf16 values
 hipError_t launch_gemm_bf16_bwd(const uint16_t *dY, const uint16_t *WdT, const uint16_t *dT, const uint16_t *L1,
                                 int32_t r, int64_t M, int64_t N, int64_t K, uint16_t *dX, bool accumulate,
-                                const SplitK &sk, hipStream_t stream);
+                                const SplitK &sk, hipStream_t stream, const uint16_t *dTlo = nullptr);
 hipError_t launch_dqgemm_bwd(const WeightView &w, const uint16_t *dY, const uint16_t *dT,
                              const uint16_t *L1, int32_t r, int64_t M, uint16_t *dX,
                              bool accumulate, const SplitK &sk, hipStream_t stream);
@@ -214,13 +215,13 @@ struct Int8Gemv {
 };
 hipError_t launch_int8_gemv(const Int8Gemv &p, hipStream_t stream);
 
-// dX = dY W' + dT L1^T through the codes, without expanding the weight first; ksplit as Int8Product's
+// dX = dY W' + (dT + dTlo) L1^T through the codes, without expanding the weight first; ksplit as Int8Product's
 // (steps of 64 weight rows), accumulate: dX is added to (with a split: by the reduction)
 struct Int8Bwd {
     const uint16_t *dY;
     const int8_t *Wq;
     const float *ws;
-    const uint16_t *dT, *L1;
+    const uint16_t *dT, *dTlo, *L1;
     uint16_t *dX;
     int64_t M, N, K;
     int32_t r;

@@ -375,6 +375,7 @@ int qlora_int8_linear_fwd(const nf4_int8_weight *w, const uint16_t *X, const int
 /*
  * Int8 QLoRA linear backward -- section 3.5: gradients for the adapters and for X only, through the
  * weight in BF16 (W' = nf4_int8_dequant); the rounding of X to its codes counts as the identity.
+ * dT enters both products as two bf16 halves (16 significant bits); dX, dL1 and dL2 are rounded once.
  *   dT = s dY L2^T;  dX = dY W' + dT L1^T;  dL1 = X^T dT;  dL2 = s T^T dY
  * Arguments, flags (QLORA_DX_ACCUMULATE) and outputs as qlora_linear_bwd; r = 0 without an adapter
  * (X, L1, L2, T, dL1 and dL2 NULL, dX required).

@@ -509,3 +509,53 @@ def test_linear_forward_adapter_alone(M, N, K, r):
     ref = s * (t @ l2)
     tol = s * (t_tol @ np.abs(l2)) + 1.01 * (H * H + (2 * r + 16) * U) * s * (np.abs(t) @ np.abs(l2))
     within("Y", Y, ref, H * (np.abs(ref) + tol) + tol)
+
+
+def plan(M, N, K):
+    """The backward's route for this shape: whether dX's product expands the weight to bf16 first or converts
+    its codes on the way, and over how many workgroups its reduction is split.  Both follow from the workspace
+    size, which holds the expansion and the splits' partials: of the two routes exactly one has that size."""
+    def split(tiles, steps):
+        s = max(1, min(256 // tiles, steps // 4, 16))
+        per = -(-steps // s)
+        per = -(-per // 4) * 4
+        return max(1, -(-steps // per))
+
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    tiles = lambda rows, cols: -(-M // rows) * -(-cols // 256)  # noqa: E731
+    fwd = 1 if M <= 64 else split(tiles(256, N), -(-K // 128))
+    steps = -(-N // 64)
+    got = {}
+    for route, s in (("expand", split(tiles(256, K), steps)), ("convert", split(tiles(64 if M <= 64 else 128, K), steps))):
+        partials = max(s * M * K if s > 1 else 0, fwd * M * N if fwd > 1 else 0)
+        got[up(M * K) + up(4 * M) + (up(2 * N * K) if route == "expand" else 0) + up(4 * partials)] = (route, s)
+    assert len(got) == 2, "the size does not tell the routes apart"
+    return got[nf4.qlora_int8_linear_workspace_size(M, N, K, 0)]
+
+
+@pytest.mark.parametrize("M,N,K,r,route,split", [
+    (37, 1032, 576, 128, "convert", 3), (20, 520, 2048, 16, "convert", 2), (200, 520, 4096, 64, "convert", 2),
+    (37, 264, 1472, 72, "convert", 1), (300, 200, 3136, 8, "convert", 1), (16, 264, 1088, 64, "expand", 1),
+    (100, 1032, 320, 24, "expand", 3), (300, 520, 320, 128, "expand", 2), (1100, 264, 448, 72, "expand", 1)])
+def test_linear_backward_adapter_alone(M, N, K, r, route, split):
+    """A weight of zeros: dX is the adapter's term, rounded once.  dT enters it as two bf16 halves (h^2 of its
+    products' sizes); its 2 r products are summed in float32, dT's as in test_linear_backward."""
+    print(f"int8 backward, adapter alone M={M} N={N} K={K} r={r}", flush=True)
+    assert plan(M, N, K) == (route, split)
+    w = nf4.Int8Weight(torch.zeros((N, K), dtype=torch.int8, device=DEV), torch.ones(N, device=DEV))
+    L1, l1 = bf16(synth.normal_f32(5100 + K, (K, r), 1.0 / r))
+    L2, l2 = bf16(synth.normal_f32(5101 + N, (r, N), 0.05))
+    X, x = bf16(synth.normal_f32(5102 + M, (M, K), 1.0))
+    dY, dy = bf16(synth.normal_f32(5103 + M, (M, N), 1.0))
+    T, _ = bf16(x @ l1)
+    s = 0.75
+    dX, _, _ = nf4.qlora_int8_linear_bwd(w, dY, X, L1, L2, T, s)
+    dt = s * (dy @ l2.T)
+    dt_tol = 1.01 * (N + 70) * U * s * (np.abs(dy) @ np.abs(l2.T))
+    ref = dt @ l1.T
+    tol = dt_tol @ np.abs(l1.T) + 1.01 * (H * H + (2 * r + 16) * U) * (np.abs(dt) @ np.abs(l1.T))
+    within("dX", dX, ref, H * (np.abs(ref) + tol) + tol)
+    base, bv = bf16(synth.normal_f32(5104, (M, K), 0.25))
+    acc, _, _ = nf4.qlora_int8_linear_bwd(w, dY, X, L1, L2, T, s, dX=base, accumulate=True)
+    ref, tol = ref + bv, tol + 2 * U * np.abs(bv)
+    within("dX accumulated", acc, ref, H * (np.abs(ref) + tol) + tol)
