@@ -73,21 +73,22 @@ __global__ __launch_bounds__(256) void skinny_tn_kernel(TnGroup grp) {
     const int64_t q0 = (int64_t)by * ST;
     const int64_t mbeg = (int64_t)bz * mchunk;
     const int64_t mend = (mbeg + mchunk < M) ? mbeg + mchunk : M;
-    const int nsteps = mend > mbeg ? (int)((mend - mbeg + ST - 1) / ST) : 0;
-    const __amdgpu_buffer_rsrc_t rU = make_rsrc(U, M * Pn * 2);
-    const __amdgpu_buffer_rsrc_t rV = make_rsrc(V, M * Qn * 2);
+    const int64_t rows = mend > mbeg ? mend - mbeg : 0;
+    const int nsteps = (int)((rows + ST - 1) / ST);
+    // descriptors of this chunk of rows alone: T and dT, [M, r], may pass 2 GiB where X and dY do not (then
+    // N and K are below 128, the rows are split 64 ways, and a chunk stays below 2^27 bytes)
+    const __amdgpu_buffer_rsrc_t rU = make_rsrc(U + mbeg * Pn, rows * Pn * 2);
+    const __amdgpu_buffer_rsrc_t rV = make_rsrc(V + mbeg * Qn, rows * Qn * 2);
     const int trow = tid >> 3, tch = tid & 7;
     const bool pok = p0 + tch * 8 < Pn, qok = q0 + tch * 8 < Qn;
 
     const bool lo = LO && pr.Vlo;
-    const __amdgpu_buffer_rsrc_t rL = make_rsrc(lo ? pr.Vlo : V, lo ? M * Qn * 2 : 0);
+    const __amdgpu_buffer_rsrc_t rL = make_rsrc((lo ? pr.Vlo : V) + mbeg * Qn, lo ? rows * Qn * 2 : 0);
     auto load = [&](int step, TileLoad &a, TileLoad &b, TileLoad &c) {
-        const int64_t mm = mbeg + (int64_t)step * ST;
-        const bool live = step < nsteps;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t gm = mm + trow + 32 * h;
-            const bool ok = live && gm < mend;
+            const int64_t gm = (int64_t)step * ST + trow + 32 * h;      // row of the chunk
+            const bool ok = gm < rows;
             a.v[h] = bload16(rU, (ok && pok) ? (uint32_t)((gm * Pn + p0 + tch * 8) * 2) : 0xFFFFFFF0u);
             b.v[h] = bload16(rV, (ok && qok) ? (uint32_t)((gm * Qn + q0 + tch * 8) * 2) : 0xFFFFFFF0u);
             if (LO) c.v[h] = bload16(rL, (ok && qok && lo) ? (uint32_t)((gm * Qn + q0 + tch * 8) * 2) : 0xFFFFFFF0u);

@@ -359,7 +359,7 @@ int nf4_int8_dequant(const nf4_int8_weight *w, uint16_t *out_bf16, void *stream)
  *   L1: [K, r] bf16, L2: [r, N] bf16, r a multiple of 8 in [8, 128]; or r = 0 without an adapter
  *         (L1, L2, T_out NULL; X may then be NULL where Xq is given).
  *   Y: [M, N] bf16.  T_out: optional [M, r] bf16 (unscaled), as qlora_linear_fwd's.
- *   scale: s, finite.  M >= 1.  Each operand below 2 GiB, as in qlora_linear_fwd.
+ *   scale: s, finite.  M >= 1.  X, Y and the codes are each below 2 GiB; T may be larger.
  *   workspace: >= qlora_int8_linear_workspace_size(M, N, K, r) bytes (forward and backward), 16-byte
  *         aligned; calls that may overlap need a workspace each.
  * s T enters its product with L2 as two bf16 halves (16 significant bits), and Y is rounded to bf16 once; the

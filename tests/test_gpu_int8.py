@@ -9,6 +9,8 @@ Tolerances, from the roundings on the way (u = 2^-24, a float32 step's half; h =
      dT's bf16 rounding, h of the adapter's products; likewise dL2 (a sum over the tokens), and dL1,
      which takes dT in two bf16 halves, h^2.
 """
+import types
+
 import numpy as np
 import pytest
 
@@ -559,3 +561,40 @@ def test_linear_backward_adapter_alone(M, N, K, r, route, split):
     acc, _, _ = nf4.qlora_int8_linear_bwd(w, dY, X, L1, L2, T, s, dX=base, accumulate=True)
     ref, tol = ref + bv, tol + 2 * U * np.abs(bv)
     within("dX accumulated", acc, ref, H * (np.abs(ref) + tol) + tol)
+
+
+@pytest.mark.parametrize("int8", [True, False])
+def test_linear_backward_with_more_than_2_gib_of_T(int8):
+    """T's limit is not X's: 128 columns against X's 64, so T passes 2 GiB while X and dY stay below.  All rows
+    are zero but the first and the last ones, so that the sums over the tokens have 27 terms."""
+    M, N, K, r, s = (1 << 23) + 24, 64, 64, 128, 0.5
+    W = dev(synth.normal_f32(5200, (N, K), 0.05))
+    w = nf4.Int8Weight.from_float(W) if int8 else nf4.NF4Weight.from_float(W)
+    L1, l1 = bf16(synth.normal_f32(5201, (K, r), 0.1))
+    L2, l2 = bf16(synth.normal_f32(5202, (r, N), 0.1))
+    live = torch.cat([torch.arange(3), torch.arange(M - 24, M)]).to(DEV)
+
+    def rows(seed, cols):
+        full = torch.zeros((M, cols), dtype=torch.bfloat16, device=DEV)
+        full[live], v = bf16(synth.normal_f32(seed, (27, cols), 1.0))
+        return full, v
+
+    X, x = rows(5203, K)
+    dY, dy = rows(5204, N)
+    T, t = rows(5205, r)
+    if int8:
+        lin = types.SimpleNamespace(l1=l1, l2=l2, Wq=w.codes.cpu().numpy(), ws=w.scales.cpu().numpy())
+        Y, T_out = nf4.qlora_int8_linear_fwd(w, X, L1, L2, s)
+        check_fwd(lin, X[live], s, Y[live], T_out[live])
+        del Y, T_out
+    bwd = nf4.qlora_int8_linear_bwd if int8 else nf4.qlora_linear_bwd
+    _, dL1, dL2 = bwd(w, dY, X, L1, L2, T, s, need_dX=False)
+    dt = s * (dy @ l2.T)
+    # dT's own rounding: two bf16 halves (h^2) in the Int8 layer, one (h) in the other
+    rest = (H * H if int8 else H) * np.abs(dt) + 1.01 * (N + 70) * U * s * (np.abs(dy) @ np.abs(l2.T))
+    ref = x.T @ dt
+    tol = np.abs(x).T @ rest + 1.01 * (2 * 27 + 70) * U * (np.abs(x).T @ np.abs(dt))
+    within("dL1", dL1, ref, H * (np.abs(ref) + tol) + tol)
+    ref = s * (t.T @ dy)
+    tol = 1.01 * (27 + 70) * U * s * (np.abs(t).T @ np.abs(dy))
+    within("dL2", dL2, ref, H * (np.abs(ref) + tol) + tol)
