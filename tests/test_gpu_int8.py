@@ -598,3 +598,22 @@ def test_linear_backward_with_more_than_2_gib_of_T(int8):
     ref = s * (t.T @ dy)
     tol = 1.01 * (27 + 70) * U * s * (np.abs(t).T @ np.abs(dy))
     within("dL2", dL2, ref, H * (np.abs(ref) + tol) + tol)
+
+
+@pytest.mark.parametrize("M,N,K,route,split", [
+    (37, 1032, 576, "convert", 3), (200, 520, 4096, "convert", 2), (37, 264, 1472, "convert", 1),
+    (300, 200, 3136, "convert", 1), (300, 520, 320, "expand", 2), (1100, 264, 448, "expand", 1)])
+def test_linear_backward_with_the_largest_constants_on_every_route(M, N, K, route, split):
+    """Constants next to FLT_MAX / 127 through both products and their splits: 128 constants, or a code turned
+    to an unsigned byte times its constant, do not fit float32; the weight's values do."""
+    assert plan(M, N, K) == (route, split)
+    codes = np.random.default_rng(32).integers(-127, 128, (N, K)).astype(np.int8)
+    scales = np.linspace(2.6e36, 2.66e36, N).astype(np.float32)
+    w = nf4.Int8Weight(dev(codes), dev(scales))
+    Wb = oracle.bf16_to_f32(oracle.int8_weight_bf16(codes, scales)).astype(np.float64)
+    assert np.isfinite(Wb).all()
+    dY, dy = bf16(synth.normal_f32(5300 + M, (M, N), 1e-10))
+    dX, _, _ = nf4.qlora_int8_linear_bwd(w, dY)
+    ref = dy @ Wb
+    tol = 1.01 * (N + 16) * U * (np.abs(dy) @ np.abs(Wb))
+    within("dX", dX, ref, H * (np.abs(ref) + tol) + tol)
