@@ -617,3 +617,61 @@ def test_linear_backward_with_the_largest_constants_on_every_route(M, N, K, rout
     ref = dy @ Wb
     tol = 1.01 * (N + 16) * U * (np.abs(dy) @ np.abs(Wb))
     within("dX", dX, ref, H * (np.abs(ref) + tol) + tol)
+
+
+def guarded(shape, guard, value=7.0):
+    """(buffer, view): the view lies between `guard` rows of one value on each side."""
+    buf = torch.full((shape[0] + 2 * guard, shape[1]), value, dtype=torch.bfloat16, device=DEV)
+    return buf, buf[guard:guard + shape[0]]
+
+
+def untouched(buf, guard, value=7.0):
+    return bool((buf[:guard] == value).all()) and bool((buf[-guard:] == value).all())
+
+
+# Both converting tiles with the reduction unsplit (stores to dX itself) and split, and the expanded product; M
+# ragged against the tile's rows, K against its 256 columns, ranks of none, one and two adapter steps.
+@pytest.mark.parametrize("M,N,K,r,route,split", [
+    (37, 264, 1472, 0, "convert", 1), (37, 264, 2112, 72, "convert", 1), (64, 264, 1472, 8, "convert", 1),
+    (130, 328, 1984, 0, "convert", 1), (300, 200, 3136, 128, "convert", 1), (600, 392, 1600, 24, "convert", 1),
+    (37, 1032, 576, 16, "convert", 3), (200, 520, 4096, 72, "convert", 2), (300, 520, 320, 16, "expand", 2),
+    (1100, 264, 448, 72, "expand", 1), (1100, 520, 448, 0, "expand", 2)])
+def test_linear_backward_writes_its_outputs_and_nothing_else(M, N, K, r, route, split):
+    """dX, dL1 and dL2 inside larger buffers, with 256 rows (a tile's) of a value on each side; dX written, then
+    added to.  Tolerances as in test_linear_backward, with dT in two halves."""
+    print(f"int8 backward in guarded buffers M={M} N={N} K={K} r={r}", flush=True)
+    assert plan(M, N, K) == (route, split)
+    lin = Lin(5400 + M + N, N, K, r)
+    Wb = oracle.bf16_to_f32(oracle.int8_weight_bf16(lin.Wq, lin.ws)).astype(np.float64)
+    dY, dy = bf16(synth.normal_f32(5401 + M, (M, N), 1.0))
+    bX, dX = guarded((M, K), 256)
+    start = synth.normal_f32(5402 + M, (M, K), 2.0)
+    ref, size, inner, s = dy @ Wb, np.abs(dy) @ np.abs(Wb), 0.0, 0.5
+    args, kw = (), {}
+    if r:
+        X, x = bf16(synth.normal_f32(5403 + M, (M, K), 1.0))
+        T, t = bf16(x @ lin.l1)
+        b1, dL1 = guarded((K, r), 256)
+        b2, dL2 = guarded((r, N), 256)
+        args, kw = (X, lin.L1, lin.L2, T, s), dict(dL1=dL1, dL2=dL2)
+        dt = s * (dy @ lin.l2.T)
+        rest = H * H * np.abs(dt) + 1.01 * (N + 70) * U * s * (np.abs(dy) @ np.abs(lin.l2.T))
+        ref, size, inner = ref + dt @ lin.l1.T, size + np.abs(dt) @ np.abs(lin.l1.T), rest @ np.abs(lin.l1.T)
+    for accumulate in (False, True):
+        base = np.zeros((M, K))
+        if accumulate:
+            v, base = bf16(start)
+            dX.copy_(v)
+        got = nf4.qlora_int8_linear_bwd(lin.w, dY, *args, dX=dX, accumulate=accumulate, **kw)
+        assert got[0] is dX
+        tol = 1.01 * (N + 2 * r + 17) * U * (size + np.abs(base)) + inner
+        within("dX", dX, ref + base, H * (np.abs(ref + base) + tol) + tol)
+        assert untouched(bX, 256)
+        if r:
+            want = x.T @ dt
+            tol = np.abs(x).T @ rest + 1.01 * (2 * M + 70) * U * (np.abs(x).T @ np.abs(dt))
+            within("dL1", dL1, want, H * (np.abs(want) + tol) + tol)
+            want = s * (t.T @ dy)
+            tol = 1.01 * (M + 70) * U * s * (np.abs(t).T @ np.abs(dy))
+            within("dL2", dL2, want, H * (np.abs(want) + tol) + tol)
+            assert untouched(b1, 256) and untouched(b2, 256)
