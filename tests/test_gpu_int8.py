@@ -675,3 +675,23 @@ def test_linear_backward_writes_its_outputs_and_nothing_else(M, N, K, r, route, 
             tol = 1.01 * (M + 70) * U * s * (np.abs(t).T @ np.abs(dy))
             within("dL2", dL2, want, H * (np.abs(want) + tol) + tol)
             assert untouched(b1, 256) and untouched(b2, 256)
+
+
+# The GEMV's forms of wide weights (from 8192 rows: 4 waves, or 8 with 32 rows; from 16384: 4 waves with 32
+# rows), with an adapter; and T's partials past 64 MiB in all workgroups together, where T is summed by a
+# launch of its own.
+@pytest.mark.parametrize("M,N,K,r", [(3, 8200, 320, 8), (3, 8200, 64, 128), (9, 8200, 320, 24), (16, 16392, 128, 40),
+                                     (20, 8200, 320, 16), (32, 16392, 192, 128), (40, 8200, 320, 72), (64, 8200, 576, 8),
+                                     (50, 16392, 192, 8), (64, 16392, 64, 64), (64, 8200, 2048, 128), (16, 28680, 2112, 128)])
+def test_linear_forward_few_tokens_wide_weights(M, N, K, r):
+    print(f"int8 forward, wide M={M} N={N} K={K} r={r}", flush=True)
+    lin = Lin(5500 + M + K, N, K, r)
+    X, _ = bf16(synth.heavy_tail_f32(5501 + M, 5502 + K, (M, K), 1.0, 20.0, 0.01))
+    by, Y = guarded((M, N), 64)
+    bt, T = guarded((M, r), 64)
+    nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, Y=Y, T=T)
+    check_fwd(lin, X, 0.5, Y, T)
+    assert untouched(by, 64) and untouched(bt, 64)
+    # the same rows through all of it again, without T
+    Y2, none = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, keep_T=False)
+    assert none is None and same(Y2, Y)
