@@ -695,3 +695,33 @@ def test_linear_forward_few_tokens_wide_weights(M, N, K, r):
     # the same rows through all of it again, without T
     Y2, none = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, keep_T=False)
     assert none is None and same(Y2, Y)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1, 72, 128, 8), (5, 264, 512, 0), (13, 72, 128, 8), (33, 264, 576, 72), (70, 264, 192, 16),
+                                     (129, 520, 128, 72), (257, 520, 128, 8), (300, 776, 320, 0), (65, 72, 4096, 8),
+                                     (257, 264, 2048, 128), (1041, 4104, 1024, 24)])
+def test_linear_forward_leaves_a_tile_around_its_outputs_alone(M, N, K, r):
+    """256 rows on each side, as many as a tile of the product has: rows of a tile past M are not written."""
+    lin = Lin(5600 + M, N, K, r)
+    X, _ = bf16(synth.normal_f32(5601 + M, (M, K), 1.0))
+    by, Y = guarded((M, N), 256)
+    bt, T = guarded((M, r), 256) if r else (None, None)
+    nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, Y=Y, T=T)
+    check_fwd(lin, X, 0.5, Y, T)
+    assert untouched(by, 256) and (not r or untouched(bt, 256))
+
+
+@pytest.mark.parametrize("M,N,K,r", [(3, 72, 128, 8), (40, 264, 576, 128), (65, 72, 4096, 8), (200, 520, 4096, 72), (257, 520, 320, 16),
+                                     (300, 520, 320, 128), (1100, 264, 448, 72)])
+def test_linear_stays_inside_its_workspace(M, N, K, r):
+    lin = Lin(5700 + M, N, K, r)
+    X, _ = bf16(synth.normal_f32(5701 + M, (M, K), 1.0))
+    dY, _ = bf16(synth.normal_f32(5702 + M, (M, N), 1.0))
+    n, guard = nf4.qlora_int8_linear_workspace_size(M, N, K, r), 4 << 20
+    buf = torch.full((n + 2 * guard,), 0x5A, dtype=torch.uint8, device=DEV)
+    ws = buf[guard:guard + n]
+    Y, T = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5, workspace=ws)
+    nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, T, 0.5, workspace=ws)
+    nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, None, 0.5, workspace=ws)
+    check_fwd(lin, X, 0.5, Y, T)
+    assert (buf[:guard] == 0x5A).all() and (buf[guard + n:] == 0x5A).all()
