@@ -725,3 +725,41 @@ def test_linear_stays_inside_its_workspace(M, N, K, r):
     nf4.qlora_int8_linear_bwd(lin.w, dY, X, lin.L1, lin.L2, None, 0.5, workspace=ws)
     check_fwd(lin, X, 0.5, Y, T)
     assert (buf[:guard] == 0x5A).all() and (buf[guard + n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("M,N,K,r,route", [(37, 264, 1472, 72, "convert"), (200, 520, 4096, 16, "convert"), (300, 520, 320, 8, "expand"),
+                                           (1100, 264, 448, 0, "expand")])
+def test_linear_backward_rows_that_are_not_finite(M, N, K, r, route):
+    """A token with a NaN or an infinity in dY, or in X, leaves the other tokens' dX as they are."""
+    assert plan(M, N, K)[0] == route
+    lin = Lin(5800 + M, N, K, r)
+    dY, _ = bf16(synth.normal_f32(5801, (M, N), 1.0))
+    X, x = bf16(synth.normal_f32(5802, (M, K), 1.0))
+    args = (X, lin.L1, lin.L2, bf16(x @ lin.l1)[0], 0.5) if r else ()
+    clean = nf4.qlora_int8_linear_bwd(lin.w, dY, *args)[0]
+    dY[3, 5] = float("nan")
+    dY[M - 1, N - 1] = float("-inf")
+    if r:
+        X[4, 7] = float("inf")
+    got = nf4.qlora_int8_linear_bwd(lin.w, dY, *args)[0]
+    assert torch.isnan(got[3]).all() and not torch.isfinite(got[M - 1]).any()
+    keep = [m for m in range(M) if m not in (3, M - 1)]
+    assert same(got[keep], clean[keep])
+
+
+def test_linear_forward_channels_that_are_not_finite():
+    """A weight row with constant NaN (nf4_int8_quantize's for a row that is not finite), or an infinity in a
+    column of L2, concerns its own output channel."""
+    N, K, r = 264, 512, 8
+    lin = Lin(5900, N, K, r)
+    scales, L2 = lin.w.scales.clone(), lin.L2.clone()
+    scales[17] = float("nan")
+    L2[3, 100] = float("inf")
+    bad = nf4.Int8Weight(lin.w.codes, scales)
+    for M in (1, 7, 20, 40, 70, 300):
+        X, _ = bf16(synth.normal_f32(5901 + M, (M, K), 1.0))
+        Y, _ = nf4.qlora_int8_linear_fwd(lin.w, X, lin.L1, lin.L2, 0.5)
+        got, _ = nf4.qlora_int8_linear_fwd(bad, X, lin.L1, L2, 0.5)
+        assert torch.isnan(got[:, 17]).all() and not torch.isfinite(got[:, 100]).any(), M
+        keep = [n for n in range(N) if n not in (17, 100)]
+        assert same(got[:, keep], Y[:, keep]), M
