@@ -1028,6 +1028,8 @@ constexpr size_t kInt8TSumBytes = (size_t)64 << 20;
 // Measured with r = 64 (expanding / converting, the whole call): 333 x 11008 x 4096 99 / 69, 768 x 4096 x
 // 11008 122 / 157 (258 tiles of 128 rows on 256 CUs), 1024 x 4096 x 4096 84 / 70, 1500 x 11008 x 4096
 // 187 / 201, 2048 x 22016 x 8192 764 / 820, 4096 x 4096 x 4096 154 / 185.
+// Launches are not counted: without an adapter the expansion is one more (about 4 us; with one it carries
+// dT's sum), which small shapes, whose two estimates differ by tenths of a us, may pay.
 bool int8_expands(int64_t M, int64_t N, int64_t K) {
     const int64_t steps = (N + kTile - 1) / kTile, ntn = (K + kGemmTile - 1) / kGemmTile;
     auto rounds = [](int64_t wgs) { return (double)((wgs + 255) / 256); };

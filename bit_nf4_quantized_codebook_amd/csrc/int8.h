@@ -205,7 +205,10 @@ __device__ __forceinline__ void int8_row_regs(const void *__restrict__ x, int64_
     });
 }
 
-// Longer rows: one workgroup of 256 threads, the row read twice (the second time from L2).
+// Longer rows: one workgroup of 256 threads, the row read twice.  The rows in flight are larger than the L2s
+// (five workgroups a CU with 88 KB each, in float32 at 22016 columns), so the second read comes from the
+// memory-side cache at best: 8192 x 22016 241 us in float32 and 143 in bf16, 3.7 TB/s of the bytes counted
+// once (5.6 up to 16384 columns).
 template <bool F32>
 __device__ __forceinline__ void int8_row_loop(const void *__restrict__ x, int64_t row, int64_t cols,
                                               int8_t *__restrict__ codes, float *__restrict__ scales) {

@@ -20,14 +20,16 @@
 // fragments read again for each, the second halves cost 3.3 us at 4096 x 4096 x 4096, r = 64; as it is,
 // 0.5.)
 //
-// Bound by the MFMA loop at the clock its power allows: 62.5 us at 4096 x 4096 x 4096 with r = 64 (2.2
-// POPS; a library int8 product of 8192 x 8192 x 8192 reaches 2.33 here) and 325 us at 2048 tokens x 22016 x
-// 8192 (2.3 POPS).  The whole forward call (codes of X, T, this product) takes 84 and 346 us; a 64 x 64
+// Bound by the MFMA loop at the clock its power allows: 63 us at 4096 x 4096 x 4096 with r = 64 (2.2
+// POPS; a library int8 product of 8192 x 8192 x 8192 reaches 2.33 here) and 331 us at 2048 tokens x 22016 x
+// 8192 (2.2 POPS).  The whole forward call (codes of X, T, this product) takes 82 and 345 us; a 64 x 64
 // tile with one LDS stage took 420 and 1667 us.
 //
-// Few output tiles (fewer than half the CUs): the reduction is split over up to 16 workgroups per
+// Few output tiles (at most half the CUs): the reduction is split over up to 16 workgroups per
 // tile, each writing its int32 sums; a second launch adds them, still exact, and has the epilogue.  So
-// without an adapter a token's Y is the same bits whatever the batch it comes in.
+// without an adapter a token's Y is the same bits whatever the batch it comes in.  The price is the
+// partials' way through memory and, below 256 tokens, a tile that is mostly padding: with r = 64 and a weight of
+// 4096 x 4096, 65 tokens take 29 us, 300 34, 1024 51 and 2048 71 (floors 4, 5, 15 and 31).
 
 #include "common.h"
 #include "dqtile.h"

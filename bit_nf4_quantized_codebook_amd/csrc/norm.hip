@@ -10,8 +10,9 @@
 // which a second launch sums in a fixed order.
 //
 // Measured (bytes read and written once, against a large copy's 5.2 TB/s): forward 39 us at 4096 x 4096 with
-// a float32 residual (201 MB, 5.1 TB/s); backward 51 us at 4096 x 4096 bf16 (201 MB; 43 the rows, 6 the sum)
-// and 35 us at 1001 x 8192 float32 (148 MB).
+// a float32 residual (201 MB, 5.1 TB/s); backward 52 us at 4096 x 4096 bf16 (201 MB; 44 the rows, 6 the sum)
+// and 35 us at 1001 x 8192 float32 (148 MB).  Above 8192 columns a thread holds four pieces and no row ahead:
+// 2048 x 16384 116 us in bf16 (403 MB, 3.5 TB/s).
 
 #include "common.h"
 #include "int8.h"
@@ -440,9 +441,13 @@ __global__ __launch_bounds__(256) void norm_sum_kernel(NormArgs g, NormRuns q, i
     }
 }
 
-// Runs aimed at: as many workgroups as the CUs hold at once (eight waves with two or more pieces per
-// thread, sixteen with one), but no fewer than eight rows each beyond the first 256, so that the
-// partials stay a small part of the traffic.
+// Runs aimed at: what the CUs hold at once in bf16 (eight waves with two or more pieces per thread, sixteen
+// with one), but no fewer than eight rows each beyond the first 256, so that the partials stay a small
+// part of the traffic.  Two things pass that count and cost a second round of workgroups:
+//   - the float32 kernels with one piece take 130 to 136 registers, so that a CU holds twelve of their
+//     waves: 8192 x 2048 74 us, against 51 in bf16 (302 and 201 MB);
+//   - norm_runs cuts each gate row by itself: at 4096 x 4096 bf16, 512 tokens per gate row give 512 runs and
+//     52 us, 500 give 567 and 71 us, 10 give 820 and 70 us.
 int64_t norm_target(int64_t M, int64_t C) {
     const int64_t per_cu = C <= 512 ? 16 : (C <= 1024 ? 8 : (C <= 2048 ? 4 : (C <= 4096 ? 2 : 1)));
     const int64_t most = M / 8 > 256 ? M / 8 : 256;
