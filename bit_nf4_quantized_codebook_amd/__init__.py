@@ -10,7 +10,7 @@ Names follow the C ABI:
   nf4_double_quant, nf4_double_quant_int8, nf4_dequant, nf4_dequant_single, qlora_linear_fwd,
   qlora_linear_fwd_static, qlora_linear_bwd, qlora_swiglu_fwd, qlora_swiglu_bwd, qlora_gated_fwd, qlora_gated_bwd,
   qlora_multi_fwd, nf4_int8_quantize, nf4_int8_dequant, qlora_int8_linear_fwd, qlora_int8_linear_bwd,
-  qlora_norm_fwd, qlora_norm_bwd.
+  qlora_norm_fwd, qlora_norm_bwd, qlora_loss_fwd, qlora_loss_grad, qlora_clip_grads.
 """
 from __future__ import annotations
 
@@ -39,6 +39,7 @@ EXPORTS = (
     "qlora_multi_workspace_size", "qlora_multi_fwd",
     "nf4_int8_quantize", "nf4_int8_dequant", "qlora_int8_linear_workspace_size", "qlora_int8_linear_fwd",
     "qlora_int8_linear_bwd", "qlora_norm_fwd", "qlora_norm_workspace_size", "qlora_norm_bwd",
+    "qlora_loss_workspace_size", "qlora_loss_fwd", "qlora_loss_grad", "qlora_clip_workspace_size", "qlora_clip_grads",
     "nf4_set_gemm_timing_events", "nf4_gemm_timing_count",
 )
 
@@ -84,6 +85,15 @@ class _NormDesc(ctypes.Structure):
         ("beta", ctypes.c_float),
         ("eps", ctypes.c_float),
         ("resid_type", ctypes.c_int32),
+    ]
+
+
+class _GradDesc(ctypes.Structure):
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("numel", ctypes.c_int64),
+        ("type", ctypes.c_int32),
     ]
 
 
@@ -137,6 +147,11 @@ def _load():
         "qlora_norm_fwd": (i, [D, P, P, i64, P, P, P, P, P]),
         "qlora_norm_workspace_size": (sz, [i64, i64]),
         "qlora_norm_bwd": (i, [D, P, P, P, P, i64, P, P, P, P, P, P, sz, P]),
+        "qlora_loss_workspace_size": (sz, [i64, i64, i64, i32]),
+        "qlora_loss_fwd": (i, [P, i64, P, P, i64, i64, P, P, P, sz, P]),
+        "qlora_loss_grad": (i, [P, i64, P, P, P, i64, i64, P, P, P, P, sz, P]),
+        "qlora_clip_workspace_size": (sz, [i32]),
+        "qlora_clip_grads": (i, [P, i32, ctypes.c_float, P, P, sz, P]),
         "nf4_set_gemm_timing_events": (i, [P, P, P, i32]),
         "nf4_gemm_timing_count": (i32, []),
     }
@@ -816,6 +831,108 @@ def qlora_norm_bwd(norm: QLoRANorm, R_out, B=None, dR_out=None, dH=None, need_we
             _at(dH), M, dR.data_ptr(), _at(dB), _at(grads.get("dw_pre")), _at(grads.get("dw_post")),
             _at(grads.get("dgate")), ws.data_ptr(), wsb)
     return dR, dB, grads
+
+
+# ------------------------------------------------------------------------------------------
+# The loss over the vocabulary, and the clipping of gradients
+# ------------------------------------------------------------------------------------------
+
+def qlora_loss_workspace_size(M: int, V: int, K: int, grad: bool) -> int:
+    return int(lib.qlora_loss_workspace_size(M, V, K, int(grad)))
+
+
+def _loss_args(W, X, labels):
+    """Checks the head, the tokens and their labels against each other; returns (M, V, K)."""
+    torch = _torch()
+    bf16 = torch.bfloat16
+    _need(X, bf16, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be [M, K]")
+    M, K = X.shape
+    _need(W, bf16, "W")
+    V = W.shape[0]
+    _expect(W, bf16, (V, K), X.device, "W")
+    _expect(labels, torch.int64, (M,), X.device, "labels")
+    return M, V, K
+
+
+def qlora_loss_fwd(W, X, labels, loss=None, mean=None, workspace=None):
+    """Softmax cross entropy of the output head, logits X W^T: W bf16 [V, K], X bf16 [M, K], labels int64 [M]
+    (negative: no label).  Returns (loss float32 [M], mean float32 [1] over the tokens with a label)."""
+    torch = _torch()
+    M, V, K = _loss_args(W, X, labels)
+    f32, dev = torch.float32, X.device
+    loss, mean = _out(loss, f32, (M,), dev, "loss"), _out(mean, f32, (1,), dev, "mean")
+    wsb = lib.qlora_loss_workspace_size(M, V, K, 0)
+    ws = _scratch(wsb, dev, workspace)
+    _launch(lib.qlora_loss_fwd, "qlora_loss_fwd", dev, W.data_ptr(), V, X.data_ptr(), labels.data_ptr(), M, K,
+            loss.data_ptr(), mean.data_ptr(), ws.data_ptr(), wsb)
+    return loss, mean
+
+
+def qlora_loss_grad(W, X, labels, dloss=None, loss=None, mean=None, dX=None, workspace=None):
+    """qlora_loss_fwd with the gradient for X (W is frozen), in one pass over the vocabulary: dloss float32 [M],
+    the gradient of each token's loss, or None: of the mean.  Returns (loss, mean, dX bf16 [M, K])."""
+    torch = _torch()
+    M, V, K = _loss_args(W, X, labels)
+    f32, dev = torch.float32, X.device
+    if dloss is not None:
+        _expect(dloss, f32, (M,), dev, "dloss")
+    loss, mean = _out(loss, f32, (M,), dev, "loss"), _out(mean, f32, (1,), dev, "mean")
+    dX = _out(dX, torch.bfloat16, (M, K), dev, "dX")
+    wsb = lib.qlora_loss_workspace_size(M, V, K, 1)
+    ws = _scratch(wsb, dev, workspace)
+    _launch(lib.qlora_loss_grad, "qlora_loss_grad", dev, W.data_ptr(), V, X.data_ptr(), labels.data_ptr(), _at(dloss), M, K,
+            loss.data_ptr(), mean.data_ptr(), dX.data_ptr(), ws.data_ptr(), wsb)
+    return loss, mean, dX
+
+
+class QLoRAGrads:
+    """A list of gradient tensors (bf16 or float32, contiguous, on one device) for qlora_clip_grads, with where the
+    scaled ones go: the tensors themselves, or outs, of the same shapes and types.  Checked once; it keeps the
+    tensors, whose contents may change between calls."""
+
+    def __init__(self, grads, outs=None):
+        torch = _torch()
+        grads = tuple(grads)
+        outs = grads if outs is None else tuple(outs)
+        if not grads:
+            raise ValueError("the list of gradients is empty")
+        if len(outs) != len(grads):
+            raise ValueError("outs must have as many tensors as grads")
+        _need(grads[0], torch.float32 if getattr(grads[0], "dtype", None) == torch.float32 else torch.bfloat16, "grads[0]")
+        self._device = grads[0].device
+        self._list = (_GradDesc * len(grads))()
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            f32 = getattr(g, "dtype", None) == torch.float32
+            _expect(g, torch.float32 if f32 else torch.bfloat16, g.shape, self._device, f"grads[{i}]")
+            _expect(o, g.dtype, g.shape, self._device, f"outs[{i}]")
+            self._list[i] = _GradDesc(g.data_ptr(), o.data_ptr(), g.numel(), int(f32))
+        self._grads, self._outs = grads, outs
+
+    grads = property(lambda self: self._grads)
+    outs = property(lambda self: self._outs)
+    device = property(lambda self: self._device)
+
+    def __len__(self):
+        return len(self._grads)
+
+
+def qlora_clip_workspace_size(n: int) -> int:
+    return int(lib.qlora_clip_workspace_size(n))
+
+
+def qlora_clip_grads(grads: QLoRAGrads, max_norm: float, norm=None, workspace=None):
+    """Scales all gradients by max_norm / norm where their global norm exceeds max_norm (a norm that is not finite
+    leaves them as they are).  Returns the norm before, float32 [1] on the device."""
+    torch = _torch()
+    dev, n = grads.device, len(grads)
+    norm = _out(norm, torch.float32, (1,), dev, "norm")
+    wsb = lib.qlora_clip_workspace_size(n)
+    ws = _scratch(wsb, dev, workspace)
+    _launch(lib.qlora_clip_grads, "qlora_clip_grads", dev, ctypes.addressof(grads._list), n, max_norm, norm.data_ptr(),
+            ws.data_ptr(), wsb)
+    return norm
 
 
 class GemmTimer:

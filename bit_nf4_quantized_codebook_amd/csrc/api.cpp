@@ -9,7 +9,9 @@
 #include <mutex>
 
 #include "../../include/nf4.h"
+#include "clip.h"
 #include "launch.h"
+#include "loss.h"
 
 // ---------------------------------------------------------------------------------------------
 // Static scratch of the forward entry point that allocates nothing (qlora_linear_fwd_static).
@@ -1392,5 +1394,182 @@ int qlora_norm_bwd(const qlora_norm *p, const void *R_out, const uint16_t *B, co
     a.dw_pre = dw_pre; a.dw_post = dw_post; a.dgate = dgate;
     a.P = ws_at<float>(workspace, 0);
     NF4_CHECK_HIP(nf4k::launch_norm_bwd(a, reinterpret_cast<hipStream_t>(stream)), "norm bwd");
+    return NF4_OK;
+}
+
+// ---------------------------------------------------------------------------------------------
+// The loss over the vocabulary and the clipping of gradients
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+// p of one piece of the vocabulary (bf16) stays within this, but a piece has at least kLossMinTiles tiles
+constexpr size_t kLossPieceBytes = (size_t)512 << 20;
+constexpr size_t kLossTableBytes = (size_t)64 << 20;     // the forward's piece: its tiles' references and sums
+constexpr int64_t kLossMinTiles = 32;
+
+struct LossPlan {
+    int32_t Mp, tiles, piece;          // rows padded to tiles; tiles of the vocabulary, and of a piece
+    int32_t first;                     // gradient: tiles of the first span, from which the references come
+    size_t off_count, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[3], off_tref, off_tsum, off_P, off_part,
+        off_sum32, total;
+};
+
+LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
+    LossPlan p;
+    const int64_t LT = nf4k::LT, ntm = (M + LT - 1) / LT, ntn = (K + LT - 1) / LT;
+    p.Mp = (int32_t)(ntm * LT);
+    p.tiles = (int32_t)((V + LT - 1) / LT);
+    int64_t piece = grad ? (int64_t)(kLossPieceBytes / ((size_t)p.Mp * LT * 2)) : (int64_t)(kLossTableBytes / ((size_t)p.Mp * 8));
+    if (piece < kLossMinTiles) piece = kLossMinTiles;
+    // the product's offsets into a piece of W stay below 2 GiB
+    const int64_t most = ((int64_t)1 << 22) / K;
+    if (grad && piece > most) piece = most;
+    p.piece = (int32_t)(piece < p.tiles ? piece : p.tiles);
+    // one round of the chip; a rest of less than two rounds is not worth a launch of its own
+    const int64_t first = ntm < 256 ? 256 / ntm : 1;
+    p.first = (int32_t)(p.piece >= 3 * first ? first : p.piece);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round256(bytes);
+        return at;
+    };
+    p.off_count = take(8);
+    p.off_row = take((size_t)p.Mp * 4);
+    p.off_label = take((size_t)p.Mp * 4);
+    p.off_zl = take((size_t)p.Mp * 4);
+    p.off_S = take((size_t)p.Mp * 4);
+    p.off_a = take((size_t)p.Mp * 4);
+    p.off_b = take((size_t)p.Mp * 4);
+    for (size_t &c : p.off_c) c = take((size_t)p.Mp * 4);
+    p.off_tref = take((size_t)p.piece * p.Mp * 4);
+    p.off_tsum = take((size_t)p.piece * p.Mp * 4);
+    p.off_P = take(grad ? (size_t)p.piece * p.Mp * LT * 2 : 0);
+    const int64_t parts = ntm * ntn > 256 ? ntm * ntn : 256;
+    p.off_part = take(grad ? (size_t)parts * LT * LT * 4 : 0);
+    p.off_sum32 = take(grad && p.piece < p.tiles ? (size_t)p.Mp * K * 4 : 0);
+    p.total = off;
+    return p;
+}
+
+constexpr int64_t kLossMaxM = (int64_t)1 << 20, kLossMaxV = (int64_t)1 << 24, kLossMaxK = 16384;
+
+int check_loss_sizes(int64_t M, int64_t V, int64_t K) {
+    if (M < 1 || V < 1) return fail(NF4_ERR_SHAPE, "M and V must be >= 1");
+    if (K < 64) return fail(NF4_ERR_SHAPE, "K must be >= 64");
+    if (K % 64) return fail(NF4_ERR_UNSUPPORTED, "K must be a multiple of 64");
+    if (K > kLossMaxK) return fail(NF4_ERR_UNSUPPORTED, "K must be at most 16384");
+    if (M > kLossMaxM) return fail(NF4_ERR_UNSUPPORTED, "M must be at most 2^20");
+    if (V > kLossMaxV) return fail(NF4_ERR_UNSUPPORTED, "V must be at most 2^24");
+    if (M * K * 2 >= (int64_t)1 << 31) return fail(NF4_ERR_UNSUPPORTED, "X exceeds 2 GiB");
+    return NF4_OK;
+}
+
+int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *labels, const float *dloss, int64_t M, int64_t K,
+             float *loss, float *mean, uint16_t *dX, bool grad, void *workspace, size_t workspace_bytes, void *stream) {
+    const int rc = check_loss_sizes(M, V, K);
+    if (rc) return rc;
+    if (!W || !X || !labels || !loss || !mean) return fail(NF4_ERR_NULL, "W, X, labels, loss and mean must be non-NULL");
+    if (grad && !dX) return fail(NF4_ERR_NULL, "dX must be non-NULL");
+    if (!aligned16(W) || !aligned16(X) || !aligned16(dX)) return fail(NF4_ERR_ALIGN, "W, X and dX must be 16-byte aligned");
+    if ((uintptr_t)labels & 7u) return fail(NF4_ERR_ALIGN, "labels must be 8-byte aligned");
+    if (((uintptr_t)loss | (uintptr_t)mean | (uintptr_t)dloss) & 3u)
+        return fail(NF4_ERR_ALIGN, "loss, mean and dloss must be 4-byte aligned");
+    const LossPlan p = make_loss_plan(M, V, K, grad);
+    if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "loss workspace too small");
+    if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const nf4k::LossRows r{ws_at<int32_t>(workspace, p.off_count), ws_at<int32_t>(workspace, p.off_row),
+                           ws_at<int32_t>(workspace, p.off_label), ws_at<float>(workspace, p.off_zl),
+                           ws_at<float>(workspace, p.off_S), ws_at<float>(workspace, p.off_a), ws_at<float>(workspace, p.off_b)};
+    float *tref = ws_at<float>(workspace, p.off_tref), *tsum = ws_at<float>(workspace, p.off_tsum);
+    uint16_t *P = grad ? ws_at<uint16_t>(workspace, p.off_P) : nullptr;
+    float *c[3];
+    for (int i = 0; i < 3; ++i) c[i] = ws_at<float>(workspace, p.off_c[i]);
+    NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");
+    int at = 0;                                  // c[at]: the rows' references so far
+    for (int32_t t0 = 0; t0 < p.tiles; t0 += p.piece) {
+        const int32_t nt = p.tiles - t0 < p.piece ? p.tiles - t0 : p.piece;
+        const bool last_piece = t0 + nt == p.tiles;
+        const int before = at;
+        for (int32_t u = 0; u < nt;) {
+            const int32_t n = grad && t0 == 0 && u == 0 && p.first < nt ? p.first : nt - u;
+            const float *ref = t0 + u > 0 ? c[at] : nullptr;
+            const nf4k::LogitsArgs a{W, X, V, K, r, p.Mp, t0 + u, n, t0, grad ? ref : nullptr, tref, tsum, P, 4 * nt};
+            NF4_CHECK_HIP(nf4k::launch_loss_logits(a, s), "loss logits");
+            const int next = (at + 1) % 3;
+            const bool last = last_piece && u + n == nt;
+            const nf4k::LossJoin j{r, M, p.Mp, tref + (int64_t)u * p.Mp, tsum + (int64_t)u * p.Mp, n, ref, c[next],
+                                   last, grad, dloss, loss, mean};
+            NF4_CHECK_HIP(nf4k::launch_loss_join(j, s), "loss sums");
+            at = next;
+            u += n;
+        }
+        if (!grad) continue;
+        NF4_CHECK_HIP(nf4k::launch_loss_rescale(P, tref, c[at], r.count, p.Mp, nt, s), "loss rescale");
+        float *part = ws_at<float>(workspace, p.off_part);
+        NF4_CHECK_HIP(nf4k::launch_loss_dx(nf4k::LossDxArgs{P, W, V, K, (int64_t)t0 * nf4k::LT, r.count, p.Mp, 4 * nt, part}, s),
+                      "loss dX");
+        const bool one = p.piece == p.tiles;
+        const nf4k::LossFold f{r, part, K, p.Mp, 4 * nt, one ? nullptr : ws_at<float>(workspace, p.off_sum32), c[at],
+                               t0 ? c[before] : nullptr, W, last_piece ? dX : nullptr};
+        NF4_CHECK_HIP(nf4k::launch_loss_fold(f, s), "loss dX sum");
+    }
+    return NF4_OK;
+}
+
+nf4k::ClipEntry clip_entry(const void *ctx, int32_t i) {
+    const qlora_grad &g = static_cast<const qlora_grad *>(ctx)[i];
+    return nf4k::ClipEntry{g.grad, g.out, g.numel, 0, g.type == NF4_ROWS_F32 ? 1 : 0, 0};
+}
+
+}  // namespace
+
+size_t qlora_loss_workspace_size(int64_t M, int64_t V, int64_t K, int32_t grad) {
+    if (check_loss_sizes(M, V, K)) return 0;
+    return make_loss_plan(M, V, K, grad != 0).total;
+}
+
+int qlora_loss_fwd(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *labels, int64_t M, int64_t K, float *loss,
+                   float *mean, void *workspace, size_t workspace_bytes, void *stream) {
+    return run_loss(W, V, X, labels, nullptr, M, K, loss, mean, nullptr, false, workspace, workspace_bytes, stream);
+}
+
+int qlora_loss_grad(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *labels, const float *dloss, int64_t M,
+                    int64_t K, float *loss, float *mean, uint16_t *dX, void *workspace, size_t workspace_bytes, void *stream) {
+    return run_loss(W, V, X, labels, dloss, M, K, loss, mean, dX, true, workspace, workspace_bytes, stream);
+}
+
+size_t qlora_clip_workspace_size(int32_t n) {
+    if (n < 0 || n > (1 << 20)) return 0;
+    return round256((size_t)nf4k::kClipParts * 8) + round256((size_t)n * sizeof(nf4k::ClipEntry));
+}
+
+int qlora_clip_grads(const qlora_grad *grads, int32_t n, float max_norm, float *norm, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    if (n < 0) return fail(NF4_ERR_SHAPE, "n must be >= 0");
+    if (n > (1 << 20)) return fail(NF4_ERR_UNSUPPORTED, "n must be at most 2^20");
+    if (!(max_norm > 0.0f)) return fail(NF4_ERR_ARG, "max_norm must be > 0");
+    if ((n && !grads) || !norm) return fail(NF4_ERR_NULL, "grads and norm must be non-NULL");
+    if ((uintptr_t)norm & 3u) return fail(NF4_ERR_ALIGN, "norm must be 4-byte aligned");
+    int64_t total = 0;
+    for (int32_t i = 0; i < n; ++i) {
+        const qlora_grad &g = grads[i];
+        if (g.type != NF4_ROWS_BF16 && g.type != NF4_ROWS_F32)
+            return fail(NF4_ERR_ARG, "a gradient's type must be NF4_ROWS_BF16 or NF4_ROWS_F32");
+        if (g.numel < 0) return fail(NF4_ERR_SHAPE, "a gradient's numel must be >= 0");
+        if (g.numel > (int64_t)1 << 46 || (total += g.numel) > (int64_t)1 << 46)
+            return fail(NF4_ERR_UNSUPPORTED, "more than 2^46 elements");
+        if (!g.numel) continue;
+        if (!g.grad || !g.out) return fail(NF4_ERR_NULL, "a gradient and its output must be non-NULL");
+        if (((uintptr_t)g.grad | (uintptr_t)g.out) & (g.type == NF4_ROWS_F32 ? 3u : 1u))
+            return fail(NF4_ERR_ALIGN, "a gradient and its output must be aligned to their elements");
+    }
+    if (!workspace || workspace_bytes < qlora_clip_workspace_size(n)) return fail(NF4_ERR_WORKSPACE, "clip workspace too small");
+    if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
+    NF4_CHECK_HIP(nf4k::launch_clip(clip_entry, grads, n, max_norm, norm,
+                                    ws_at<nf4k::ClipEntry>(workspace, round256((size_t)nf4k::kClipParts * 8)),
+                                    ws_at<double>(workspace, 0), reinterpret_cast<hipStream_t>(stream)),
+                  "clip");
     return NF4_OK;
 }

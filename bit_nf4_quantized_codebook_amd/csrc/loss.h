@@ -1,0 +1,100 @@
+// Softmax cross entropy of the output head: what its kernels share (gfx950).
+//
+// Tokens without a label take no part: the others' indices are gathered once ("live rows", in
+// order), every kernel counts in live rows, and how many there are stays on the device.
+//
+// Logits are handled in units of log2: l = z log2(e), and a row's reference c is an integer, so that
+// moving a sum or a probability from one reference to another is a product with a power of two,
+// which rounds nothing.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace nf4k {
+
+constexpr int LT = 256;                  // tokens, vocabulary rows or columns of dX of a tile
+constexpr int LSTEP = 64;                // reduction of one step of a tile's loop
+constexpr int64_t LBLOCK = LT * LSTEP;   // elements of one step's operand tile (32 KB)
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Per-row state in the workspace; row arrays have Mp = M rounded up to 256 entries.
+struct LossRows {
+    int32_t *count;        // [0]: live rows; [1]: workgroups of the last join that are done
+    int32_t *row;          // [M] live row -> token
+    int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
+    float *zl;             // [M] the label's logit in log2 units
+    float *S;              // [M] sum over the other vocabulary rows of 2^(l - c)
+    float *a, *b;          // [M] dX = a (sum P W) - b W[label]
+};
+
+// dX's product: workgroups per tile of a reduction of `steps` steps, for `tiles` tiles (device and host)
+struct LossSplit {
+    int ks, per;
+};
+__host__ __device__ inline LossSplit loss_split(int tiles, int steps) {
+    int ks = tiles > 0 && tiles < 256 ? 256 / tiles : 1;
+    if (ks > steps / 8) ks = steps / 8 > 0 ? steps / 8 : 1;
+    const int per = (steps + ks - 1) / ks;
+    return LossSplit{(steps + per - 1) / per, per};
+}
+
+struct LogitsArgs {
+    const uint16_t *W, *X;
+    int64_t V, K;
+    LossRows r;
+    int32_t Mp;
+    int32_t tile0, ntile;     // vocabulary tiles of this launch
+    int32_t table0;           // the tile whose entries stand first in tref and tsum (and in P)
+    const float *ref;         // [M] references, or NULL: each tile takes its own maximum
+    float *tref, *tsum;       // [tiles][Mp]: a tile's reference and its sum of 2^(l - reference)
+    uint16_t *P;              // 2^(l - reference) in bf16, or NULL; blocks of one step (see loss_logits.hip)
+    int32_t psteps;           // steps of P's row of blocks
+};
+hipError_t launch_loss_logits(const LogitsArgs &a, hipStream_t stream);
+
+struct LossDxArgs {
+    const uint16_t *P, *W;
+    int64_t V, K, v0;         // v0: first vocabulary row of the piece
+    const int32_t *count;
+    int32_t Mp, steps;
+    float *part;              // [split][tile] blocks of 256 x 256 float32 (row: token)
+};
+hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream);
+
+// labels -> live rows; loss and dX of the other tokens set to zero
+hipError_t launch_loss_prep(const int64_t *labels, int64_t M, int64_t V, int64_t K, const LossRows &r, float *loss,
+                            uint16_t *dX, hipStream_t stream);
+// the tiles' references and sums into the rows' (c_in NULL: the first)
+struct LossJoin {
+    LossRows r;
+    int64_t M;
+    int32_t Mp;
+    const float *tref, *tsum;
+    int32_t ntile;
+    const float *c_in;
+    float *c_out;
+    // the last join: losses, their mean, and with grad the coefficients of dX
+    bool last, grad;
+    const float *dloss;
+    float *loss, *mean;
+};
+hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream);
+// P's tiles brought from their own references to the rows'
+hipError_t launch_loss_rescale(uint16_t *P, const float *tref, const float *c, const int32_t *count, int32_t Mp,
+                               int32_t ntile, hipStream_t stream);
+// dX's partials summed: into sum32 (with what it holds, from the references c_old to c), or as the result
+struct LossFold {
+    LossRows r;
+    const float *part;
+    int64_t K;
+    int32_t Mp, steps;
+    float *sum32;             // [Mp, K], or NULL: one piece only
+    const float *c, *c_old;   // c_old NULL: the first piece
+    const uint16_t *W;
+    uint16_t *dX;             // NULL: not the last piece
+};
+hipError_t launch_loss_fold(const LossFold &a, hipStream_t stream);
+
+}  // namespace nf4k

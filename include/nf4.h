@@ -431,6 +431,62 @@ int qlora_norm_bwd(const qlora_norm *p, const void *R_out, const uint16_t *B, co
                    void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * The loss over the vocabulary: the two ends of a finetuning step are this and qlora_clip_grads.  Softmax
+ * cross entropy of the output head, whose weight is frozen like every weight here and stays in bf16 (the
+ * notes train on the responses only: a prompt's tokens have no label):
+ *   z = X W^T;   loss[m] = log(sum_v exp(z[m, v])) - z[m, labels[m]]
+ *   mean = sum of the losses over the number of tokens with a label (0 where no token has one)
+ *   W: [V, K] bf16;  X: [M, K] bf16;  labels: int64 [M]: 0 .. V - 1, or negative: no label (loss 0).
+ *      A label of V or more gives that token (and the mean) NaN; nothing is read for it.
+ *   loss: float32 [M];  mean: float32 [1].
+ *   1 <= M <= 2^20, 1 <= V <= 2^24, K a multiple of 64 up to 16384, X below 2 GiB (W may be larger).
+ * The logits are formed in pieces of the vocabulary and never kept; sums are float32 and the mean's float64.
+ * A loss keeps its relative accuracy down to tokens that are predicted almost surely (it is computed from the
+ * other entries' sum, not as a difference).  Values of X or W that are not finite give NaN to the tokens that
+ * meet them and leave the others as they are.
+ *   workspace: >= qlora_loss_workspace_size(M, V, K, 0) bytes, 16-byte aligned; calls that may overlap need
+ *      a workspace each.
+ */
+size_t qlora_loss_workspace_size(int64_t M, int64_t V, int64_t K, int32_t grad);
+int qlora_loss_fwd(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *labels, int64_t M, int64_t K,
+                   float *loss, float *mean, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The same with the gradient for X, in one pass over the vocabulary:
+ *   dX[m] = dloss[m] sum_v (softmax(z[m])_v - [v == labels[m]]) W[v]
+ *   dloss: float32 [M], the gradient of each token's loss, or NULL: of the mean (1 / tokens with a label).
+ *   dX: [M, K] bf16, rounded once; zero for a token without a label, whatever its X.  Probabilities enter
+ *      their product with W in bf16 (the label's own in float32).  dX must not overlap X or W.
+ *   loss and mean as qlora_loss_fwd's, up to the rounding of float32.
+ *   workspace: >= qlora_loss_workspace_size(M, V, K, 1) bytes.
+ */
+int qlora_loss_grad(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *labels, const float *dloss,
+                    int64_t M, int64_t K, float *loss, float *mean, uint16_t *dX, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/*
+ * The global norm of the adapters' gradients, and all of them scaled down to a largest norm:
+ *   norm = sqrt(sum over all tensors of g^2);   out = norm > max_norm ? g (max_norm / norm) : g
+ * A norm that is not finite in float32 leaves the gradients as they are (a program skips that step).
+ */
+typedef struct qlora_grad {
+    const void *grad;             /* [numel], aligned to its elements */
+    void *out;                    /* [numel] of the same type: grad itself, or memory that overlaps no gradient */
+    int64_t numel;                /* >= 0 */
+    int32_t type;                 /* NF4_ROWS_BF16 or NF4_ROWS_F32 */
+} qlora_grad;
+
+/*
+ *   grads: HOST array of n tensors (0 <= n <= 2^20), read during the call only.  max_norm > 0; infinity:
+ *      only the norm is wanted.  norm: device float32 [1].
+ *   workspace: >= qlora_clip_workspace_size(n) bytes, 16-byte aligned; calls that may overlap need one each.
+ * Squares are summed and the products formed in float64, then rounded to the gradient's type.
+ */
+size_t qlora_clip_workspace_size(int32_t n);
+int qlora_clip_grads(const qlora_grad *grads, int32_t n, float max_norm, float *norm, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
  * Timing instrumentation (not part of the method).  While set on the calling thread, the library
  * records begin[i] and end[i] (hipEvent_t handles created by the caller) on the launch stream
  * immediately before and after the i-th subsequent launch of an instrumented kernel -- the

@@ -476,6 +476,46 @@ def norm_bwd(R_out, B=None, dR_out=None, dH=None, w_pre=None, w_post=None, gate=
 
 
 # ------------------------------------------------------------------------------------------
+# The loss over the vocabulary and the clipping of gradients, in float64 from the definitions
+# ------------------------------------------------------------------------------------------
+
+def loss(X, W, labels, dloss=None):
+    """Softmax cross entropy of logits X W^T, token by token (a negative label: none; a label past the
+    vocabulary: NaN).  Returns (loss [M], mean over the tokens with a label, dX [M, K]); dloss None: dX is the
+    mean's gradient."""
+    X, W = _f64(X), _f64(W)
+    M, V = X.shape[0], W.shape[0]
+    each, dX = np.zeros(M), np.zeros(X.shape)
+    count = int((np.asarray(labels) >= 0).sum())
+    for m in range(M):
+        y = int(labels[m])
+        if y < 0:
+            continue
+        if y >= V:
+            each[m], dX[m] = np.nan, np.nan
+            continue
+        z = W @ X[m]
+        rel = z - z[y]                       # against the label: loss = ln(1 + sum of the others' exp)
+        rest = np.delete(rel, y)
+        top = rest.max() if V > 1 else -np.inf
+        gap = top + np.log(np.exp(rest - top).sum()) if V > 1 else -np.inf
+        each[m] = np.logaddexp(0.0, gap)
+        p = np.exp(rel - each[m])
+        p[y] = -1.0 / (1.0 + np.exp(-gap)) if gap > -np.inf else 0.0
+        dX[m] = (1.0 / count if dloss is None else float(dloss[m])) * (p @ W)
+    return each, (each.sum() / count if count else 0.0), dX
+
+
+def clip(grads, max_norm):
+    """The global norm of a list of arrays, and all of them scaled to at most max_norm (left as they are where the
+    norm is not finite in float32, the type it is returned in)."""
+    norm = float(np.sqrt(sum(float((_f64(g) ** 2).sum()) for g in grads)))
+    with np.errstate(over="ignore"):
+        f = max_norm / norm if np.isfinite(np.float32(norm)) and norm > max_norm else 1.0
+    return norm, [_f64(g) * f for g in grads]
+
+
+# ------------------------------------------------------------------------------------------
 # Error measures used by the parity tests
 # ------------------------------------------------------------------------------------------
 

@@ -1,0 +1,291 @@
+"""GPU parity of the loss over the vocabulary (forward, and with its gradient) against the float64 oracle.
+
+Tolerances, from the roundings on the way (u = 2^-24, h = 2^-8 for bf16).  A logit is a float32 sum of K exact
+products in some order: off by at most Ez = K u sum |x w|.  In log2 units it is rounded again in one fma, so with the
+constant's own error l - c is off by Ez / ln 2 + 4 u (|l| + |c|); 2^x in hardware adds 2 u, and a row's sum (64 in a
+lane, then 4 across lanes and waves, then the tiles) at most (80 + tiles) u of itself.  With A = max |z| + 64 (c lies
+within 48 of a maximum) every term of a row is off by the factor
+  D = 2 (Ez + 8 u A) + (80 + tiles) u + 16 u,
+d = ln S + c - z_label by D as well, and
+  |loss error| <= sigmoid(d) D + 8 u loss,
+  |dX error| <= |g| (sum_{v != y} p |W| (h + 2 D + V u) + (1 - p_y) |W_y| 2 D) (1 + h) + h |dX|.
+"""
+import numpy as np
+import pytest
+
+import oracle
+import synth
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import bit_nf4_quantized_codebook_amd as nf4  # noqa: E402
+
+DEV = torch.device("cuda:0")
+U, H = 2.0 ** -24, 2.0 ** -8
+NONE = -100
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(DEV).bfloat16()
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def make(M, V, K, seed=0, std=0.05, none=0.0, lift=0.0):
+    rng = np.random.default_rng(100 + seed)
+    X, W = synth.normal_f32(9000 + seed, (M, K), 1.0), synth.normal_f32(9500 + seed, (V, K), std)
+    labels = rng.integers(0, V, M)
+    W16 = f64(bf16(W))
+    X = X + (lift * rng.random((M, 1)) * W16[labels] / np.maximum((W16[labels] ** 2).sum(1, keepdims=True), 1e-30)).astype(np.float32)
+    labels[rng.random(M) < none] = NONE
+    return bf16(X), bf16(W), torch.from_numpy(labels).to(DEV)
+
+
+def check(X, W, labels, dloss=None, rows=None, fwd=True, grad=True):
+    """Both entry points on these inputs, against the oracle at `rows` (all of them by default)."""
+    M, K = X.shape
+    V = W.shape[0]
+    x, w, y = f64(X), f64(W), labels.cpu().numpy()
+    rows = np.arange(M) if rows is None else rows
+    count = int((y >= 0).sum())
+    g = np.full(M, 1.0 / max(count, 1)) if dloss is None else f64(dloss)
+    ref, _, dX = oracle.loss(x[rows], w, y[rows], g[rows])
+    z = x[rows] @ w.T
+    Ez = K * U * (np.abs(x[rows]) @ np.abs(w).T).max(1)
+    tiles = -(-V // 256)
+    D = 2 * (Ez + 8 * U * (np.abs(z).max(1) + 64)) + (96 + tiles) * U
+    tol = -np.expm1(-ref) * D + 8 * U * ref
+    out = []
+    if fwd:
+        out.append(nf4.qlora_loss_fwd(W, X, labels))
+    if grad:
+        out.append(nf4.qlora_loss_grad(W, X, labels, dloss))
+    for o in out:
+        got = f64(o[0])[rows]
+        bad = ~(np.abs(got - ref) <= tol)
+        assert not bad.any(), (int(bad.sum()), rows[bad][:5], got[bad][:5], ref[bad][:5], tol[bad][:5])
+        assert not f64(o[0])[y < 0].any()
+        assert abs(float(o[1]) - f64(o[0]).sum() / max(count, 1)) <= 2 * U * abs(float(o[1]))
+    if grad:
+        got = f64(out[-1][2])[rows]
+        p = np.exp(z - (z[np.arange(len(rows)), np.maximum(y[rows], 0)] + ref)[:, None])
+        p[np.arange(len(rows)), np.maximum(y[rows], 0)] = 0.0
+        p[y[rows] < 0] = 0.0
+        miss = -np.expm1(-ref)
+        size = (p @ np.abs(w)) * (H + 2 * D + V * U)[:, None] + (miss * 2 * D)[:, None] * np.abs(w[np.maximum(y[rows], 0)])
+        tolx = np.abs(g[rows])[:, None] * size * (1 + H) + H * np.abs(dX)
+        bad = ~(np.abs(got - dX) <= tolx)
+        assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], dX[bad][:4], tolx[bad][:4])
+        assert not f64(out[-1][2])[y < 0].any()
+    return out
+
+
+@pytest.mark.parametrize("M,V,K", [
+    (1, 1, 64), (1, 2, 64), (3, 255, 64), (2, 256, 128), (5, 257, 64), (1, 1000, 512), (31, 300, 192), (64, 511, 64),
+    (65, 513, 320), (255, 700, 64), (256, 256, 256), (257, 1025, 128), (300, 2049, 576), (513, 999, 1024)])
+def test_sizes(M, V, K):
+    X, W, labels = make(M, V, K, seed=M + V, none=0.2 if M > 4 else 0.0, lift=12.0)
+    check(X, W, labels)
+
+
+@pytest.mark.parametrize("none", [0.0, 0.5, 0.97, 1.0])
+def test_tokens_without_a_label(none):
+    M = 600
+    X, W, labels = make(M, 777, 128, seed=3, none=none, lift=8.0)
+    g = torch.rand(M, device=DEV) - 0.3
+    check(X, W, labels, g)
+    loss, mean, dX = nf4.qlora_loss_grad(W, X, labels)
+    if none == 1.0:
+        assert float(mean) == 0.0 and not dX.any() and not loss.any()
+    # their X may hold anything; they are left as they are, whatever the others do
+    X2 = X.clone()
+    X2[labels < 0] = float("nan")
+    again = nf4.qlora_loss_grad(W, X2, labels)
+    assert same(again[0], loss) and same(again[1], mean) and same(again[2], dX)
+
+
+def test_any_negative_label_counts_as_none():
+    X, W, labels = make(40, 300, 64, seed=5)
+    a, b = labels.clone(), labels.clone()
+    a[::3], b[::3] = NONE, torch.iinfo(torch.int64).min
+    for p, q in zip(nf4.qlora_loss_grad(W, X, a), nf4.qlora_loss_grad(W, X, b)):
+        assert same(p, q)
+
+
+def test_label_past_the_vocabulary_is_nan_alone():
+    X, W, labels = make(50, 300, 64, seed=6)
+    ref = nf4.qlora_loss_grad(W, X, labels, torch.ones(50, device=DEV))
+    bad = labels.clone()
+    bad[7], bad[41] = 300, torch.iinfo(torch.int64).max
+    loss, mean, dX = nf4.qlora_loss_grad(W, X, bad, torch.ones(50, device=DEV))
+    keep = torch.ones(50, dtype=torch.bool, device=DEV)
+    keep[[7, 41]] = False
+    assert torch.isnan(loss[~keep]).all() and torch.isnan(dX[~keep]).all() and torch.isnan(mean).all()
+    assert same(loss[keep], ref[0][keep]) and same(dX[keep], ref[2][keep])
+    loss, mean = nf4.qlora_loss_fwd(W, X, bad)
+    assert torch.isnan(loss[~keep]).all() and torch.isnan(mean).all() and torch.isfinite(loss[keep]).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_tokens_that_are_not_finite_stay_alone(value):
+    X, W, labels = make(300, 700, 128, seed=7)
+    g = torch.ones(300, device=DEV)
+    ref = nf4.qlora_loss_grad(W, X, labels, g)
+    X2 = X.clone()
+    X2[129, 5] = value
+    loss, mean, dX = nf4.qlora_loss_grad(W, X2, labels, g)
+    keep = torch.arange(300, device=DEV) != 129
+    assert torch.isnan(loss[129]) and torch.isnan(dX[129]).all() and torch.isnan(mean).all()
+    assert same(loss[keep], ref[0][keep]) and same(dX[keep], ref[2][keep])
+
+
+def test_sure_labels_keep_relative_accuracy():
+    """Losses from 1e-30 up to hundreds: logits ahead of or behind the others by far."""
+    M, V, K = 64, 600, 64
+    X, W = np.zeros((M, K), np.float32), synth.normal_f32(31, (V, K), 0.05)
+    W[:, 0] = 0.0
+    labels = np.arange(M) * 9
+    W[labels, 0] = 1.0                       # the label's logit moves with X[:, 0]
+    others = np.setdiff1d(np.arange(V), labels)
+    W[others, 0] = 0.0
+    X[:] = synth.normal_f32(32, (M, K), 1.0)
+    X[:, 0] = np.linspace(-250, 75, M)
+    W[labels, 1:] = 0.0
+    for m in range(M):                       # other tokens' label rows would answer too: one token a call
+        w = W.copy()
+        w[np.setdiff1d(labels, labels[m]), 0] = 0.0
+        check(bf16(X[m:m + 1]), bf16(w), torch.tensor([labels[m]], device=DEV), torch.ones(1, device=DEV))
+
+
+def test_references_move_far():
+    """Each tile's largest logit exceeds the one before by more than a reference allows, up and down."""
+    K, V, M = 64, 256 * 12, 300
+    for order in (1, -1):
+        W = synth.normal_f32(41, (V, K), 0.05)
+        W[:, 0] = np.repeat(np.arange(12)[::order] * 10.0, 256)
+        X = synth.normal_f32(42, (M, K), 1.0)
+        X[:, 0] = np.linspace(-6, 6, M)
+        labels = np.random.default_rng(43).integers(0, V, M)
+        check(bf16(X), bf16(W), torch.from_numpy(labels).to(DEV), torch.ones(M, device=DEV))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_pieces_of_the_vocabulary(order):
+    """32768 tokens: a piece holds 8192 vocabulary rows, so three of them; the largest logits move from piece to
+    piece.  Rows sampled."""
+    M, V, K = 32768, 20001, 64
+    assert nf4.qlora_loss_workspace_size(M, V, K, True) < 2 * M * V
+    X, W, labels = make(M, V, K, seed=9, none=0.1, lift=10.0)
+    W[:, 0] = (torch.arange(V, device=DEV) // 8192 * 9.0 * order).bfloat16()
+    X[:, 0] = torch.linspace(-8, 8, M, device=DEV).bfloat16()
+    rows = np.random.default_rng(10).choice(M, 150, replace=False)
+    print(f"pieces: M={M} V={V} K={K} order={order}", flush=True)
+    check(X, W, labels, rows=np.concatenate([rows, [0, M - 1]]))
+
+
+def test_outputs_and_workspace_given():
+    M, V, K = 130, 600, 128
+    X, W, labels = make(M, V, K, seed=12, none=0.3)
+    ref = nf4.qlora_loss_grad(W, X, labels)
+    guard = torch.full((M + 2, K), 7.0, dtype=torch.bfloat16, device=DEV)
+    loss, mean = torch.full((M + 2,), 7.0, device=DEV), torch.full((1,), 7.0, device=DEV)
+    ws = torch.full((nf4.qlora_loss_workspace_size(M, V, K, True) + 64,), 0xA5, dtype=torch.uint8, device=DEV)
+    out = nf4.qlora_loss_grad(W, X, labels, loss=loss[1:-1], mean=mean, dX=guard[1:-1], workspace=ws)
+    for a, b in zip(out, ref):
+        assert same(a, b)
+    assert (guard[[0, -1]] == 7).all() and (loss[[0, -1]] == 7).all() and (ws[-64:] == 0xA5).all()
+    out = nf4.qlora_loss_fwd(W, X, labels, loss=loss[1:-1], mean=mean, workspace=ws)
+    assert out[1] is mean and (loss[[0, -1]] == 7).all()
+    with pytest.raises(ValueError):
+        nf4.qlora_loss_fwd(W, X, labels, workspace=ws[:64])
+
+
+def test_refuses_what_does_not_fit():
+    X, W, labels = make(8, 100, 64, seed=13)
+    bad = [lambda: nf4.qlora_loss_fwd(W[:, :32], X, labels), lambda: nf4.qlora_loss_fwd(W.t(), X, labels),
+           lambda: nf4.qlora_loss_fwd(W, X, labels[:-1]), lambda: nf4.qlora_loss_fwd(W, X[:, ::2], labels),
+           lambda: nf4.qlora_loss_grad(W, X, labels, torch.ones(7, device=DEV)),
+           lambda: nf4.qlora_loss_grad(W, X, labels, dX=torch.empty((8, 32), dtype=torch.bfloat16, device=DEV))]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: nf4.qlora_loss_fwd(W.float(), X, labels), lambda: nf4.qlora_loss_fwd(W, X, labels.int()),
+              lambda: nf4.qlora_loss_grad(W, X, labels, torch.ones(8, device=DEV).double())):
+        with pytest.raises(TypeError):
+            f()
+    with pytest.raises(nf4.NF4Error):
+        nf4.qlora_loss_fwd(W[:, :32].contiguous(), X[:, :32].contiguous(), labels)
+
+
+def test_gradient_against_differences_of_the_forward():
+    """mean(X + D) - mean(X - D) = 2 <dX, D> up to a third of the third derivative along D.  That is the third central
+    moment of (W D) under the token's softmax: at most 0.77 a^3 for values within [-a, a].  X and D are multiples of
+    2^-6 below 4, so that X + D and X - D are exact in bf16."""
+    M, V, K = 200, 3000, 256
+    X, W, labels = make(M, V, K, seed=14, none=0.2, lift=6.0)
+    X = (torch.round(X.float().clamp(-3.9, 3.9) * 64) / 64).bfloat16()
+    _, _, dX = nf4.qlora_loss_grad(W, X, labels)
+    D = torch.sign(dX.float()) / 64
+    up, down = X.float() + D, X.float() - D
+    assert (up.bfloat16().float() == up).all() and (down.bfloat16().float() == down).all()
+    a, b = (nf4.qlora_loss_fwd(W, t.bfloat16(), labels)[1] for t in (up, down))
+    live = labels >= 0
+    count = int(live.sum())
+    along = 2 * (dX.double() * D.double()).sum()
+    moved = (D[live].double() @ W.double().t()).abs().max(1).values
+    z = X[live].double() @ W.double().t()
+    size = torch.softmax(z, 1) @ W.double().abs() + W[labels[live]].double().abs()
+    tol = (0.77 * moved ** 3).sum() / 3 / count + 2 * H * (size * 2 / 64).sum() / count
+    # both means are off by at most the logits' own error
+    tol += 2 * K * U * (X.double().abs() @ W.double().abs().t()).max() * 2
+    assert abs(float(a.double() - b.double()) - float(along)) <= float(tol)
+    assert float(tol) < 0.1 * float(along)
+
+
+def test_other_stream_and_repeats():
+    X, W, labels = make(400, 5000, 512, seed=15, none=0.3, lift=9.0)
+    ref = nf4.qlora_loss_grad(W, X, labels)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        outs = [nf4.qlora_loss_grad(W, X, labels) for _ in range(3)]
+    s.synchronize()
+    for out in outs:
+        for a, b in zip(out, ref):
+            assert same(a, b)
+
+
+def test_graph_replays_match_eager():
+    M, V, K = 300, 2000, 256
+    X, W, labels = make(M, V, K, seed=16, none=0.3)
+    loss, mean = torch.empty(M, device=DEV), torch.empty(1, device=DEV)
+    dX = torch.empty((M, K), dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(nf4.qlora_loss_workspace_size(M, V, K, True), dtype=torch.uint8, device=DEV)
+    nf4.qlora_loss_grad(W, X, labels, None, loss, mean, dX, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nf4.qlora_loss_grad(W, X, labels, None, loss, mean, dX, ws)
+    torch.cuda.synchronize()
+    for rep in range(3):
+        X2, _, lab2 = make(M, V, K, seed=20 + rep, none=0.2 * rep)
+        X.copy_(X2)
+        labels.copy_(lab2)
+        dX.fill_(float("nan"))
+        loss.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        ref = nf4.qlora_loss_grad(W, X, labels)
+        torch.cuda.synchronize()
+        for a, b in zip((loss, mean, dX), ref):
+            assert same(a, b), rep
