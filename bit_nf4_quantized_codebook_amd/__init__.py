@@ -39,7 +39,8 @@ EXPORTS = (
     "qlora_multi_workspace_size", "qlora_multi_fwd",
     "nf4_int8_quantize", "nf4_int8_dequant", "qlora_int8_linear_workspace_size", "qlora_int8_linear_fwd",
     "qlora_int8_linear_bwd", "qlora_norm_fwd", "qlora_norm_workspace_size", "qlora_norm_bwd",
-    "qlora_loss_workspace_size", "qlora_loss_fwd", "qlora_loss_grad", "qlora_clip_workspace_size", "qlora_clip_grads",
+    "qlora_loss_workspace_size", "qlora_loss_fwd", "qlora_loss_grad", "qlora_grad_table_size", "qlora_grad_table",
+    "qlora_clip_workspace_size", "qlora_clip_grads",
     "nf4_set_gemm_timing_events", "nf4_gemm_timing_count",
 )
 
@@ -150,8 +151,10 @@ def _load():
         "qlora_loss_workspace_size": (sz, [i64, i64, i64, i32]),
         "qlora_loss_fwd": (i, [P, i64, P, P, i64, i64, P, P, P, sz, P]),
         "qlora_loss_grad": (i, [P, i64, P, P, P, i64, i64, P, P, P, P, sz, P]),
-        "qlora_clip_workspace_size": (sz, [i32]),
-        "qlora_clip_grads": (i, [P, i32, ctypes.c_float, P, P, sz, P]),
+        "qlora_grad_table_size": (sz, [i32]),
+        "qlora_grad_table": (i, [P, i32, P, sz, P]),
+        "qlora_clip_workspace_size": (sz, []),
+        "qlora_clip_grads": (i, [P, i32, i64, ctypes.c_float, P, P, sz, P]),
         "nf4_set_gemm_timing_events": (i, [P, P, P, i32]),
         "nf4_gemm_timing_count": (i32, []),
     }
@@ -889,8 +892,9 @@ def qlora_loss_grad(W, X, labels, dloss=None, loss=None, mean=None, dX=None, wor
 
 class QLoRAGrads:
     """A list of gradient tensors (bf16 or float32, contiguous, on one device) for qlora_clip_grads, with where the
-    scaled ones go: the tensors themselves, or outs, of the same shapes and types.  Checked once; it keeps the
-    tensors, whose contents may change between calls."""
+    scaled ones go: the tensors themselves, or outs, of the same shapes and types, in memory that overlaps no gradient.
+    Checked and laid out once (a small table on the device); it keeps the tensors, whose contents may change between
+    calls."""
 
     def __init__(self, grads, outs=None):
         torch = _torch()
@@ -900,38 +904,45 @@ class QLoRAGrads:
             raise ValueError("the list of gradients is empty")
         if len(outs) != len(grads):
             raise ValueError("outs must have as many tensors as grads")
-        _need(grads[0], torch.float32 if getattr(grads[0], "dtype", None) == torch.float32 else torch.bfloat16, "grads[0]")
-        self._device = grads[0].device
-        self._list = (_GradDesc * len(grads))()
+        dev = getattr(grads[0], "device", None)
+        n = len(grads)
+        desc = (_GradDesc * n)()
         for i, (g, o) in enumerate(zip(grads, outs)):
             f32 = getattr(g, "dtype", None) == torch.float32
-            _expect(g, torch.float32 if f32 else torch.bfloat16, g.shape, self._device, f"grads[{i}]")
-            _expect(o, g.dtype, g.shape, self._device, f"outs[{i}]")
-            self._list[i] = _GradDesc(g.data_ptr(), o.data_ptr(), g.numel(), int(f32))
+            _need(g, torch.float32 if f32 else torch.bfloat16, f"grads[{i}]")
+            _expect(g, g.dtype, g.shape, dev, f"grads[{i}]")
+            _expect(o, g.dtype, g.shape, dev, f"outs[{i}]")
+            desc[i] = _GradDesc(g.data_ptr(), o.data_ptr(), g.numel(), int(f32))
+        host = np.zeros(int(lib.qlora_grad_table_size(n)) // 8, dtype=np.int64)
+        chunks = ctypes.c_int64()
+        _check(lib.qlora_grad_table(ctypes.addressof(desc), n, host.ctypes.data, host.nbytes, ctypes.addressof(chunks)),
+               "qlora_grad_table")
+        # a copy from pageable memory has arrived when it returns: any stream may read the table
+        self._table = torch.from_numpy(host).to(dev)
+        self._chunks = chunks.value
         self._grads, self._outs = grads, outs
 
     grads = property(lambda self: self._grads)
     outs = property(lambda self: self._outs)
-    device = property(lambda self: self._device)
+    device = property(lambda self: self._table.device)
 
     def __len__(self):
         return len(self._grads)
 
 
-def qlora_clip_workspace_size(n: int) -> int:
-    return int(lib.qlora_clip_workspace_size(n))
+def qlora_clip_workspace_size() -> int:
+    return int(lib.qlora_clip_workspace_size())
 
 
 def qlora_clip_grads(grads: QLoRAGrads, max_norm: float, norm=None, workspace=None):
     """Scales all gradients by max_norm / norm where their global norm exceeds max_norm (a norm that is not finite
     leaves them as they are).  Returns the norm before, float32 [1] on the device."""
-    torch = _torch()
-    dev, n = grads.device, len(grads)
-    norm = _out(norm, torch.float32, (1,), dev, "norm")
-    wsb = lib.qlora_clip_workspace_size(n)
+    dev = grads._table.device
+    norm = _out(norm, _torch().float32, (1,), dev, "norm")
+    wsb = lib.qlora_clip_workspace_size()
     ws = _scratch(wsb, dev, workspace)
-    _launch(lib.qlora_clip_grads, "qlora_clip_grads", dev, ctypes.addressof(grads._list), n, max_norm, norm.data_ptr(),
-            ws.data_ptr(), wsb)
+    _launch(lib.qlora_clip_grads, "qlora_clip_grads", dev, grads._table.data_ptr(), len(grads._grads), grads._chunks,
+            max_norm, norm.data_ptr(), ws.data_ptr(), wsb)
     return norm
 
 

@@ -1409,8 +1409,7 @@ constexpr int64_t kLossMinTiles = 32;
 
 struct LossPlan {
     int32_t Mp, tiles, piece;          // rows padded to tiles; tiles of the vocabulary, and of a piece
-    int32_t first;                     // gradient: tiles of the first span, from which the references come
-    size_t off_count, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[3], off_tref, off_tsum, off_P, off_part,
+    size_t off_count, off_sums, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[2], off_tref, off_tsum, off_P, off_part,
         off_sum32, total;
 };
 
@@ -1425,9 +1424,6 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     const int64_t most = ((int64_t)1 << 22) / K;
     if (grad && piece > most) piece = most;
     p.piece = (int32_t)(piece < p.tiles ? piece : p.tiles);
-    // one round of the chip; a rest of less than two rounds is not worth a launch of its own
-    const int64_t first = ntm < 256 ? 256 / ntm : 1;
-    p.first = (int32_t)(p.piece >= 3 * first ? first : p.piece);
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -1435,6 +1431,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         return at;
     };
     p.off_count = take(8);
+    p.off_sums = take((size_t)(p.Mp / nf4k::kLossJoinRows) * 8);
     p.off_row = take((size_t)p.Mp * 4);
     p.off_label = take((size_t)p.Mp * 4);
     p.off_zl = take((size_t)p.Mp * 4);
@@ -1479,48 +1476,37 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
     if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "loss workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const nf4k::LossRows r{ws_at<int32_t>(workspace, p.off_count), ws_at<int32_t>(workspace, p.off_row),
+    const nf4k::LossRows r{ws_at<int32_t>(workspace, p.off_count), ws_at<double>(workspace, p.off_sums), ws_at<int32_t>(workspace, p.off_row),
                            ws_at<int32_t>(workspace, p.off_label), ws_at<float>(workspace, p.off_zl),
                            ws_at<float>(workspace, p.off_S), ws_at<float>(workspace, p.off_a), ws_at<float>(workspace, p.off_b)};
     float *tref = ws_at<float>(workspace, p.off_tref), *tsum = ws_at<float>(workspace, p.off_tsum);
     uint16_t *P = grad ? ws_at<uint16_t>(workspace, p.off_P) : nullptr;
-    float *c[3];
-    for (int i = 0; i < 3; ++i) c[i] = ws_at<float>(workspace, p.off_c[i]);
+    float *c[2];
+    for (int i = 0; i < 2; ++i) c[i] = ws_at<float>(workspace, p.off_c[i]);
     NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");
-    int at = 0;                                  // c[at]: the rows' references so far
-    for (int32_t t0 = 0; t0 < p.tiles; t0 += p.piece) {
+    // c[piece % 2]: the rows' references after that piece
+    for (int32_t t0 = 0, piece = 1; t0 < p.tiles; t0 += p.piece, ++piece) {
         const int32_t nt = p.tiles - t0 < p.piece ? p.tiles - t0 : p.piece;
-        const bool last_piece = t0 + nt == p.tiles;
-        const int before = at;
-        for (int32_t u = 0; u < nt;) {
-            const int32_t n = grad && t0 == 0 && u == 0 && p.first < nt ? p.first : nt - u;
-            const float *ref = t0 + u > 0 ? c[at] : nullptr;
-            const nf4k::LogitsArgs a{W, X, V, K, r, p.Mp, t0 + u, n, t0, grad ? ref : nullptr, tref, tsum, P, 4 * nt};
-            NF4_CHECK_HIP(nf4k::launch_loss_logits(a, s), "loss logits");
-            const int next = (at + 1) % 3;
-            const bool last = last_piece && u + n == nt;
-            const nf4k::LossJoin j{r, M, p.Mp, tref + (int64_t)u * p.Mp, tsum + (int64_t)u * p.Mp, n, ref, c[next],
-                                   last, grad, dloss, loss, mean};
-            NF4_CHECK_HIP(nf4k::launch_loss_join(j, s), "loss sums");
-            at = next;
-            u += n;
-        }
+        const bool last = t0 + nt == p.tiles;
+        const float *before = t0 ? c[(piece - 1) % 2] : nullptr;
+        float *now = c[piece % 2];
+        NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, t0, before, tref, tsum, P, 4 * nt}, s),
+                      "loss logits");
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, piece, last, grad, dloss,
+                                                            loss, mean}, s), "loss sums");
+        // one workgroup of the join writes the mean itself
+        float *mean_here = last && M > nf4k::kLossJoinRows ? mean : nullptr;
+        if (grad || mean_here)
+            NF4_CHECK_HIP(nf4k::launch_loss_rescale(nf4k::LossRescale{r, M, p.Mp, nt, piece, P, tref, now, mean_here}, s),
+                          "loss rescale");
         if (!grad) continue;
-        NF4_CHECK_HIP(nf4k::launch_loss_rescale(P, tref, c[at], r.count, p.Mp, nt, s), "loss rescale");
-        float *part = ws_at<float>(workspace, p.off_part);
-        NF4_CHECK_HIP(nf4k::launch_loss_dx(nf4k::LossDxArgs{P, W, V, K, (int64_t)t0 * nf4k::LT, r.count, p.Mp, 4 * nt, part}, s),
-                      "loss dX");
         const bool one = p.piece == p.tiles;
-        const nf4k::LossFold f{r, part, K, p.Mp, 4 * nt, one ? nullptr : ws_at<float>(workspace, p.off_sum32), c[at],
-                               t0 ? c[before] : nullptr, W, last_piece ? dX : nullptr};
-        NF4_CHECK_HIP(nf4k::launch_loss_fold(f, s), "loss dX sum");
+        const nf4k::LossDxArgs d{P, W, V, K, (int64_t)t0 * nf4k::LT, r, p.Mp, 4 * nt, ws_at<float>(workspace, p.off_part),
+                                 one ? nullptr : ws_at<float>(workspace, p.off_sum32), now, before, last ? dX : nullptr};
+        NF4_CHECK_HIP(nf4k::launch_loss_dx(d, s), "loss dX");
+        NF4_CHECK_HIP(nf4k::launch_loss_fold(d, s), "loss dX sum");
     }
     return NF4_OK;
-}
-
-nf4k::ClipEntry clip_entry(const void *ctx, int32_t i) {
-    const qlora_grad &g = static_cast<const qlora_grad *>(ctx)[i];
-    return nf4k::ClipEntry{g.grad, g.out, g.numel, 0, g.type == NF4_ROWS_F32 ? 1 : 0, 0};
 }
 
 }  // namespace
@@ -1540,35 +1526,46 @@ int qlora_loss_grad(const uint16_t *W, int64_t V, const uint16_t *X, const int64
     return run_loss(W, V, X, labels, dloss, M, K, loss, mean, dX, true, workspace, workspace_bytes, stream);
 }
 
-size_t qlora_clip_workspace_size(int32_t n) {
-    if (n < 0 || n > (1 << 20)) return 0;
-    return round256((size_t)nf4k::kClipParts * 8) + round256((size_t)n * sizeof(nf4k::ClipEntry));
-}
+size_t qlora_grad_table_size(int32_t n) { return n < 0 || n > (1 << 20) ? 0 : (size_t)(n ? n : 1) * sizeof(nf4k::ClipEntry); }
 
-int qlora_clip_grads(const qlora_grad *grads, int32_t n, float max_norm, float *norm, void *workspace, size_t workspace_bytes,
-                     void *stream) {
+int qlora_grad_table(const qlora_grad *grads, int32_t n, void *table, size_t table_bytes, int64_t *chunks) {
     if (n < 0) return fail(NF4_ERR_SHAPE, "n must be >= 0");
     if (n > (1 << 20)) return fail(NF4_ERR_UNSUPPORTED, "n must be at most 2^20");
-    if (!(max_norm > 0.0f)) return fail(NF4_ERR_ARG, "max_norm must be > 0");
-    if ((n && !grads) || !norm) return fail(NF4_ERR_NULL, "grads and norm must be non-NULL");
-    if ((uintptr_t)norm & 3u) return fail(NF4_ERR_ALIGN, "norm must be 4-byte aligned");
-    int64_t total = 0;
+    if ((n && !grads) || !table || !chunks) return fail(NF4_ERR_NULL, "grads, table and chunks must be non-NULL");
+    if ((uintptr_t)table & 7u) return fail(NF4_ERR_ALIGN, "table must be 8-byte aligned");
+    if (table_bytes < qlora_grad_table_size(n)) return fail(NF4_ERR_WORKSPACE, "gradient table too small");
+    int64_t total = 0, at = 0;
     for (int32_t i = 0; i < n; ++i) {
         const qlora_grad &g = grads[i];
-        if (g.type != NF4_ROWS_BF16 && g.type != NF4_ROWS_F32)
-            return fail(NF4_ERR_ARG, "a gradient's type must be NF4_ROWS_BF16 or NF4_ROWS_F32");
+        const bool f32 = g.type == NF4_ROWS_F32;
+        if (!f32 && g.type != NF4_ROWS_BF16) return fail(NF4_ERR_ARG, "a gradient's type must be NF4_ROWS_BF16 or NF4_ROWS_F32");
         if (g.numel < 0) return fail(NF4_ERR_SHAPE, "a gradient's numel must be >= 0");
         if (g.numel > (int64_t)1 << 46 || (total += g.numel) > (int64_t)1 << 46)
             return fail(NF4_ERR_UNSUPPORTED, "more than 2^46 elements");
-        if (!g.numel) continue;
-        if (!g.grad || !g.out) return fail(NF4_ERR_NULL, "a gradient and its output must be non-NULL");
-        if (((uintptr_t)g.grad | (uintptr_t)g.out) & (g.type == NF4_ROWS_F32 ? 3u : 1u))
+        if (g.numel && (!g.grad || !g.out)) return fail(NF4_ERR_NULL, "a gradient and its output must be non-NULL");
+        if (((uintptr_t)g.grad | (uintptr_t)g.out) & (f32 ? 3u : 1u))
             return fail(NF4_ERR_ALIGN, "a gradient and its output must be aligned to their elements");
+        static_cast<nf4k::ClipEntry *>(table)[i] = nf4k::ClipEntry{g.grad, g.out, g.numel, 2 * at + (f32 ? 1 : 0)};
+        at += (g.numel + nf4k::kClipChunk - 1) / nf4k::kClipChunk;
     }
-    if (!workspace || workspace_bytes < qlora_clip_workspace_size(n)) return fail(NF4_ERR_WORKSPACE, "clip workspace too small");
+    *chunks = at;
+    return NF4_OK;
+}
+
+size_t qlora_clip_workspace_size(void) { return (size_t)nf4k::kClipParts * 8; }
+
+int qlora_clip_grads(const void *table, int32_t n, int64_t chunks, float max_norm, float *norm, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    if (n < 0 || chunks < 0) return fail(NF4_ERR_SHAPE, "n and chunks must be >= 0");
+    if (n > (1 << 20)) return fail(NF4_ERR_UNSUPPORTED, "n must be at most 2^20");
+    if (chunks && !n) return fail(NF4_ERR_SHAPE, "chunks without gradients");
+    if (!(max_norm > 0.0f)) return fail(NF4_ERR_ARG, "max_norm must be > 0");
+    if ((n && !table) || !norm) return fail(NF4_ERR_NULL, "table and norm must be non-NULL");
+    if ((uintptr_t)table & 7u) return fail(NF4_ERR_ALIGN, "table must be 8-byte aligned");
+    if ((uintptr_t)norm & 3u) return fail(NF4_ERR_ALIGN, "norm must be 4-byte aligned");
+    if (!workspace || workspace_bytes < qlora_clip_workspace_size()) return fail(NF4_ERR_WORKSPACE, "clip workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
-    NF4_CHECK_HIP(nf4k::launch_clip(clip_entry, grads, n, max_norm, norm,
-                                    ws_at<nf4k::ClipEntry>(workspace, round256((size_t)nf4k::kClipParts * 8)),
+    NF4_CHECK_HIP(nf4k::launch_clip(static_cast<const nf4k::ClipEntry *>(table), n, chunks, max_norm, norm,
                                     ws_at<double>(workspace, 0), reinterpret_cast<hipStream_t>(stream)),
                   "clip");
     return NF4_OK;

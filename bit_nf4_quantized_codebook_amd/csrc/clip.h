@@ -1,4 +1,4 @@
-// Gradient clipping over a list of tensors: launcher (clip.hip).
+// Gradient clipping over a list of tensors: its table and launcher (clip.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -10,16 +10,13 @@ struct ClipEntry {
     const void *g;
     void *out;           // may be g
     int64_t numel;
-    int64_t chunk;       // chunks of the tensors before it
-    int32_t f32, pad;
+    int64_t chunk;       // chunks of the tensors before it, times two; + 1: float32
 };
-constexpr int kClipList = 96;        // entries of a launch that writes the list: 3840 bytes of arguments
-constexpr int kClipParts = 2048;     // workgroups of a pass at most
+constexpr int kClipChunk = 8192;     // elements
+constexpr int kClipParts = 2048;     // workgroups of a pass at most: eight on each CU
 
-int64_t clip_chunks(int64_t numel);
-// get(i): entry i of the caller's list (its chunk field is filled here); list: device [n]; part: device
-// [kClipParts]
-hipError_t launch_clip(ClipEntry (*get)(const void *, int32_t), const void *ctx, int32_t n, float max_norm, float *norm,
-                       ClipEntry *list, double *part, hipStream_t stream);
+// table: device [n]; part: device [kClipParts]
+hipError_t launch_clip(const ClipEntry *table, int32_t n, int64_t chunks, float max_norm, float *norm, double *part,
+                       hipStream_t stream);
 
 }  // namespace nf4k

@@ -7,8 +7,9 @@
 // (the stream leaves room for some 60 operations an element).  Each workgroup leaves one partial sum; the
 // second pass sums them again in every workgroup, in a fixed order, which is cheaper than a launch between.
 //
-// The list itself (pointers, sizes) comes in kernel arguments, LIST entries a launch, and is written to the
-// workspace for the two passes.
+// The second pass walks backwards: what the first read last still lies in the memory-side cache.
+//
+// The list (pointers, sizes, first chunks) is a table in device memory that the caller keeps with the gradients.
 
 #include "common.h"
 #include "clip.h"
@@ -17,37 +18,94 @@ namespace nf4k {
 
 namespace {
 
-constexpr int CHUNK = 8192;      // elements; a workgroup's threads take 32 each
+constexpr int CHUNK = kClipChunk;      // a workgroup's threads take 32 elements each
 constexpr int NT = 256;
 
-struct ClipBatch {
-    ClipEntry e[kClipList];
-    int32_t first, n;
-};
+__device__ __forceinline__ int64_t first(const ClipEntry &e) { return e.chunk >> 1; }
 
-__global__ __launch_bounds__(64) void clip_list_kernel(ClipBatch b, ClipEntry *list) {
-    for (int i = threadIdx.x; i < b.n; i += 64) list[b.first + i] = b.e[i];
-}
-
-// the tensor that holds chunk c
+// the tensor that holds chunk c: the last one that begins at or before it (tensors without elements have no chunk)
 __device__ __forceinline__ int find(const ClipEntry *list, int n, int64_t c) {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (list[mid].chunk <= c) lo = mid;
+        if (first(list[mid]) <= c) lo = mid;
         else hi = mid - 1;
     }
     return lo;
 }
 
-// f(element index, value) over a chunk of a tensor
-template <class T, class F>
-__device__ __forceinline__ void each(const void *base, int64_t i0, int64_t i1, F f) {
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += NT) f(i, reinterpret_cast<const T *>(base)[i]);
-}
-
 __device__ __forceinline__ float value(uint16_t x) { return bf16_to_f32(x); }
 __device__ __forceinline__ float value(float x) { return x; }
+__device__ __forceinline__ float rounded(float x, float) { return x; }
+__device__ __forceinline__ uint16_t rounded(float x, uint16_t) { return (uint16_t)f32_to_bf16(x); }
+
+// A chunk's elements as 16-byte vectors: VEC of them to a vector, PER vectors to a thread, whose loads are all
+// issued before the first is used.
+template <class T>
+struct Vec {
+    static constexpr int VEC = 16 / (int)sizeof(T), PER = CHUNK / NT / VEC;
+    typedef T type __attribute__((ext_vector_type(VEC)));
+};
+
+// first elements of a chunk before its address is a multiple of 16 bytes
+template <class T>
+__device__ __forceinline__ int head(const T *p) {
+    return (int)(((16 - ((uintptr_t)p & 15u)) & 15u) / sizeof(T));
+}
+
+template <class T>
+__device__ __forceinline__ double squares(const T *p, int n) {
+    typedef typename Vec<T>::type V;
+    constexpr int VEC = Vec<T>::VEC, PER = Vec<T>::PER;
+    const int tid = threadIdx.x;
+    double s = 0.0;
+    auto add = [&](T x) {
+        const double v = (double)value(x);
+        s = __builtin_fma(v, v, s);
+    };
+    const int h = min(head(p), n), nv = (n - h) / VEC;
+    const V *q = reinterpret_cast<const V *>(p + h);
+    V v[PER];
+#pragma unroll
+    for (int u = 0; u < PER; ++u) v[u] = u * NT + tid < nv ? q[u * NT + tid] : (V)(T)0;
+    if (tid < h) add(p[tid]);
+    const int rest = h + nv * VEC + tid;
+    if (rest < n) add(p[rest]);
+#pragma unroll
+    for (int u = 0; u < PER; ++u)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) add(v[u][k]);
+    return s;
+}
+
+template <class T>
+__device__ __forceinline__ void scale(const T *p, T *o, int n, bool clip, double f) {
+    typedef typename Vec<T>::type V;
+    constexpr int VEC = Vec<T>::VEC, PER = Vec<T>::PER;
+    const int tid = threadIdx.x;
+    auto to = [&](T x) { return clip ? rounded((float)((double)value(x) * f), x) : x; };
+    int h = 0, nv = 0;
+    // where the two addresses differ modulo 16 bytes, element by element
+    if ((((uintptr_t)p ^ (uintptr_t)o) & 15u) == 0) {
+        h = min(head(p), n);
+        nv = (n - h) / VEC;
+        const V *q = reinterpret_cast<const V *>(p + h);
+        V *w = reinterpret_cast<V *>(o + h);
+        V v[PER];
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+            if (u * NT + tid < nv) v[u] = q[u * NT + tid];
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            if (u * NT + tid >= nv) continue;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[u][k] = to(v[u][k]);
+            w[u * NT + tid] = v[u];
+        }
+        if (tid < h) o[tid] = to(p[tid]);
+    }
+    for (int i = h + nv * VEC + tid; i < n; i += NT) o[i] = to(p[i]);
+}
 
 __global__ __launch_bounds__(NT) void clip_norm_kernel(const ClipEntry *__restrict__ list, int n, int64_t chunks,
                                                        double *__restrict__ part) {
@@ -57,15 +115,11 @@ __global__ __launch_bounds__(NT) void clip_norm_kernel(const ClipEntry *__restri
     if (c0 < c1) {
         int t = find(list, n, c0);
         for (int64_t c = c0; c < c1; ++c) {
-            while (t + 1 < n && list[t + 1].chunk <= c) ++t;
+            while (t + 1 < n && first(list[t + 1]) <= c) ++t;
             const ClipEntry e = list[t];
-            const int64_t i0 = (c - e.chunk) * CHUNK, i1 = min(i0 + CHUNK, e.numel);
-            auto add = [&](int64_t, auto x) {
-                const double v = (double)value(x);
-                s = __builtin_fma(v, v, s);
-            };
-            if (e.f32) each<float>(e.g, i0, i1, add);
-            else each<uint16_t>(e.g, i0, i1, add);
+            const int64_t i0 = (c - first(e)) * CHUNK, i1 = min(i0 + CHUNK, e.numel);
+            if (e.chunk & 1) s += squares(reinterpret_cast<const float *>(e.g) + i0, (int)(i1 - i0));
+            else s += squares(reinterpret_cast<const uint16_t *>(e.g) + i0, (int)(i1 - i0));
         }
     }
     sh[threadIdx.x] = s;
@@ -97,45 +151,26 @@ __global__ __launch_bounds__(NT) void clip_scale_kernel(const ClipEntry *__restr
     const double f = clip ? (double)max_norm / norm : 1.0;
     const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
     if (c0 >= c1) return;
-    int t = find(list, n, c0);
-    for (int64_t c = c0; c < c1; ++c) {
-        while (t + 1 < n && list[t + 1].chunk <= c) ++t;
+    int t = find(list, n, c1 - 1);
+    for (int64_t c = c1 - 1; c >= c0; --c) {
+        while (first(list[t]) > c) --t;
         const ClipEntry e = list[t];
         if (!clip && e.out == e.g) continue;
-        const int64_t i0 = (c - e.chunk) * CHUNK, i1 = min(i0 + CHUNK, e.numel);
-        if (e.f32) each<float>(e.g, i0, i1, [&](int64_t i, float x) { reinterpret_cast<float *>(e.out)[i] = clip ? (float)((double)x * f) : x; });
-        else
-            each<uint16_t>(e.g, i0, i1, [&](int64_t i, uint16_t x) {
-                reinterpret_cast<uint16_t *>(e.out)[i] = clip ? (uint16_t)f32_to_bf16((float)((double)bf16_to_f32(x) * f)) : x;
-            });
+        const int64_t i0 = (c - first(e)) * CHUNK, i1 = min(i0 + CHUNK, e.numel);
+        if (e.chunk & 1) scale(reinterpret_cast<const float *>(e.g) + i0, reinterpret_cast<float *>(e.out) + i0, (int)(i1 - i0), clip, f);
+        else scale(reinterpret_cast<const uint16_t *>(e.g) + i0, reinterpret_cast<uint16_t *>(e.out) + i0, (int)(i1 - i0), clip, f);
     }
 }
 
 }  // namespace
 
-int64_t clip_chunks(int64_t numel) { return (numel + CHUNK - 1) / CHUNK; }
-
-hipError_t launch_clip(ClipEntry (*get)(const void *, int32_t), const void *ctx, int32_t n, float max_norm, float *norm,
-                       ClipEntry *list, double *part, hipStream_t stream) {
-    int64_t chunks = 0;
-    for (int32_t i = 0; i < n; i += kClipList) {
-        ClipBatch b{};
-        b.first = i;
-        b.n = n - i < kClipList ? n - i : kClipList;
-        for (int k = 0; k < b.n; ++k) {
-            b.e[k] = get(ctx, i + k);
-            b.e[k].chunk = chunks;
-            chunks += clip_chunks(b.e[k].numel);
-        }
-        hipLaunchKernelGGL(clip_list_kernel, dim3(1), dim3(64), 0, stream, b, list);
-        const hipError_t rc = hipGetLastError();
-        if (rc != hipSuccess) return rc;
-    }
+hipError_t launch_clip(const ClipEntry *table, int32_t n, int64_t chunks, float max_norm, float *norm, double *part,
+                       hipStream_t stream) {
     const int grid = (int)(chunks < kClipParts ? (chunks > 0 ? chunks : 1) : kClipParts);
-    hipLaunchKernelGGL(clip_norm_kernel, dim3(grid), dim3(NT), 0, stream, list, n, chunks, part);
-    hipError_t rc = hipGetLastError();
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(grid), dim3(NT), 0, stream, table, n, chunks, part);
+    const hipError_t rc = hipGetLastError();
     if (rc != hipSuccess) return rc;
-    hipLaunchKernelGGL(clip_scale_kernel, dim3(grid), dim3(NT), 0, stream, list, n, chunks, part, grid, max_norm, norm);
+    hipLaunchKernelGGL(clip_scale_kernel, dim3(grid), dim3(NT), 0, stream, table, n, chunks, part, grid, max_norm, norm);
     return hipGetLastError();
 }
 

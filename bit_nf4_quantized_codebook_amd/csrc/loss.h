@@ -16,12 +16,14 @@ namespace nf4k {
 constexpr int LT = 256;                  // tokens, vocabulary rows or columns of dX of a tile
 constexpr int LSTEP = 64;                // reduction of one step of a tile's loop
 constexpr int64_t LBLOCK = LT * LSTEP;   // elements of one step's operand tile (32 KB)
+constexpr int kLossJoinRows = 16;        // rows of a workgroup that joins the tiles
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Per-row state in the workspace; row arrays have Mp = M rounded up to 256 entries.
 struct LossRows {
-    int32_t *count;        // [0]: live rows; [1]: workgroups of the last join that are done
+    int32_t *count;        // [0]: live rows; [1]: the last piece with a tile that needs rescaling
+    double *sums;          // [ceil(M / kLossJoinRows)] sums of the losses of each workgroup of the last join
     int32_t *row;          // [M] live row -> token
     int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
     float *zl;             // [M] the label's logit in log2 units
@@ -47,21 +49,28 @@ struct LogitsArgs {
     int32_t Mp;
     int32_t tile0, ntile;     // vocabulary tiles of this launch
     int32_t table0;           // the tile whose entries stand first in tref and tsum (and in P)
-    const float *ref;         // [M] references, or NULL: each tile takes its own maximum
+    const float *ref;         // [M] references, or NULL: 0
     float *tref, *tsum;       // [tiles][Mp]: a tile's reference and its sum of 2^(l - reference)
     uint16_t *P;              // 2^(l - reference) in bf16, or NULL; blocks of one step (see loss_logits.hip)
     int32_t psteps;           // steps of P's row of blocks
 };
 hipError_t launch_loss_logits(const LogitsArgs &a, hipStream_t stream);
 
+// dX's product over a piece.  Where a tile's reduction is not split, the product itself adds what earlier pieces
+// left (sum32, moved from the references c_old to c) and writes sum32 or, with the last piece, dX.
 struct LossDxArgs {
     const uint16_t *P, *W;
     int64_t V, K, v0;         // v0: first vocabulary row of the piece
-    const int32_t *count;
+    LossRows r;
     int32_t Mp, steps;
-    float *part;              // [split][tile] blocks of 256 x 256 float32 (row: token)
+    float *part;              // split: [split][tile] blocks of 256 x 256 float32 (row: token)
+    float *sum32;             // [Mp, K]; NULL: one piece only
+    const float *c, *c_old;   // c_old NULL: the first piece
+    uint16_t *dX;             // NULL: not the last piece
 };
 hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream);
+// the same for a split reduction, from its partials (nothing to do without a split)
+hipError_t launch_loss_fold(const LossDxArgs &a, hipStream_t stream);
 
 // labels -> live rows; loss and dX of the other tokens set to zero
 hipError_t launch_loss_prep(const int64_t *labels, int64_t M, int64_t V, int64_t K, const LossRows &r, float *loss,
@@ -75,26 +84,22 @@ struct LossJoin {
     int32_t ntile;
     const float *c_in;
     float *c_out;
-    // the last join: losses, their mean, and with grad the coefficients of dX
+    int32_t piece;            // from 1
+    // the last join: losses, the sums for their mean, and with grad the coefficients of dX
     bool last, grad;
     const float *dloss;
     float *loss, *mean;
 };
 hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream);
-// P's tiles brought from their own references to the rows'
-hipError_t launch_loss_rescale(uint16_t *P, const float *tref, const float *c, const int32_t *count, int32_t Mp,
-                               int32_t ntile, hipStream_t stream);
-// dX's partials summed: into sum32 (with what it holds, from the references c_old to c), or as the result
-struct LossFold {
+// P's tiles brought from their own references to the rows', where any differs; mean (or NULL) from the sums
+struct LossRescale {
     LossRows r;
-    const float *part;
-    int64_t K;
-    int32_t Mp, steps;
-    float *sum32;             // [Mp, K], or NULL: one piece only
-    const float *c, *c_old;   // c_old NULL: the first piece
-    const uint16_t *W;
-    uint16_t *dX;             // NULL: not the last piece
+    int64_t M;
+    int32_t Mp, ntile, piece;
+    uint16_t *P;              // NULL: only the mean
+    const float *tref, *c;
+    float *mean;
 };
-hipError_t launch_loss_fold(const LossFold &a, hipStream_t stream);
+hipError_t launch_loss_rescale(const LossRescale &a, hipStream_t stream);
 
 }  // namespace nf4k

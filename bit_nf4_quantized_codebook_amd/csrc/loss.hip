@@ -14,17 +14,19 @@ namespace nf4k {
 namespace {
 
 constexpr int PREP = 1024;
+constexpr int PREP_REST = 128;       // workgroups that clear the rows without a label, a wave a row
 
 // Workgroup 0: the live rows, in order.  The others: loss and dX of the rest set to zero.
 __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restrict__ labels, int64_t M, int64_t V, int64_t K,
                                                          LossRows r, float *__restrict__ loss, uint16_t *__restrict__ dX) {
     const int tid = threadIdx.x;
     if (blockIdx.x > 0) {
-        for (int64_t m = blockIdx.x - 1; m < M; m += gridDim.x - 1) {
+        const int lane = tid & 63;
+        for (int64_t m = (int64_t)(blockIdx.x - 1) * (PREP / 64) + (tid >> 6); m < M; m += (int64_t)(gridDim.x - 1) * (PREP / 64)) {
             if (labels[m] >= 0) continue;
-            if (tid == 0) loss[m] = 0.0f;
+            if (lane == 0) loss[m] = 0.0f;
             if (dX)
-                for (int64_t k = tid * 8; k < K; k += PREP * 8) *reinterpret_cast<u32x4 *>(dX + m * K + k) = u32x4{0, 0, 0, 0};
+                for (int64_t k = lane * 8; k < K; k += 64 * 8) *reinterpret_cast<u32x4 *>(dX + m * K + k) = u32x4{0, 0, 0, 0};
         }
         return;
     }
@@ -55,137 +57,132 @@ __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restri
     }
 }
 
-constexpr int JR = 32, JS = 8;      // rows of a workgroup, and threads over the tiles of a row
+constexpr int JR = kLossJoinRows, JS = 256 / JR;      // rows of a workgroup, and threads over the tiles of a row
 
-__global__ __launch_bounds__(JR * JS) void loss_join_kernel(LossJoin g) {
-    __shared__ float part[JS][JR];
-    __shared__ double total[JR * JS];
-    __shared__ bool final_wg;
+__device__ __forceinline__ void write_mean(const double *sums, int n, int count, float *mean) {
+    __shared__ double total[256];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += 256) s += sums[i];
+    total[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 128; d > 0; d >>= 1) {
+        if ((int)threadIdx.x < d) total[threadIdx.x] += total[threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) mean[0] = count ? (float)(total[0] / count) : 0.0f;
+}
+
+__global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
+    __shared__ float pc[JS][JR], ps[JS][JR];
+    __shared__ double sl[JR];
     const int count = g.r.count[0];
     const int tid = threadIdx.x, lr = tid % JR, slice = tid / JR;
     const int row = blockIdx.x * JR + lr;
     const bool live = row < count;
-    const int nwg = (count + JR - 1) / JR;
-    if ((int)blockIdx.x >= nwg && !(g.last && blockIdx.x == 0)) return;
-
-    // the new reference: the old one unless a tile went past it
+    if ((int)blockIdx.x * JR >= count) {
+        if (g.last && tid == 0) {
+            g.r.sums[blockIdx.x] = 0.0;
+            if (gridDim.x == 1) g.mean[0] = 0.0f;
+        }
+        return;
+    }
     const float NEG = -__builtin_inff();
     const float c_old = g.c_in && live ? g.c_in[row] : NEG;
-    float c = c_old;
+    // the new reference: the largest there is; eight tiles' loads at a time
+    float c = c_old, sum = 0.0f, low = -NEG;
     if (live)
-        for (int t = slice; t < g.ntile; t += JS) c = fmaxf(c, g.tref[(int64_t)t * g.Mp + row]);
-    part[slice][lr] = c;
-    __syncthreads();
+        for (int t0 = slice; t0 < g.ntile; t0 += JS * 8) {
+            float f[8], s[8], m = c;
 #pragma unroll
-    for (int s = 0; s < JS; ++s) c = fmaxf(c, part[s][lr]);
-    __syncthreads();
-    float sum = 0.0f;
-    if (live)
-        for (int t = slice; t < g.ntile; t += JS) {
-            const int64_t o = (int64_t)t * g.Mp + row;
-            sum += g.tsum[o] * __builtin_amdgcn_exp2f(g.tref[o] - c);
+            for (int u = 0; u < 8; ++u) {
+                const int t = t0 + u * JS;
+                const int64_t o = (int64_t)t * g.Mp + row;
+                f[u] = t < g.ntile ? g.tref[o] : NEG;
+                s[u] = t < g.ntile ? g.tsum[o] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                m = fmaxf(m, f[u]);
+                low = fminf(low, t0 + u * JS < g.ntile ? f[u] : -NEG);
+            }
+            // c = m also before the first tile, where there is nothing to move (and both may be -inf)
+            sum *= m == c ? 1.0f : __builtin_amdgcn_exp2f(c - m);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (t0 + u * JS < g.ntile) sum += s[u] * __builtin_amdgcn_exp2f(f[u] - m);
+            c = m;
         }
-    part[slice][lr] = sum;
+    pc[slice][lr] = c;
+    ps[slice][lr] = sum;
     __syncthreads();
-    if (slice == 0 && live) {
-        float S = g.c_in ? g.r.S[row] * __builtin_amdgcn_exp2f(c_old - c) : 0.0f;
+    float top = c_old;
 #pragma unroll
-        for (int s = 0; s < JS; ++s) S += part[s][lr];
-        g.r.S[row] = S;
-        g.c_out[row] = c;
-        if (g.last) {
-            const float zl = g.r.zl[row];
-            // ln S + (c - zl) ln 2
-            const float d = (log2f(S) + (c - zl)) * kLn2;
-            const int32_t m = g.r.row[row];
-            g.loss[m] = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
-            if (g.grad) {
-                const float w = g.dloss ? g.dloss[m] : 1.0f / (float)count;
-                g.r.a[row] = w / (S + __builtin_amdgcn_exp2f(zl - c));
-                g.r.b[row] = w / (1.0f + expf(-d));
+    for (int s = 0; s < JS; ++s) top = fmaxf(top, pc[s][lr]);
+    // a tile (or, in earlier pieces' order, nothing else) below the row's reference: P has to be rescaled
+    if (g.grad && live && !(low >= top)) g.r.count[1] = g.piece;
+    if (slice == 0) {
+        double value = 0.0;
+        if (live) {
+            float S = g.c_in ? g.r.S[row] * __builtin_amdgcn_exp2f(c_old - top) : 0.0f;
+#pragma unroll
+            for (int s = 0; s < JS; ++s) S += ps[s][lr] == 0.0f ? 0.0f : ps[s][lr] * __builtin_amdgcn_exp2f(pc[s][lr] - top);
+            g.r.S[row] = S;
+            g.c_out[row] = top;
+            if (g.last) {
+                const float zl = g.r.zl[row];
+                // ln S + (c - zl) ln 2
+                const float d = (log2f(S) + (top - zl)) * kLn2;
+                const int32_t m = g.r.row[row];
+                const float loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
+                g.loss[m] = loss;
+                value = (double)loss;
+                if (g.grad) {
+                    const float w = g.dloss ? g.dloss[m] : 1.0f / (float)count;
+                    g.r.a[row] = w / (S + __builtin_amdgcn_exp2f(zl - top));
+                    g.r.b[row] = w / (1.0f + expf(-d));
+                }
             }
         }
+        sl[lr] = value;
     }
     if (!g.last) return;
-    // the workgroup that ends last sums the losses, in a fixed order
-    __threadfence();
     __syncthreads();
-    if (tid == 0) final_wg = atomicAdd(&g.r.count[1], 1) + 1 == (nwg > 0 ? nwg : 1);
-    __syncthreads();
-    if (!final_wg) return;
-    __threadfence();
-    double s = 0.0;
-    for (int i = tid; i < count; i += JR * JS)
-        s += (double)__hip_atomic_load(&g.loss[g.r.row[i]], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    total[tid] = s;
-    __syncthreads();
-    for (int d = JR * JS / 2; d > 0; d >>= 1) {
-        if (tid < d) total[tid] += total[tid + d];
-        __syncthreads();
+    if (tid == 0) {
+        double s = 0.0;
+        for (int i = 0; i < JR; ++i) s += sl[i];
+        g.r.sums[blockIdx.x] = s;
+        if (gridDim.x == 1) g.mean[0] = (float)(s / count);
     }
-    if (tid == 0) g.mean[0] = count ? (float)(total[0] / count) : 0.0f;
 }
 
-// One workgroup for 256 rows and one tile of the vocabulary: four blocks of P.
-__global__ __launch_bounds__(256) void loss_rescale_kernel(uint16_t *__restrict__ P, const float *__restrict__ tref,
-                                                           const float *__restrict__ c, const int32_t *__restrict__ cnt,
-                                                           int32_t Mp, int32_t ntile) {
+// Grid-stride over tiles (256 rows and 256 vocabulary rows: four blocks of P); workgroup 0 also writes the mean.
+__global__ __launch_bounds__(256) void loss_rescale_kernel(LossRescale g) {
     __shared__ float f[LT];
-    const int count = cnt[0], tid = threadIdx.x;
-    const int tm = blockIdx.x / ntile, t = blockIdx.x % ntile;
-    if (tm * LT >= count) return;
-    const int row = tm * LT + tid;
-    const float from = row < count ? tref[(int64_t)t * Mp + row] : 0.0f, to = row < count ? c[row] : 0.0f;
-    f[tid] = __builtin_amdgcn_exp2f(from - to);
-    if (!__syncthreads_or(!(from == to))) return;
-    uint16_t *base = P + ((int64_t)tm * ntile + t) * 4 * LBLOCK;
-    for (int i = tid; i < 4 * LBLOCK / 8; i += 256) {
-        const float s = f[(i >> 3) & (LT - 1)];     // 8 chunks a row, 256 rows a block
-        u32x4 v = reinterpret_cast<u32x4 *>(base)[i];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            v[k] = pack_bf16x2(bf16_to_f32(v[k] & 0xFFFFu) * s, __uint_as_float(v[k] & 0xFFFF0000u) * s);
-        reinterpret_cast<u32x4 *>(base)[i] = v;
+    const int count = g.r.count[0], tid = threadIdx.x;
+    if (g.mean && blockIdx.x == 0) {
+        write_mean(g.r.sums, (int)((g.M + JR - 1) / JR), count, g.mean);
+        return;
     }
-}
-
-__global__ __launch_bounds__(256) void loss_fold_kernel(LossFold g) {
-    const int count = g.r.count[0];
-    const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT), tiles = ntm * ntn;
-    const LossSplit sp = loss_split(tiles, g.steps);
-    const int k8 = (int)(g.K >> 3);
-    const int64_t n = (int64_t)count * k8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int row = (int)(i / k8), k = (int)(i % k8) * 8;
-        const float *p = g.part + ((int64_t)(row / LT) * ntn + k / LT) * (LT * LT) + (row % LT) * LT + k % LT;
-        f32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
-        if (g.c_old) {
-            const float s = __builtin_amdgcn_exp2f(g.c_old[row] - g.c[row]);
-            const f32x4 *o = reinterpret_cast<const f32x4 *>(g.sum32 + (int64_t)row * g.K + k);
-            lo = o[0] * s;
-            hi = o[1] * s;
-        }
-        for (int s = 0; s < sp.ks; ++s) {
-            const f32x4 *q = reinterpret_cast<const f32x4 *>(p + (int64_t)s * tiles * (LT * LT));
-            lo += q[0];
-            hi += q[1];
-        }
-        if (!g.dX) {
-            f32x4 *o = reinterpret_cast<f32x4 *>(g.sum32 + (int64_t)row * g.K + k);
-            o[0] = lo;
-            o[1] = hi;
-            continue;
-        }
-        const float a = g.r.a[row], b = g.r.b[row];
-        const int32_t lab = g.r.label[row];
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(g.W + (int64_t)(lab < 0 ? 0 : lab) * g.K + k);
-        u32x4 out;
+    if (!g.P || g.r.count[1] != g.piece) return;
+    const int first = g.mean ? 1 : 0, ntm = (count + LT - 1) / LT;
+    for (int x = blockIdx.x - first; x < ntm * g.ntile; x += gridDim.x - first) {
+        const int tm = x / g.ntile, t = x % g.ntile;
+        const int row = tm * LT + tid;
+        const float from = row < count ? g.tref[(int64_t)t * g.Mp + row] : 0.0f, to = row < count ? g.c[row] : 0.0f;
+        f[tid] = __builtin_amdgcn_exp2f(from - to);
+        const bool any = __syncthreads_or(!(from == to));
+        if (any) {
+            uint16_t *base = g.P + ((int64_t)tm * g.ntile + t) * 4 * LBLOCK;
+            for (int i = tid; i < 4 * LBLOCK / 8; i += 256) {
+                const float s = f[(i >> 3) & (LT - 1)];     // 8 chunks a row, 256 rows a block
+                u32x4 v = reinterpret_cast<u32x4 *>(base)[i];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = j < 2 ? lo[2 * j] : hi[2 * j - 4], y = j < 2 ? lo[2 * j + 1] : hi[2 * j - 3];
-            out[j] = pack_bf16x2(a * x - b * bf16_to_f32(w[j] & 0xFFFFu), a * y - b * __uint_as_float(w[j] & 0xFFFF0000u));
+                for (int k = 0; k < 4; ++k)
+                    v[k] = pack_bf16x2(bf16_to_f32(v[k] & 0xFFFFu) * s, __uint_as_float(v[k] & 0xFFFF0000u) * s);
+                reinterpret_cast<u32x4 *>(base)[i] = v;
+            }
         }
-        *reinterpret_cast<u32x4 *>(g.dX + (int64_t)g.r.row[row] * g.K + k) = out;
+        __syncthreads();
     }
 }
 
@@ -193,26 +190,19 @@ __global__ __launch_bounds__(256) void loss_fold_kernel(LossFold g) {
 
 hipError_t launch_loss_prep(const int64_t *labels, int64_t M, int64_t V, int64_t K, const LossRows &r, float *loss,
                             uint16_t *dX, hipStream_t stream) {
-    const uint32_t rest = (uint32_t)(M < 2048 ? M : 2048);
-    hipLaunchKernelGGL(loss_prep_kernel, dim3(1 + rest), dim3(PREP), 0, stream, labels, M, V, K, r, loss, dX);
+    const int64_t rest = (M + PREP / 64 - 1) / (PREP / 64);
+    hipLaunchKernelGGL(loss_prep_kernel, dim3(1 + (uint32_t)(rest < PREP_REST ? rest : PREP_REST)), dim3(PREP), 0, stream,
+                       labels, M, V, K, r, loss, dX);
     return hipGetLastError();
 }
 
 hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream) {
-    hipLaunchKernelGGL(loss_join_kernel, dim3((uint32_t)((a.M + JR - 1) / JR)), dim3(JR * JS), 0, stream, a);
+    hipLaunchKernelGGL(loss_join_kernel, dim3((uint32_t)((a.M + JR - 1) / JR)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
-hipError_t launch_loss_rescale(uint16_t *P, const float *tref, const float *c, const int32_t *count, int32_t Mp,
-                               int32_t ntile, hipStream_t stream) {
-    hipLaunchKernelGGL(loss_rescale_kernel, dim3((uint32_t)(Mp / LT) * (uint32_t)ntile), dim3(256), 0, stream, P, tref, c,
-                       count, Mp, ntile);
-    return hipGetLastError();
-}
-
-hipError_t launch_loss_fold(const LossFold &a, hipStream_t stream) {
-    const int64_t blocks = ((int64_t)a.Mp * (a.K >> 3) + 255) / 256;
-    hipLaunchKernelGGL(loss_fold_kernel, dim3((uint32_t)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, stream, a);
+hipError_t launch_loss_rescale(const LossRescale &a, hipStream_t stream) {
+    hipLaunchKernelGGL(loss_rescale_kernel, dim3(a.P ? 1024 : 1), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

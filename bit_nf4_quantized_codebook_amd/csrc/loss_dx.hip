@@ -7,10 +7,10 @@
 // four rows that half a wave reads at once lie in different banks.  P's blocks are copied as they are.
 //
 // The MFMAs take W's columns as the first operand and the tokens as the second: a lane holds four
-// consecutive columns of a token.
+// consecutive columns of a token; the results are turned through LDS into rows.
 //
 // Few tiles (the live rows are counted on the device): a tile's reduction is split over several
-// workgroups; all write float32 partials, which loss_fold_kernel sums in a fixed order.
+// workgroups, which write float32 partials, and loss_fold_kernel sums them in a fixed order.
 
 #include "common.h"
 #include "dqtile.h"
@@ -21,13 +21,22 @@ namespace nf4k {
 
 namespace {
 
+// A token's last step: dX = a (sum P W) - b W[label], rounded once.
+struct LossFinal {
+    float a, b;
+    __device__ __forceinline__ uint2 value(const f32x4 &x, const uint2 &v) const {
+        return uint2{pack_bf16x2(a * x[0] - b * bf16_to_f32(v.x & 0xFFFFu), a * x[1] - b * __uint_as_float(v.x & 0xFFFF0000u)),
+                     pack_bf16x2(a * x[2] - b * bf16_to_f32(v.y & 0xFFFFu), a * x[3] - b * __uint_as_float(v.y & 0xFFFF0000u))};
+    }
+};
+
 __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     __shared__ __align__(16) uint8_t As0[LBLOCK * 2];
     __shared__ __align__(16) uint8_t As1[LBLOCK * 2];
     __shared__ __align__(16) uint8_t Bs0[LBLOCK * 2];
     __shared__ __align__(16) uint8_t Bs1[LBLOCK * 2];
 
-    const int count = __builtin_amdgcn_readfirstlane(g.count[0]);
+    const int count = __builtin_amdgcn_readfirstlane(g.r.count[0]);
     const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT);
     const int tiles = ntm * ntn;
     const LossSplit sp = loss_split(tiles, g.steps);
@@ -63,15 +72,15 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     const uint32_t boff = (uint32_t)(wave * 8192 + lane * 16);
     auto load = [&](int step, uint8_t *A, uint8_t *B, int q0, int q1) {
         lds_u8 *da = (lds_u8 *)A + wave * 8192, *db = (lds_u8 *)B + wave * 8192;
-        const bool live = step < steps;
+        const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past every descriptor's end
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if (q < q0 || q >= q1) continue;
             // rows 2q and 2q + 1 of the wave's 16: q and q + 2 share row % 4
             const uint32_t v = aoff[q & 1] + (uint32_t)(q >> 1) * row4_off + (uint32_t)step * step_off;
             const uint32_t x = boff + (uint32_t)q * 1024u + (uint32_t)step * (uint32_t)(LBLOCK * 2);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + q * 1024), 16, live && aoff[q & 1] != 0x80000000u ? v : 0x80000000u, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, live ? x : 0x80000000u, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + q * 1024), 16, v | dead, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, x | dead, 0, 0, 0);
         }
     };
     // W's fragment of sub-step s, columns wm*128 + 32 i ..: 16-lane group (hh, half) reads rows
@@ -104,18 +113,107 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
     loss_loop<12>(steps, As0, Bs0, As1, Bs1, acc, load, read);
 
-    // lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and columns wm*128 + 32 i + 8 (v/4) + 4 hh + v%4
-    float *out = g.part + ((int64_t)split * tiles + (int64_t)tm * ntn + tn) * (LT * LT);
+    // Lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and columns wm*128 + 32 i + 8 (v/4) + 4 hh + v%4.
+    // Each wave turns its 128 x 128 values in its own stage of LDS, 64 tokens at a time, into rows of 512 bytes (their
+    // 16-byte chunks XOR-swizzled by the row), so that all that follows moves whole lines, two tokens at a time.
     const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    const int c32 = lane_e & 31, he = lane_e >> 5;
+    uint8_t *turn = wave == 0 ? As0 : (wave == 1 ? As1 : (wave == 2 ? Bs0 : Bs1));
+    const bool split_up = sp.ks > 1, add = !split_up && g.c_old, last = !split_up && g.dX;
+    // K is a multiple of 64: what lies past it are whole lanes here
+    const int64_t col = n0 + wm * 128 + 4 * c32;
+    const bool in = split_up || col < g.K;
+    const int64_t colc = in ? col : 0, ld = split_up ? LT : g.K;
+    float *dst32 = split_up ? g.part + ((int64_t)split * tiles + (int64_t)tm * ntn + tn) * (LT * LT) + wm * 128 + 4 * c32
+                            : g.sum32 + (int64_t)tm * LT * g.K + colc;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float *p = out + (wn * 128 + 32 * j + (lane_e & 31)) * LT + wm * 128 + 4 * (lane_e >> 5);
+    for (int jh = 0; jh < 2; ++jh) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4)
-                *reinterpret_cast<f32x4 *>(p + 32 * i + 8 * v4) =
-                    f32x4{acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int v4 = 0; v4 < 4; ++v4) {
+                    const f32x16 &x = acc[i][2 * jh + j];
+                    *reinterpret_cast<f32x4 *>(turn + (32 * j + c32) * 512 + (((8 * i + 2 * v4 + he) ^ c32) * 16)) =
+                        f32x4{x[4 * v4], x[4 * v4 + 1], x[4 * v4 + 2], x[4 * v4 + 3]};
+                }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        // lane l: what row l of these 64 needs (dead rows: row 0's, not stored)
+        const int r0 = wn * 128 + 64 * jh, live = count - tm * LT - r0;
+        const int tl = lane_e < live ? tm * LT + r0 + lane_e : 0;
+        const float move = add ? __builtin_amdgcn_exp2f(g.c_old[tl] - g.c[tl]) : 0.0f;
+        const float fa = last ? g.r.a[tl] : 0.0f, fb = last ? g.r.b[tl] : 0.0f;
+        const int frow = last ? g.r.row[tl] : 0, flab = last ? max(g.r.label[tl], 0) : 0;
+        auto of = [&](int v, int u) {      // row 2u's value in the lower half, row 2u + 1's in the upper
+            const int a = __builtin_amdgcn_readlane(v, 2 * u), b = __builtin_amdgcn_readlane(v, 2 * u + 1);
+            return he ? b : a;
+        };
+        auto off = [&](float v, int u) { return __int_as_float(of(__float_as_int(v), u)); };
+        // eight loads at a time: nothing tells the compiler that the stores between do not change what is read
+        constexpr int B = 8;
+#pragma unroll 1
+        for (int u0 = 0; u0 < 32; u0 += B) {
+            if (2 * u0 >= live) break;
+            f32x4 x[B], o[B];
+            uint2 w[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int r = 2 * (u0 + u) + he;
+                const int rc = r < live ? r0 + r : 0;
+                if (add) o[u] = *reinterpret_cast<const f32x4 *>(dst32 + (int64_t)rc * ld);
+                if (last) w[u] = *reinterpret_cast<const uint2 *>(g.W + (int64_t)of(flab, u0 + u) * g.K + colc);
+                x[u] = *reinterpret_cast<const f32x4 *>(turn + r * 512 + ((c32 ^ (r & 31)) * 16));
+            }
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int r = 2 * (u0 + u) + he;
+                if (add) x[u] += o[u] * off(move, u0 + u);
+                const LossFinal fin{off(fa, u0 + u), off(fb, u0 + u)};
+                const int row = of(frow, u0 + u);
+                if (r >= live || !in) continue;
+                if (last) *reinterpret_cast<uint2 *>(g.dX + (int64_t)row * g.K + col) = fin.value(x[u], w[u]);
+                else *reinterpret_cast<f32x4 *>(dst32 + (int64_t)(r0 + r) * ld) = x[u];
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+}
+
+__global__ __launch_bounds__(256) void loss_fold_kernel(LossDxArgs g) {
+    const int count = g.r.count[0];
+    const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT), tiles = ntm * ntn;
+    const LossSplit sp = loss_split(tiles, g.steps);
+    if (sp.ks == 1) return;
+    const int k4 = (int)(g.K >> 2);
+    const int64_t n = (int64_t)count * k4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int row = (int)(i / k4), k = (int)(i % k4) * 4;
+        const float *p = g.part + ((int64_t)(row / LT) * ntn + k / LT) * (LT * LT) + (row % LT) * LT + k % LT;
+        f32x4 x = *reinterpret_cast<const f32x4 *>(p);
+        // eight partials' loads at a time
+        for (int s0 = 1; s0 < sp.ks; s0 += 8) {
+            f32x4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (s0 + u < sp.ks) v[u] = *reinterpret_cast<const f32x4 *>(p + (int64_t)(s0 + u) * tiles * (LT * LT));
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (s0 + u < sp.ks) x += v[u];
+        }
+        f32x4 *sum = g.sum32 ? reinterpret_cast<f32x4 *>(g.sum32 + (int64_t)row * g.K + k) : nullptr;
+        if (g.c_old) x += *sum * __builtin_amdgcn_exp2f(g.c_old[row] - g.c[row]);
+        if (!g.dX) {
+            *sum = x;
+            continue;
+        }
+        // a label out of the vocabulary: a and b are NaN
+        const uint2 w = *reinterpret_cast<const uint2 *>(g.W + (int64_t)max(g.r.label[row], 0) * g.K + k);
+        *reinterpret_cast<uint2 *>(g.dX + (int64_t)g.r.row[row] * g.K + k) = LossFinal{g.r.a[row], g.r.b[row]}.value(x, w);
     }
 }
 
@@ -125,6 +223,12 @@ hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream) {
     const int64_t tiles = (int64_t)(a.Mp / LT) * ((a.K + LT - 1) / LT);
     const int64_t grid = tiles > 256 ? tiles : 256;
     hipLaunchKernelGGL(loss_dx_kernel, dim3((uint32_t)grid), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_fold(const LossDxArgs &a, hipStream_t stream) {
+    const int64_t blocks = ((int64_t)a.Mp * (a.K >> 2) + 255) / 256;
+    hipLaunchKernelGGL(loss_fold_kernel, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -25,8 +25,9 @@ namespace nf4k {
 
 namespace {
 
-// A row's reference is kept while no logit exceeds it by more than this (log2 units): p stays far from
-// bf16's and float32's limits (2^127), and a tile needs no rescaling.
+// A row's reference is kept while no logit exceeds it by more than this (log2 units): p stays far from bf16's and
+// float32's limits (2^127).  The first is 0, which lies within this of the largest logit of nearly every tile there
+// is (33 in natural units), and where it does not, the tile takes its own maximum and is rescaled afterwards.
 constexpr float kSlack = 48.0f;
 
 template <bool GRAD>
@@ -73,12 +74,13 @@ __global__ __launch_bounds__(256, 1) void loss_logits_kernel(LogitsArgs g) {
     auto load = [&](int step, uint8_t *A, uint8_t *B, int q0, int q1) {
         lds_u8 *da = (lds_u8 *)A + wave * 8192, *db = (lds_u8 *)B + wave * 8192;
         const uint32_t at = (uint32_t)step * (LSTEP * 2);
+        const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past every descriptor's end
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if (q < q0 || q >= q1) continue;
             const uint32_t v = voff[q & 1] + (uint32_t)q * row8_off + at, x = xoff[q] + at;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + q * 1024), 16, step < steps ? v : 0x80000000u, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, step < steps ? x : 0x80000000u, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + q * 1024), 16, v | dead, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, x | dead, 0, 0, 0);
         }
     };
     uint32_t lds_off[4];
@@ -127,11 +129,11 @@ __global__ __launch_bounds__(256, 1) void loss_logits_kernel(LogitsArgs g) {
         if (he == 0) red[0][wm][wn * 128 + 32 * j + c32] = z;
     }
     __syncthreads();
-    // a token's reference: the one it has, unless this tile goes past it by more than kSlack
+    // a token's reference: the one it has, or 0, unless this tile lies too far from it
     auto reference = [&](int tl) {
         const float top = fmaxf(red[0][0][tl], red[0][1][tl]) * kLog2e;
-        const float ref = g.ref && m0 + tl < count ? g.ref[m0 + tl] : NEG;
-        return top <= ref + kSlack ? ref : ceilf(top);
+        const float ref = g.ref ? (m0 + tl < count ? g.ref[m0 + tl] : 0.0f) : 0.0f;
+        return top <= ref + kSlack && (g.ref || top >= -kSlack) ? ref : ceilf(top);
     };
     const __amdgpu_buffer_rsrc_t rP = make_rsrc(
         GRAD ? g.P + ((int64_t)tm * g.psteps + (int64_t)(tn - g.table0) * 4 + wm * 2) * LBLOCK : nullptr, GRAD ? LBLOCK * 4 : 0);

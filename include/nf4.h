@@ -477,13 +477,23 @@ typedef struct qlora_grad {
 } qlora_grad;
 
 /*
- *   grads: HOST array of n tensors (0 <= n <= 2^20), read during the call only.  max_norm > 0; infinity:
- *      only the norm is wanted.  norm: device float32 [1].
- *   workspace: >= qlora_clip_workspace_size(n) bytes, 16-byte aligned; calls that may overlap need one each.
+ * The list as a table, made once for gradients that stay where they are.  Host-only and synchronous; the caller
+ * copies the table to the device and keeps it as long as the list is used.
+ *   grads: HOST array of n tensors, 0 <= n <= 2^20, 2^46 elements at most.
+ *   table: HOST memory of qlora_grad_table_size(n) bytes, 8-byte aligned.
+ *   chunks: HOST, written: the table's size in units of work, for qlora_clip_grads.
+ */
+size_t qlora_grad_table_size(int32_t n);
+int qlora_grad_table(const qlora_grad *grads, int32_t n, void *table, size_t table_bytes, int64_t *chunks);
+
+/*
+ *   table: the table on the device, 8-byte aligned;  n, chunks: as made.  max_norm > 0; infinity: only the norm is
+ *      wanted.  norm: device float32 [1].
+ *   workspace: >= qlora_clip_workspace_size() bytes, 16-byte aligned; calls that may overlap need one each.
  * Squares are summed and the products formed in float64, then rounded to the gradient's type.
  */
-size_t qlora_clip_workspace_size(int32_t n);
-int qlora_clip_grads(const qlora_grad *grads, int32_t n, float max_norm, float *norm, void *workspace,
+size_t qlora_clip_workspace_size(void);
+int qlora_clip_grads(const void *table, int32_t n, int64_t chunks, float max_norm, float *norm, void *workspace,
                      size_t workspace_bytes, void *stream);
 
 /*

@@ -134,7 +134,7 @@ def test_workspace_and_norm_given_other_stream_and_graph():
     assert len(lst) == 3 and lst.grads[0] is grads[0] and lst.outs[1] is outs[1]
     ref = nf4.qlora_clip_grads(lst, 1.0).clone()
     want = [o.clone() for o in outs]
-    n = nf4.qlora_clip_workspace_size(3)
+    n = nf4.qlora_clip_workspace_size()
     ws = torch.full((n + 64,), 0xA5, dtype=torch.uint8, device=DEV)
     norm = torch.zeros(1, device=DEV)
     torch.cuda.synchronize()

@@ -113,27 +113,44 @@ def _grads(*entries):
     return a
 
 
-def test_clip_refusals():
-    wsb = lib.qlora_clip_workspace_size(2)
-    assert wsb > lib.qlora_clip_workspace_size(0) > 0
-    assert lib.qlora_clip_workspace_size(-1) == 0 and lib.qlora_clip_workspace_size((1 << 20) + 1) == 0
+def test_grad_table_refusals():
+    size = lib.qlora_grad_table_size
+    assert size(-1) == 0 and size((1 << 20) + 1) == 0 and size(2) == 2 * size(1) == 2 * size(0)
     good = (0x100000, 0x100000, 10, 0)
+    table, chunks = np.zeros(size(3) // 8, np.int64), ctypes.c_int64(-1)
 
-    def clip(*entries, n=None, max_norm=1.0, norm=FAKE, ws=FAKE, size=wsb, null=False):
+    def make(*entries, n=None, null=False, at=0, bytes_=table.nbytes, out=True):
         a = _grads(*entries)
-        return lib.qlora_clip_grads(None if null else ctypes.addressof(a), len(entries) if n is None else n, max_norm, norm, ws, size, None)
+        return lib.qlora_grad_table(None if null else ctypes.addressof(a), len(entries) if n is None else n,
+                                    None if at is None else table.ctypes.data + at, bytes_,
+                                    ctypes.addressof(chunks) if out else None)
 
-    assert clip(good, n=-1) == ESHAPE and clip(good, n=(1 << 20) + 1) == EUNSUP
+    assert make(good, n=-1) == ESHAPE and make(good, n=(1 << 20) + 1) == EUNSUP
+    assert make(good, n=1, null=True) == ENULL and make(good, at=None) == ENULL and make(good, out=False) == ENULL
+    assert make(good, at=4) == EALIGN and make(good, good, bytes_=size(2) - 1) == EWS
+    assert make(good, (0x100000, 0x100000, 10, 2)) == EARG and make(good, (0x100000, 0x100000, -1, 0)) == ESHAPE
+    assert make(good, (None, 0x100000, 1, 0)) == ENULL and make(good, (0x100000, None, 1, 0)) == ENULL
+    assert make((0x100001, 0x100000, 1, 0)) == EALIGN and make((0x100000, 0x100001, 1, 0)) == EALIGN
+    assert make((0x100002, 0x100000, 1, 1)) == EALIGN and make((0x100000, 0x100002, 1, 1)) == EALIGN
+    assert make((0x100000, 0x100000, (1 << 46) + 1, 0)) == EUNSUP
+    assert make(good, (0x100000, 0x100000, 1 << 46, 1)) == EUNSUP
+    assert chunks.value == -1
+    assert make((0x100002, 0x100004, 3, 0), (None, None, 0, 1), (0x200004, 0x200004, 1 << 30, 1)) == OK and chunks.value > 1
+    assert make(null=True) == OK and chunks.value == 0
+
+
+def test_clip_refusals():
+    wsb = lib.qlora_clip_workspace_size()
+
+    def clip(table=FAKE, n=3, chunks=7, max_norm=1.0, norm=FAKE, ws=FAKE, size=wsb):
+        return lib.qlora_clip_grads(table, n, chunks, max_norm, norm, ws, size, None)
+
+    assert clip(n=-1) == ESHAPE and clip(chunks=-1) == ESHAPE and clip(n=0) == ESHAPE and clip(n=(1 << 20) + 1) == EUNSUP
     for bad in (0.0, -1.0, float("nan"), float("-inf")):
-        assert clip(good, max_norm=bad) == EARG
-    assert clip(good, norm=None) == ENULL and clip(good, n=1, null=True) == ENULL and clip(good, norm=ODD) == EALIGN
-    assert clip(good, (0x100000, 0x100000, 10, 2)) == EARG and clip(good, (0x100000, 0x100000, -1, 0)) == ESHAPE
-    assert clip(good, (None, 0x100000, 1, 0)) == ENULL and clip(good, (0x100000, None, 1, 0)) == ENULL
-    assert clip((0x100001, 0x100000, 1, 0)) == EALIGN and clip((0x100000, 0x100001, 1, 0)) == EALIGN
-    assert clip((0x100002, 0x100000, 1, 1)) == EALIGN and clip((0x100000, 0x100002, 1, 1)) == EALIGN
-    assert clip((0x100000, 0x100000, (1 << 46) + 1, 0)) == EUNSUP
-    assert clip(good, (0x100000, 0x100000, 1 << 46, 1)) == EUNSUP
-    assert clip(good, good, size=wsb - 1) == EWS and clip(good, ws=None) == EWS and clip(good, ws=MIS) == EALIGN
+        assert clip(max_norm=bad) == EARG
+    assert clip(table=None) == ENULL and clip(norm=None) == ENULL
+    assert clip(table=MIS) == EALIGN and clip(norm=ODD) == EALIGN and clip(ws=MIS) == EALIGN
+    assert clip(size=wsb - 1) == EWS and clip(ws=None) == EWS
 
 
 def test_binding_refuses_host_tensors_and_empty_lists():
