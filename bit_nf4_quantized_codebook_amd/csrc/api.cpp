@@ -1408,6 +1408,7 @@ constexpr size_t kLossTableBytes = (size_t)64 << 20;     // the forward's piece:
 constexpr int64_t kLossMinTiles = 32;
 
 struct LossPlan {
+    bool gemv;                         // few tokens, forward: its table lies at off_tref
     int32_t Mp, tiles, piece;          // rows padded to tiles; tiles of the vocabulary, and of a piece
     size_t off_count, off_sums, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[2], off_tref, off_tsum, off_P, off_part,
         off_sum32, total;
@@ -1439,6 +1440,12 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.off_a = take((size_t)p.Mp * 4);
     p.off_b = take((size_t)p.Mp * 4);
     for (size_t &c : p.off_c) c = take((size_t)p.Mp * 4);
+    p.gemv = !grad && M <= nf4k::kLossGemvMaxM;
+    if (p.gemv) {
+        p.off_tref = take((size_t)M * ((V + 15) / 16) * 8);
+        p.off_tsum = p.off_P = p.off_part = p.off_sum32 = p.total = off;
+        return p;
+    }
     p.off_tref = take((size_t)p.piece * p.Mp * 4);
     p.off_tsum = take((size_t)p.piece * p.Mp * 4);
     p.off_P = take(grad ? (size_t)p.piece * p.Mp * LT * 2 : 0);
@@ -1483,6 +1490,11 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
     uint16_t *P = grad ? ws_at<uint16_t>(workspace, p.off_P) : nullptr;
     float *c[2];
     for (int i = 0; i < 2; ++i) c[i] = ws_at<float>(workspace, p.off_c[i]);
+    if (p.gemv) {
+        const nf4k::LossGemv a{W, X, V, K, M, labels, ws_at<float2>(workspace, p.off_tref), r.zl, r.S, r.count, loss, mean};
+        NF4_CHECK_HIP(nf4k::launch_loss_gemv(a, s), "loss of few tokens");
+        return NF4_OK;
+    }
     NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");
     // c[piece % 2]: the rows' references after that piece
     for (int32_t t0 = 0, piece = 1; t0 < p.tiles; t0 += p.piece, ++piece) {

@@ -102,4 +102,17 @@ struct LossRescale {
 };
 hipError_t launch_loss_rescale(const LossRescale &a, hipStream_t stream);
 
+// the forward for up to kLossGemvMaxM tokens
+constexpr int64_t kLossGemvMaxM = 64;
+struct LossGemv {
+    const uint16_t *W, *X;
+    int64_t V, K, M;
+    const int64_t *labels;
+    float2 *table;            // [M][ceil(V / 16)] reference and sum of each 16 vocabulary rows
+    float *zl, *each;         // [M]
+    int32_t *done;
+    float *loss, *mean;
+};
+hipError_t launch_loss_gemv(const LossGemv &g, hipStream_t stream);
+
 }  // namespace nf4k

@@ -92,7 +92,8 @@ def check(X, W, labels, dloss=None, rows=None, fwd=True, grad=True):
 
 @pytest.mark.parametrize("M,V,K", [
     (1, 1, 64), (1, 2, 64), (3, 255, 64), (2, 256, 128), (5, 257, 64), (1, 1000, 512), (31, 300, 192), (64, 511, 64),
-    (65, 513, 320), (255, 700, 64), (256, 256, 256), (257, 1025, 128), (300, 2049, 576), (513, 999, 1024)])
+    (65, 513, 320), (255, 700, 64), (256, 256, 256), (257, 1025, 128), (300, 2049, 576), (513, 999, 1024),
+    (4, 4099, 192), (16, 300, 64), (17, 4099, 192), (33, 16, 2048), (48, 129, 4160), (49, 30001, 64), (64, 15, 448)])
 def test_sizes(M, V, K):
     X, W, labels = make(M, V, K, seed=M + V, none=0.2 if M > 4 else 0.0, lift=12.0)
     check(X, W, labels)
