@@ -1419,7 +1419,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     const int64_t LT = nf4k::LT, ntm = (M + LT - 1) / LT, ntn = (K + LT - 1) / LT;
     p.Mp = (int32_t)(ntm * LT);
     p.tiles = (int32_t)((V + LT - 1) / LT);
-    int64_t piece = grad ? (int64_t)(kLossPieceBytes / ((size_t)p.Mp * LT * 2)) : (int64_t)(kLossTableBytes / ((size_t)p.Mp * 8));
+    int64_t piece = grad ? (int64_t)(kLossPieceBytes / ((size_t)p.Mp * LT * 2)) : (int64_t)(kLossTableBytes / ((size_t)p.Mp * 16));
     if (piece < kLossMinTiles) piece = kLossMinTiles;
     // the product's offsets into a piece of W stay below 2 GiB
     const int64_t most = ((int64_t)1 << 22) / K;
@@ -1446,8 +1446,8 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         p.off_tsum = p.off_P = p.off_part = p.off_sum32 = p.total = off;
         return p;
     }
-    p.off_tref = take((size_t)p.piece * p.Mp * 4);
-    p.off_tsum = take((size_t)p.piece * p.Mp * 4);
+    p.off_tref = take((size_t)p.piece * p.Mp * 8);
+    p.off_tsum = take((size_t)p.piece * p.Mp * 8);
     p.off_P = take(grad ? (size_t)p.piece * p.Mp * LT * 2 : 0);
     const int64_t parts = ntm * ntn > 256 ? ntm * ntn : 256;
     p.off_part = take(grad ? (size_t)parts * LT * LT * 4 : 0);
@@ -1502,7 +1502,7 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         const bool last = t0 + nt == p.tiles;
         const float *before = t0 ? c[(piece - 1) % 2] : nullptr;
         float *now = c[piece % 2];
-        NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, t0, before, tref, tsum, P, 4 * nt}, s),
+        NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, P, 4 * nt}, s),
                       "loss logits");
         NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, piece, last, grad, dloss,
                                                             loss, mean}, s), "loss sums");

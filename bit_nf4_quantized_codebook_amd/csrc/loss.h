@@ -16,7 +16,7 @@ namespace nf4k {
 constexpr int LT = 256;                  // tokens, vocabulary rows or columns of dX of a tile
 constexpr int LSTEP = 64;                // reduction of one step of a tile's loop
 constexpr int64_t LBLOCK = LT * LSTEP;   // elements of one step's operand tile (32 KB)
-constexpr int kLossJoinRows = 16;        // rows of a workgroup that joins the tiles
+constexpr int kLossJoinRows = 8;        // rows of a workgroup that joins the tiles
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -42,15 +42,37 @@ __host__ __device__ inline LossSplit loss_split(int tiles, int steps) {
     return LossSplit{(steps + per - 1) / per, per};
 }
 
+// Tiles of the logits of a piece, for ntm tiles of rows and ntn of the vocabulary.  They are numbered along the
+// vocabulary within groups of four tiles of rows (an XCD's concurrent tiles then share both operands in its L2).
+// Where they fill the chip's last round at most half, that round's tiles are cut in two along the vocabulary: their
+// second halves' statistics stand ntn entries further in the tables.
+struct LossTiles {
+    int ntm, ntn, whole;      // whole: tiles that are not cut, the first ones
+    __host__ __device__ LossTiles(int m, int n) : ntm(m), ntn(n) {
+        const int64_t t = (int64_t)m * n;
+        const int rest = (int)(t % 256);
+        whole = (int)(rest <= 128 ? t - rest : t);
+    }
+    __device__ __forceinline__ void place(int t, int &tm, int &tn) const {
+        const int grp = t / (4 * ntn), first = 4 * grp, size = ntm - first < 4 ? ntm - first : 4, in = t - 4 * grp * ntn;
+        tm = first + in % size;
+        tn = in / size;
+    }
+    // the first tile of the vocabulary that is cut for these rows; all after it are too
+    __device__ __forceinline__ int first_cut(int tm) const {
+        const int first = tm & ~3, size = ntm - first < 4 ? ntm - first : 4, left = whole - first * ntn - (tm - first);
+        return left <= 0 ? 0 : min((left + size - 1) / size, ntn);
+    }
+};
+
 struct LogitsArgs {
     const uint16_t *W, *X;
     int64_t V, K;
     LossRows r;
     int32_t Mp;
-    int32_t tile0, ntile;     // vocabulary tiles of this launch
-    int32_t table0;           // the tile whose entries stand first in tref and tsum (and in P)
+    int32_t tile0, ntile;     // vocabulary tiles of this piece
     const float *ref;         // [M] references, or NULL: 0
-    float *tref, *tsum;       // [tiles][Mp]: a tile's reference and its sum of 2^(l - reference)
+    float *tref, *tsum;       // [2 ntile][Mp]: a tile's reference and its sum of 2^(l - reference)
     uint16_t *P;              // 2^(l - reference) in bf16, or NULL; blocks of one step (see loss_logits.hip)
     int32_t psteps;           // steps of P's row of blocks
 };

@@ -90,26 +90,31 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     const float c_old = g.c_in && live ? g.c_in[row] : NEG;
     // the new reference: the largest there is; eight tiles' loads at a time
     float c = c_old, sum = 0.0f, low = -NEG;
+    // entries of this row's tiles: ntile, and the second halves of the tiles that are cut
+    const LossTiles tiles((count + LT - 1) / LT, g.ntile);
+    const int cut = tiles.first_cut(row / LT), entries = 2 * g.ntile - cut;
     if (live)
-        for (int t0 = slice; t0 < g.ntile; t0 += JS * 8) {
+        for (int t0 = slice; t0 < entries; t0 += JS * 8) {
             float f[8], s[8], m = c;
+            bool has[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const int t = t0 + u * JS;
-                const int64_t o = (int64_t)t * g.Mp + row;
-                f[u] = t < g.ntile ? g.tref[o] : NEG;
-                s[u] = t < g.ntile ? g.tsum[o] : 0.0f;
+                const int64_t o = (int64_t)(t < g.ntile ? t : t + cut) * g.Mp + row;
+                has[u] = t < entries;
+                f[u] = has[u] ? g.tref[o] : NEG;
+                s[u] = has[u] ? g.tsum[o] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 m = fmaxf(m, f[u]);
-                low = fminf(low, t0 + u * JS < g.ntile ? f[u] : -NEG);
+                low = fminf(low, has[u] ? f[u] : -NEG);
             }
             // c = m also before the first tile, where there is nothing to move (and both may be -inf)
             sum *= m == c ? 1.0f : __builtin_amdgcn_exp2f(c - m);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (t0 + u * JS < g.ntile) sum += s[u] * __builtin_amdgcn_exp2f(f[u] - m);
+                if (has[u]) sum += s[u] * __builtin_amdgcn_exp2f(f[u] - m);
             c = m;
         }
     pc[slice][lr] = c;
@@ -155,7 +160,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     }
 }
 
-// Grid-stride over tiles (256 rows and 256 vocabulary rows: four blocks of P); workgroup 0 also writes the mean.
+// Grid-stride over half tiles (256 rows and 128 vocabulary rows: two blocks of P); workgroup 0 also writes the mean.
 __global__ __launch_bounds__(256) void loss_rescale_kernel(LossRescale g) {
     __shared__ float f[LT];
     const int count = g.r.count[0], tid = threadIdx.x;
@@ -164,16 +169,18 @@ __global__ __launch_bounds__(256) void loss_rescale_kernel(LossRescale g) {
         return;
     }
     if (!g.P || g.r.count[1] != g.piece) return;
-    const int first = g.mean ? 1 : 0, ntm = (count + LT - 1) / LT;
-    for (int x = blockIdx.x - first; x < ntm * g.ntile; x += gridDim.x - first) {
-        const int tm = x / g.ntile, t = x % g.ntile;
+    const LossTiles tiles((count + LT - 1) / LT, g.ntile);
+    const int first = g.mean ? 1 : 0;
+    for (int x = blockIdx.x - first; x < tiles.ntm * 2 * g.ntile; x += gridDim.x - first) {
+        const int tm = x / (2 * g.ntile), t = x % (2 * g.ntile) / 2, h = x & 1;
+        const int64_t entry = (h && t >= tiles.first_cut(tm) ? g.ntile : 0) + t;
         const int row = tm * LT + tid;
-        const float from = row < count ? g.tref[(int64_t)t * g.Mp + row] : 0.0f, to = row < count ? g.c[row] : 0.0f;
+        const float from = row < count ? g.tref[entry * g.Mp + row] : 0.0f, to = row < count ? g.c[row] : 0.0f;
         f[tid] = __builtin_amdgcn_exp2f(from - to);
         const bool any = __syncthreads_or(!(from == to));
         if (any) {
-            uint16_t *base = g.P + ((int64_t)tm * g.ntile + t) * 4 * LBLOCK;
-            for (int i = tid; i < 4 * LBLOCK / 8; i += 256) {
+            uint16_t *base = g.P + (((int64_t)tm * g.ntile + t) * 4 + 2 * h) * LBLOCK;
+            for (int i = tid; i < 2 * LBLOCK / 8; i += 256) {
                 const float s = f[(i >> 3) & (LT - 1)];     // 8 chunks a row, 256 rows a block
                 u32x4 v = reinterpret_cast<u32x4 *>(base)[i];
 #pragma unroll

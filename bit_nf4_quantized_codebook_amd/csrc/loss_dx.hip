@@ -70,12 +70,12 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     const uint32_t row4_off = (uint32_t)(4 * g.K * 2);
     const uint32_t step_off = (uint32_t)(LSTEP * g.K * 2);
     const uint32_t boff = (uint32_t)(wave * 8192 + lane * 16);
-    auto load = [&](int step, uint8_t *A, uint8_t *B, int q0, int q1) {
+    auto load = [&](int step, uint8_t *A, uint8_t *B, int part) {
         lds_u8 *da = (lds_u8 *)A + wave * 8192, *db = (lds_u8 *)B + wave * 8192;
         const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past every descriptor's end
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-            if (q < q0 || q >= q1) continue;
+            if ((q >> 2) != part) continue;
             // rows 2q and 2q + 1 of the wave's 16: q and q + 2 share row % 4
             const uint32_t v = aoff[q & 1] + (uint32_t)(q >> 1) * row4_off + (uint32_t)step * step_off;
             const uint32_t x = boff + (uint32_t)q * 1024u + (uint32_t)step * (uint32_t)(LBLOCK * 2);
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     uint32_t bread[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) bread[s] = (uint32_t)(r32 * 128 + (((2 * s + hh) ^ ((r32 >> 1) & 7)) * 16));
-    auto read = [&](const uint8_t *A, const uint8_t *B, int s, LossFrags &f) {
+    auto read = [&](const uint8_t *A, const uint8_t *B, int s, LossFrags<4> &f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint8_t *p = A + aread[i] + s * 16 * 512;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    loss_loop<12>(steps, As0, Bs0, As1, Bs1, acc, load, read);
+    loss_loop<4, 12, 8>(steps, As0, Bs0, As1, Bs1, acc, load, read);
 
     // Lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and columns wm*128 + 32 i + 8 (v/4) + 4 hh + v%4.
     // Each wave turns its 128 x 128 values in its own stage of LDS, 64 tokens at a time, into rows of 512 bytes (their
