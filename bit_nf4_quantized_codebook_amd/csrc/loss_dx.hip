@@ -31,10 +31,10 @@ struct LossFinal {
 };
 
 __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
-    __shared__ __align__(16) uint8_t As0[LBLOCK * 2];
-    __shared__ __align__(16) uint8_t As1[LBLOCK * 2];
-    __shared__ __align__(16) uint8_t Bs0[LBLOCK * 2];
-    __shared__ __align__(16) uint8_t Bs1[LBLOCK * 2];
+    // one LDS object per stage: a fragment read of one stage provably never aliases the
+    // direct-to-LDS loads in flight into the other
+    __shared__ __align__(16) uint8_t S0[2 * LOPB];
+    __shared__ __align__(16) uint8_t S1[2 * LOPB];
 
     const int count = __builtin_amdgcn_readfirstlane(g.r.count[0]);
     const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT);
@@ -70,17 +70,17 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     const uint32_t row4_off = (uint32_t)(4 * g.K * 2);
     const uint32_t step_off = (uint32_t)(LSTEP * g.K * 2);
     const uint32_t boff = (uint32_t)(wave * 8192 + lane * 16);
-    auto load = [&](int step, uint8_t *A, uint8_t *B, int part) {
-        lds_u8 *da = (lds_u8 *)A + wave * 8192, *db = (lds_u8 *)B + wave * 8192;
-        const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past every descriptor's end
+    auto load = [&](int step, uint8_t *st, int part) {
+        lds_u8 *da = (lds_u8 *)st + wave * 8192, *db = (lds_u8 *)(st + LOPB) + wave * 8192;
+        const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past the descriptor's end
+        const int bstep = min(step, steps - 1) * (int)(LBLOCK * 2);    // P's blocks are whole: the last one again
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if ((q >> 2) != part) continue;
             // rows 2q and 2q + 1 of the wave's 16: q and q + 2 share row % 4
             const uint32_t v = aoff[q & 1] + (uint32_t)(q >> 1) * row4_off + (uint32_t)step * step_off;
-            const uint32_t x = boff + (uint32_t)q * 1024u + (uint32_t)step * (uint32_t)(LBLOCK * 2);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + q * 1024), 16, v | dead, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, x | dead, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, boff, bstep + q * 1024, 0, 0);
         }
     };
     // W's fragment of sub-step s, columns wm*128 + 32 i ..: 16-lane group (hh, half) reads rows
@@ -93,7 +93,8 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     uint32_t bread[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) bread[s] = (uint32_t)(r32 * 128 + (((2 * s + hh) ^ ((r32 >> 1) & 7)) * 16));
-    auto read = [&](const uint8_t *A, const uint8_t *B, int s, LossFrags<4> &f) {
+    auto read = [&](const uint8_t *A, int s, LossFrags<4> &f) {
+        const uint8_t *B = A + LOPB;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint8_t *p = A + aread[i] + s * 16 * 512;
@@ -111,14 +112,16 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    loss_loop<4, 12, 8>(steps, As0, Bs0, As1, Bs1, acc, load, read);
+    load(0, S0, 0);
+    load(0, S0, 1);
+    loss_loop<4, 12, 8, 0>(steps, false, S0, S1, acc, load, read);
 
     // Lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and columns wm*128 + 32 i + 8 (v/4) + 4 hh + v%4.
     // Each wave turns its 128 x 128 values in its own stage of LDS, 64 tokens at a time, into rows of 512 bytes (their
     // 16-byte chunks XOR-swizzled by the row), so that all that follows moves whole lines, two tokens at a time.
     const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     const int c32 = lane_e & 31, he = lane_e >> 5;
-    uint8_t *turn = wave == 0 ? As0 : (wave == 1 ? As1 : (wave == 2 ? Bs0 : Bs1));
+    uint8_t *turn = (wave < 2 ? S0 : S1) + (wave & 1) * LOPB;
     const bool split_up = sp.ks > 1, add = !split_up && g.c_old, last = !split_up && g.dX;
     // K is a multiple of 64: what lies past it are whole lanes here
     const int64_t col = n0 + wm * 128 + 4 * c32;

@@ -33,11 +33,17 @@ namespace {
 constexpr int kSlack = 48;
 
 struct LossStages {
-    uint8_t *As0, *Bs0, *As1, *Bs1;
+    uint8_t *S0, *S1;
     float *refs;              // [LT]
     int *labs;                // [LT] labels, counted from the tile's first vocabulary row; -1: not in the tile
     float (*sums)[LT];        // [2] by the waves along the vocabulary
     float (*tops)[LT];
+};
+
+struct LossPlace {
+    int tm;                   // tile of rows
+    int64_t n0;               // first vocabulary row
+    int entry, p0;            // row of the tables; first step of P's blocks
 };
 
 // the sum or maximum over groups of N lanes (8 or 16), in all of them
@@ -53,10 +59,10 @@ __device__ __forceinline__ float over_lanes(float x, Op op) {
     return x;
 }
 
-// One tile: 64 IA vocabulary rows from n0, tokens from m0; entry: its row of the tables; P's blocks from step p0
-template <bool GRAD, int IA>
-__device__ __forceinline__ void logits_tile(const LogitsArgs &g, const LossStages &st, int count, int tm, int64_t n0, int entry, int p0) {
-    const int m0 = tm * LT;
+// A workgroup's tiles of 64 IA vocabulary rows, one after the other: place(i), i < n.  The next tile's first step is
+// loaded (into S1) before this one's epilogue, which works in S0.
+template <bool GRAD, int IA, class Place>
+__device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStages &st, int count, int n, Place place) {
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -65,52 +71,79 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs &g, const LossStage
     constexpr int WV = 32 * IA;                   // vocabulary rows of a wave
     constexpr int QA = 2 * IA;                    // a wave's loads of W a step
 
-    {
-        const int t = m0 + tid;
-        const int64_t lab = t < count ? (int64_t)g.r.label[t] - n0 : -1;
-        st.labs[tid] = lab >= 0 && lab < 64 * IA ? (int)lab : -1;
-        st.refs[tid] = g.ref && t < count ? g.ref[t] : 0.0f;
-    }
-    // rows of W past V read zeros; the whole of X is one descriptor, its rows gathered
-    const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.W + n0 * g.K, (g.V - n0) * g.K * 2);
+    // Instruction q of wave w writes stage rows 8u .. 8u+7 (u = 8w + q; W: QA w + q); lane l takes row 8u + l/8 and
+    // physical chunk l%8, which holds logical chunk (l%8) ^ ((row/2)%8).  Rows of W past V read zeros; the whole of X is
+    // one descriptor, its rows gathered.  A row out of range is so by its lane offset alone, so the step goes into the
+    // scalar offset and a load costs no VALU; steps past the last load the last one again (never used, and in range).
+    const int l8 = lane >> 3;
+    auto chunk = [&](int q) { return (uint32_t)(((lane & 7) ^ ((4 * q + (l8 >> 1)) & 7)) * 16); };
+    __amdgpu_buffer_rsrc_t rA;
     const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.X, 0x7FFFFFF0LL);
-
-    // instruction q of wave w writes stage rows 8u .. 8u+7 (u = 8w + q; W: QA w + q); lane l takes row 8u + l/8 and
-    // physical chunk l%8, which holds logical chunk (l%8) ^ ((row/2)%8)
-    uint32_t voff[2], xoff[8];
+    uint32_t voff[QA], xoff[8];
+    int rows[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        const int row = 8 * (8 * wave + q) + (lane >> 3);
-        const uint32_t col = (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) * 16);
-        if (q < 2) voff[q] = (uint32_t)(8 * QA * wave + (lane >> 3)) * (uint32_t)(g.K * 2) + col;
-        xoff[q] = m0 + row < count ? (uint32_t)g.r.row[m0 + row] * (uint32_t)(g.K * 2) + col : 0x80000000u;
-    }
-    const uint32_t row8_off = (uint32_t)(8 * g.K * 2);
+    for (int q = 0; q < QA; ++q) voff[q] = (uint32_t)(8 * (QA * wave + q) + l8) * (uint32_t)(g.K * 2) + chunk(q);
     const int steps = (int)(g.K / LSTEP);
-    auto load = [&](int step, uint8_t *A, uint8_t *B, int part) {
-        lds_u8 *da = (lds_u8 *)A + wave * (QA * 1024), *db = (lds_u8 *)B + wave * 8192;
-        const uint32_t at = (uint32_t)step * (LSTEP * 2);
-        const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past every descriptor's end
+    // what a tile needs of its rows: their tokens, and this thread's label and reference
+    int label;
+    float ref;
+    auto fetch = [&](const LossPlace &p) {
+        const int m0 = p.tm * LT;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const int row = m0 + 8 * (8 * wave + q) + l8;
+            rows[q] = row < count ? g.r.row[row] : -1;
+        }
+        label = m0 + tid < count ? g.r.label[m0 + tid] : -1;
+        ref = g.ref && m0 + tid < count ? g.ref[m0 + tid] : 0.0f;
+    };
+    auto load = [&](int step, uint8_t *stage, int part) {
+        lds_u8 *da = (lds_u8 *)stage + wave * (QA * 1024), *db = (lds_u8 *)(stage + LOPB) + wave * 8192;
+        const int at = min(step, steps - 1) * (LSTEP * 2);
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if ((q >> 2) != part) continue;
             if (IA == 4 || (q & 1) == 0) {
                 const int qa = IA == 4 ? q : q >> 1;
-                const uint32_t v = voff[qa & 1] + (uint32_t)qa * row8_off + at;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + qa * 1024), 16, v | dead, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + qa * 1024), 16, voff[qa], at, 0, 0);
             }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, (xoff[q] + at) | dead, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, xoff[q], at, 0, 0);
         }
+    };
+    auto first_loads = [&](const LossPlace &p) {
+        rA = make_rsrc(g.W + p.n0 * g.K, (g.V - p.n0) * g.K * 2);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            xoff[q] = rows[q] >= 0 ? (uint32_t)rows[q] * (uint32_t)(g.K * 2) + chunk(q) : 0x80000000u;
+        load(0, st.S1, 0);
+        load(0, st.S1, 1);
     };
     uint32_t lds_off[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) lds_off[s] = (uint32_t)(r32 * 128 + (((2 * s + hh) ^ ((r32 >> 1) & 7)) * 16));
-    auto read = [&](const uint8_t *A, const uint8_t *B, int s, LossFrags<IA> &f) {
+    auto read = [&](const uint8_t *A, int s, LossFrags<IA> &f) {
+        const uint8_t *B = A + LOPB;
 #pragma unroll
         for (int i = 0; i < IA; ++i) f.a[i] = *reinterpret_cast<const bf16x8 *>(A + lds_off[s] + (wm * WV + 32 * i) * 128);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f.b[j] = *reinterpret_cast<const bf16x8 *>(B + lds_off[s] + (wn * 128 + 32 * j) * 128);
     };
+    if (n <= 0) return;
+    LossPlace cur = place(0);
+    fetch(cur);
+    first_loads(cur);
+#pragma unroll 1
+    for (int index = 0;; ++index) {
+    const int m0 = cur.tm * LT;
+    const int64_t n0 = cur.n0;
+    {
+        const int64_t lab = (int64_t)label - n0;
+        st.labs[tid] = label >= 0 && lab >= 0 && lab < 64 * IA ? (int)lab : -1;
+        st.refs[tid] = ref;
+    }
+    const bool more = index + 1 < n;
+    const LossPlace next = more ? place(index + 1) : cur;
+    fetch(next);
     f32x16 acc[IA][4];
 #pragma unroll
     for (int i = 0; i < IA; ++i)
@@ -118,13 +151,16 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs &g, const LossStage
         for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    loss_loop<IA, 4 + IA, 4 + IA>(steps, st.As0, st.Bs0, st.As1, st.Bs1, acc, load, read);
+    // between the first step's loads and here lie p's stores, whose end nothing waits for
+    constexpr int STORES = GRAD ? 32 * WV / 128 : 0;
+    loss_loop<IA, 4 + IA, 4 + IA, STORES>(steps, index > 0, st.S1, st.S0, acc, load, read);
+    if (more) first_loads(next);
 
     // ---- epilogue.  Lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and vocabulary rows
     // wm*WV + 32 i + 8 (v/4) + 4 hh + v%4.  turn(j) lays token group j out as rows of WV floats, whose 16-byte pieces are
     // permuted by the token so that neither the writes nor the reads of two neighbouring pieces meet in a bank. ----
     const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-    uint8_t *lds = wave == 0 ? st.As0 : (wave == 1 ? st.As1 : (wave == 2 ? st.Bs0 : st.Bs1));
+    uint8_t *lds = st.S0 + wave * 16384;          // 32 tokens of WV floats
     constexpr int PIECES = WV / 4;                // a row's pieces of four vocabulary rows
     auto piece = [](int p, int token) { return ((p ^ (p / (PIECES / 2))) ^ (token & (PIECES - 1))) * 16; };
     auto order = [&]() {
@@ -160,7 +196,7 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs &g, const LossStage
     const int end = (int)min(max(left - 8 * q, (int64_t)0), (int64_t)8);
     const bool ragged = left < WV;
     const __amdgpu_buffer_rsrc_t rP = make_rsrc(
-        GRAD ? g.P + ((int64_t)tm * g.psteps + p0 + wm * (IA / 2)) * LBLOCK : nullptr, GRAD ? LBLOCK * IA : 0);
+        GRAD ? g.P + ((int64_t)cur.tm * g.psteps + cur.p0 + wm * (IA / 2)) * LBLOCK : nullptr, GRAD ? LBLOCK * IA : 0);
     auto group = [&](auto jc) {
         turn(jc);
         // B iterations' reads at a time: a wave is alone on its SIMD, nothing else hides their latency
@@ -183,29 +219,34 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs &g, const LossStage
                 lab[b] = lab[b] < 0 ? -1 : lab[b] - wm * WV - 8 * q;
                 any |= (uint32_t)lab[b] < 8u;
             }
-            // few batches hold a label
-            const bool masked = __builtin_amdgcn_ballot_w64(any) != 0;
+            // few batches hold a label; the empty statement keeps this a branch (as selects for every element it doubled
+            // the epilogue's time)
+            if (__builtin_amdgcn_ballot_w64(any)) {
+                asm volatile("");
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                float zl = 0.0f;
-                s[b] = 0.0f;
+                for (int b = 0; b < B; ++b) {
+                    float zl = 0.0f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float z = x[b][k];
-                    x[b][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -c[b]));
-                    if (masked) {
-                        zl = lab[b] == k ? z : zl;
-                        x[b][k] = lab[b] == k || k >= end ? 0.0f : x[b][k];
+                    for (int k = 0; k < 8; ++k) {
+                        zl = lab[b] == k ? x[b][k] : zl;
+                        x[b][k] = lab[b] == k || k >= end ? -__builtin_inff() : x[b][k];
                     }
-                    s[b] += x[b][k];
+                    if ((uint32_t)lab[b] < 8u) g.r.zl[m0 + tl0 + TI * b] = zl * kLog2e;
                 }
-                if (masked && (uint32_t)lab[b] < 8u) g.r.zl[m0 + tl0 + TI * b] = zl * kLog2e;
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                s[b] = over_lanes<NQ>(s[b], [](float a, float b) { return a + b; });
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[b][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][k], kLog2e, -c[b]));
+                const float *e = x[b];
+                s[b] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) s[b] = over_lanes<NQ>(s[b], [](float a, float b) { return a + b; });
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
                 const int row = tl0 + TI * b;
-                if (q == 0) st.sums[wm][row] = s[b];
+                st.sums[wm][row] = s[b];      // the same from all of a token's lanes
                 if (GRAD) {
                     const float *e = x[b];
                     __builtin_amdgcn_raw_buffer_store_b128(
@@ -255,9 +296,13 @@ __device__ __forceinline__ void logits_tile(const LogitsArgs &g, const LossStage
         sum = st.sums[0][tid] + st.sums[1][tid];
     }
     if (m0 + tid < count) {
-        const int64_t o = (int64_t)entry * g.Mp + m0 + tid;
+        const int64_t o = (int64_t)cur.entry * g.Mp + m0 + tid;
         g.tref[o] = st.refs[tid];
         g.tsum[o] = sum;
+    }
+    if (!more) break;
+    __syncthreads();       // sums and refs are read
+    cur = next;
     }
 }
 
@@ -265,38 +310,48 @@ template <bool GRAD>
 __global__ __launch_bounds__(256, 1) void loss_logits_kernel(LogitsArgs g) {
     // one LDS object per stage: a fragment read of one stage provably never aliases the
     // direct-to-LDS loads in flight into the other
-    __shared__ __align__(16) uint8_t As0[LBLOCK * 2];
-    __shared__ __align__(16) uint8_t As1[LBLOCK * 2];
-    __shared__ __align__(16) uint8_t Bs0[LBLOCK * 2];
-    __shared__ __align__(16) uint8_t Bs1[LBLOCK * 2];
+    __shared__ __align__(16) uint8_t S0[2 * LOPB];
+    __shared__ __align__(16) uint8_t S1[2 * LOPB];
     __shared__ float refs[LT], sums[2][LT], tops[2][LT];
     __shared__ int labs[LT];
-    const LossStages st{As0, Bs0, As1, Bs1, refs, labs, sums, tops};
+    const LossStages st{S0, S1, refs, labs, sums, tops};
 
     const int count = __builtin_amdgcn_readfirstlane(g.r.count[0]);
     const LossTiles tiles((count + LT - 1) / LT, g.ntile);
-    const int all = tiles.ntm * tiles.ntn, bid = (int)blockIdx.x;
-    int tm, tn;
-    if (bid < tiles.whole) {
-        // each XCD (bid % 8) takes a contiguous run of tiles
-        const int q = tiles.whole / 8;
-        tiles.place(bid < 8 * q ? (bid % 8) * q + bid / 8 : bid, tm, tn);
-        logits_tile<GRAD, 4>(g, st, count, tm, (int64_t)(g.tile0 + tn) * LT, tn, 4 * tn);
-    } else if (bid < 2 * all - tiles.whole) {
-        const int h = (bid - tiles.whole) / (all - tiles.whole);
-        tiles.place(bid - h * (all - tiles.whole), tm, tn);
-        logits_tile<GRAD, 2>(g, st, count, tm, (int64_t)(g.tile0 + tn) * LT + 128 * h, tn + h * g.ntile, 4 * tn + 2 * h);
-    }
+    // each XCD (blockIdx % 8) takes a contiguous run of the whole tiles, its 32 workgroups 32 of them at a time
+    const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
+    const int first = (int)((int64_t)tiles.whole * xcd / 8), last = (int)((int64_t)tiles.whole * (xcd + 1) / 8);
+    logits_tiles<GRAD, 4>(g, st, count, (last - first - slot + 31) / 32, [&](int i) {
+        LossPlace p;
+        int tn;
+        tiles.place(first + slot + 32 * i, p.tm, tn);
+        p.n0 = (int64_t)(g.tile0 + tn) * LT;
+        p.entry = tn;
+        p.p0 = 4 * tn;
+        return p;
+    });
+    // halves of the tiles that are cut: at most one a workgroup
+    const int cut = tiles.ntm * tiles.ntn - tiles.whole;
+    if ((int)blockIdx.x >= 2 * cut) return;
+    __syncthreads();
+    logits_tiles<GRAD, 2>(g, st, count, 1, [&](int) {
+        LossPlace p;
+        int tn;
+        const int h = (int)blockIdx.x / cut;
+        tiles.place(tiles.whole + (int)blockIdx.x - h * cut, p.tm, tn);
+        p.n0 = (int64_t)(g.tile0 + tn) * LT + 128 * h;
+        p.entry = tn + h * g.ntile;
+        p.p0 = 4 * tn + 2 * h;
+        return p;
+    });
 }
 
 }  // namespace
 
 hipError_t launch_loss_logits(const LogitsArgs &a, hipStream_t stream) {
-    // the live rows may have any number of tiles up to Mp's; 128 more workgroups for tiles that are cut
-    const int64_t grid = (int64_t)(a.Mp / LT) * a.ntile + 128;
-    if (grid > 0x7FFFFFFFLL) return hipErrorInvalidValue;
-    if (a.P) hipLaunchKernelGGL(loss_logits_kernel<true>, dim3((uint32_t)grid), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(loss_logits_kernel<false>, dim3((uint32_t)grid), dim3(256), 0, stream, a);
+    const uint32_t grid = 256;      // a workgroup on each CU
+    if (a.P) hipLaunchKernelGGL(loss_logits_kernel<true>, dim3(grid), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL(loss_logits_kernel<false>, dim3(grid), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -40,19 +40,23 @@ __device__ __forceinline__ void loss_interleave(int nvmem) {
     }
 }
 
-// load(step, a, b, half): issues half (0 or 1; NV loads) of the loads of both operands of a step; past the last step they
-// read zeros.  read(a, b, s, frags): fragments of sub-step s (NDS LDS reads).
-template <int IA, int NDS, int NV, class Load, class Read>
-__device__ __forceinline__ void loss_loop(int steps, uint8_t *As0, uint8_t *Bs0, uint8_t *As1, uint8_t *Bs1,
-                                          f32x16 acc[IA][4], Load load, Read read) {
+// A stage holds a step's two operands: 32 KB for the first, from LOPB on the second.
+constexpr int LOPB = LBLOCK * 2;
+
+// load(step, stage, half): issues half (0 or 1; NV loads) of the loads of both operands of a step; past the last step
+// anything that is in range.  read(stage, s, frags): fragments of sub-step s (NDS LDS reads).  On entry step 0 is
+// on its way into stage c; where `younger` is set, YOUNGER memory operations were surely issued after its loads.  At the
+// end both stages are free.
+template <int IA, int NDS, int NV, int YOUNGER, class Load, class Read>
+__device__ __forceinline__ void loss_loop(int steps, bool younger, uint8_t *c, uint8_t *n, f32x16 acc[IA][4], Load load, Read read) {
     LossFrags<IA> f0, f1;
-    auto step_body = [&](int step, uint8_t *Ac, uint8_t *Bc, uint8_t *An, uint8_t *Bn) {
+    auto step_body = [&](int step, uint8_t *sc, uint8_t *sn) {
 #pragma unroll
         for (int s = 0; s < 3; ++s) {
             LossFrags<IA> &cur = (s & 1) ? f1 : f0;
             LossFrags<IA> &nxt = (s & 1) ? f0 : f1;
-            if (s == 0) load(step + 1, An, Bn, 1);
-            read(Ac, Bc, s + 1, nxt);
+            if (s == 0) load(step + 1, sn, 1);
+            read(sc, s + 1, nxt);
             loss_mma<IA>(cur, acc);
             loss_interleave<IA, NDS>(s == 0 ? NV : 0);
             __builtin_amdgcn_sched_barrier(0);
@@ -60,24 +64,26 @@ __device__ __forceinline__ void loss_loop(int steps, uint8_t *As0, uint8_t *Bs0,
         // step + 1 landed (this wave's loads) and this wave's fragment reads of stage c are done
         __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (0 << 8));
         __syncthreads();
-        read(An, Bn, 0, f0);
-        load(step + 2, Ac, Bc, 0);
+        read(sn, 0, f0);
+        load(step + 2, sc, 0);
         loss_mma<IA>(f1, acc);
         loss_interleave<IA, NDS>(NV);
         __builtin_amdgcn_sched_barrier(0);
     };
-    load(0, As0, Bs0, 0);
-    load(0, As0, Bs0, 1);
-    load(1, As1, Bs1, 0);
-    __builtin_amdgcn_s_waitcnt(0);
+    load(1, n, 0);
+    // gfx9 layout: vmcnt[3:0] | expcnt << 4 | lgkmcnt << 8 | vmcnt[5:4] << 14
+    constexpr int left = NV + YOUNGER;
+    static_assert(left < 64, "vmcnt's range");
+    if (YOUNGER && younger) __builtin_amdgcn_s_waitcnt((left & 15) | (7 << 4) | (0 << 8) | ((left >> 4) << 14));
+    else __builtin_amdgcn_s_waitcnt(NV | (7 << 4) | (0 << 8));
     __syncthreads();
-    read(As0, Bs0, 0, f0);
+    read(c, 0, f0);
     int step = 0;
     for (; step + 1 < steps; step += 2) {
-        step_body(step, As0, Bs0, As1, Bs1);
-        step_body(step + 1, As1, Bs1, As0, Bs0);
+        step_body(step, c, n);
+        step_body(step + 1, n, c);
     }
-    if (step < steps) step_body(step, As0, Bs0, As1, Bs1);
+    if (step < steps) step_body(step, c, n);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 }
