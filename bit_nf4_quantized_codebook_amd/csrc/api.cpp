@@ -1421,8 +1421,8 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.tiles = (int32_t)((V + LT - 1) / LT);
     int64_t piece = grad ? (int64_t)(kLossPieceBytes / ((size_t)p.Mp * LT * 2)) : (int64_t)(kLossTableBytes / ((size_t)p.Mp * 16));
     if (piece < kLossMinTiles) piece = kLossMinTiles;
-    // the product's offsets into a piece of W stay below 2 GiB
-    const int64_t most = ((int64_t)1 << 22) / K;
+    // the product's offsets into a piece of W stay below 2 GiB - 16
+    const int64_t most = (((int64_t)1 << 22) - 1) / K;
     if (grad && piece > most) piece = most;
     p.piece = (int32_t)(piece < p.tiles ? piece : p.tiles);
     size_t off = 0;
@@ -1449,8 +1449,9 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.off_tref = take((size_t)p.piece * p.Mp * 8);
     p.off_tsum = take((size_t)p.piece * p.Mp * 8);
     p.off_P = take(grad ? (size_t)p.piece * p.Mp * LT * 2 : 0);
-    const int64_t parts = ntm * ntn > 256 ? ntm * ntn : 256;
-    p.off_part = take(grad ? (size_t)parts * LT * LT * 4 : 0);
+    // a tile has partials only among the last, fewer than 256, and then as many as shares and tiles
+    const int64_t rest = ntm * ntn < 256 ? ntm * ntn : 256;
+    p.off_part = take(grad ? (size_t)(256 + rest) * LT * LT * 4 : 0);
     p.off_sum32 = take(grad && p.piece < p.tiles ? (size_t)p.Mp * K * 4 : 0);
     p.total = off;
     return p;

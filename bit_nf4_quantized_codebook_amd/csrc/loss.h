@@ -31,20 +31,57 @@ struct LossRows {
     float *a, *b;          // [M] dX = a (sum P W) - b W[label]
 };
 
-// dX's product: workgroups per tile of a reduction of `steps` steps, for `tiles` tiles (device and host)
-struct LossSplit {
-    int ks, per;
-};
-__host__ __device__ inline LossSplit loss_split(int tiles, int steps) {
-    int ks = tiles > 0 && tiles < 256 ? 256 / tiles : 1;
-    if (ks > steps / 8) ks = steps / 8 > 0 ? steps / 8 : 1;
-    const int per = (steps + ks - 1) / ks;
-    return LossSplit{(steps + per - 1) / per, per};
+// Tiles of rows and columns, numbered along the columns within groups of four tiles of rows (an XCD's concurrent
+// tiles then share both operands in its L2).
+__device__ __forceinline__ void loss_place(int ntm, int ntn, int t, int &tm, int &tn) {
+    const int grp = t / (4 * ntn), first = 4 * grp, size = ntm - first < 4 ? ntm - first : 4, in = t - 4 * grp * ntn;
+    tm = first + in % size;
+    tn = in / size;
 }
 
-// Tiles of the logits of a piece, for ntm tiles of rows and ntn of the vocabulary.  They are numbered along the
-// vocabulary within groups of four tiles of rows (an XCD's concurrent tiles then share both operands in its L2).
-// Where they fill the chip's last round at most half, that round's tiles are cut in two along the vocabulary: their
+// How dX's product shares its tiles' reductions of `steps` steps among 256 workgroups: whole rounds of tiles first, a
+// tile a workgroup.  The `rest` tiles are split ks ways, len steps each.  Where that leaves workgroups over (extra), the
+// ks parts are cut to about rest steps / 256 and the tails they leave, laid end to end, go to the extra ones in equal
+// runs.  A split tile's parts are float32 partials.  (All of it laid end to end in 256 runs had as many partials and
+// every workgroup at another step: nothing to share in the L2s, 527 instead of 414 us for 112 tiles of 500 steps.)
+// The extra ones are used where the time they save, at 1.6 us a step, exceeds their partials', 0.114 us each to write
+// and read.
+struct LossShares {
+    int tiles, steps, whole, rest, ks, len, extra, tail;
+    __host__ __device__ LossShares(int tiles_, int steps_) : tiles(tiles_), steps(steps_) {
+        whole = tiles / 256 * 256;
+        rest = tiles - whole;
+        ks = extra = tail = 0;
+        len = steps;
+        if (!rest) return;
+        ks = 256 / rest;
+        if (ks > steps / 8) ks = steps / 8 > 0 ? steps / 8 : 1;
+        len = (steps + ks - 1) / ks;
+        ks = (steps + len - 1) / len;
+        // (starting and storing a part takes about six steps' time, once more for every tile of a run)
+        const int cut = (int)((int64_t)rest * (steps + 6) / 256), over = 256 - rest * ks;
+        // in units of 1/1000 us; a run of tails may begin in one tile and end in another
+        const int64_t shorter = (int64_t)(len - cut) * 1600, parts = (int64_t)(over + rest + (ks == 1 ? rest : 0)) * 114;
+        if (over <= 0 || cut < 8 || ks * cut >= steps || shorter <= parts) return;
+        len = cut;
+        extra = over;
+        tail = steps - ks * len;
+    }
+    __device__ __forceinline__ bool partial() const { return ks > 1 || extra; }
+    // runs of the tails, in steps of all tails
+    __device__ __forceinline__ int64_t begin(int e) const { return (int64_t)rest * tail * e / extra; }
+    __device__ __forceinline__ int run_of(int64_t u) const {
+        const int64_t all = (int64_t)rest * tail;
+        return (int)(((u + 1) * extra + all - 1) / all) - 1;
+    }
+    // partials: part j of tile x; a run's part in the tile that it begins in; a tile whose tail begins inside a run
+    __device__ __forceinline__ int slot_part(int j, int x) const { return j * rest + x; }
+    __device__ __forceinline__ int slot_run(int e, int x) const {
+        return ks * rest + (begin(e) >= (int64_t)x * tail ? e : extra + x);
+    }
+};
+
+// Tiles of the logits of a piece, for ntm tiles of rows and ntn of the vocabulary.  Where they fill the chip's last round at most half, that round's tiles are cut in two along the vocabulary: their
 // second halves' statistics stand ntn entries further in the tables.
 struct LossTiles {
     int ntm, ntn, whole;      // whole: tiles that are not cut, the first ones
@@ -53,11 +90,7 @@ struct LossTiles {
         const int rest = (int)(t % 256);
         whole = (int)(rest <= 128 ? t - rest : t);
     }
-    __device__ __forceinline__ void place(int t, int &tm, int &tn) const {
-        const int grp = t / (4 * ntn), first = 4 * grp, size = ntm - first < 4 ? ntm - first : 4, in = t - 4 * grp * ntn;
-        tm = first + in % size;
-        tn = in / size;
-    }
+    __device__ __forceinline__ void place(int t, int &tm, int &tn) const { loss_place(ntm, ntn, t, tm, tn); }
     // the first tile of the vocabulary that is cut for these rows; all after it are too
     __device__ __forceinline__ int first_cut(int tm) const {
         const int first = tm & ~3, size = ntm - first < 4 ? ntm - first : 4, left = whole - first * ntn - (tm - first);
@@ -78,20 +111,20 @@ struct LogitsArgs {
 };
 hipError_t launch_loss_logits(const LogitsArgs &a, hipStream_t stream);
 
-// dX's product over a piece.  Where a tile's reduction is not split, the product itself adds what earlier pieces
+// dX's product over a piece.  Where a tile's reduction is not shared, the product itself adds what earlier pieces
 // left (sum32, moved from the references c_old to c) and writes sum32 or, with the last piece, dX.
 struct LossDxArgs {
     const uint16_t *P, *W;
     int64_t V, K, v0;         // v0: first vocabulary row of the piece
     LossRows r;
     int32_t Mp, steps;
-    float *part;              // split: [split][tile] blocks of 256 x 256 float32 (row: token)
+    float *part;              // [256 + rest] blocks of 256 x 256 float32 (row: token)
     float *sum32;             // [Mp, K]; NULL: one piece only
     const float *c, *c_old;   // c_old NULL: the first piece
     uint16_t *dX;             // NULL: not the last piece
 };
 hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream);
-// the same for a split reduction, from its partials (nothing to do without a split)
+// the same for the tiles with partials
 hipError_t launch_loss_fold(const LossDxArgs &a, hipStream_t stream);
 
 // labels -> live rows; loss and dX of the other tokens set to zero

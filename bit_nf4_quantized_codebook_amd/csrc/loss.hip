@@ -30,30 +30,52 @@ __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restri
         }
         return;
     }
-    __shared__ int scan[PREP];
-    const int64_t per = (M + PREP - 1) / PREP, m0 = tid * per, m1 = min(m0 + per, M);
-    int n = 0;
-    for (int64_t m = m0; m < m1; ++m) n += labels[m] >= 0;
-    scan[tid] = n;
-    __syncthreads();
-    for (int d = 1; d < PREP; d <<= 1) {
-        const int v = tid >= d ? scan[tid - d] : 0;
+    // runs of 64 labels, a wave each: how many are live, where each run's rows begin, then the rows themselves; 1024
+    // runs at a time
+    __shared__ int begin[PREP], waves[PREP / 64];
+    const int lane = tid & 63, wave = tid >> 6;
+    auto label = [&](int64_t m) { return m < M ? labels[m] : (int64_t)-1; };
+    int base = 0;
+    for (int64_t b = 0; b < M; b += (int64_t)PREP * 64) {
+        const int runs = (int)min((M - b + 63) / 64, (int64_t)PREP);
+        for (int run = wave; run < runs; run += PREP / 64) {
+            const uint64_t live = __builtin_amdgcn_ballot_w64(label(b + 64 * run + lane) >= 0);
+            if (lane == 0) begin[run] = __popcll(live);
+        }
         __syncthreads();
-        scan[tid] += v;
+        // exclusive sums of the runs' counts: within a wave, then over the waves
+        const int n = tid < runs ? begin[tid] : 0;
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(sum, d);
+            if (lane >= d) sum += v;
+        }
+        if (lane == 63) waves[wave] = sum;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < PREP / 64; ++w) {
+            before += w < wave ? waves[w] : 0;
+            all += waves[w];
+        }
+        begin[tid] = base + before + sum - n;
+        __syncthreads();
+        for (int run = wave; run < runs; run += PREP / 64) {
+            const int64_t m = b + 64 * run + lane, l = label(m);
+            const uint64_t live = __builtin_amdgcn_ballot_w64(l >= 0);
+            if (l < 0) continue;
+            const int at = begin[run] + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(live >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)live, 0u));
+            r.row[at] = (int32_t)m;
+            r.label[at] = l < V ? (int32_t)l : -1;
+            r.zl[at] = __builtin_nanf("");      // a label in the vocabulary writes its logit over it
+        }
+        base += all;
         __syncthreads();
     }
-    if (tid == PREP - 1) {
-        r.count[0] = scan[tid];
+    if (tid == 0) {
+        r.count[0] = base;
         r.count[1] = 0;
-    }
-    int at = scan[tid] - n;
-    for (int64_t m = m0; m < m1; ++m) {
-        const int64_t l = labels[m];
-        if (l < 0) continue;
-        r.row[at] = (int32_t)m;
-        r.label[at] = l < V ? (int32_t)l : -1;
-        r.zl[at] = __builtin_nanf("");      // a label in the vocabulary writes its logit over it
-        ++at;
     }
 }
 

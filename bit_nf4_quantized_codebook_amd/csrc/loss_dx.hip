@@ -9,8 +9,8 @@
 // The MFMAs take W's columns as the first operand and the tokens as the second: a lane holds four
 // consecutive columns of a token; the results are turned through LDS into rows.
 //
-// Few tiles (the live rows are counted on the device): a tile's reduction is split over several
-// workgroups, which write float32 partials, and loss_fold_kernel sums them in a fixed order.
+// One workgroup a CU; the tiles beyond whole rounds are shared evenly (LossShares; the live rows are counted on the
+// device), with float32 partials that loss_fold_kernel sums in a fixed order.
 
 #include "common.h"
 #include "dqtile.h"
@@ -38,14 +38,17 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
 
     const int count = __builtin_amdgcn_readfirstlane(g.r.count[0]);
     const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT);
-    const int tiles = ntm * ntn;
-    const LossSplit sp = loss_split(tiles, g.steps);
-    if ((int)blockIdx.x >= tiles * sp.ks) return;
-    const int split = (int)blockIdx.x / tiles;
-    int tm, tn;
-    tile_coords_grouped<4>(ntm, ntn, (int)blockIdx.x - split * tiles, tm, tn);
-    const int64_t n0 = (int64_t)tn * LT;
-    const int kb = split * sp.per, steps = min(g.steps - kb, sp.per);
+    const LossShares sh(ntm * ntn, g.steps);
+    // each XCD (blockIdx % 8) takes a contiguous run of tiles, of parts, and of the tails' runs
+    const int xcd = (int)blockIdx.x & 7, slot = (int)blockIdx.x >> 3;
+    const int rounds = sh.whole / 256, parts = sh.ks * sh.rest;
+    const int p0 = parts * xcd / 8, p1 = parts * (xcd + 1) / 8, mine = p0 + slot;
+    bool part_left = mine < p1;
+    // with runs, parts and runs are 256 together: what an XCD's 32 workgroups have left over
+    const bool runs = sh.extra && !part_left;
+    const int run = 32 * xcd - p0 + slot - (p1 - p0);
+    int64_t at = runs ? sh.begin(run) : 0;
+    const int64_t until = runs ? sh.begin(run + 1) : 0;
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -53,7 +56,38 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     const int wm = wave >> 1, wn = wave & 1;      // along dX's columns, along the tokens
     const int r32 = lane & 31, hh = lane >> 5;
 
-    // W from this workgroup's first row; rows past V read zeros
+#pragma unroll 1
+    for (int round = 0;; ++round) {
+    // this turn's tile and its steps
+    int tile, kb = 0, steps = g.steps;
+    bool split_up = false;
+    float *part = nullptr;
+    if (round < rounds) {
+        tile = sh.whole / 8 * xcd + 32 * round + slot;
+    } else if (part_left) {
+        const int j = mine / sh.rest, x = mine % sh.rest;
+        part_left = false;
+        tile = sh.whole + x;
+        kb = j * sh.len;
+        steps = min(sh.len, g.steps - kb);
+        split_up = sh.partial();
+        part = g.part + (int64_t)sh.slot_part(j, x) * (LT * LT);
+    } else if (at < until) {
+        const int x = (int)(at / sh.tail), in = (int)(at - (int64_t)x * sh.tail);
+        tile = sh.whole + x;
+        kb = sh.ks * sh.len + in;
+        steps = (int)min(until - at, (int64_t)(sh.tail - in));
+        split_up = true;
+        part = g.part + (int64_t)sh.slot_run(run, x) * (LT * LT);
+        at += steps;
+    } else {
+        break;
+    }
+    int tm, tn;
+    loss_place(ntm, ntn, tile, tm, tn);
+    const int64_t n0 = (int64_t)tn * LT;
+
+    // W from this turn's first row; rows past V read zeros
     const int64_t v0 = g.v0 + (int64_t)kb * LSTEP;
     const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.W + v0 * g.K, (g.V - v0) * g.K * 2);
     const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.P + ((int64_t)tm * g.steps + kb) * LBLOCK, (int64_t)steps * LBLOCK * 2);
@@ -122,13 +156,12 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
     const int c32 = lane_e & 31, he = lane_e >> 5;
     uint8_t *turn = (wave < 2 ? S0 : S1) + (wave & 1) * LOPB;
-    const bool split_up = sp.ks > 1, add = !split_up && g.c_old, last = !split_up && g.dX;
+    const bool add = !split_up && g.c_old, last = !split_up && g.dX;
     // K is a multiple of 64: what lies past it are whole lanes here
     const int64_t col = n0 + wm * 128 + 4 * c32;
     const bool in = split_up || col < g.K;
     const int64_t colc = in ? col : 0, ld = split_up ? LT : g.K;
-    float *dst32 = split_up ? g.part + ((int64_t)split * tiles + (int64_t)tm * ntn + tn) * (LT * LT) + wm * 128 + 4 * c32
-                            : g.sum32 + (int64_t)tm * LT * g.K + colc;
+    float *dst32 = split_up ? part + wm * 128 + 4 * c32 : g.sum32 + (int64_t)tm * LT * g.K + colc;
 #pragma unroll
     for (int jh = 0; jh < 2; ++jh) {
 #pragma unroll
@@ -185,53 +218,80 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
+    __syncthreads();       // the stages are free
+    }
 }
 
+// Workgroup: FR rows of a tile with partials
+constexpr int FR = 8;
 __global__ __launch_bounds__(256) void loss_fold_kernel(LossDxArgs g) {
     const int count = g.r.count[0];
-    const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT), tiles = ntm * ntn;
-    const LossSplit sp = loss_split(tiles, g.steps);
-    if (sp.ks == 1) return;
-    const int k4 = (int)(g.K >> 2);
-    const int64_t n = (int64_t)count * k4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int row = (int)(i / k4), k = (int)(i % k4) * 4;
-        const float *p = g.part + ((int64_t)(row / LT) * ntn + k / LT) * (LT * LT) + (row % LT) * LT + k % LT;
-        f32x4 x = *reinterpret_cast<const f32x4 *>(p);
-        // eight partials' loads at a time
-        for (int s0 = 1; s0 < sp.ks; s0 += 8) {
-            f32x4 v[8];
+    const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT);
+    const LossShares sh(ntm * ntn, g.steps);
+    const int x = (int)blockIdx.x / (LT / FR), r0 = (int)blockIdx.x % (LT / FR) * FR;
+    if (x >= sh.rest || !sh.partial()) return;
+    int tm, tn;
+    loss_place(ntm, ntn, sh.whole + x, tm, tn);
+    if (tm * LT + r0 >= count) return;
+    // the tile's parts and the runs of its tail, in the order of its steps
+    const int e0 = sh.extra ? sh.run_of((int64_t)x * sh.tail) : 0;
+    const int np = sh.ks, n = np + (sh.extra ? sh.run_of((int64_t)(x + 1) * sh.tail - 1) - e0 + 1 : 0);
+    auto of = [&](int i) { return i < np ? sh.slot_part(i, x) : sh.slot_run(e0 + i - np, x); };
+    // two columns' worth of 16 bytes a thread, four partials of both at a time
+    constexpr int N = FR * (LT / 4) / 256;
+    const int c = threadIdx.x % (LT / 4) * 4, k = tn * LT + c;
+    int row[N];
+    const float *p[N];
+    f32x4 x4[N];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (s0 + u < sp.ks) v[u] = *reinterpret_cast<const f32x4 *>(p + (int64_t)(s0 + u) * tiles * (LT * LT));
+    for (int i = 0; i < N; ++i) {
+        const int tl = r0 + i * (256 / (LT / 4)) + (int)threadIdx.x / (LT / 4);
+        row[i] = tm * LT + tl;
+        p[i] = g.part + tl * LT + c;
+        x4[i] = f32x4{0, 0, 0, 0};
+    }
+    for (int s0 = 0; s0 < n; s0 += 4) {
+        f32x4 v[N][4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (s0 + u < sp.ks) x += v[u];
+        for (int u = 0; u < 4; ++u) {
+            const int64_t o = s0 + u < n ? (int64_t)of(s0 + u) * (LT * LT) : 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (s0 + u < n && row[i] < count) v[i][u] = *reinterpret_cast<const f32x4 *>(p[i] + o);
         }
-        f32x4 *sum = g.sum32 ? reinterpret_cast<f32x4 *>(g.sum32 + (int64_t)row * g.K + k) : nullptr;
-        if (g.c_old) x += *sum * __builtin_amdgcn_exp2f(g.c_old[row] - g.c[row]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (s0 + u < n) x4[i] += v[i][u];
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (row[i] >= count || k >= g.K) continue;
+        const int t = row[i];
+        f32x4 *sum = g.sum32 ? reinterpret_cast<f32x4 *>(g.sum32 + (int64_t)t * g.K + k) : nullptr;
+        if (g.c_old) x4[i] += *sum * __builtin_amdgcn_exp2f(g.c_old[t] - g.c[t]);
         if (!g.dX) {
-            *sum = x;
+            *sum = x4[i];
             continue;
         }
         // a label out of the vocabulary: a and b are NaN
-        const uint2 w = *reinterpret_cast<const uint2 *>(g.W + (int64_t)max(g.r.label[row], 0) * g.K + k);
-        *reinterpret_cast<uint2 *>(g.dX + (int64_t)g.r.row[row] * g.K + k) = LossFinal{g.r.a[row], g.r.b[row]}.value(x, w);
+        const uint2 w = *reinterpret_cast<const uint2 *>(g.W + (int64_t)max(g.r.label[t], 0) * g.K + k);
+        *reinterpret_cast<uint2 *>(g.dX + (int64_t)g.r.row[t] * g.K + k) = LossFinal{g.r.a[t], g.r.b[t]}.value(x4[i], w);
     }
 }
 
 }  // namespace
 
 hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream) {
-    const int64_t tiles = (int64_t)(a.Mp / LT) * ((a.K + LT - 1) / LT);
-    const int64_t grid = tiles > 256 ? tiles : 256;
-    hipLaunchKernelGGL(loss_dx_kernel, dim3((uint32_t)grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(loss_dx_kernel, dim3(256), dim3(256), 0, stream, a);      // a workgroup on each CU
     return hipGetLastError();
 }
 
 hipError_t launch_loss_fold(const LossDxArgs &a, hipStream_t stream) {
-    const int64_t blocks = ((int64_t)a.Mp * (a.K >> 2) + 255) / 256;
-    hipLaunchKernelGGL(loss_fold_kernel, dim3((uint32_t)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, a);
+    // fewer than 256 tiles have partials, and no more than there are
+    const int64_t tiles = (int64_t)(a.Mp / LT) * ((a.K + LT - 1) / LT);
+    hipLaunchKernelGGL(loss_fold_kernel, dim3((uint32_t)((tiles < 255 ? tiles : 255) * (LT / FR))), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

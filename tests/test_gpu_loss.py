@@ -115,6 +115,21 @@ def test_tokens_without_a_label(none):
     assert same(again[0], loss) and same(again[1], mean) and same(again[2], dX)
 
 
+@pytest.mark.parametrize("M", [65, 1024, 65536, 65537, 140001])
+def test_live_rows_of_many_tokens(M):
+    """Which rows take part, and in which order, over the runs that the list of live rows is made of."""
+    V, K = 70, 64
+    X, W, _ = make(64, V, K, seed=17)
+    X = X[torch.arange(M, device=DEV) % 64].contiguous()          # 64 different tokens
+    labels = torch.from_numpy(np.random.default_rng(M).integers(-V, V, M)).to(DEV)
+    labels[200:400] = NONE
+    labels[-1] = 5
+    g = torch.rand(M, device=DEV)
+    print(f"live rows: M={M} V={V} K={K}", flush=True)
+    check(X, W, labels, g, rows=np.unique(np.concatenate([np.arange(min(M, 300)), np.arange(M - 65, M),
+                                                          np.arange(max(0, min(M, 65536) - 70), min(M, 65606))])))
+
+
 def test_any_negative_label_counts_as_none():
     X, W, labels = make(40, 300, 64, seed=5)
     a, b = labels.clone(), labels.clone()
