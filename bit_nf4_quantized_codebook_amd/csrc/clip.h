@@ -12,7 +12,7 @@ struct ClipEntry {
     int64_t numel;
     int64_t chunk;       // chunks of the tensors before it, times two; + 1: float32
 };
-constexpr int kClipChunk = 8192;     // elements
+constexpr int kClipChunk = 4096;     // elements
 constexpr int kClipParts = 2048;     // workgroups of a pass at most: eight on each CU
 
 // table: device [n]; part: device [kClipParts]

@@ -7,7 +7,12 @@
 // (the stream leaves room for some 60 operations an element).  Each workgroup leaves one partial sum; the
 // second pass sums them again in every workgroup, in a fixed order, which is cheaper than a launch between.
 //
-// The second pass walks backwards: what the first read last still lies in the memory-side cache.
+// The second pass walks backwards, since what the first read last still lies in the memory-side cache, and both its loads
+// and its stores are nontemporal, so as not to drive the rest out.
+//
+// Bound by HBM: 224 adapter pairs of the 7B width in bf16 (320 MB) take 163 us, where reading them twice and writing
+// them once at a copy's 5.0 TB/s takes 192; 217 us with plain loads and stores and 8192 elements a chunk, 167 walking
+// forwards, 185 with nontemporal loads in the first pass too.  One pair takes 8.5 us of kernels, 11 as a call.
 //
 // The list (pointers, sizes, first chunks) is a table in device memory that the caller keeps with the gradients.
 
@@ -18,7 +23,7 @@ namespace nf4k {
 
 namespace {
 
-constexpr int CHUNK = kClipChunk;      // a workgroup's threads take 32 elements each
+constexpr int CHUNK = kClipChunk;      // a workgroup's threads take 16 elements each
 constexpr int NT = 256;
 
 __device__ __forceinline__ int64_t first(const ClipEntry &e) { return e.chunk >> 1; }
@@ -94,13 +99,13 @@ __device__ __forceinline__ void scale(const T *p, T *o, int n, bool clip, double
         V v[PER];
 #pragma unroll
         for (int u = 0; u < PER; ++u)
-            if (u * NT + tid < nv) v[u] = q[u * NT + tid];
+            if (u * NT + tid < nv) v[u] = __builtin_nontemporal_load(&q[u * NT + tid]);
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             if (u * NT + tid >= nv) continue;
 #pragma unroll
             for (int k = 0; k < VEC; ++k) v[u][k] = to(v[u][k]);
-            w[u * NT + tid] = v[u];
+            __builtin_nontemporal_store(v[u], &w[u * NT + tid]);
         }
         if (tid < h) o[tid] = to(p[tid]);
     }

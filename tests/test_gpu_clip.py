@@ -59,7 +59,7 @@ def check(grads, max_norm, outs=None):
     return norm
 
 
-SIZES = [1, 2, 3, 7, 8, 9, 63, 64, 65, 0, 1000, 8191, 8192, 8193, 20000, 5, 100001]
+SIZES = [1, 2, 3, 7, 8, 9, 63, 64, 65, 0, 1000, 4095, 4096, 4097, 8191, 8192, 8193, 20000, 5, 100001]
 
 
 @pytest.mark.parametrize("kinds", ["b", "f", "bf", "fbb"])
