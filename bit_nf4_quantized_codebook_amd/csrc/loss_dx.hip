@@ -103,7 +103,11 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     }
     const uint32_t row4_off = (uint32_t)(4 * g.K * 2);
     const uint32_t step_off = (uint32_t)(LSTEP * g.K * 2);
-    const uint32_t boff = (uint32_t)(wave * 8192 + lane * 16);
+    // P: instruction q of wave w copies rows 64 w + 8 q ..; past the live rows there is nothing to read
+    uint32_t boff[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        boff[q] = tm * LT + 64 * wave + 8 * q + (lane >> 3) < count ? (uint32_t)(wave * 8192 + q * 1024 + lane * 16) : 0x80000000u;
     auto load = [&](int step, uint8_t *st, int part) {
         lds_u8 *da = (lds_u8 *)st + wave * 8192, *db = (lds_u8 *)(st + LOPB) + wave * 8192;
         const uint32_t dead = step < steps ? 0u : 0x80000000u;      // past the descriptor's end
@@ -114,7 +118,7 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
             // rows 2q and 2q + 1 of the wave's 16: q and q + 2 share row % 4
             const uint32_t v = aoff[q & 1] + (uint32_t)(q >> 1) * row4_off + (uint32_t)step * step_off;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void *)(da + q * 1024), 16, v | dead, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, boff, bstep + q * 1024, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rB, (lds_void *)(db + q * 1024), 16, boff[q], bstep, 0, 0);
         }
     };
     // W's fragment of sub-step s, columns wm*128 + 32 i ..: 16-lane group (hh, half) reads rows

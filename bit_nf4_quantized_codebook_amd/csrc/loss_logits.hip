@@ -247,11 +247,11 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
             for (int b = 0; b < B; ++b) {
                 const int row = tl0 + TI * b;
                 st.sums[wm][row] = s[b];      // the same from all of a token's lanes
-                if (GRAD) {
+                if (GRAD) {      // nontemporal: 1659 -> 1647 us for the whole call at 4096 x 32000 x 4096
                     const float *e = x[b];
                     __builtin_amdgcn_raw_buffer_store_b128(
                         u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])}, rP,
-                        (uint32_t)((q >> 3) * (int)(LBLOCK * 2) + row * 128 + (((q & 7) ^ ((row >> 1) & 7)) * 16)), 0, 0);
+                        (uint32_t)((q >> 3) * (int)(LBLOCK * 2) + row * 128 + (((q & 7) ^ ((row >> 1) & 7)) * 16)), 0, 2);
                 }
             }
         }
