@@ -1431,7 +1431,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         off += round256(bytes);
         return at;
     };
-    p.off_count = take(8);
+    p.off_count = take(4);
     p.off_sums = take((size_t)(p.Mp / nf4k::kLossJoinRows) * 8);
     p.off_row = take((size_t)p.Mp * 4);
     p.off_label = take((size_t)p.Mp * 4);
@@ -1498,24 +1498,25 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
     }
     NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");
     // c[piece % 2]: the rows' references after that piece
-    for (int32_t t0 = 0, piece = 1; t0 < p.tiles; t0 += p.piece, ++piece) {
+    for (int32_t t0 = 0, piece = 0; t0 < p.tiles; t0 += p.piece, ++piece) {
         const int32_t nt = p.tiles - t0 < p.piece ? p.tiles - t0 : p.piece;
         const bool last = t0 + nt == p.tiles;
-        const float *before = t0 ? c[(piece - 1) % 2] : nullptr;
+        const float *before = t0 ? c[(piece + 1) % 2] : nullptr;
         float *now = c[piece % 2];
         NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, P, 4 * nt}, s),
                       "loss logits");
-        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, piece, last, grad, dloss,
-                                                            loss, mean}, s), "loss sums");
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, P, last, grad, dloss, loss,
+                                                            mean}, s), "loss sums");
         // one workgroup of the join writes the mean itself
-        float *mean_here = last && M > nf4k::kLossJoinRows ? mean : nullptr;
-        if (grad || mean_here)
-            NF4_CHECK_HIP(nf4k::launch_loss_rescale(nf4k::LossRescale{r, M, p.Mp, nt, piece, P, tref, now, mean_here}, s),
-                          "loss rescale");
-        if (!grad) continue;
+        float *mean_after = last && M > nf4k::kLossJoinRows ? mean : nullptr;
+        if (!grad) {
+            if (mean_after) NF4_CHECK_HIP(nf4k::launch_loss_mean(r, M, mean, s), "loss mean");
+            continue;
+        }
         const bool one = p.piece == p.tiles;
         const nf4k::LossDxArgs d{P, W, V, K, (int64_t)t0 * nf4k::LT, r, p.Mp, 4 * nt, ws_at<float>(workspace, p.off_part),
-                                 one ? nullptr : ws_at<float>(workspace, p.off_sum32), now, before, last ? dX : nullptr};
+                                 one ? nullptr : ws_at<float>(workspace, p.off_sum32), now, before, last ? dX : nullptr, M,
+                                 mean_after};
         NF4_CHECK_HIP(nf4k::launch_loss_dx(d, s), "loss dX");
         NF4_CHECK_HIP(nf4k::launch_loss_fold(d, s), "loss dX sum");
     }

@@ -22,7 +22,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // Per-row state in the workspace; row arrays have Mp = M rounded up to 256 entries.
 struct LossRows {
-    int32_t *count;        // [0]: live rows; [1]: the last piece with a tile that needs rescaling
+    int32_t *count;        // [1] live rows
     double *sums;          // [ceil(M / kLossJoinRows)] sums of the losses of each workgroup of the last join
     int32_t *row;          // [M] live row -> token
     int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
@@ -122,6 +122,8 @@ struct LossDxArgs {
     float *sum32;             // [Mp, K]; NULL: one piece only
     const float *c, *c_old;   // c_old NULL: the first piece
     uint16_t *dX;             // NULL: not the last piece
+    int64_t M;
+    float *mean;              // written by the fold, or NULL
 };
 hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream);
 // the same for the tiles with partials
@@ -130,7 +132,8 @@ hipError_t launch_loss_fold(const LossDxArgs &a, hipStream_t stream);
 // labels -> live rows; loss and dX of the other tokens set to zero
 hipError_t launch_loss_prep(const int64_t *labels, int64_t M, int64_t V, int64_t K, const LossRows &r, float *loss,
                             uint16_t *dX, hipStream_t stream);
-// the tiles' references and sums into the rows' (c_in NULL: the first)
+// the tiles' references and sums into the rows' (c_in NULL: the first), and P's tiles brought from their own references to
+// the rows' where any differs
 struct LossJoin {
     LossRows r;
     int64_t M;
@@ -139,23 +142,29 @@ struct LossJoin {
     int32_t ntile;
     const float *c_in;
     float *c_out;
-    int32_t piece;            // from 1
+    uint16_t *P;              // or NULL: the forward
     // the last join: losses, the sums for their mean, and with grad the coefficients of dX
     bool last, grad;
     const float *dloss;
     float *loss, *mean;
 };
 hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream);
-// P's tiles brought from their own references to the rows', where any differs; mean (or NULL) from the sums
-struct LossRescale {
-    LossRows r;
-    int64_t M;
-    int32_t Mp, ntile, piece;
-    uint16_t *P;              // NULL: only the mean
-    const float *tref, *c;
-    float *mean;
-};
-hipError_t launch_loss_rescale(const LossRescale &a, hipStream_t stream);
+// the mean from the last join's sums (with grad, dX's last launch writes it; one workgroup of the join writes it itself)
+hipError_t launch_loss_mean(const LossRows &r, int64_t M, float *mean, hipStream_t stream);
+
+// by 256 threads
+__device__ __forceinline__ void loss_write_mean(const double *sums, int n, int count, float *mean) {
+    __shared__ double total[256];
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += 256) s += sums[i];
+    total[threadIdx.x] = s;
+    __syncthreads();
+    for (int d = 128; d > 0; d >>= 1) {
+        if ((int)threadIdx.x < d) total[threadIdx.x] += total[threadIdx.x + d];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) mean[0] = count ? (float)(total[0] / count) : 0.0f;
+}
 
 // the forward for up to kLossGemvMaxM tokens
 constexpr int64_t kLossGemvMaxM = 64;

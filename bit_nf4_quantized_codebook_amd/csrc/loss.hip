@@ -75,24 +75,10 @@ __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restri
     }
     if (tid == 0) {
         r.count[0] = base;
-        r.count[1] = 0;
     }
 }
 
 constexpr int JR = kLossJoinRows, JS = 256 / JR;      // rows of a workgroup, and threads over the tiles of a row
-
-__device__ __forceinline__ void write_mean(const double *sums, int n, int count, float *mean) {
-    __shared__ double total[256];
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n; i += 256) s += sums[i];
-    total[threadIdx.x] = s;
-    __syncthreads();
-    for (int d = 128; d > 0; d >>= 1) {
-        if ((int)threadIdx.x < d) total[threadIdx.x] += total[threadIdx.x + d];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) mean[0] = count ? (float)(total[0] / count) : 0.0f;
-}
 
 __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     __shared__ float pc[JS][JR], ps[JS][JR];
@@ -145,8 +131,27 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     float top = c_old;
 #pragma unroll
     for (int s = 0; s < JS; ++s) top = fmaxf(top, pc[s][lr]);
-    // a tile (or, in earlier pieces' order, nothing else) below the row's reference: P has to be rescaled
-    if (g.grad && live && !(low >= top)) g.r.count[1] = g.piece;
+    // Tiles with a reference below the row's: p is brought to it (rare, and only this workgroup's rows).  Row `row` of
+    // P's blocks: 128 bytes for each 64 vocabulary rows, so 512 for a whole tile.
+    if (g.P && __syncthreads_or(live && !(low >= top))) {
+        for (int t = slice; live && t < entries; t += JS) {
+            const int tile = t < g.ntile ? t : t - g.ntile + cut;
+            const int half0 = t >= g.ntile, half1 = t < g.ntile && tile >= cut ? 1 : 2;      // halves this entry stands for
+            const float from = g.tref[(int64_t)(t < g.ntile ? t : t + cut) * g.Mp + row];
+            if (from == top) continue;
+            const float f = __builtin_amdgcn_exp2f(from - top);
+            for (int b = 2 * half0; b < 2 * half1; ++b) {
+                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + (((int64_t)(row / LT) * g.ntile + tile) * 4 + b) * LBLOCK + (row % LT) * LSTEP);
+                for (int i = 0; i < 8; ++i) {
+                    u32x4 v = p[i];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = pack_bf16x2(bf16_to_f32(v[k] & 0xFFFFu) * f, __uint_as_float(v[k] & 0xFFFF0000u) * f);
+                    p[i] = v;
+                }
+            }
+        }
+    }
     if (slice == 0) {
         double value = 0.0;
         if (live) {
@@ -182,37 +187,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     }
 }
 
-// Grid-stride over half tiles (256 rows and 128 vocabulary rows: two blocks of P); workgroup 0 also writes the mean.
-__global__ __launch_bounds__(256) void loss_rescale_kernel(LossRescale g) {
-    __shared__ float f[LT];
-    const int count = g.r.count[0], tid = threadIdx.x;
-    if (g.mean && blockIdx.x == 0) {
-        write_mean(g.r.sums, (int)((g.M + JR - 1) / JR), count, g.mean);
-        return;
-    }
-    if (!g.P || g.r.count[1] != g.piece) return;
-    const LossTiles tiles((count + LT - 1) / LT, g.ntile);
-    const int first = g.mean ? 1 : 0;
-    for (int x = blockIdx.x - first; x < tiles.ntm * 2 * g.ntile; x += gridDim.x - first) {
-        const int tm = x / (2 * g.ntile), t = x % (2 * g.ntile) / 2, h = x & 1;
-        const int64_t entry = (h && t >= tiles.first_cut(tm) ? g.ntile : 0) + t;
-        const int row = tm * LT + tid;
-        const float from = row < count ? g.tref[entry * g.Mp + row] : 0.0f, to = row < count ? g.c[row] : 0.0f;
-        f[tid] = __builtin_amdgcn_exp2f(from - to);
-        const bool any = __syncthreads_or(!(from == to));
-        if (any) {
-            uint16_t *base = g.P + (((int64_t)tm * g.ntile + t) * 4 + 2 * h) * LBLOCK;
-            for (int i = tid; i < 2 * LBLOCK / 8; i += 256) {
-                const float s = f[(i >> 3) & (LT - 1)];     // 8 chunks a row, 256 rows a block
-                u32x4 v = reinterpret_cast<u32x4 *>(base)[i];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = pack_bf16x2(bf16_to_f32(v[k] & 0xFFFFu) * s, __uint_as_float(v[k] & 0xFFFF0000u) * s);
-                reinterpret_cast<u32x4 *>(base)[i] = v;
-            }
-        }
-        __syncthreads();
-    }
+__global__ __launch_bounds__(256) void loss_mean_kernel(LossRows r, int64_t M, float *mean) {
+    loss_write_mean(r.sums, (int)((M + JR - 1) / JR), r.count[0], mean);
 }
 
 }  // namespace
@@ -230,8 +206,8 @@ hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_loss_rescale(const LossRescale &a, hipStream_t stream) {
-    hipLaunchKernelGGL(loss_rescale_kernel, dim3(a.P ? 1024 : 1), dim3(256), 0, stream, a);
+hipError_t launch_loss_mean(const LossRows &r, int64_t M, float *mean, hipStream_t stream) {
+    hipLaunchKernelGGL(loss_mean_kernel, dim3(1), dim3(256), 0, stream, r, M, mean);
     return hipGetLastError();
 }
 

@@ -226,12 +226,16 @@ __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     }
 }
 
-// Workgroup: FR rows of a tile with partials
+// Workgroup: FR rows of a tile with partials; the last one: the losses' mean
 constexpr int FR = 8;
 __global__ __launch_bounds__(256) void loss_fold_kernel(LossDxArgs g) {
     const int count = g.r.count[0];
     const int ntm = (count + LT - 1) / LT, ntn = (int)((g.K + LT - 1) / LT);
     const LossShares sh(ntm * ntn, g.steps);
+    if (blockIdx.x == gridDim.x - 1) {
+        if (g.mean) loss_write_mean(g.r.sums, (int)((g.M + kLossJoinRows - 1) / kLossJoinRows), count, g.mean);
+        return;
+    }
     const int x = (int)blockIdx.x / (LT / FR), r0 = (int)blockIdx.x % (LT / FR) * FR;
     if (x >= sh.rest || !sh.partial()) return;
     int tm, tn;
@@ -295,7 +299,7 @@ hipError_t launch_loss_dx(const LossDxArgs &a, hipStream_t stream) {
 hipError_t launch_loss_fold(const LossDxArgs &a, hipStream_t stream) {
     // fewer than 256 tiles have partials, and no more than there are
     const int64_t tiles = (int64_t)(a.Mp / LT) * ((a.K + LT - 1) / LT);
-    hipLaunchKernelGGL(loss_fold_kernel, dim3((uint32_t)((tiles < 255 ? tiles : 255) * (LT / FR))), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(loss_fold_kernel, dim3((uint32_t)((tiles < 255 ? tiles : 255) * (LT / FR) + 1)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
