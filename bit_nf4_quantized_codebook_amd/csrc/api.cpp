@@ -1408,6 +1408,7 @@ constexpr size_t kLossTableBytes = (size_t)64 << 20;     // the forward's piece:
 constexpr int64_t kLossMinTiles = 32;
 
 struct LossPlan {
+    bool narrow;                       // few tokens, with the gradient
     bool gemv;                         // few tokens, forward: its table lies at off_tref
     int32_t Mp, tiles, piece;          // rows padded to tiles; tiles of the vocabulary, and of a piece
     size_t off_count, off_sums, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[2], off_tref, off_tsum, off_P, off_part,
@@ -1432,7 +1433,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         return at;
     };
     p.off_count = take(4);
-    p.off_sums = take((size_t)(p.Mp / nf4k::kLossJoinRows) * 8);
+    p.off_sums = take((size_t)(p.Mp / nf4k::kLossJoinRowsNarrow) * 8);
     p.off_row = take((size_t)p.Mp * 4);
     p.off_label = take((size_t)p.Mp * 4);
     p.off_zl = take((size_t)p.Mp * 4);
@@ -1440,6 +1441,17 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.off_a = take((size_t)p.Mp * 4);
     p.off_b = take((size_t)p.Mp * 4);
     for (size_t &c : p.off_c) c = take((size_t)p.Mp * 4);
+    p.narrow = grad && M <= nf4k::kLossNarrowMaxM && p.piece == p.tiles;
+    if (p.narrow) {
+        const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
+        p.off_tref = take((size_t)n.steps * p.Mp * 4);
+        p.off_tsum = take((size_t)n.steps * p.Mp * 4);
+        p.off_P = take((size_t)n.steps * nf4k::LBLOCK * 2);
+        p.off_part = take(n.parts * 4);
+        p.off_sum32 = p.total = off;
+        p.gemv = false;
+        return p;
+    }
     p.gemv = !grad && M <= nf4k::kLossGemvMaxM;
     if (p.gemv) {
         p.off_tref = take((size_t)M * ((V + 15) / 16) * 8);
@@ -1496,6 +1508,16 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         NF4_CHECK_HIP(nf4k::launch_loss_gemv(a, s), "loss of few tokens");
         return NF4_OK;
     }
+    float *part = ws_at<float>(workspace, p.off_part);
+    if (p.narrow) {
+        const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
+        const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.Mp, n.steps, n.per, tref, tsum, P, part, loss, mean, dX};
+        NF4_CHECK_HIP(nf4k::launch_loss_narrow_logits(a, s), "loss logits of few tokens");
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, n.steps, nullptr, c[0], P, true, true,
+                                                            dloss, loss, mean}, true, s), "loss sums");
+        NF4_CHECK_HIP(nf4k::launch_loss_narrow_dx(a, s), "loss dX of few tokens");
+        return NF4_OK;
+    }
     NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");
     // c[piece % 2]: the rows' references after that piece
     for (int32_t t0 = 0, piece = 0; t0 < p.tiles; t0 += p.piece, ++piece) {
@@ -1506,7 +1528,7 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, P, 4 * nt}, s),
                       "loss logits");
         NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, P, last, grad, dloss, loss,
-                                                            mean}, s), "loss sums");
+                                                            mean}, false, s), "loss sums");
         // one workgroup of the join writes the mean itself
         float *mean_after = last && M > nf4k::kLossJoinRows ? mean : nullptr;
         if (!grad) {
@@ -1514,7 +1536,7 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
             continue;
         }
         const bool one = p.piece == p.tiles;
-        const nf4k::LossDxArgs d{P, W, V, K, (int64_t)t0 * nf4k::LT, r, p.Mp, 4 * nt, ws_at<float>(workspace, p.off_part),
+        const nf4k::LossDxArgs d{P, W, V, K, (int64_t)t0 * nf4k::LT, r, p.Mp, 4 * nt, part,
                                  one ? nullptr : ws_at<float>(workspace, p.off_sum32), now, before, last ? dX : nullptr, M,
                                  mean_after};
         NF4_CHECK_HIP(nf4k::launch_loss_dx(d, s), "loss dX");

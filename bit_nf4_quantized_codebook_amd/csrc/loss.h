@@ -17,16 +17,17 @@ constexpr int LT = 256;                  // tokens, vocabulary rows or columns o
 constexpr int LSTEP = 64;                // reduction of one step of a tile's loop
 constexpr int64_t LBLOCK = LT * LSTEP;   // elements of one step's operand tile (32 KB)
 constexpr int kLossJoinRows = 8;        // rows of a workgroup that joins the tiles
+constexpr int kLossJoinRowsNarrow = 2;  // the same for few tokens
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Per-row state in the workspace; row arrays have Mp = M rounded up to 256 entries.
 struct LossRows {
     int32_t *count;        // [1] live rows
-    double *sums;          // [ceil(M / kLossJoinRows)] sums of the losses of each workgroup of the last join
+    double *sums;          // [a join's workgroups] sums of the losses of each workgroup of the last join
     int32_t *row;          // [M] live row -> token
     int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
-    float *zl;             // [M] the label's logit in log2 units
+    float *zl;             // [M] the label's logit in log2 units (unset without one)
     float *S;              // [M] sum over the other vocabulary rows of 2^(l - c)
     float *a, *b;          // [M] dX = a (sum P W) - b W[label]
 };
@@ -148,7 +149,8 @@ struct LossJoin {
     const float *dloss;
     float *loss, *mean;
 };
-hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream);
+// narrow: the tables of loss_narrow.hip
+hipError_t launch_loss_join(const LossJoin &a, bool narrow, hipStream_t stream);
 // the mean from the last join's sums (with grad, dX's last launch writes it; one workgroup of the join writes it itself)
 hipError_t launch_loss_mean(const LossRows &r, int64_t M, float *mean, hipStream_t stream);
 
@@ -165,6 +167,28 @@ __device__ __forceinline__ void loss_write_mean(const double *sums, int n, int c
     }
     if (threadIdx.x == 0) mean[0] = count ? (float)(total[0] / count) : 0.0f;
 }
+
+// with the gradient, for up to kLossNarrowMaxM tokens and one piece
+constexpr int64_t kLossNarrowMaxM = 128;
+struct LossNarrowPlan {
+    int32_t TT, steps, per, splits;
+    size_t parts;             // float32 partials
+};
+LossNarrowPlan loss_narrow_plan(int64_t M, int64_t V, int64_t K);
+struct LossNarrow {
+    const uint16_t *W, *X;
+    int64_t V, K, M;
+    const int64_t *labels;
+    LossRows r;
+    int32_t Mp, steps, per;   // steps of 64 vocabulary rows: all, and of dX's workgroup
+    float *tref, *tsum;       // [Mp][steps]
+    uint16_t *P;              // [steps] blocks
+    float *part;
+    float *loss, *mean;
+    uint16_t *dX;
+};
+hipError_t launch_loss_narrow_logits(const LossNarrow &g, hipStream_t stream);
+hipError_t launch_loss_narrow_dx(const LossNarrow &g, hipStream_t stream);
 
 // the forward for up to kLossGemvMaxM tokens
 constexpr int64_t kLossGemvMaxM = 64;

@@ -68,7 +68,6 @@ __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restri
             const int at = begin[run] + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(live >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)live, 0u));
             r.row[at] = (int32_t)m;
             r.label[at] = l < V ? (int32_t)l : -1;
-            r.zl[at] = __builtin_nanf("");      // a label in the vocabulary writes its logit over it
         }
         base += all;
         __syncthreads();
@@ -78,13 +77,17 @@ __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restri
     }
 }
 
-constexpr int JR = kLossJoinRows, JS = 256 / JR;      // rows of a workgroup, and threads over the tiles of a row
-
+// JR rows a workgroup and 256 / JR threads over the tiles of a row.  NARROW: tiles of one step, never cut, and tables by
+// row ([row][tile]); otherwise tiles of four steps, cut ones among them, and tables by tile ([tile][Mp]).
+template <int JR, bool NARROW>
 __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
-    __shared__ float pc[JS][JR], ps[JS][JR];
+    constexpr int JS = 256 / JR, BLOCKS = NARROW ? 1 : 4;
+    constexpr int W0 = NARROW ? 1 : JR, NWR = NARROW ? 4 / JR : 4;      // first lane step of a row; waves that share one
+    __shared__ float pc[4][JR], ps[4][JR];
     __shared__ double sl[JR];
     const int count = g.r.count[0];
-    const int tid = threadIdx.x, lr = tid % JR, slice = tid / JR;
+    const int tid = threadIdx.x, lr = NARROW ? tid / JS : tid % JR, slice = NARROW ? tid % JS : tid / JR;
+    const int wave = tid >> 6, w0 = NARROW ? lr * NWR : 0;
     const int row = blockIdx.x * JR + lr;
     const bool live = row < count;
     if ((int)blockIdx.x * JR >= count) {
@@ -100,48 +103,64 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     float c = c_old, sum = 0.0f, low = -NEG;
     // entries of this row's tiles: ntile, and the second halves of the tiles that are cut
     const LossTiles tiles((count + LT - 1) / LT, g.ntile);
-    const int cut = tiles.first_cut(row / LT), entries = 2 * g.ntile - cut;
+    const int cut = NARROW ? g.ntile : tiles.first_cut(row / LT), entries = 2 * g.ntile - cut;
+    auto at = [&](int t) { return NARROW ? (int64_t)row * g.ntile + t : (int64_t)(t < g.ntile ? t : t + cut) * g.Mp + row; };
+    // what the row's own results take, on its way already
+    int m = 0, label = -1;
+    float zl = 0.0f, weight = 0.0f;
+    if (g.last && live && slice == 0) {
+        m = g.r.row[row];
+        label = g.r.label[row];
+        zl = g.r.zl[row];
+        weight = g.dloss ? g.dloss[m] : 1.0f / (float)count;
+    }
     if (live)
         for (int t0 = slice; t0 < entries; t0 += JS * 8) {
-            float f[8], s[8], m = c;
+            float f[8], s[8], most = c;
             bool has[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const int t = t0 + u * JS;
-                const int64_t o = (int64_t)(t < g.ntile ? t : t + cut) * g.Mp + row;
                 has[u] = t < entries;
-                f[u] = has[u] ? g.tref[o] : NEG;
-                s[u] = has[u] ? g.tsum[o] : 0.0f;
+                f[u] = has[u] ? g.tref[at(t)] : NEG;
+                s[u] = has[u] ? g.tsum[at(t)] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                m = fmaxf(m, f[u]);
+                most = fmaxf(most, f[u]);
                 low = fminf(low, has[u] ? f[u] : -NEG);
             }
-            // c = m also before the first tile, where there is nothing to move (and both may be -inf)
-            sum *= m == c ? 1.0f : __builtin_amdgcn_exp2f(c - m);
+            // c = most also before the first tile, where there is nothing to move (and both may be -inf)
+            sum *= most == c ? 1.0f : __builtin_amdgcn_exp2f(c - most);
 #pragma unroll
             for (int u = 0; u < 8; ++u)
-                if (has[u]) sum += s[u] * __builtin_amdgcn_exp2f(f[u] - m);
-            c = m;
+                if (has[u]) sum += s[u] * __builtin_amdgcn_exp2f(f[u] - most);
+            c = most;
         }
-    pc[slice][lr] = c;
-    ps[slice][lr] = sum;
-    __syncthreads();
-    float top = c_old;
+    float top = c;
 #pragma unroll
-    for (int s = 0; s < JS; ++s) top = fmaxf(top, pc[s][lr]);
+    for (int d = W0; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    pc[wave][lr] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NWR; ++w) top = fmaxf(top, pc[w0 + w][lr]);
+    sum = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(c - top);
+#pragma unroll
+    for (int d = W0; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    ps[wave][lr] = sum;
+    __syncthreads();
     // Tiles with a reference below the row's: p is brought to it (rare, and only this workgroup's rows).  Row `row` of
     // P's blocks: 128 bytes for each 64 vocabulary rows, so 512 for a whole tile.
     if (g.P && __syncthreads_or(live && !(low >= top))) {
         for (int t = slice; live && t < entries; t += JS) {
             const int tile = t < g.ntile ? t : t - g.ntile + cut;
-            const int half0 = t >= g.ntile, half1 = t < g.ntile && tile >= cut ? 1 : 2;      // halves this entry stands for
-            const float from = g.tref[(int64_t)(t < g.ntile ? t : t + cut) * g.Mp + row];
+            // blocks this entry stands for: all of its tile's, or the half's
+            const int b0 = t < g.ntile ? 0 : BLOCKS / 2, b1 = t < g.ntile && tile >= cut ? BLOCKS / 2 : BLOCKS;
+            const float from = g.tref[at(t)];
             if (from == top) continue;
             const float f = __builtin_amdgcn_exp2f(from - top);
-            for (int b = 2 * half0; b < 2 * half1; ++b) {
-                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + (((int64_t)(row / LT) * g.ntile + tile) * 4 + b) * LBLOCK + (row % LT) * LSTEP);
+            for (int b = b0; b < b1; ++b) {
+                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + (((int64_t)(row / LT) * g.ntile + tile) * BLOCKS + b) * LBLOCK + (row % LT) * LSTEP);
                 for (int i = 0; i < 8; ++i) {
                     u32x4 v = p[i];
 #pragma unroll
@@ -157,21 +176,19 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
         if (live) {
             float S = g.c_in ? g.r.S[row] * __builtin_amdgcn_exp2f(c_old - top) : 0.0f;
 #pragma unroll
-            for (int s = 0; s < JS; ++s) S += ps[s][lr] == 0.0f ? 0.0f : ps[s][lr] * __builtin_amdgcn_exp2f(pc[s][lr] - top);
+            for (int w = 0; w < NWR; ++w) S += ps[w0 + w][lr];
             g.r.S[row] = S;
             g.c_out[row] = top;
             if (g.last) {
-                const float zl = g.r.zl[row];
-                // ln S + (c - zl) ln 2
+                // ln S + (c - zl) ln 2; a label out of the vocabulary has no logit
+                if (label < 0) zl = __builtin_nanf("");
                 const float d = (log2f(S) + (top - zl)) * kLn2;
-                const int32_t m = g.r.row[row];
                 const float loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
                 g.loss[m] = loss;
                 value = (double)loss;
                 if (g.grad) {
-                    const float w = g.dloss ? g.dloss[m] : 1.0f / (float)count;
-                    g.r.a[row] = w / (S + __builtin_amdgcn_exp2f(zl - top));
-                    g.r.b[row] = w / (1.0f + expf(-d));
+                    g.r.a[row] = weight / (S + __builtin_amdgcn_exp2f(zl - top));
+                    g.r.b[row] = weight / (1.0f + expf(-d));
                 }
             }
         }
@@ -188,7 +205,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
 }
 
 __global__ __launch_bounds__(256) void loss_mean_kernel(LossRows r, int64_t M, float *mean) {
-    loss_write_mean(r.sums, (int)((M + JR - 1) / JR), r.count[0], mean);
+    loss_write_mean(r.sums, (int)((M + kLossJoinRows - 1) / kLossJoinRows), r.count[0], mean);
 }
 
 }  // namespace
@@ -201,8 +218,14 @@ hipError_t launch_loss_prep(const int64_t *labels, int64_t M, int64_t V, int64_t
     return hipGetLastError();
 }
 
-hipError_t launch_loss_join(const LossJoin &a, hipStream_t stream) {
-    hipLaunchKernelGGL(loss_join_kernel, dim3((uint32_t)((a.M + JR - 1) / JR)), dim3(256), 0, stream, a);
+hipError_t launch_loss_join(const LossJoin &a, bool narrow, hipStream_t stream) {
+    if (narrow) {
+        const uint32_t grid = (uint32_t)((a.M + kLossJoinRowsNarrow - 1) / kLossJoinRowsNarrow);
+        hipLaunchKernelGGL((loss_join_kernel<kLossJoinRowsNarrow, true>), dim3(grid), dim3(256), 0, stream, a);
+    } else {
+        const uint32_t grid = (uint32_t)((a.M + kLossJoinRows - 1) / kLossJoinRows);
+        hipLaunchKernelGGL((loss_join_kernel<kLossJoinRows, false>), dim3(grid), dim3(256), 0, stream, a);
+    }
     return hipGetLastError();
 }
 

@@ -21,15 +21,6 @@ namespace nf4k {
 
 namespace {
 
-// A token's last step: dX = a (sum P W) - b W[label], rounded once.
-struct LossFinal {
-    float a, b;
-    __device__ __forceinline__ uint2 value(const f32x4 &x, const uint2 &v) const {
-        return uint2{pack_bf16x2(a * x[0] - b * bf16_to_f32(v.x & 0xFFFFu), a * x[1] - b * __uint_as_float(v.x & 0xFFFF0000u)),
-                     pack_bf16x2(a * x[2] - b * bf16_to_f32(v.y & 0xFFFFu), a * x[3] - b * __uint_as_float(v.y & 0xFFFF0000u))};
-    }
-};
-
 __global__ __launch_bounds__(256, 1) void loss_dx_kernel(LossDxArgs g) {
     // one LDS object per stage: a fragment read of one stage provably never aliases the
     // direct-to-LDS loads in flight into the other

@@ -14,8 +14,6 @@
 //
 // p is rounded to bf16 because it is an operand of the next product; the sum takes the unrounded values.
 
-#include <type_traits>
-
 #include "common.h"
 #include "dqtile.h"
 #include "loss.h"
@@ -24,13 +22,6 @@
 namespace nf4k {
 
 namespace {
-
-// A row's reference is kept while no logit exceeds it by more than about this (log2 units): p stays far from bf16's
-// and float32's limits (2^127).  The first is 0, which lies within this of the largest logit of nearly every tile there
-// is (33 in natural units); the sums tell where it does not, and such a tile is done once more against its own maxima
-// and rescaled afterwards.  (The maximum first and then the sums, as two passes over the accumulators for every tile,
-// was slower.)
-constexpr int kSlack = 48;
 
 struct LossStages {
     uint8_t *S0, *S1;
@@ -45,19 +36,6 @@ struct LossPlace {
     int64_t n0;               // first vocabulary row
     int entry, p0;            // row of the tables; first step of P's blocks
 };
-
-// the sum or maximum over groups of N lanes (8 or 16), in all of them
-template <int N, class Op>
-__device__ __forceinline__ float over_lanes(float x, Op op) {
-    auto dpp = [](float v, auto ctrl) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
-    };
-    x = op(x, dpp(x, std::integral_constant<int, 0xB1>{}));       // lane ^ 1
-    x = op(x, dpp(x, std::integral_constant<int, 0x4E>{}));       // lane ^ 2
-    x = op(x, dpp(x, std::integral_constant<int, 0x141>{}));      // mirrored within 8
-    if (N == 16) x = op(x, dpp(x, std::integral_constant<int, 0x140>{}));      // mirrored within 16
-    return x;
-}
 
 // A workgroup's tiles of 64 IA vocabulary rows, one after the other: place(i), i < n.  The next tile's first step is
 // loaded (into S1) before this one's epilogue, which works in S0.
@@ -265,10 +243,10 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
     };
     groups();
     float sum = st.sums[0][tid] + st.sums[1][tid];
-    // Is every token's sum where it should be?  Above 2^kSlack a logit lies too far above the reference; below
-    // 2^-kSlack all lie too far below it, or there are none but the label (a reference of an earlier piece may lie
+    // Is every token's sum where it should be?  Above 2^kLossSlack a logit lies too far above the reference; below
+    // 2^-kLossSlack all lie too far below it, or there are none but the label (a reference of an earlier piece may lie
     // above all of this tile); NaN fails too.
-    const bool ok = m0 + tid >= count || (sum <= __builtin_ldexpf(1.0f, kSlack) && (g.ref || sum >= __builtin_ldexpf(1.0f, -kSlack)));
+    const bool ok = m0 + tid >= count || (sum <= __builtin_ldexpf(1.0f, kLossSlack) && (g.ref || sum >= __builtin_ldexpf(1.0f, -kLossSlack)));
     if (!__syncthreads_and(ok)) {
         // the tile once more, those tokens against their own largest logit
         auto top = [&](auto jc) {

@@ -5,6 +5,8 @@
 // stands before the last sub-step, and a step's loads go out in two halves, spread over the MFMAs.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 #include "dqtile.h"
 #include "loss.h"
@@ -12,6 +14,35 @@
 namespace nf4k {
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+// A row's reference is kept while no logit exceeds it by more than about this (log2 units): p stays far from bf16's
+// and float32's limits (2^127).  The first is 0, which lies within this of the largest logit of nearly every tile there
+// is (33 in natural units); the sums tell where it does not, and such a tile is done once more against its own maxima
+// and rescaled afterwards.  (The maximum first and then the sums, as two passes over the accumulators for every tile,
+// was slower.)
+constexpr int kLossSlack = 48;
+
+// the sum or maximum over groups of N lanes (4, 8 or 16), in all of them
+template <int N, class Op>
+__device__ __forceinline__ float over_lanes(float x, Op op) {
+    auto dpp = [](float v, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, true));
+    };
+    x = op(x, dpp(x, std::integral_constant<int, 0xB1>{}));       // lane ^ 1
+    x = op(x, dpp(x, std::integral_constant<int, 0x4E>{}));       // lane ^ 2
+    if (N >= 8) x = op(x, dpp(x, std::integral_constant<int, 0x141>{}));      // mirrored within 8
+    if (N == 16) x = op(x, dpp(x, std::integral_constant<int, 0x140>{}));      // mirrored within 16
+    return x;
+}
+
+// A token's last step: dX = a (sum P W) - b W[label], rounded once.
+struct LossFinal {
+    float a, b;
+    __device__ __forceinline__ uint2 value(const f32x4 &x, const uint2 &v) const {
+        return uint2{pack_bf16x2(a * x[0] - b * bf16_to_f32(v.x & 0xFFFFu), a * x[1] - b * __uint_as_float(v.x & 0xFFFF0000u)),
+                     pack_bf16x2(a * x[2] - b * bf16_to_f32(v.y & 0xFFFFu), a * x[3] - b * __uint_as_float(v.y & 0xFFFF0000u))};
+    }
+};
 
 // IA: 32-row tiles of a wave along the first operand, 4 or 2 (a tile of 256 or 128 rows there)
 template <int IA>

@@ -93,15 +93,16 @@ def check(X, W, labels, dloss=None, rows=None, fwd=True, grad=True):
 @pytest.mark.parametrize("M,V,K", [
     (1, 1, 64), (1, 2, 64), (3, 255, 64), (2, 256, 128), (5, 257, 64), (1, 1000, 512), (31, 300, 192), (64, 511, 64),
     (65, 513, 320), (255, 700, 64), (256, 256, 256), (257, 1025, 128), (300, 2049, 576), (513, 999, 1024),
-    (4, 4099, 192), (16, 300, 64), (17, 4099, 192), (33, 16, 2048), (48, 129, 4160), (49, 30001, 64), (64, 15, 448)])
+    (4, 4099, 192), (16, 300, 64), (17, 4099, 192), (33, 16, 2048), (48, 129, 4160), (49, 30001, 64), (64, 15, 448), (128, 65, 192),
+    (127, 64, 64), (128, 40000, 64), (100, 3000, 1984), (128, 7, 4096), (66, 641, 16384), (20, 129, 8256)])
 def test_sizes(M, V, K):
     X, W, labels = make(M, V, K, seed=M + V, none=0.2 if M > 4 else 0.0, lift=12.0)
     check(X, W, labels)
 
 
+@pytest.mark.parametrize("M", [60, 120, 600])
 @pytest.mark.parametrize("none", [0.0, 0.5, 0.97, 1.0])
-def test_tokens_without_a_label(none):
-    M = 600
+def test_tokens_without_a_label(none, M):
     X, W, labels = make(M, 777, 128, seed=3, none=none, lift=8.0)
     g = torch.rand(M, device=DEV) - 0.3
     check(X, W, labels, g)
@@ -138,13 +139,14 @@ def test_any_negative_label_counts_as_none():
         assert same(p, q)
 
 
-def test_label_past_the_vocabulary_is_nan_alone():
-    X, W, labels = make(50, 300, 64, seed=6)
-    ref = nf4.qlora_loss_grad(W, X, labels, torch.ones(50, device=DEV))
+@pytest.mark.parametrize("M", [50, 100, 300])
+def test_label_past_the_vocabulary_is_nan_alone(M):
+    X, W, labels = make(M, 300, 64, seed=6)
+    ref = nf4.qlora_loss_grad(W, X, labels, torch.ones(M, device=DEV))
     bad = labels.clone()
     bad[7], bad[41] = 300, torch.iinfo(torch.int64).max
-    loss, mean, dX = nf4.qlora_loss_grad(W, X, bad, torch.ones(50, device=DEV))
-    keep = torch.ones(50, dtype=torch.bool, device=DEV)
+    loss, mean, dX = nf4.qlora_loss_grad(W, X, bad, torch.ones(M, device=DEV))
+    keep = torch.ones(M, dtype=torch.bool, device=DEV)
     keep[[7, 41]] = False
     assert torch.isnan(loss[~keep]).all() and torch.isnan(dX[~keep]).all() and torch.isnan(mean).all()
     assert same(loss[keep], ref[0][keep]) and same(dX[keep], ref[2][keep])
@@ -152,16 +154,17 @@ def test_label_past_the_vocabulary_is_nan_alone():
     assert torch.isnan(loss[~keep]).all() and torch.isnan(mean).all() and torch.isfinite(loss[keep]).all()
 
 
+@pytest.mark.parametrize("M", [40, 128, 300])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
-def test_tokens_that_are_not_finite_stay_alone(value):
-    X, W, labels = make(300, 700, 128, seed=7)
-    g = torch.ones(300, device=DEV)
+def test_tokens_that_are_not_finite_stay_alone(value, M):
+    X, W, labels = make(M, 700, 128, seed=7)
+    g = torch.ones(M, device=DEV)
     ref = nf4.qlora_loss_grad(W, X, labels, g)
-    X2 = X.clone()
-    X2[129, 5] = value
+    X2, bad = X.clone(), M // 2 + 3
+    X2[bad, 5] = value
     loss, mean, dX = nf4.qlora_loss_grad(W, X2, labels, g)
-    keep = torch.arange(300, device=DEV) != 129
-    assert torch.isnan(loss[129]) and torch.isnan(dX[129]).all() and torch.isnan(mean).all()
+    keep = torch.arange(M, device=DEV) != bad
+    assert torch.isnan(loss[bad]) and torch.isnan(dX[bad]).all() and torch.isnan(mean).all()
     assert same(loss[keep], ref[0][keep]) and same(dX[keep], ref[2][keep])
 
 
@@ -185,8 +188,8 @@ def test_sure_labels_keep_relative_accuracy():
 
 def test_references_move_far():
     """Each tile's largest logit exceeds the one before by more than a reference allows, up and down."""
-    K, V, M = 64, 256 * 12, 300
-    for order in (1, -1):
+    K, V = 64, 256 * 12
+    for M, order in ((300, 1), (300, -1), (60, 1), (100, -1)):
         W = synth.normal_f32(41, (V, K), 0.05)
         W[:, 0] = np.repeat(np.arange(12)[::order] * 10.0, 256)
         X = synth.normal_f32(42, (M, K), 1.0)
@@ -209,8 +212,9 @@ def test_pieces_of_the_vocabulary(order):
     check(X, W, labels, rows=np.concatenate([rows, [0, M - 1]]))
 
 
-def test_outputs_and_workspace_given():
-    M, V, K = 130, 600, 128
+@pytest.mark.parametrize("M", [60, 110, 130])
+def test_outputs_and_workspace_given(M):
+    V, K = 600, 128
     X, W, labels = make(M, V, K, seed=12, none=0.3)
     ref = nf4.qlora_loss_grad(W, X, labels)
     guard = torch.full((M + 2, K), 7.0, dtype=torch.bfloat16, device=DEV)
@@ -268,8 +272,9 @@ def test_gradient_against_differences_of_the_forward():
     assert float(tol) < 0.1 * float(along)
 
 
-def test_other_stream_and_repeats():
-    X, W, labels = make(400, 5000, 512, seed=15, none=0.3, lift=9.0)
+@pytest.mark.parametrize("M", [33, 90, 400])
+def test_other_stream_and_repeats(M):
+    X, W, labels = make(M, 5000, 512, seed=15, none=0.3, lift=9.0)
     ref = nf4.qlora_loss_grad(W, X, labels)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
@@ -281,8 +286,9 @@ def test_other_stream_and_repeats():
             assert same(a, b)
 
 
-def test_graph_replays_match_eager():
-    M, V, K = 300, 2000, 256
+@pytest.mark.parametrize("M", [50, 128, 300])
+def test_graph_replays_match_eager(M):
+    V, K = 2000, 256
     X, W, labels = make(M, V, K, seed=16, none=0.3)
     loss, mean = torch.empty(M, device=DEV), torch.empty(1, device=DEV)
     dX = torch.empty((M, K), dtype=torch.bfloat16, device=DEV)
