@@ -1441,21 +1441,21 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.off_a = take((size_t)p.Mp * 4);
     p.off_b = take((size_t)p.Mp * 4);
     for (size_t &c : p.off_c) c = take((size_t)p.Mp * 4);
-    p.narrow = grad && M <= nf4k::kLossNarrowMaxM && p.piece == p.tiles;
+    p.gemv = !grad && M <= nf4k::kLossGemvMaxM;
+    p.narrow = !p.gemv && M <= nf4k::kLossNarrowMaxM && p.piece == p.tiles;
+    p.off_tsum = p.off_P = p.off_part = p.off_sum32 = 0;
+    if (p.gemv) {
+        p.off_tref = take((size_t)M * ((V + 15) / 16) * 8);
+        p.total = off;
+        return p;
+    }
     if (p.narrow) {
         const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
         p.off_tref = take((size_t)n.steps * p.Mp * 4);
         p.off_tsum = take((size_t)n.steps * p.Mp * 4);
-        p.off_P = take((size_t)n.steps * nf4k::LBLOCK * 2);
-        p.off_part = take(n.parts * 4);
-        p.off_sum32 = p.total = off;
-        p.gemv = false;
-        return p;
-    }
-    p.gemv = !grad && M <= nf4k::kLossGemvMaxM;
-    if (p.gemv) {
-        p.off_tref = take((size_t)M * ((V + 15) / 16) * 8);
-        p.off_tsum = p.off_P = p.off_part = p.off_sum32 = p.total = off;
+        p.off_P = take(grad ? (size_t)n.steps * nf4k::LBLOCK * 2 : 0);
+        p.off_part = take(grad ? n.parts * 4 : 0);
+        p.total = off;
         return p;
     }
     p.off_tref = take((size_t)p.piece * p.Mp * 8);
@@ -1513,9 +1513,9 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
         const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.Mp, n.steps, n.per, tref, tsum, P, part, loss, mean, dX};
         NF4_CHECK_HIP(nf4k::launch_loss_narrow_logits(a, s), "loss logits of few tokens");
-        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, n.steps, nullptr, c[0], P, true, true,
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, n.steps, nullptr, c[0], P, true, grad,
                                                             dloss, loss, mean}, true, s), "loss sums");
-        NF4_CHECK_HIP(nf4k::launch_loss_narrow_dx(a, s), "loss dX of few tokens");
+        NF4_CHECK_HIP(grad ? nf4k::launch_loss_narrow_dx(a, s) : nf4k::launch_loss_narrow_mean(a, s), "loss of few tokens");
         return NF4_OK;
     }
     NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");

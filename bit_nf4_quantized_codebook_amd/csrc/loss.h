@@ -168,7 +168,7 @@ __device__ __forceinline__ void loss_write_mean(const double *sums, int n, int c
     if (threadIdx.x == 0) mean[0] = count ? (float)(total[0] / count) : 0.0f;
 }
 
-// with the gradient, for up to kLossNarrowMaxM tokens and one piece
+// up to kLossNarrowMaxM tokens, in one piece
 constexpr int64_t kLossNarrowMaxM = 128;
 struct LossNarrowPlan {
     int32_t TT, steps, per, splits;
@@ -182,16 +182,17 @@ struct LossNarrow {
     LossRows r;
     int32_t Mp, steps, per;   // steps of 64 vocabulary rows: all, and of dX's workgroup
     float *tref, *tsum;       // [Mp][steps]
-    uint16_t *P;              // [steps] blocks
+    uint16_t *P;              // [steps] blocks; NULL: the forward
     float *part;
     float *loss, *mean;
     uint16_t *dX;
 };
 hipError_t launch_loss_narrow_logits(const LossNarrow &g, hipStream_t stream);
-hipError_t launch_loss_narrow_dx(const LossNarrow &g, hipStream_t stream);
+hipError_t launch_loss_narrow_mean(const LossNarrow &g, hipStream_t stream);      // forward
+hipError_t launch_loss_narrow_dx(const LossNarrow &g, hipStream_t stream);        // with dX and the mean
 
 // the forward for up to kLossGemvMaxM tokens
-constexpr int64_t kLossGemvMaxM = 64;
+constexpr int64_t kLossGemvMaxM = 16;
 struct LossGemv {
     const uint16_t *W, *X;
     int64_t V, K, M;

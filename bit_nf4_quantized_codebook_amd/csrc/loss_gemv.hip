@@ -1,8 +1,8 @@
-// Loss over the vocabulary for up to 64 tokens, forward (gfx950): W's 2 V K bytes stream once from HBM, and
+// Loss over the vocabulary for up to 16 tokens, forward (gfx950): W's 2 V K bytes stream once from HBM, and
 // everything else stays out of the way of those loads.  Two launches:
 //   1. logits and statistics.  A workgroup of 4 waves owns 16 RG vocabulary rows; the waves take turns along K
 //      (256-byte chunks, wave w takes chunks w, w + 4, ..), a chunk loaded while the one before it is multiplied
-//      (v_mfma_f32_16x16x32_bf16: 16 vocabulary rows by 16 tokens, G groups of them).  A row's bytes go from the load
+//      (v_mfma_f32_16x16x32_bf16: 16 vocabulary rows by 16 tokens).  A row's bytes go from the load
 //      straight into the MFMA.  The waves' sums meet in LDS in a fixed order; then each token's maximum and its sum of
 //      2^(l - c) over the 16 rows;
 //   2. a workgroup per token joins its tiles, and the one that ends last sums the losses.
@@ -21,10 +21,11 @@ constexpr int CS = CHUNK / 64;     // MFMA steps of a chunk
 constexpr int NW = 4;
 
 // DIRECT (up to 4 tokens): the tokens are loaded in the operands' own layout, too few lines to matter.
-template <int RG, int G, bool DIRECT>
+template <int RG, bool DIRECT>
 __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
-    // a wave's tokens of a chunk, and after the last its sums [tile][4][lane]
-    constexpr int XW = DIRECT ? RG * 1024 : G * (RG > 4 ? RG * 1024 : 4096);
+    // a wave's tokens of a chunk, and after the last its sums [16 rows][4][lane]
+    constexpr int XW = DIRECT ? RG * 1024 : 4096;
+    static_assert(RG <= 4, "a wave's sums fit where its tokens were");
     __shared__ __align__(16) uint8_t xtile[NW * XW];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -52,31 +53,27 @@ __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
     };
     // Tokens: 16 lanes load a row's 256 bytes (four rows per load), and the wave turns them into operands through
     // its own LDS tile, 16-byte pieces XOR-ed with the row so that neither side has bank conflicts.
-    u32x4 xr[G][4];
+    u32x4 xr[4];
     auto load_x = [&](int c) {
         if (DIRECT) {
 #pragma unroll
             for (int s = 0; s < CS; ++s) {
                 const uint32_t k = (uint32_t)c * CHUNK + s * 64;
-                xr[0][s] = bload16(rX, k < KB ? lane_off + k : 0xFFFFFFF0u);
+                xr[s] = bload16(rX, k < KB ? lane_off + k : 0xFFFFFFF0u);
             }
             return;
         }
 #pragma unroll
-        for (int q = 0; q < G; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 4 * i + lg;
-                const uint32_t k = (uint32_t)c * CHUNK + ((ln ^ row) * 16);
-                xr[q][i] = bload16(rX, k < KB ? (uint32_t)(16 * q + row) * KB + k : 0xFFFFFFF0u);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * i + lg;
+            const uint32_t k = (uint32_t)c * CHUNK + ((ln ^ row) * 16);
+            xr[i] = bload16(rX, k < KB ? (uint32_t)row * KB + k : 0xFFFFFFF0u);
+        }
     };
     uint8_t *xt = xtile + wave * XW;
-    f32x4 acc[RG][G];
+    f32x4 acc[RG];
 #pragma unroll
-    for (int a = 0; a < RG; ++a)
-#pragma unroll
-        for (int b = 0; b < G; ++b) acc[a][b] = f32x4{0, 0, 0, 0};
+    for (int a = 0; a < RG; ++a) acc[a] = f32x4{0, 0, 0, 0};
     // The tile is the wave's own: its LDS operations complete in order, so no barrier is needed, only that the
     // compiler keeps the order of one lane's writes and another's reads.
     auto wave_order = [&]() {
@@ -87,29 +84,22 @@ __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
     auto put_x = [&]() {
         if (DIRECT) {
 #pragma unroll
-            for (int s = 0; s < CS; ++s) xd[s] = xr[0][s];
+            for (int s = 0; s < CS; ++s) xd[s] = xr[s];
             return;
         }
         wave_order();
 #pragma unroll
-        for (int q = 0; q < G; ++q)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(xt + q * 4096 + i * 1024 + lane * 16) = xr[q][i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<u32x4 *>(xt + i * 1024 + lane * 16) = xr[i];
         wave_order();
     };
     auto mul = [&](const WStage &st) {
 #pragma unroll
         for (int s = 0; s < CS; ++s) {
-            bf16x8 x[G];
-#pragma unroll
-            for (int b = 0; b < G; ++b)
-                x[b] = DIRECT ? __builtin_bit_cast(bf16x8, xd[s])
-                              : *reinterpret_cast<const bf16x8 *>(xt + b * 4096 + ln * 256 + (((4 * s + lg) ^ ln) * 16));
+            const bf16x8 x = DIRECT ? __builtin_bit_cast(bf16x8, xd[s])
+                                    : *reinterpret_cast<const bf16x8 *>(xt + ln * 256 + (((4 * s + lg) ^ ln) * 16));
 #pragma unroll
             for (int a = 0; a < RG; ++a)
-#pragma unroll
-                for (int b = 0; b < G; ++b)
-                    acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.w[s][a]), x[b], acc[a][b], 0, 0, 0);
+                acc[a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, st.w[s][a]), x, acc[a], 0, 0, 0);
         }
     };
 
@@ -129,14 +119,12 @@ __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
     }
     wave_order();
 #pragma unroll
-    for (int a = 0; a < RG; ++a)
-#pragma unroll
-        for (int b = 0; b < G; ++b) *reinterpret_cast<f32x4 *>(xt + (b * RG + a) * 1024 + lane * 16) = acc[a][b];
+    for (int a = 0; a < RG; ++a) *reinterpret_cast<f32x4 *>(xt + a * 1024 + lane * 16) = acc[a];
     __syncthreads();
 
-    // wave b finishes token group b: lane (ln, lg) holds token 16 b + ln, vocabulary rows 16 a + 4 lg + v
-    const int t = 16 * wave + ln;
-    if (wave >= G || 16 * wave >= g.M) return;
+    // wave 0: lane (ln, lg) holds token ln, vocabulary rows 16 a + 4 lg + v
+    if (wave) return;
+    const int t = ln;
     f32x4 z[RG];
     const int64_t lab = t < g.M ? g.labels[t] : -1;
     float top = -__builtin_inff(), s = 0.0f;
@@ -144,7 +132,7 @@ __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
     for (int a = 0; a < RG; ++a) {
         z[a] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < NW; ++w) z[a] += *reinterpret_cast<const f32x4 *>(xtile + w * XW + (wave * RG + a) * 1024 + lane * 16);
+        for (int w = 0; w < NW; ++w) z[a] += *reinterpret_cast<const f32x4 *>(xtile + w * XW + a * 1024 + lane * 16);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int64_t n = n0 + 16 * a + 4 * lg + v;
@@ -224,7 +212,7 @@ __global__ __launch_bounds__(256) void loss_gemv_join_kernel(LossGemv g, int nti
         last = __hip_atomic_fetch_add(g.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 == (int)gridDim.x;
     }
     if (!__builtin_amdgcn_readfirstlane(last)) return;
-    // the workgroup that ends last: one loss a lane (M <= 64), summed in a fixed order
+    // the workgroup that ends last: one loss a lane, summed in a fixed order
     __shared__ double each[64];
     const bool has = tid < g.M && g.labels[tid < g.M ? tid : 0] >= 0;
     const int count = __popcll(__builtin_amdgcn_ballot_w64(has));
@@ -237,10 +225,10 @@ __global__ __launch_bounds__(256) void loss_gemv_join_kernel(LossGemv g, int nti
     g.mean[0] = count ? (float)(total / count) : 0.0f;
 }
 
-template <int RG, int G, bool DIRECT>
+template <int RG, bool DIRECT>
 hipError_t run(const LossGemv &g, hipStream_t stream) {
     const uint32_t tiles = (uint32_t)((g.V + 16 * RG - 1) / (16 * RG));
-    hipLaunchKernelGGL((loss_gemv_kernel<RG, G, DIRECT>), dim3(tiles), dim3(NW * 64), 0, stream, g);
+    hipLaunchKernelGGL((loss_gemv_kernel<RG, DIRECT>), dim3(tiles), dim3(NW * 64), 0, stream, g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(loss_gemv_join_kernel, dim3((uint32_t)g.M), dim3(256), 0, stream, g, (int)tiles);
@@ -250,16 +238,13 @@ hipError_t run(const LossGemv &g, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_loss_gemv(const LossGemv &g, hipStream_t stream) {
-    // Weight rows of a workgroup: 16 while the weight's stream is all there is (many small workgroups hide its
-    // latency: one token at 50001 x 4096 takes 77 us with 16 rows, 90 with 48), more where every workgroup reads
-    // many tokens (37 tokens at 50001 x 4096 131 us with 16 rows, 109 with 48; 64 tokens at 32000 x 8192 197, 145
-    // and with 64 rows 133)
-    if (g.M <= 4) return run<1, 1, true>(g, stream);
-    if (g.M <= 8) return run<1, 1, false>(g, stream);
-    if (g.M <= 16) return run<3, 1, false>(g, stream);
-    if (g.M <= 32) return run<3, 2, false>(g, stream);
-    if (g.M <= 48) return run<3, 3, false>(g, stream);
-    return run<4, 4, false>(g, stream);
+    // Weight rows of a workgroup: 16 while the weight's stream is all there is (many small workgroups hide its latency:
+    // one token at 50001 x 4096 takes 77 us with 16 rows, 90 with 48), more where the tokens' LDS traffic counts (16
+    // tokens at 131072 x 4096 230 us with 16 rows, 204 with 48).  Beyond 16 tokens the narrow tiles are faster (33 at
+    // 32000 x 4096 61 us, 70 here).
+    if (g.M <= 4) return run<1, true>(g, stream);
+    if (g.M <= 8) return run<1, false>(g, stream);
+    return run<3, false>(g, stream);
 }
 
 }  // namespace nf4k

@@ -1,10 +1,10 @@
-// The loss with its gradient for up to 128 tokens (gfx950): both products stream the weight, and tiles of 256 tokens with
+// The loss for up to 128 tokens, forward and with its gradient (gfx950): both products stream the weight, and tiles of 256 tokens with
 // two stages in flight leave the memory idle.  Tiles here are narrow and their stages many:
 //   1. logits: 64 vocabulary rows x TT tokens (64 or 128) a workgroup, two workgroups a CU.  Each makes the list of live
 //      rows for itself, from at most 128 labels;
 //   2. the join of the tiles (loss.hip);
 //   3. dX's product: 128 columns x TT tokens over a part of the vocabulary, float32 partials;
-//   4. their sum, dX, and the mean.
+//   4. their sum, dX, and the mean (forward: the mean alone).
 // The layouts of p, of the LDS stages and of the fragments are those of loss_logits.hip and loss_dx.hip.
 
 #include "common.h"
@@ -25,7 +25,7 @@ __device__ __forceinline__ void step_barrier() {
     asm volatile("s_barrier" ::: "memory");
 }
 
-template <int TT>
+template <int TT, bool GRAD>
 __device__ __forceinline__ void narrow_logits(const LossNarrow &g) {
     constexpr int NST = TT == 64 ? 4 : 3;            // stages; NST - 1 of them in flight
     constexpr int VB = 64 * LSTEP * 2;               // bytes of W in a stage, before the tokens'
@@ -180,7 +180,7 @@ __device__ __forceinline__ void narrow_logits(const LossNarrow &g) {
             tops[wm][32 * JN * wn + 16 * b + tt] = x;
         }
     };
-    const __amdgpu_buffer_rsrc_t rP = make_rsrc(g.P + (int64_t)blockIdx.x * LBLOCK, LBLOCK * 2);
+    const __amdgpu_buffer_rsrc_t rP = make_rsrc(GRAD ? g.P + (int64_t)blockIdx.x * LBLOCK : nullptr, GRAD ? LBLOCK * 2 : 0);
     auto groups = [&]() {
 #pragma unroll
         for (int b = 0; b < B; ++b) {
@@ -195,7 +195,7 @@ __device__ __forceinline__ void narrow_logits(const LossNarrow &g) {
             }
             s = over_lanes<4>(s, [](float a, float b) { return a + b; });
             sums[wm][tl] = s;                        // the same from all of a token's lanes
-            __builtin_amdgcn_raw_buffer_store_b128(
+            if (GRAD) __builtin_amdgcn_raw_buffer_store_b128(
                 u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])}, rP,
                 (uint32_t)(tl * 128 + (((4 * wm + q) ^ ((tl >> 1) & 7)) * 16)), 0, 0);
         }
@@ -320,9 +320,9 @@ __device__ __forceinline__ void narrow_dx(const LossNarrow &g) {
     }
 }
 
-template <int TT>
+template <int TT, bool GRAD>
 __global__ __launch_bounds__(256, 2) void loss_narrow_logits_kernel(LossNarrow g) {
-    narrow_logits<TT>(g);
+    narrow_logits<TT, GRAD>(g);
 }
 template <int TT>
 __global__ __launch_bounds__(256, TT == 64 ? 2 : 1) void loss_narrow_dx_kernel(LossNarrow g) {
@@ -370,6 +370,12 @@ __global__ __launch_bounds__(256) void loss_narrow_fold_kernel(LossNarrow g, int
     *reinterpret_cast<uint2 *>(g.dX + (int64_t)t * g.K + k) = LossFinal{a, b}.value(x, w);
 }
 
+// forward: the mean, and the losses of tokens without a label
+__global__ __launch_bounds__(256) void loss_narrow_mean_kernel(LossNarrow g) {
+    if ((int)threadIdx.x < g.M && g.labels[threadIdx.x] < 0) g.loss[threadIdx.x] = 0.0f;
+    loss_write_mean(g.r.sums, (int)((g.M + kLossJoinRowsNarrow - 1) / kLossJoinRowsNarrow), g.r.count[0], g.mean);
+}
+
 }  // namespace
 
 LossNarrowPlan loss_narrow_plan(int64_t M, int64_t V, int64_t K) {
@@ -387,8 +393,16 @@ LossNarrowPlan loss_narrow_plan(int64_t M, int64_t V, int64_t K) {
 }
 
 hipError_t launch_loss_narrow_logits(const LossNarrow &g, hipStream_t stream) {
-    if (g.M <= 64) hipLaunchKernelGGL(loss_narrow_logits_kernel<64>, dim3((uint32_t)g.steps), dim3(256), 0, stream, g);
-    else hipLaunchKernelGGL(loss_narrow_logits_kernel<128>, dim3((uint32_t)g.steps), dim3(256), 0, stream, g);
+    const dim3 grid((uint32_t)g.steps), block(256);
+    if (g.P && g.M <= 64) hipLaunchKernelGGL((loss_narrow_logits_kernel<64, true>), grid, block, 0, stream, g);
+    else if (g.P) hipLaunchKernelGGL((loss_narrow_logits_kernel<128, true>), grid, block, 0, stream, g);
+    else if (g.M <= 64) hipLaunchKernelGGL((loss_narrow_logits_kernel<64, false>), grid, block, 0, stream, g);
+    else hipLaunchKernelGGL((loss_narrow_logits_kernel<128, false>), grid, block, 0, stream, g);
+    return hipGetLastError();
+}
+
+hipError_t launch_loss_narrow_mean(const LossNarrow &g, hipStream_t stream) {
+    hipLaunchKernelGGL(loss_narrow_mean_kernel, dim3(1), dim3(256), 0, stream, g);
     return hipGetLastError();
 }
 
