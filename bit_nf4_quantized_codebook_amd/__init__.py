@@ -875,7 +875,7 @@ def qlora_loss_fwd(W, X, labels, loss=None, mean=None, workspace=None):
 
 def qlora_loss_grad(W, X, labels, dloss=None, loss=None, mean=None, dX=None, workspace=None):
     """qlora_loss_fwd with the gradient for X (W is frozen), in one pass over the vocabulary: dloss float32 [M],
-    the gradient of each token's loss, or None: of the mean.  Returns (loss, mean, dX bf16 [M, K])."""
+    the gradient of each token's loss, or None: of the mean; dX overlaps neither X nor W.  Returns (loss, mean, dX bf16 [M, K])."""
     torch = _torch()
     M, V, K = _loss_args(W, X, labels)
     f32, dev = torch.float32, X.device
@@ -892,8 +892,8 @@ def qlora_loss_grad(W, X, labels, dloss=None, loss=None, mean=None, dX=None, wor
 
 class QLoRAGrads:
     """A list of gradient tensors (bf16 or float32, contiguous, on one device) for qlora_clip_grads, with where the
-    scaled ones go: the tensors themselves, or outs, of the same shapes and types, in memory that overlaps no gradient.
-    Checked and laid out once (a small table on the device); it keeps the tensors, whose contents may change between
+    scaled ones go: the tensors themselves, or outs, of the same shapes and types, in memory that overlaps no gradient
+    and no other of outs (so a gradient scaled in place is in the list once).  Checked and laid out once (a small table on the device); it keeps the tensors, whose contents may change between
     calls."""
 
     def __init__(self, grads, outs=None):

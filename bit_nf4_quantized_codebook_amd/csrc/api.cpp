@@ -3,6 +3,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -1451,8 +1452,8 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     }
     if (p.narrow) {
         const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
-        p.off_tref = take((size_t)n.steps * p.Mp * 4);
-        p.off_tsum = take((size_t)n.steps * p.Mp * 4);
+        p.off_tref = take((size_t)n.steps * M * 4);
+        p.off_tsum = take((size_t)n.steps * M * 4);
         p.off_P = take(grad ? (size_t)n.steps * nf4k::LBLOCK * 2 : 0);
         p.off_part = take(grad ? n.parts * 4 : 0);
         p.total = off;
@@ -1467,6 +1468,11 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.off_sum32 = take(grad && p.piece < p.tiles ? (size_t)p.Mp * K * 4 : 0);
     p.total = off;
     return p;
+}
+
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + (uint64_t)nb && y < x + (uint64_t)na;
 }
 
 constexpr int64_t kLossMaxM = (int64_t)1 << 20, kLossMaxV = (int64_t)1 << 24, kLossMaxK = 16384;
@@ -1495,6 +1501,8 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
     const LossPlan p = make_loss_plan(M, V, K, grad);
     if (!workspace || workspace_bytes < p.total) return fail(NF4_ERR_WORKSPACE, "loss workspace too small");
     if (!aligned16(workspace)) return fail(NF4_ERR_ALIGN, "workspace must be 16-byte aligned");
+    if (grad && (overlap(dX, M * K * 2, X, M * K * 2) || overlap(dX, M * K * 2, W, V * K * 2)))
+        return fail(NF4_ERR_ARG, "dX must not overlap X or W");
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const nf4k::LossRows r{ws_at<int32_t>(workspace, p.off_count), ws_at<double>(workspace, p.off_sums), ws_at<int32_t>(workspace, p.off_row),
                            ws_at<int32_t>(workspace, p.off_label), ws_at<float>(workspace, p.off_zl),
@@ -1570,7 +1578,9 @@ int qlora_grad_table(const qlora_grad *grads, int32_t n, void *table, size_t tab
     if ((n && !grads) || !table || !chunks) return fail(NF4_ERR_NULL, "grads, table and chunks must be non-NULL");
     if ((uintptr_t)table & 7u) return fail(NF4_ERR_ALIGN, "table must be 8-byte aligned");
     if (table_bytes < qlora_grad_table_size(n)) return fail(NF4_ERR_WORKSPACE, "gradient table too small");
+    nf4k::ClipEntry *const e = static_cast<nf4k::ClipEntry *>(table);
     int64_t total = 0, at = 0;
+    int32_t m = 0;
     for (int32_t i = 0; i < n; ++i) {
         const qlora_grad &g = grads[i];
         const bool f32 = g.type == NF4_ROWS_F32;
@@ -1581,7 +1591,26 @@ int qlora_grad_table(const qlora_grad *grads, int32_t n, void *table, size_t tab
         if (g.numel && (!g.grad || !g.out)) return fail(NF4_ERR_NULL, "a gradient and its output must be non-NULL");
         if (((uintptr_t)g.grad | (uintptr_t)g.out) & (f32 ? 3u : 1u))
             return fail(NF4_ERR_ALIGN, "a gradient and its output must be aligned to their elements");
-        static_cast<nf4k::ClipEntry *>(table)[i] = nf4k::ClipEntry{g.grad, g.out, g.numel, 2 * at + (f32 ? 1 : 0)};
+        if (g.numel) e[m++] = nf4k::ClipEntry{g.grad, g.out, g.numel * (f32 ? 4 : 2), i};
+    }
+    // What is written once must be written by nothing else, and read only as the gradient it stands for: the outputs in
+    // order (bytes for now, and the entry's index), then the output that each gradient could meet.
+    std::sort(e, e + m, [](const nf4k::ClipEntry &a, const nf4k::ClipEntry &b) { return (uintptr_t)a.out < (uintptr_t)b.out; });
+    for (int32_t i = 0; i + 1 < m; ++i)
+        if (overlap(e[i].out, e[i].numel, e[i + 1].out, e[i + 1].numel))
+            return fail(NF4_ERR_ARG, "the list's outputs overlap (a gradient in it twice?)");
+    for (int32_t i = 0; i < n; ++i) {
+        const qlora_grad &g = grads[i];
+        const int64_t bytes = g.numel * (g.type == NF4_ROWS_F32 ? 4 : 2);
+        // the last output that begins before the gradient's end
+        const nf4k::ClipEntry *o = std::lower_bound(e, e + m, (uintptr_t)g.grad + (uint64_t)bytes,
+                                                    [](const nf4k::ClipEntry &a, uintptr_t end) { return (uintptr_t)a.out < end; });
+        if (!g.numel || o == e || !overlap((--o)->out, o->numel, g.grad, bytes)) continue;
+        if (o->chunk != i || o->out != g.grad) return fail(NF4_ERR_ARG, "an output overlaps a gradient that is not its own");
+    }
+    for (int32_t i = 0; i < n; ++i) {
+        const qlora_grad &g = grads[i];
+        e[i] = nf4k::ClipEntry{g.grad, g.out, g.numel, 2 * at + (g.type == NF4_ROWS_F32 ? 1 : 0)};
         at += (g.numel + nf4k::kClipChunk - 1) / nf4k::kClipChunk;
     }
     *chunks = at;

@@ -181,7 +181,7 @@ struct LossNarrow {
     const int64_t *labels;
     LossRows r;
     int32_t Mp, steps, per;   // steps of 64 vocabulary rows: all, and of dX's workgroup
-    float *tref, *tsum;       // [Mp][steps]
+    float *tref, *tsum;       // [M][steps]
     uint16_t *P;              // [steps] blocks; NULL: the forward
     float *part;
     float *loss, *mean;

@@ -456,7 +456,8 @@ int qlora_loss_fwd(const uint16_t *W, int64_t V, const uint16_t *X, const int64_
  *   dX[m] = dloss[m] sum_v (softmax(z[m])_v - [v == labels[m]]) W[v]
  *   dloss: float32 [M], the gradient of each token's loss, or NULL: of the mean (1 / tokens with a label).
  *   dX: [M, K] bf16, rounded once; zero for a token without a label, whatever its X.  Probabilities enter
- *      their product with W in bf16 (the label's own in float32).  dX must not overlap X or W.
+ *      their product with W in bf16 (the label's own in float32).  dX must not overlap X or W
+ *      (NF4_ERR_ARG).
  *   loss and mean as qlora_loss_fwd's, up to the rounding of float32.
  *   workspace: >= qlora_loss_workspace_size(M, V, K, 1) bytes.
  */
@@ -479,7 +480,9 @@ typedef struct qlora_grad {
 /*
  * The list as a table, made once for gradients that stay where they are.  Host-only and synchronous; the caller
  * copies the table to the device and keeps it as long as the list is used.
- *   grads: HOST array of n tensors, 0 <= n <= 2^20, 2^46 elements at most.
+ *   grads: HOST array of n tensors, 0 <= n <= 2^20, 2^46 elements at most.  An output that overlaps another
+ *      one, or a gradient other than exactly its own, is refused (NF4_ERR_ARG): so is a gradient scaled in
+ *      place that is in the list twice.
  *   table: HOST memory of qlora_grad_table_size(n) bytes, 8-byte aligned.
  *   chunks: HOST, written: the table's size in units of work, for qlora_clip_grads.
  */

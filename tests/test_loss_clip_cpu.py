@@ -96,6 +96,9 @@ def test_loss_refusals():
         assert f(loss=ODD) == EALIGN and f(mean=ODD) == EALIGN and f(ws=MIS) == EALIGN
         assert f(ws=None) == EWS and f(n=n - 1) == EWS
     assert grad(dX=None) == ENULL and grad(dX=MIS) == EALIGN and grad(dloss=ODD) == EALIGN
+    # dX over X, over the end of W, and ending inside X
+    far, at = FAKE.value + (1 << 30), FAKE.value
+    assert grad(W=far) == EARG and grad(X=far, dX=at + V * K * 2 - 16) == EARG and grad(W=far, dX=at - M * K * 2 + 16) == EARG
 
 
 def test_loss_workspace_is_bounded_by_pieces():
@@ -135,8 +138,45 @@ def test_grad_table_refusals():
     assert make((0x100000, 0x100000, (1 << 46) + 1, 0)) == EUNSUP
     assert make(good, (0x100000, 0x100000, 1 << 46, 1)) == EUNSUP
     assert chunks.value == -1
-    assert make((0x100002, 0x100004, 3, 0), (None, None, 0, 1), (0x200004, 0x200004, 1 << 30, 1)) == OK and chunks.value > 1
+    assert make((0x100002, 0x100104, 3, 0), (None, None, 0, 1), (0x200004, 0x200004, 1 << 30, 1)) == OK and chunks.value > 1
     assert make(null=True) == OK and chunks.value == 0
+
+
+def test_grad_table_refuses_outputs_that_overlap():
+    """Plain check of every pair of byte ranges against the table's answer, over lists of few, close tensors."""
+    table, chunks = np.zeros(lib.qlora_grad_table_size(8) // 8, np.int64), ctypes.c_int64()
+
+    def make(entries):
+        a = _grads(*entries)
+        return lib.qlora_grad_table(ctypes.addressof(a), len(entries), table.ctypes.data, table.nbytes, ctypes.addressof(chunks))
+
+    def meet(a, b):
+        return a[0] < b[1] and b[0] < a[1]
+
+    def allowed(entries):
+        full = [e for e in entries if e[2]]
+        size = [e[2] * (4 if e[3] else 2) for e in full]
+        g = [(e[0], e[0] + s) for e, s in zip(full, size)]
+        o = [(e[1], e[1] + s) for e, s in zip(full, size)]
+        pairs = [(i, j) for i in range(len(full)) for j in range(len(full)) if i != j]
+        return (not any(meet(o[i], o[j]) or meet(o[i], g[j]) for i, j in pairs)
+                and all(a == b or not meet(a, b) for a, b in zip(o, g)))
+
+    rng = np.random.default_rng(3)
+    seen = {OK: 0, EARG: 0}
+    for _ in range(4000):
+        entries = []
+        for _ in range(int(rng.integers(1, 9))):
+            g = 0x10000 + 16 * int(rng.integers(60))
+            o = g if rng.integers(2) else 0x10000 + 8 * int(rng.integers(120))
+            entries.append((g, o, int(rng.integers(0, 6)), int(rng.integers(2))))
+        want = OK if allowed(entries) else EARG
+        assert make(entries) == want, entries
+        seen[want] += 1
+    assert min(seen.values()) > 500, seen
+    one = (0x1000, 0x1000, 8, 0)
+    assert make([one, one]) == EARG                                                # scaled twice in place
+    assert make([(0x1000, 0x2000, 8, 0), (0x1000, 0x3000, 8, 0)]) == OK            # counted twice, scaled to two places
 
 
 def test_clip_refusals():
