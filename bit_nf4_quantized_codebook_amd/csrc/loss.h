@@ -16,8 +16,8 @@ namespace nf4k {
 constexpr int LT = 256;                  // tokens, vocabulary rows or columns of dX of a tile
 constexpr int LSTEP = 64;                // reduction of one step of a tile's loop
 constexpr int64_t LBLOCK = LT * LSTEP;   // elements of one step's operand tile (32 KB)
-constexpr int kLossJoinRows = 8;        // rows of a workgroup that joins the tiles
-constexpr int kLossJoinRowsNarrow = 2;  // the same for few tokens
+constexpr int kLossJoinRows = 8;         // rows of a workgroup that joins the tiles
+constexpr int kLossJoinRowsNarrow = 2;   // the same for few tokens
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -82,8 +82,13 @@ struct LossShares {
     }
 };
 
-// Tiles of the logits of a piece, for ntm tiles of rows and ntn of the vocabulary.  Where they fill the chip's last round at most half, that round's tiles are cut in two along the vocabulary: their
-// second halves' statistics stand ntn entries further in the tables.
+// Tiles of the logits of a piece, for ntm tiles of rows and ntn of the vocabulary.  Where they fill the chip's last round
+// at most half, that round's tiles are cut in two along the vocabulary (129 x 32000 x 4096 170 us, 188 uncut): their second
+// halves' statistics stand ntn entries further in the tables.
+//
+// The last tile of rows is a whole one however few of them are live.  Tiles of 128 tokens there took 923 us against 796 at
+// 1639 x 32000 x 4096 (a step of half the MFMAs does not hide its loads with two stages), and 128 x 512 ones 1343 against
+// 1335 at 777 x 50001 x 8192: rows of zeros cost the MFMAs little power, and the wide tiles read W once more.
 struct LossTiles {
     int ntm, ntn, whole;      // whole: tiles that are not cut, the first ones
     __host__ __device__ LossTiles(int m, int n) : ntm(m), ntn(n) {

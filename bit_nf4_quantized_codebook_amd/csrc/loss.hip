@@ -5,6 +5,9 @@
 //   dX = g (sum_{v != y} p_v W_v - (1 - p_y) W_y)
 // Nothing here subtracts two large numbers: a label that is nearly certain keeps a loss and a gradient of full
 // precision.
+//
+// All of it is latency: 4 us for the list of live rows, 7 to 14 for the join (125 tiles of 4096 rows 7.5, 512 of 511 rows
+// 12).
 
 #include "common.h"
 #include "loss.h"
@@ -72,9 +75,7 @@ __global__ __launch_bounds__(PREP) void loss_prep_kernel(const int64_t *__restri
         base += all;
         __syncthreads();
     }
-    if (tid == 0) {
-        r.count[0] = base;
-    }
+    if (tid == 0) r.count[0] = base;
 }
 
 // JR rows a workgroup and 256 / JR threads over the tiles of a row.  NARROW: tiles of one step, never cut, and tables by
@@ -160,7 +161,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
             if (from == top) continue;
             const float f = __builtin_amdgcn_exp2f(from - top);
             for (int b = b0; b < b1; ++b) {
-                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + (((int64_t)(row / LT) * g.ntile + tile) * BLOCKS + b) * LBLOCK + (row % LT) * LSTEP);
+                const int64_t block = ((int64_t)(row / LT) * g.ntile + tile) * BLOCKS + b;
+                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + block * LBLOCK + (row % LT) * LSTEP);
                 for (int i = 0; i < 8; ++i) {
                     u32x4 v = p[i];
 #pragma unroll

@@ -7,6 +7,8 @@
 //      2^(l - c) over the 16 rows;
 //   2. a workgroup per token joins its tiles, and the one that ends last sums the losses.
 // All tokens are computed, also those without a label: the weight's stream costs the same.
+//
+// Bound by HBM: one token at 32000 x 4096 43 us (6.1 TB/s) and 4 for the join.
 
 #include "common.h"
 #include "dqtile.h"

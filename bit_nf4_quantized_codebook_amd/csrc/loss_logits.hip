@@ -13,6 +13,11 @@
 // -(1 - p_label), which a rounded p_label near 1 would lose; the sum leaves it out for the same reason.
 //
 // p is rounded to bf16 because it is an operand of the next product; the sum takes the unrounded values.
+//
+// 256 x 256 tiles: both operands of a step are then 64 KB for 2048 cycles of MFMAs, two stages fill the LDS.  Bound by
+// the MFMAs at the clock that their power allows: a step of 64 takes 1.57 us (1.37 PFLOP/s over the chip), a tile's
+// epilogue 8.  4096 x 32000 x 4096 with p: 860 us of kernel, 1.25 PFLOP/s; 2048 x 32000 x 8192 without: 827 us, 1.30.
+// A library product of the same operands, which writes the logits, reaches 1.34.
 
 #include "common.h"
 #include "dqtile.h"
@@ -112,175 +117,177 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
     first_loads(cur);
 #pragma unroll 1
     for (int index = 0;; ++index) {
-    const int m0 = cur.tm * LT;
-    const int64_t n0 = cur.n0;
-    {
-        const int64_t lab = (int64_t)label - n0;
-        st.labs[tid] = label >= 0 && lab >= 0 && lab < 64 * IA ? (int)lab : -1;
-        st.refs[tid] = ref;
-    }
-    const bool more = index + 1 < n;
-    const LossPlace next = more ? place(index + 1) : cur;
-    fetch(next);
-    f32x16 acc[IA][4];
-#pragma unroll
-    for (int i = 0; i < IA; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-    // between the first step's loads and here lie p's stores, whose end nothing waits for
-    constexpr int STORES = GRAD ? 32 * WV / 128 : 0;
-    loss_loop<IA, 4 + IA, 4 + IA, STORES>(steps, index > 0, st.S1, st.S0, acc, load, read);
-    if (more) first_loads(next);
-
-    // ---- epilogue.  Lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and vocabulary rows
-    // wm*WV + 32 i + 8 (v/4) + 4 hh + v%4.  turn(j) lays token group j out as rows of WV floats, whose 16-byte pieces are
-    // permuted by the token so that neither the writes nor the reads of two neighbouring pieces meet in a bank. ----
-    const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
-    uint8_t *lds = st.S0 + wave * 16384;          // 32 tokens of WV floats
-    constexpr int PIECES = WV / 4;                // a row's pieces of four vocabulary rows
-    auto piece = [](int p, int token) { return ((p ^ (p / (PIECES / 2))) ^ (token & (PIECES - 1))) * 16; };
-    auto order = [&]() {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    };
-    auto turn = [&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        const int c32 = lane_e & 31, he = lane_e >> 5;
-        order();
+        const int m0 = cur.tm * LT;
+        const int64_t n0 = cur.n0;
+        {
+            const int64_t lab = (int64_t)label - n0;
+            st.labs[tid] = label >= 0 && lab >= 0 && lab < 64 * IA ? (int)lab : -1;
+            st.refs[tid] = ref;
+        }
+        const bool more = index + 1 < n;
+        const LossPlace next = more ? place(index + 1) : cur;
+        fetch(next);
+        f32x16 acc[IA][4];
 #pragma unroll
         for (int i = 0; i < IA; ++i)
 #pragma unroll
-            for (int v4 = 0; v4 < 4; ++v4)
-                *reinterpret_cast<f32x4 *>(lds + c32 * (WV * 4) + piece(8 * i + 2 * v4 + he, c32)) =
-                    f32x4{acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
-        order();
-    };
-    // a lane's eight vocabulary rows: chunk q of token TI it + tt of the group
-    constexpr int NQ = WV / 8, TI = 64 / NQ;
-    const int q = lane_e & (NQ - 1), tt = lane_e / NQ;
-    auto eight = [&](int token, float (&x)[8]) {
-        const f32x4 lo = *reinterpret_cast<const f32x4 *>(lds + token * (WV * 4) + piece(2 * q, token));
-        const f32x4 hi = *reinterpret_cast<const f32x4 *>(lds + token * (WV * 4) + piece(2 * q + 1, token));
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[k] = lo[k];
-            x[4 + k] = hi[k];
-        }
-    };
-    // this lane's vocabulary rows from here on are past V (they hold zeros)
-    const int64_t left = g.V - n0 - wm * WV;
-    const int end = (int)min(max(left - 8 * q, (int64_t)0), (int64_t)8);
-    const bool ragged = left < WV;
-    const __amdgpu_buffer_rsrc_t rP = make_rsrc(
-        GRAD ? g.P + ((int64_t)cur.tm * g.psteps + cur.p0 + wm * (IA / 2)) * LBLOCK : nullptr, GRAD ? LBLOCK * IA : 0);
-    auto group = [&](auto jc) {
-        turn(jc);
-        // B iterations' reads at a time: a wave is alone on its SIMD, nothing else hides their latency
-        constexpr int B = 4;
-#pragma unroll 1
-        for (int it = 0; it < 32 / TI; it += B) {
-            float x[B][8], c[B], s[B];
-            int lab[B];
-            const int tl0 = wn * 128 + 32 * decltype(jc)::value + TI * it + tt;
-            bool any = ragged;
+                for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+        // between the first step's loads and here lie p's stores, whose end nothing waits for
+        constexpr int STORES = GRAD ? 32 * WV / 128 : 0;
+        loss_loop<IA, 4 + IA, 4 + IA, STORES>(steps, index > 0, st.S1, st.S0, acc, load, read);
+        if (more) first_loads(next);
+
+        // ---- epilogue.  Lane (r32, hh) of tile (i, j) holds token wn*128 + 32 j + r32 and vocabulary rows
+        // wm*WV + 32 i + 8 (v/4) + 4 hh + v%4.  turn(j) lays token group j out as rows of WV floats, whose 16-byte pieces are
+        // permuted by the token so that neither the writes nor the reads of two neighbouring pieces meet in a bank. ----
+        const int lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        uint8_t *lds = st.S0 + wave * 16384;          // 32 tokens of WV floats
+        constexpr int PIECES = WV / 4;                // a row's pieces of four vocabulary rows
+        auto piece = [](int p, int token) { return ((p ^ (p / (PIECES / 2))) ^ (token & (PIECES - 1))) * 16; };
+        auto order = [&]() {
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        };
+        auto turn = [&](auto jc) {
+            constexpr int j = decltype(jc)::value;
+            const int c32 = lane_e & 31, he = lane_e >> 5;
+            order();
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                eight(TI * (it + b) + tt, x[b]);
-                c[b] = st.refs[tl0 + TI * b];
-                lab[b] = st.labs[tl0 + TI * b];
-            }
+            for (int i = 0; i < IA; ++i)
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                // the label's place among this lane's eight, or anything else
-                lab[b] = lab[b] < 0 ? -1 : lab[b] - wm * WV - 8 * q;
-                any |= (uint32_t)lab[b] < 8u;
-            }
-            // few batches hold a label; the empty statement keeps this a branch (as selects for every element it doubled
-            // the epilogue's time)
-            if (__builtin_amdgcn_ballot_w64(any)) {
-                asm volatile("");
+                for (int v4 = 0; v4 < 4; ++v4)
+                    *reinterpret_cast<f32x4 *>(lds + c32 * (WV * 4) + piece(8 * i + 2 * v4 + he, c32)) =
+                        f32x4{acc[i][j][4 * v4], acc[i][j][4 * v4 + 1], acc[i][j][4 * v4 + 2], acc[i][j][4 * v4 + 3]};
+            order();
+        };
+        // a lane's eight vocabulary rows: chunk q of token TI it + tt of the group
+        constexpr int NQ = WV / 8, TI = 64 / NQ;
+        const int q = lane_e & (NQ - 1), tt = lane_e / NQ;
+        auto eight = [&](int token, float (&x)[8]) {
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(lds + token * (WV * 4) + piece(2 * q, token));
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(lds + token * (WV * 4) + piece(2 * q + 1, token));
 #pragma unroll
-                for (int b = 0; b < B; ++b) {
-                    float zl = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        zl = lab[b] == k ? x[b][k] : zl;
-                        x[b][k] = lab[b] == k || k >= end ? -__builtin_inff() : x[b][k];
-                    }
-                    if ((uint32_t)lab[b] < 8u) g.r.zl[m0 + tl0 + TI * b] = zl * kLog2e;
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[b][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][k], kLog2e, -c[b]));
-                const float *e = x[b];
-                s[b] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            }
-#pragma unroll
-            for (int b = 0; b < B; ++b) s[b] = over_lanes<NQ>(s[b], [](float a, float b) { return a + b; });
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int row = tl0 + TI * b;
-                st.sums[wm][row] = s[b];      // the same from all of a token's lanes
-                if (GRAD) {      // nontemporal: 1659 -> 1647 us for the whole call at 4096 x 32000 x 4096
-                    const float *e = x[b];
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])}, rP,
-                        (uint32_t)((q >> 3) * (int)(LBLOCK * 2) + row * 128 + (((q & 7) ^ ((row >> 1) & 7)) * 16)), 0, 2);
-                }
-            }
-        }
-    };
-    auto groups = [&]() {
-        group(std::integral_constant<int, 0>{});
-        group(std::integral_constant<int, 1>{});
-        group(std::integral_constant<int, 2>{});
-        group(std::integral_constant<int, 3>{});
-        __syncthreads();
-    };
-    groups();
-    float sum = st.sums[0][tid] + st.sums[1][tid];
-    // Is every token's sum where it should be?  Above 2^kLossSlack a logit lies too far above the reference; below
-    // 2^-kLossSlack all lie too far below it, or there are none but the label (a reference of an earlier piece may lie
-    // above all of this tile); NaN fails too.
-    const bool ok = m0 + tid >= count || (sum <= __builtin_ldexpf(1.0f, kLossSlack) && (g.ref || sum >= __builtin_ldexpf(1.0f, -kLossSlack)));
-    if (!__syncthreads_and(ok)) {
-        // the tile once more, those tokens against their own largest logit
-        auto top = [&](auto jc) {
-            turn(jc);
-            for (int it = 0; it < 32 / TI; ++it) {
-                const int token = TI * it + tt;
-                float x[8], z = -__builtin_inff();
-                eight(token, x);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z = fmaxf(z, k < end ? x[k] : -__builtin_inff());
-                z = over_lanes<NQ>(z, [](float a, float b) { return fmaxf(a, b); });
-                if (q == 0) st.tops[wm][wn * 128 + 32 * decltype(jc)::value + token] = z;
+            for (int k = 0; k < 4; ++k) {
+                x[k] = lo[k];
+                x[4 + k] = hi[k];
             }
         };
-        top(std::integral_constant<int, 0>{});
-        top(std::integral_constant<int, 1>{});
-        top(std::integral_constant<int, 2>{});
-        top(std::integral_constant<int, 3>{});
-        __syncthreads();
-        // (no logit at all, past the vocabulary's end, or NaN only: the reference stays)
-        const float most = fmaxf(st.tops[0][tid], st.tops[1][tid]);
-        if (!ok && most > -__builtin_inff()) st.refs[tid] = ceilf(most * kLog2e);
-        __syncthreads();
+        // this lane's vocabulary rows from here on are past V (they hold zeros)
+        const int64_t left = g.V - n0 - wm * WV;
+        const int end = (int)min(max(left - 8 * q, (int64_t)0), (int64_t)8);
+        const bool ragged = left < WV;
+        const __amdgpu_buffer_rsrc_t rP = make_rsrc(
+            GRAD ? g.P + ((int64_t)cur.tm * g.psteps + cur.p0 + wm * (IA / 2)) * LBLOCK : nullptr, GRAD ? LBLOCK * IA : 0);
+        auto group = [&](auto jc) {
+            turn(jc);
+            // B iterations' reads at a time: a wave is alone on its SIMD, nothing else hides their latency
+            constexpr int B = 4;
+#pragma unroll 1
+            for (int it = 0; it < 32 / TI; it += B) {
+                float x[B][8], c[B], s[B];
+                int lab[B];
+                const int tl0 = wn * 128 + 32 * decltype(jc)::value + TI * it + tt;
+                bool any = ragged;
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    eight(TI * (it + b) + tt, x[b]);
+                    c[b] = st.refs[tl0 + TI * b];
+                    lab[b] = st.labs[tl0 + TI * b];
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    // the label's place among this lane's eight, or anything else
+                    lab[b] = lab[b] < 0 ? -1 : lab[b] - wm * WV - 8 * q;
+                    any |= (uint32_t)lab[b] < 8u;
+                }
+                // few batches hold a label; the empty statement keeps this a branch (as selects for every element it doubled
+                // the epilogue's time)
+                if (__builtin_amdgcn_ballot_w64(any)) {
+                    asm volatile("");
+#pragma unroll
+                    for (int b = 0; b < B; ++b) {
+                        float zl = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            zl = lab[b] == k ? x[b][k] : zl;
+                            x[b][k] = lab[b] == k || k >= end ? -__builtin_inff() : x[b][k];
+                        }
+                        if ((uint32_t)lab[b] < 8u) g.r.zl[m0 + tl0 + TI * b] = zl * kLog2e;
+                    }
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) x[b][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][k], kLog2e, -c[b]));
+                    const float *e = x[b];
+                    s[b] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) s[b] = over_lanes<NQ>(s[b], [](float a, float b) { return a + b; });
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const int row = tl0 + TI * b;
+                    st.sums[wm][row] = s[b];      // the same from all of a token's lanes
+                    if (GRAD) {      // nontemporal: 1647 us for the whole call at 4096 x 32000 x 4096, 1659 without
+                        const float *e = x[b];
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
+                                  pack_bf16x2(e[6], e[7])}, rP,
+                            (uint32_t)((q >> 3) * (int)(LBLOCK * 2) + row * 128 + (((q & 7) ^ ((row >> 1) & 7)) * 16)), 0, 2);
+                    }
+                }
+            }
+        };
+        auto groups = [&]() {
+            group(std::integral_constant<int, 0>{});
+            group(std::integral_constant<int, 1>{});
+            group(std::integral_constant<int, 2>{});
+            group(std::integral_constant<int, 3>{});
+            __syncthreads();
+        };
         groups();
-        sum = st.sums[0][tid] + st.sums[1][tid];
-    }
-    if (m0 + tid < count) {
-        const int64_t o = (int64_t)cur.entry * g.Mp + m0 + tid;
-        g.tref[o] = st.refs[tid];
-        g.tsum[o] = sum;
-    }
-    if (!more) break;
-    __syncthreads();       // sums and refs are read
-    cur = next;
+        float sum = st.sums[0][tid] + st.sums[1][tid];
+        // Is every token's sum where it should be?  Above 2^kLossSlack a logit lies too far above the reference; below
+        // 2^-kLossSlack all lie too far below it, or there are none but the label (a reference of an earlier piece may lie
+        // above all of this tile); NaN fails too.
+        const bool ok = m0 + tid >= count || (sum <= __builtin_ldexpf(1.0f, kLossSlack) &&
+                                              (g.ref || sum >= __builtin_ldexpf(1.0f, -kLossSlack)));
+        if (!__syncthreads_and(ok)) {
+            // the tile once more, those tokens against their own largest logit
+            auto top = [&](auto jc) {
+                turn(jc);
+                for (int it = 0; it < 32 / TI; ++it) {
+                    const int token = TI * it + tt;
+                    float x[8], z = -__builtin_inff();
+                    eight(token, x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) z = fmaxf(z, k < end ? x[k] : -__builtin_inff());
+                    z = over_lanes<NQ>(z, [](float a, float b) { return fmaxf(a, b); });
+                    if (q == 0) st.tops[wm][wn * 128 + 32 * decltype(jc)::value + token] = z;
+                }
+            };
+            top(std::integral_constant<int, 0>{});
+            top(std::integral_constant<int, 1>{});
+            top(std::integral_constant<int, 2>{});
+            top(std::integral_constant<int, 3>{});
+            __syncthreads();
+            // (no logit at all, past the vocabulary's end, or NaN only: the reference stays)
+            const float most = fmaxf(st.tops[0][tid], st.tops[1][tid]);
+            if (!ok && most > -__builtin_inff()) st.refs[tid] = ceilf(most * kLog2e);
+            __syncthreads();
+            groups();
+            sum = st.sums[0][tid] + st.sums[1][tid];
+        }
+        if (m0 + tid < count) {
+            const int64_t o = (int64_t)cur.entry * g.Mp + m0 + tid;
+            g.tref[o] = st.refs[tid];
+            g.tsum[o] = sum;
+        }
+        if (!more) break;
+        __syncthreads();       // sums and refs are read
+        cur = next;
     }
 }
 
