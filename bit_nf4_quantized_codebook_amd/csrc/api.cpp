@@ -1443,7 +1443,8 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.off_b = take((size_t)p.Mp * 4);
     for (size_t &c : p.off_c) c = take((size_t)p.Mp * 4);
     p.gemv = !grad && M <= nf4k::kLossGemvMaxM;
-    p.narrow = !p.gemv && M <= nf4k::kLossNarrowMaxM && p.piece == p.tiles;
+    p.narrow = !p.gemv && p.piece == p.tiles &&
+               (M <= nf4k::kLossNarrowMaxM || (M <= nf4k::kLossNarrowMaxM2 && p.tiles <= nf4k::kLossNarrowMaxTiles));
     p.off_tsum = p.off_P = p.off_part = p.off_sum32 = 0;
     if (p.gemv) {
         p.off_tref = take((size_t)M * ((V + 15) / 16) * 8);

@@ -173,10 +173,12 @@ __device__ __forceinline__ void loss_write_mean(const double *sums, int n, int c
     if (threadIdx.x == 0) mean[0] = count ? (float)(total[0] / count) : 0.0f;
 }
 
-// up to kLossNarrowMaxM tokens, in one piece
-constexpr int64_t kLossNarrowMaxM = 128;
+// Up to kLossNarrowMaxM tokens, in one piece; up to kLossNarrowMaxM2 where the vocabulary is at most kLossNarrowMaxTiles
+// tiles of 256, half a round of the chip (with the gradient, 200 tokens: 32000 x 4096 183 us, tiles of 256 189, of those
+// 60 labelled 120 and 156; 8000 x 4096 85 and 107; 160 x 4000 x 1024 42 and 59.  Above: 50001 x 4096 304 and 264).
+constexpr int64_t kLossNarrowMaxM = 128, kLossNarrowMaxM2 = 256, kLossNarrowMaxTiles = 128;
 struct LossNarrowPlan {
-    int32_t TT, steps, per, splits;
+    int32_t MT, steps, per, splits;
     size_t parts;             // float32 partials
 };
 LossNarrowPlan loss_narrow_plan(int64_t M, int64_t V, int64_t K);

@@ -100,6 +100,62 @@ def test_sizes(M, V, K):
     check(X, W, labels)
 
 
+@pytest.mark.parametrize("M", [129, 192, 256])
+@pytest.mark.parametrize("none", [0.0, 0.4, 0.8])
+@pytest.mark.parametrize("V,K", [(700, 320), (16384, 64), (16385, 64), (16500, 128), (32768, 64), (32769, 64)])
+def test_129_to_256_tokens(M, V, K, none):
+    """Tiles for 64, 128 and 256 live tokens in one launch; one block of the vocabulary or two at a time, a last pair of
+    one; the vocabulary from which tiles of 256 take over."""
+    X, W, labels = make(M, V, K, seed=M + V, none=none, lift=10.0)
+    labels[0], labels[-1] = V - 1, 0
+    check(X, W, labels, torch.rand(M, device=DEV) - 0.3)
+
+
+@pytest.mark.parametrize("M,none", [(256, 0.0), (200, 0.3), (200, 0.5), (130, 0.8)])
+def test_references_move_within_pairs_of_blocks(M, none):
+    """Logits of neighbouring blocks of 64 vocabulary rows far apart, either way round, and tokens that are not finite, a
+    label past the vocabulary and tokens without one among them."""
+    V, K = 16448 + 30, 64
+    X, W, labels = make(M, V, K, seed=23, none=none)
+    W[:, 0] = (torch.arange(V, device=DEV) // 64 % 5 * 9.0).bfloat16()
+    X[:, 0] = torch.linspace(-7, 7, M, device=DEV).bfloat16()
+    labels[1:4] = torch.tensor([5, 70, V - 1], device=DEV)
+    check(X, W, labels, torch.ones(M, device=DEV))
+    ref = nf4.qlora_loss_grad(W, X, labels, torch.ones(M, device=DEV))
+    X[1, 3], labels[2] = float("nan"), V
+    loss, mean, dX = nf4.qlora_loss_grad(W, X, labels, torch.ones(M, device=DEV))
+    others = torch.ones(M, dtype=torch.bool, device=DEV)
+    others[1:3] = False
+    assert loss[1:3].isnan().all() and dX[1:3].isnan().all() and mean.isnan().all()
+    assert same(loss[others], ref[0][others]) and same(dX[others], ref[2][others])
+
+
+def test_graph_follows_the_number_of_live_tokens():
+    M, V, K = 200, 16500, 128
+    X, W, labels = make(M, V, K, seed=24)
+    dX = torch.empty((M, K), dtype=torch.bfloat16, device=DEV)
+    loss, mean = torch.empty(M, device=DEV), torch.empty(1, device=DEV)
+    ws = torch.empty(nf4.qlora_loss_workspace_size(M, V, K, True), dtype=torch.uint8, device=DEV)
+    nf4.qlora_loss_grad(W, X, labels, None, loss, mean, dX, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nf4.qlora_loss_grad(W, X, labels, None, loss, mean, dX, ws)
+    torch.cuda.synchronize()
+    for live in (200, 40, 128, 0, 129, 64, 65, 1):
+        lab = torch.full((M,), NONE, device=DEV, dtype=torch.int64)
+        lab[torch.randperm(M, device=DEV)[:live]] = torch.randint(0, V, (live,), device=DEV)
+        labels.copy_(lab)
+        for t in (loss, mean, dX):
+            t.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        ref = nf4.qlora_loss_grad(W, X, labels)
+        torch.cuda.synchronize()
+        for a, b in zip((loss, mean, dX), ref):
+            assert same(a, b), live
+
+
 @pytest.mark.parametrize("M", [60, 120, 600])
 @pytest.mark.parametrize("none", [0.0, 0.5, 0.97, 1.0])
 def test_tokens_without_a_label(none, M):
