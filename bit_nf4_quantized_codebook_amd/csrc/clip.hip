@@ -2,7 +2,7 @@
 //   norm = sqrt(sum over all tensors of g^2);   out = norm > max_norm ? g (max_norm / norm) : g
 //
 // Two passes over the gradients, both streams.  The list is cut into chunks of CHUNK elements, numbered
-// through; a workgroup takes a contiguous run of chunks and finds its first tensor by bisection.  Squares
+// through; a workgroup takes a contiguous run of chunks and looks for its first tensor.  Squares
 // are summed in float64: nothing overflows or vanishes, whatever the gradients' size, and the VALU has the time
 // (the stream leaves room for some 60 operations an element).  Each workgroup leaves one partial sum; the
 // second pass sums them again in every workgroup, in a fixed order, which is cheaper than a launch between.
@@ -10,9 +10,11 @@
 // The second pass walks backwards, since what the first read last still lies in the memory-side cache, and both its loads
 // and its stores are nontemporal, so as not to drive the rest out.
 //
-// Bound by HBM: 224 adapter pairs of the 7B width in bf16 (320 MB) take 163 us, where reading them twice and writing
+// Bound by HBM: 224 adapter pairs of the 7B width in bf16 (320 MB) take 160 us, where reading them twice and writing
 // them once at a copy's 5.0 TB/s takes 192; 217 us with plain loads and stores and 8192 elements a chunk, 167 walking
-// forwards, 185 with nontemporal loads in the first pass too.  One pair takes 8.5 us of kernels, 11 as a call.
+// forwards, 185 with nontemporal loads in the first pass too.  61 mixed pairs of odd sizes 29.5 us: 33
+// with the first tensor found by bisection and each chunk's entry read again.  One pair takes 8 us of kernels, 11 as a
+// call.
 //
 // The list (pointers, sizes, first chunks) is a table in device memory that the caller keeps with the gradients.
 
@@ -28,13 +30,15 @@ constexpr int NT = 256;
 
 __device__ __forceinline__ int64_t first(const ClipEntry &e) { return e.chunk >> 1; }
 
-// the tensor that holds chunk c: the last one that begins at or before it (tensors without elements have no chunk)
+// The tensor that holds chunk c: the last one that begins at or before it (tensors without elements have no chunk).  The
+// whole workgroup looks, each thread at one of NT places: a load's latency for 256 tensors, two for 65536.
 __device__ __forceinline__ int find(const ClipEntry *list, int n, int64_t c) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first(list[mid]) <= c) lo = mid;
-        else hi = mid - 1;
+    int lo = 0;
+    while (n > 1) {
+        const int step = (n + NT - 1) / NT, i = (int)threadIdx.x * step;
+        const int k = __syncthreads_count(i < n && first(list[lo + i]) <= c) - 1;
+        lo += k * step;
+        n = min(step, n - k * step);
     }
     return lo;
 }
@@ -112,54 +116,60 @@ __device__ __forceinline__ void scale(const T *p, T *o, int n, bool clip, double
     for (int i = h + nv * VEC + tid; i < n; i += NT) o[i] = to(p[i]);
 }
 
+// the workgroup's sum, in every thread
+__device__ __forceinline__ double over_block(double s) {
+    __shared__ double sh[NT / 64];
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = s;
+    __syncthreads();
+    return (sh[0] + sh[1]) + (sh[2] + sh[3]);
+}
+
 __global__ __launch_bounds__(NT) void clip_norm_kernel(const ClipEntry *__restrict__ list, int n, int64_t chunks,
                                                        double *__restrict__ part) {
-    __shared__ double sh[NT];
     const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
     double s = 0.0;
     if (c0 < c1) {
         int t = find(list, n, c0);
+        ClipEntry e = list[t];
+        auto next = [&]() { return t + 1 < n ? first(list[t + 1]) : chunks; };
+        int64_t end = next();
         for (int64_t c = c0; c < c1; ++c) {
-            while (t + 1 < n && first(list[t + 1]) <= c) ++t;
-            const ClipEntry e = list[t];
+            while (c >= end) {
+                e = list[++t];
+                end = next();
+            }
             const int64_t i0 = (c - first(e)) * CHUNK, i1 = min(i0 + CHUNK, e.numel);
             if (e.chunk & 1) s += squares(reinterpret_cast<const float *>(e.g) + i0, (int)(i1 - i0));
             else s += squares(reinterpret_cast<const uint16_t *>(e.g) + i0, (int)(i1 - i0));
         }
     }
-    sh[threadIdx.x] = s;
-    __syncthreads();
-    for (int d = NT / 2; d > 0; d >>= 1) {
-        if ((int)threadIdx.x < d) sh[threadIdx.x] += sh[threadIdx.x + d];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) part[blockIdx.x] = sh[0];
+    s = over_block(s);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
 __global__ __launch_bounds__(NT) void clip_scale_kernel(const ClipEntry *__restrict__ list, int n, int64_t chunks,
                                                         const double *__restrict__ part, int nparts, float max_norm,
                                                         float *__restrict__ norm_out) {
-    __shared__ double sh[NT];
-    double s = 0.0;
-    for (int i = threadIdx.x; i < nparts; i += NT) s += part[i];
-    sh[threadIdx.x] = s;
-    __syncthreads();
-    for (int d = NT / 2; d > 0; d >>= 1) {
-        if ((int)threadIdx.x < d) sh[threadIdx.x] += sh[threadIdx.x + d];
-        __syncthreads();
-    }
-    const double norm = __builtin_sqrt(sh[0]);
+    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+    // the partials and the workgroup's tensor are on their way together
+    double p[kClipParts / NT], s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kClipParts / NT; ++i) p[i] = i * NT + (int)threadIdx.x < nparts ? part[i * NT + threadIdx.x] : 0.0;
+    int t = c0 < c1 ? find(list, n, c1 - 1) : 0;
+#pragma unroll
+    for (int i = 0; i < kClipParts / NT; ++i) s += p[i];
+    const double norm = __builtin_sqrt(over_block(s));
     if (blockIdx.x == 0 && threadIdx.x == 0) norm_out[0] = (float)norm;
     // a norm that is not finite, as the caller sees it in float32, leaves the gradients as they are
     const bool clip = norm > (double)max_norm && (float)norm < __builtin_inff();
     // the factor stays in float64: it may be far below float32's range where the products are not
     const double f = clip ? (double)max_norm / norm : 1.0;
-    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
     if (c0 >= c1) return;
-    int t = find(list, n, c1 - 1);
+    ClipEntry e = list[t];
     for (int64_t c = c1 - 1; c >= c0; --c) {
-        while (first(list[t]) > c) --t;
-        const ClipEntry e = list[t];
+        while (first(e) > c) e = list[--t];
         if (!clip && e.out == e.g) continue;
         const int64_t i0 = (c - first(e)) * CHUNK, i1 = min(i0 + CHUNK, e.numel);
         if (e.chunk & 1) scale(reinterpret_cast<const float *>(e.g) + i0, reinterpret_cast<float *>(e.out) + i0, (int)(i1 - i0), clip, f);

@@ -102,7 +102,7 @@ def test_sizes(M, V, K):
 
 @pytest.mark.parametrize("M", [129, 192, 256])
 @pytest.mark.parametrize("none", [0.0, 0.4, 0.8])
-@pytest.mark.parametrize("V,K", [(700, 320), (16384, 64), (16385, 64), (16500, 128), (32768, 64), (32769, 64)])
+@pytest.mark.parametrize("V,K", [(700, 320), (16384, 64), (16385, 64), (16500, 128), (32768, 64), (32769, 64), (300, 16384)])
 def test_129_to_256_tokens(M, V, K, none):
     """Tiles for 64, 128 and 256 live tokens in one launch; one block of the vocabulary or two at a time, a last pair of
     one; the vocabulary from which tiles of 256 take over."""
