@@ -1433,7 +1433,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         off += round256(bytes);
         return at;
     };
-    p.off_count = take(4);
+    p.off_count = take(8);
     p.off_sums = take((size_t)(p.Mp / nf4k::kLossJoinRowsNarrow) * 8);
     p.off_row = take((size_t)p.Mp * 4);
     p.off_label = take((size_t)p.Mp * 4);
@@ -1523,8 +1523,8 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.Mp, n.steps, n.per, tref, tsum, P, part, loss, mean, dX};
         NF4_CHECK_HIP(nf4k::launch_loss_narrow_logits(a, s), "loss logits of few tokens");
         NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, n.steps, nullptr, c[0], P, true, grad,
-                                                            dloss, loss, mean}, true, s), "loss sums");
-        NF4_CHECK_HIP(grad ? nf4k::launch_loss_narrow_dx(a, s) : nf4k::launch_loss_narrow_mean(a, s), "loss of few tokens");
+                                                            dloss, loss, mean, !grad}, true, s), "loss sums");
+        if (grad) NF4_CHECK_HIP(nf4k::launch_loss_narrow_dx(a, s), "loss dX of few tokens");
         return NF4_OK;
     }
     NF4_CHECK_HIP(nf4k::launch_loss_prep(labels, M, V, K, r, loss, grad ? dX : nullptr, s), "loss rows");
@@ -1537,7 +1537,7 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, P, 4 * nt}, s),
                       "loss logits");
         NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, P, last, grad, dloss, loss,
-                                                            mean}, false, s), "loss sums");
+                                                            mean, false}, false, s), "loss sums");
         // one workgroup of the join writes the mean itself
         float *mean_after = last && M > nf4k::kLossJoinRows ? mean : nullptr;
         if (!grad) {

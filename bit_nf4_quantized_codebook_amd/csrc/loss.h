@@ -23,7 +23,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 // Per-row state in the workspace; row arrays have Mp = M rounded up to 256 entries.
 struct LossRows {
-    int32_t *count;        // [1] live rows
+    int32_t *count;        // [2] live rows; workgroups of a join that have ended (few tokens, forward)
     double *sums;          // [a join's workgroups] sums of the losses of each workgroup of the last join
     int32_t *row;          // [M] live row -> token
     int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
@@ -153,10 +153,12 @@ struct LossJoin {
     bool last, grad;
     const float *dloss;
     float *loss, *mean;
+    bool tickets;             // its last workgroup writes the mean (count[1] is 0 before)
 };
 // narrow: the tables of loss_narrow.hip
 hipError_t launch_loss_join(const LossJoin &a, bool narrow, hipStream_t stream);
-// the mean from the last join's sums (with grad, dX's last launch writes it; one workgroup of the join writes it itself)
+// the mean from the last join's sums (with grad, dX's last launch writes it; one workgroup of the join writes it itself, and
+// with tickets the join does)
 hipError_t launch_loss_mean(const LossRows &r, int64_t M, float *mean, hipStream_t stream);
 
 // by 256 threads
@@ -195,7 +197,6 @@ struct LossNarrow {
     uint16_t *dX;
 };
 hipError_t launch_loss_narrow_logits(const LossNarrow &g, hipStream_t stream);
-hipError_t launch_loss_narrow_mean(const LossNarrow &g, hipStream_t stream);      // forward
 hipError_t launch_loss_narrow_dx(const LossNarrow &g, hipStream_t stream);        // with dX and the mean
 
 // the forward for up to kLossGemvMaxM tokens

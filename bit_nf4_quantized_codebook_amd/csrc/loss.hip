@@ -91,11 +91,30 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     const int wave = tid >> 6, w0 = NARROW ? lr * NWR : 0;
     const int row = blockIdx.x * JR + lr;
     const bool live = row < count;
-    if ((int)blockIdx.x * JR >= count) {
-        if (g.last && tid == 0) {
-            g.r.sums[blockIdx.x] = 0.0;
-            if (gridDim.x == 1) g.mean[0] = 0.0f;
+    // the workgroup's sum of losses, by thread 0
+    auto finish = [&](double s) {
+        if (!NARROW || !g.tickets) {
+            if (tid) return;
+            g.r.sums[blockIdx.x] = s;
+            if (gridDim.x == 1) g.mean[0] = count ? (float)(s / count) : 0.0f;
+            return;
         }
+        if (wave) return;
+        int ended = 0;
+        if (tid == 0) {
+            __hip_atomic_store(&g.r.sums[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            ended = __hip_atomic_fetch_add(&g.r.count[1], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1;
+        }
+        if (__builtin_amdgcn_readfirstlane(ended) != (int)gridDim.x) return;
+        // the workgroup that ends last: the sums in a fixed order
+        double all = 0.0;
+        for (int i = tid; i < (int)gridDim.x; i += 64) all += __hip_atomic_load(&g.r.sums[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d);
+        if (tid == 0) g.mean[0] = count ? (float)(all / count) : 0.0f;
+    };
+    if ((int)blockIdx.x * JR >= count) {
+        if (g.last) finish(0.0);
         return;
     }
     const float NEG = -__builtin_inff();
@@ -198,12 +217,10 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     }
     if (!g.last) return;
     __syncthreads();
-    if (tid == 0) {
-        double s = 0.0;
+    double s = 0.0;
+    if (tid == 0)
         for (int i = 0; i < JR; ++i) s += sl[i];
-        g.r.sums[blockIdx.x] = s;
-        if (gridDim.x == 1) g.mean[0] = (float)(s / count);
-    }
+    finish(s);
 }
 
 __global__ __launch_bounds__(256) void loss_mean_kernel(LossRows r, int64_t M, float *mean) {

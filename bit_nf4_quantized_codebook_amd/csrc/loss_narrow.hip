@@ -2,9 +2,9 @@
 // 256 x 256 with two stages in flight leave the memory idle.  Tiles here are narrow and their stages many:
 //   1. logits: 64 vocabulary rows a workgroup (more than 128 live tokens: 64 or 128).  Each makes the list of live rows for
 //      itself, from at most 256 labels;
-//   2. the join of the blocks of 64 rows (loss.hip);
+//   2. the join of the blocks of 64 rows (loss.hip; forward: and the mean);
 //   3. dX's product: 128 columns over a part of the vocabulary, float32 partials;
-//   4. their sum, dX, and the mean (forward: the mean alone).
+//   4. their sum, dX, and the mean.
 // A launch is made for the M tokens there may be (MT = 64, 128 or 256: its LDS and its grid), a tile for those that are
 // live (TT): 60 labelled of 200 cost what 60 do.
 // The layouts of p, of the LDS stages and of the fragments are those of loss_logits.hip and loss_dx.hip.
@@ -386,7 +386,13 @@ __device__ __forceinline__ void narrow_logits_any(const LossNarrow &g) {
             g.r.label[at] = lab64 < g.V ? (int32_t)lab64 : -1;
         }
     }
-    if (blockIdx.x == 0 && tid == 0) g.r.count[0] = count;
+    if (blockIdx.x == 0) {
+        if (tid == 0) {
+            g.r.count[0] = count;
+            g.r.count[1] = 0;
+        }
+        if (tid < g.M && lab64 < 0) g.loss[tid] = 0.0f;
+    }
     __syncthreads();
     count = __builtin_amdgcn_readfirstlane(count);
     const NarrowLds<MT> l{{S0, S1, S2, S3, S4, S5}, refs, sums, tops, labs, rows};
@@ -448,7 +454,6 @@ __global__ __launch_bounds__(256) void loss_narrow_fold_kernel(LossNarrow g, int
     if (k >= g.K) return;
     if (!(own & bit)) {
         *reinterpret_cast<uint2 *>(g.dX + (int64_t)t * g.K + k) = uint2{0, 0};
-        if (k == 0) g.loss[t] = 0.0f;
         return;
     }
     const int ntn = (int)((g.K + 127) / 128), splits = (g.steps + g.per - 1) / g.per;
@@ -469,12 +474,6 @@ __global__ __launch_bounds__(256) void loss_narrow_fold_kernel(LossNarrow g, int
     }
     // a label out of the vocabulary: a and b are NaN
     *reinterpret_cast<uint2 *>(g.dX + (int64_t)t * g.K + k) = LossFinal{a, b}.value(x, w);
-}
-
-// forward: the mean, and the losses of tokens without a label
-__global__ __launch_bounds__(256) void loss_narrow_mean_kernel(LossNarrow g) {
-    if ((int)threadIdx.x < g.M && g.labels[threadIdx.x] < 0) g.loss[threadIdx.x] = 0.0f;
-    loss_write_mean(g.r.sums, (int)((g.M + kLossJoinRowsNarrow - 1) / kLossJoinRowsNarrow), g.r.count[0], g.mean);
 }
 
 }  // namespace
@@ -506,11 +505,6 @@ void narrow_logits_of(const LossNarrow &g, hipStream_t stream) {
 hipError_t launch_loss_narrow_logits(const LossNarrow &g, hipStream_t stream) {
     if (g.P) narrow_logits_of<true>(g, stream);
     else narrow_logits_of<false>(g, stream);
-    return hipGetLastError();
-}
-
-hipError_t launch_loss_narrow_mean(const LossNarrow &g, hipStream_t stream) {
-    hipLaunchKernelGGL(loss_narrow_mean_kernel, dim3(1), dim3(256), 0, stream, g);
     return hipGetLastError();
 }
 
