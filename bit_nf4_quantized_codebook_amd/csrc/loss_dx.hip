@@ -253,6 +253,17 @@ __global__ __launch_bounds__(256) void loss_fold_kernel(LossDxArgs g) {
         p[i] = g.part + tl * LT + c;
         x4[i] = f32x4{0, 0, 0, 0};
     }
+    // what the last step takes, on its way beside the partials (a label out of the vocabulary: a and b are NaN)
+    uint2 w[N];
+    LossFinal fin[N];
+    int token[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (!g.dX || row[i] >= count || k >= g.K) continue;
+        w[i] = *reinterpret_cast<const uint2 *>(g.W + (int64_t)max(g.r.label[row[i]], 0) * g.K + k);
+        fin[i] = LossFinal{g.r.a[row[i]], g.r.b[row[i]]};
+        token[i] = g.r.row[row[i]];
+    }
     for (int s0 = 0; s0 < n; s0 += 4) {
         f32x4 v[N][4];
 #pragma unroll
@@ -278,9 +289,7 @@ __global__ __launch_bounds__(256) void loss_fold_kernel(LossDxArgs g) {
             *sum = x4[i];
             continue;
         }
-        // a label out of the vocabulary: a and b are NaN
-        const uint2 w = *reinterpret_cast<const uint2 *>(g.W + (int64_t)max(g.r.label[t], 0) * g.K + k);
-        *reinterpret_cast<uint2 *>(g.dX + (int64_t)g.r.row[t] * g.K + k) = LossFinal{g.r.a[t], g.r.b[t]}.value(x4[i], w);
+        *reinterpret_cast<uint2 *>(g.dX + (int64_t)token[i] * g.K + k) = fin[i].value(x4[i], w[i]);
     }
 }
 

@@ -16,7 +16,7 @@
 //
 // 256 x 256 tiles: both operands of a step are then 64 KB for 2048 cycles of MFMAs, two stages fill the LDS.  Bound by
 // the MFMAs at the clock that their power allows: a step of 64 takes 1.57 us (1.37 PFLOP/s over the chip), a tile's
-// epilogue 8.  4096 x 32000 x 4096 with p: 860 us of kernel, 1.25 PFLOP/s; 2048 x 32000 x 8192 without: 827 us, 1.30.
+// epilogue 8.  4096 x 32000 x 4096 with p: 860 us of kernel, 1.25 PFLOP/s; 2048 x 32000 x 8192 without: 805 us, 1.33.
 // A library product of the same operands, which writes the logits, reaches 1.34.
 
 #include "common.h"
