@@ -29,7 +29,7 @@ struct LossRows {
     int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
     float *zl;             // [M] the label's logit in log2 units (unset without one)
     float *S;              // [M] sum over the other vocabulary rows of 2^(l - c)
-    float *a, *b;          // [M] dX = a (sum P W) - b W[label]
+    float *a, *b;          // [M] dX = b (a sum P W - W[label])
 };
 
 // Tiles of rows and columns, numbered along the columns within groups of four tiles of rows (an XCD's concurrent

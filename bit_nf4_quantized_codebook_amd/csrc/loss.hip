@@ -2,7 +2,7 @@
 // the vocabulary's tiles, the losses, and dX from its partials.  With d = ln sum_{v != y} e^z_v - z_y (the
 // log odds against the label y):
 //   loss = ln(1 + e^d) = max(d, 0) + ln(1 + e^-|d|),   1 - p_y = 1 / (1 + e^-d)
-//   dX = g (sum_{v != y} p_v W_v - (1 - p_y) W_y)
+//   dX = g (sum_{v != y} p_v W_v - (1 - p_y) W_y) = g (1 - p_y) (sum_{v != y} e^z_v W_v / sum_{v != y} e^z_v - W_y)
 // Nothing here subtracts two large numbers: a label that is nearly certain keeps a loss and a gradient of full
 // precision.
 //
@@ -119,7 +119,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     }
     const float NEG = -__builtin_inff();
     const float c_old = g.c_in && live ? g.c_in[row] : NEG;
-    // the new reference: the largest there is; eight tiles' loads at a time
+    // The new reference: the largest there is; eight tiles' loads at a time.  A tile with nothing but the label has a sum of
+    // zero and a reference that says nothing.
     float c = c_old, sum = 0.0f, low = -NEG;
     // entries of this row's tiles: ntile, and the second halves of the tiles that are cut
     const LossTiles tiles((count + LT - 1) / LT, g.ntile);
@@ -147,7 +148,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                most = fmaxf(most, f[u]);
+                has[u] = has[u] && s[u] != 0.0f;
+                most = fmaxf(most, has[u] ? f[u] : NEG);
                 low = fminf(low, has[u] ? f[u] : -NEG);
             }
             // c = most also before the first tile, where there is nothing to move (and both may be -inf)
@@ -177,7 +179,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
             // blocks this entry stands for: all of its tile's, or the half's
             const int b0 = t < g.ntile ? 0 : BLOCKS / 2, b1 = t < g.ntile && tile >= cut ? BLOCKS / 2 : BLOCKS;
             const float from = g.tref[at(t)];
-            if (from == top) continue;
+            if (from == top || g.tsum[at(t)] == 0.0f) continue;
             const float f = __builtin_amdgcn_exp2f(from - top);
             for (int b = b0; b < b1; ++b) {
                 const int64_t block = ((int64_t)(row / LT) * g.ntile + tile) * BLOCKS + b;
@@ -199,7 +201,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
 #pragma unroll
             for (int w = 0; w < NWR; ++w) S += ps[w0 + w][lr];
             g.r.S[row] = S;
-            g.c_out[row] = top;
+            g.c_out[row] = top > NEG ? top : 0.0f;
             if (g.last) {
                 // ln S + (c - zl) ln 2; a label out of the vocabulary has no logit
                 if (label < 0) zl = __builtin_nanf("");
@@ -208,7 +210,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
                 g.loss[m] = loss;
                 value = (double)loss;
                 if (g.grad) {
-                    g.r.a[row] = weight / (S + __builtin_amdgcn_exp2f(zl - top));
+                    // (p_v's own factor, 1 / (S + 2^(zl - top)), leaves float32 where the label lies 2^128 above the reference)
+                    g.r.a[row] = S == 0.0f ? 0.0f : 1.0f / S;
                     g.r.b[row] = weight / (1.0f + expf(-d));
                 }
             }

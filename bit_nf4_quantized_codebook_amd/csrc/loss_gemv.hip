@@ -138,12 +138,13 @@ __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int64_t n = n0 + 16 * a + 4 * lg + v;
-            if (n < g.V) top = fmaxf(top, z[a][v]);
+            if (n < g.V && n != lab) top = fmaxf(top, z[a][v]);
             if (n == lab) g.zl[t] = z[a][v] * kLog2e;
         }
     }
     top = fmaxf(top, __shfl_xor(top, 16));
-    top = ceilf(fmaxf(top, __shfl_xor(top, 32)) * kLog2e);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    top = top > -__builtin_inff() ? ceilf(top * kLog2e) : 0.0f;      // none: a sum of zero, which the join passes over
 #pragma unroll
     for (int a = 0; a < RG; ++a)
 #pragma unroll
@@ -169,11 +170,11 @@ __global__ __launch_bounds__(256) void loss_gemv_join_kernel(LossGemv g, int nti
         for (int u = 0; u < 8; ++u) v[u] = i0 + 256 * u < ntile ? tab[i0 + 256 * u] : float2{NEG, 0.0f};
         float m = c;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) m = fmaxf(m, v[u].x);
+        for (int u = 0; u < 8; ++u) m = fmaxf(m, v[u].y != 0.0f ? v[u].x : NEG);
         sum *= m == c ? 1.0f : __builtin_amdgcn_exp2f(c - m);
 #pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (i0 + 256 * u < ntile) sum += v[u].y * __builtin_amdgcn_exp2f(v[u].x - m);
+            if (v[u].y != 0.0f) sum += v[u].y * __builtin_amdgcn_exp2f(v[u].x - m);
         c = m;
     }
     auto join = [&](float c2, float s2) {

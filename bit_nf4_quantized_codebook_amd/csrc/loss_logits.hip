@@ -255,15 +255,17 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
         const bool ok = m0 + tid >= count || (sum <= __builtin_ldexpf(1.0f, kLossSlack) &&
                                               (g.ref || sum >= __builtin_ldexpf(1.0f, -kLossSlack)));
         if (!__syncthreads_and(ok)) {
-            // the tile once more, those tokens against their own largest logit
+            // the tile once more, those tokens against their largest logit but the label's (which may lie so far above the others
+            // that float32 would hold nothing of them beside it)
             auto top = [&](auto jc) {
                 turn(jc);
                 for (int it = 0; it < 32 / TI; ++it) {
                     const int token = TI * it + tt;
                     float x[8], z = -__builtin_inff();
                     eight(token, x);
+                    const int at = st.labs[wn * 128 + 32 * decltype(jc)::value + token], lab = at < 0 ? -1 : at - wm * WV - 8 * q;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) z = fmaxf(z, k < end ? x[k] : -__builtin_inff());
+                    for (int k = 0; k < 8; ++k) z = fmaxf(z, k < end && k != lab ? x[k] : -__builtin_inff());
                     z = over_lanes<NQ>(z, [](float a, float b) { return fmaxf(a, b); });
                     if (q == 0) st.tops[wm][wn * 128 + 32 * decltype(jc)::value + token] = z;
                 }

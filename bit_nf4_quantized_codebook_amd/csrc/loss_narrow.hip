@@ -170,10 +170,13 @@ struct NarrowLogits {
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 float x = -__builtin_inff();
+                const int at = labs[32 * JN * wn + 16 * b + tt];
 #pragma unroll
-                for (int i = 0; i < VI; ++i)
+                for (int i = 0; i < VI; ++i) {
+                    const int lab = at < 0 ? -1 : at - 32 * (VI * wm + i) - 8 * q;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x = fmaxf(x, k < end[i] ? z[i][b][k] : -__builtin_inff());
+                    for (int k = 0; k < 8; ++k) x = fmaxf(x, k < end[i] && k != lab ? z[i][b][k] : -__builtin_inff());
+                }
                 x = over_lanes<4>(x, [](float a, float b) { return fmaxf(a, b); });
                 tops[wm][32 * JN * wn + 16 * b + tt] = x;
             }

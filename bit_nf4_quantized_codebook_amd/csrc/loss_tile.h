@@ -35,12 +35,12 @@ __device__ __forceinline__ float over_lanes(float x, Op op) {
     return x;
 }
 
-// A token's last step: dX = a (sum P W) - b W[label], rounded once.
+// A token's last step: dX = b (a sum P W - W[label]), a = 1 / S, rounded once.
 struct LossFinal {
     float a, b;
     __device__ __forceinline__ uint2 value(const f32x4 &x, const uint2 &v) const {
-        return uint2{pack_bf16x2(a * x[0] - b * bf16_to_f32(v.x & 0xFFFFu), a * x[1] - b * __uint_as_float(v.x & 0xFFFF0000u)),
-                     pack_bf16x2(a * x[2] - b * bf16_to_f32(v.y & 0xFFFFu), a * x[3] - b * __uint_as_float(v.y & 0xFFFF0000u))};
+        return uint2{pack_bf16x2(b * (a * x[0] - bf16_to_f32(v.x & 0xFFFFu)), b * (a * x[1] - __uint_as_float(v.x & 0xFFFF0000u))),
+                     pack_bf16x2(b * (a * x[2] - bf16_to_f32(v.y & 0xFFFFu)), b * (a * x[3] - __uint_as_float(v.y & 0xFFFF0000u)))};
     }
 };
 

@@ -9,6 +9,8 @@ within 48 of a maximum) every term of a row is off by the factor
 d = ln S + c - z_label by D as well, and
   |loss error| <= sigmoid(d) D + 8 u loss,
   |dX error| <= |g| (sum_{v != y} p |W| (h + 2 D + V u) + (1 - p_y) |W_y| 2 D) (1 + h) + h |dX|.
+Below float32's (and bf16's) smallest normal number, 2^-126, a value may be lost whole: a loss then is off by as much, and
+dX, where 1 - p_y is such a value, by that times |sum p W / sum p - W_y| <= 2 max |W|, and its own rounding by 2^-126 again.
 """
 import numpy as np
 import pytest
@@ -25,7 +27,7 @@ if not torch.cuda.is_available():
 import bit_nf4_quantized_codebook_amd as nf4  # noqa: E402
 
 DEV = torch.device("cuda:0")
-U, H = 2.0 ** -24, 2.0 ** -8
+U, H, TINY = 2.0 ** -24, 2.0 ** -8, 2.0 ** -126
 NONE = -100
 
 
@@ -64,7 +66,7 @@ def check(X, W, labels, dloss=None, rows=None, fwd=True, grad=True):
     Ez = K * U * (np.abs(x[rows]) @ np.abs(w).T).max(1)
     tiles = -(-V // 256)
     D = 2 * (Ez + 8 * U * (np.abs(z).max(1) + 64)) + (96 + tiles) * U
-    tol = -np.expm1(-ref) * D + 8 * U * ref
+    tol = -np.expm1(-ref) * D + 8 * U * ref + TINY
     out = []
     if fwd:
         out.append(nf4.qlora_loss_fwd(W, X, labels))
@@ -83,7 +85,7 @@ def check(X, W, labels, dloss=None, rows=None, fwd=True, grad=True):
         p[y[rows] < 0] = 0.0
         miss = -np.expm1(-ref)
         size = (p @ np.abs(w)) * (H + 2 * D + V * U)[:, None] + (miss * 2 * D)[:, None] * np.abs(w[np.maximum(y[rows], 0)])
-        tolx = np.abs(g[rows])[:, None] * size * (1 + H) + H * np.abs(dX)
+        tolx = np.abs(g[rows])[:, None] * size * (1 + H) + H * np.abs(dX) + TINY * (1 + 2 * np.abs(w).max())
         bad = ~(np.abs(got - dX) <= tolx)
         assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4], dX[bad][:4], tolx[bad][:4])
         assert not f64(out[-1][2])[y < 0].any()
@@ -240,6 +242,31 @@ def test_sure_labels_keep_relative_accuracy():
         w = W.copy()
         w[np.setdiff1d(labels, labels[m]), 0] = 0.0
         check(bf16(X[m:m + 1]), bf16(w), torch.tensor([labels[m]], device=DEV), torch.ones(1, device=DEV))
+
+
+@pytest.mark.parametrize("M,V", [(3, 200), (12, 200), (20, 200), (100, 200), (200, 200), (200, 20000), (300, 200), (140, 33000)])
+@pytest.mark.parametrize("above", [20.0, 64.0, 72.0])
+def test_labels_far_above_the_reference(M, V, above):
+    """The label's logit is e^94 and more, of which the references of the other entries, around e^30, know nothing."""
+    X, W, labels = make(M, V, 64, seed=31)
+    X[:, 0], W[:, 0] = 1.0, 30.0
+    labels[:] = 7
+    W[7, 0] = 30.0 + above
+    check(X, W, labels, torch.ones(M, device=DEV))
+
+
+@pytest.mark.parametrize("M", [1, 12, 30, 100, 200, 300])
+@pytest.mark.parametrize("V", [1, 65, 193, 257, 2561])
+def test_label_alone_in_its_tile(M, V):
+    """The label is the last row of the vocabulary, alone in a tile of 16, 64 or 256, and all other logits lie far below a
+    first reference of 0 (or above)."""
+    for level, label in ((-150.0, -150.0), (-150.0, 40.0), (60.0, 60.0), (-40.0, 30.0)):
+        X, W, labels = make(M, V, 64, seed=37)
+        X[:, 0], W[:, 0], W[-1, 0] = 1.0, level, label
+        labels[:] = V - 1
+        check(X, W, labels, torch.ones(M, device=DEV))
+        labels[:] = 0
+        check(X, W, labels, torch.ones(M, device=DEV))
 
 
 def test_references_move_far():
