@@ -1412,7 +1412,7 @@ struct LossPlan {
     bool narrow;                       // few tokens, with the gradient
     bool gemv;                         // few tokens, forward: its table lies at off_tref
     int32_t Mp, tiles, piece;          // rows padded to tiles; tiles of the vocabulary, and of a piece
-    size_t off_count, off_sums, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[2], off_tref, off_tsum, off_P, off_part,
+    size_t off_count, off_sums, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[2], off_tref, off_tsum, off_tp, off_P, off_part,
         off_sum32, total;
 };
 
@@ -1445,7 +1445,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     p.gemv = !grad && M <= nf4k::kLossGemvMaxM;
     p.narrow = !p.gemv && p.piece == p.tiles &&
                (M <= nf4k::kLossNarrowMaxM || (M <= nf4k::kLossNarrowMaxM2 && p.tiles <= nf4k::kLossNarrowMaxTiles));
-    p.off_tsum = p.off_P = p.off_part = p.off_sum32 = 0;
+    p.off_tsum = p.off_tp = p.off_P = p.off_part = p.off_sum32 = 0;
     if (p.gemv) {
         p.off_tref = take((size_t)M * ((V + 15) / 16) * 8);
         p.total = off;
@@ -1455,6 +1455,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
         p.off_tref = take((size_t)n.steps * M * 4);
         p.off_tsum = take((size_t)n.steps * M * 4);
+        p.off_tp = take(grad ? (size_t)n.steps * M * 4 : 0);
         p.off_P = take(grad ? (size_t)n.steps * nf4k::LBLOCK * 2 : 0);
         p.off_part = take(grad ? n.parts * 4 : 0);
         p.total = off;
@@ -1462,6 +1463,7 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
     }
     p.off_tref = take((size_t)p.piece * p.Mp * 8);
     p.off_tsum = take((size_t)p.piece * p.Mp * 8);
+    p.off_tp = take(grad ? (size_t)p.piece * p.Mp * 8 : 0);
     p.off_P = take(grad ? (size_t)p.piece * p.Mp * LT * 2 : 0);
     // a tile has partials only among the last, fewer than 256, and then as many as shares and tiles
     const int64_t rest = ntm * ntn < 256 ? ntm * ntn : 256;
@@ -1509,6 +1511,7 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
                            ws_at<int32_t>(workspace, p.off_label), ws_at<float>(workspace, p.off_zl),
                            ws_at<float>(workspace, p.off_S), ws_at<float>(workspace, p.off_a), ws_at<float>(workspace, p.off_b)};
     float *tref = ws_at<float>(workspace, p.off_tref), *tsum = ws_at<float>(workspace, p.off_tsum);
+    float *tp = grad ? ws_at<float>(workspace, p.off_tp) : nullptr;
     uint16_t *P = grad ? ws_at<uint16_t>(workspace, p.off_P) : nullptr;
     float *c[2];
     for (int i = 0; i < 2; ++i) c[i] = ws_at<float>(workspace, p.off_c[i]);
@@ -1520,9 +1523,9 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
     float *part = ws_at<float>(workspace, p.off_part);
     if (p.narrow) {
         const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
-        const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.Mp, n.steps, n.per, tref, tsum, P, part, loss, mean, dX};
+        const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.Mp, n.steps, n.per, tref, tsum, tp, P, part, loss, mean, dX};
         NF4_CHECK_HIP(nf4k::launch_loss_narrow_logits(a, s), "loss logits of few tokens");
-        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, n.steps, nullptr, c[0], P, true, grad,
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, tp, n.steps, nullptr, c[0], P, true, grad,
                                                             dloss, loss, mean, !grad}, true, s), "loss sums");
         if (grad) NF4_CHECK_HIP(nf4k::launch_loss_narrow_dx(a, s), "loss dX of few tokens");
         return NF4_OK;
@@ -1534,9 +1537,9 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         const bool last = t0 + nt == p.tiles;
         const float *before = t0 ? c[(piece + 1) % 2] : nullptr;
         float *now = c[piece % 2];
-        NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, P, 4 * nt}, s),
+        NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, tp, P, 4 * nt}, s),
                       "loss logits");
-        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, nt, before, now, P, last, grad, dloss, loss,
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, tp, nt, before, now, P, last, grad, dloss, loss,
                                                             mean, false}, false, s), "loss sums");
         // one workgroup of the join writes the mean itself
         float *mean_after = last && M > nf4k::kLossJoinRows ? mean : nullptr;

@@ -29,7 +29,7 @@ struct LossRows {
     int32_t *label;        // [M] its label; -1: out of the vocabulary (its results are NaN)
     float *zl;             // [M] the label's logit in log2 units (unset without one)
     float *S;              // [M] sum over the other vocabulary rows of 2^(l - c)
-    float *a, *b;          // [M] dX = b (a sum P W - W[label])
+    float *a, *b;          // [M] dX = b (a sum P W - W[label]); a: between pieces, the sum of P
 };
 
 // Tiles of rows and columns, numbered along the columns within groups of four tiles of rows (an XCD's concurrent
@@ -112,6 +112,7 @@ struct LogitsArgs {
     int32_t tile0, ntile;     // vocabulary tiles of this piece
     const float *ref;         // [M] references, or NULL: 0
     float *tref, *tsum;       // [2 ntile][Mp]: a tile's reference and its sum of 2^(l - reference)
+    float *tp;                // the same of P, which is rounded, or NULL
     uint16_t *P;              // 2^(l - reference) in bf16, or NULL; blocks of one step (see loss_logits.hip)
     int32_t psteps;           // steps of P's row of blocks
 };
@@ -144,7 +145,7 @@ struct LossJoin {
     LossRows r;
     int64_t M;
     int32_t Mp;
-    const float *tref, *tsum;
+    const float *tref, *tsum, *tp;
     int32_t ntile;
     const float *c_in;
     float *c_out;
@@ -190,7 +191,7 @@ struct LossNarrow {
     const int64_t *labels;
     LossRows r;
     int32_t Mp, steps, per;   // steps of 64 vocabulary rows: all, and of dX's workgroup
-    float *tref, *tsum;       // [M][steps]
+    float *tref, *tsum, *tp;  // [M][steps]; tp: as in LogitsArgs
     uint16_t *P;              // [steps] blocks; NULL: the forward
     float *part;
     float *loss, *mean;

@@ -3,6 +3,7 @@
 // log odds against the label y):
 //   loss = ln(1 + e^d) = max(d, 0) + ln(1 + e^-|d|),   1 - p_y = 1 / (1 + e^-d)
 //   dX = g (sum_{v != y} p_v W_v - (1 - p_y) W_y) = g (1 - p_y) (sum_{v != y} e^z_v W_v / sum_{v != y} e^z_v - W_y)
+// The e^z_v of the last form are bf16 above and below the line; in d they are not rounded.
 // Nothing here subtracts two large numbers: a label that is nearly certain keeps a loss and a gradient of full
 // precision.
 //
@@ -84,7 +85,7 @@ template <int JR, bool NARROW>
 __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     constexpr int JS = 256 / JR, BLOCKS = NARROW ? 1 : 4;
     constexpr int W0 = NARROW ? 1 : JR, NWR = NARROW ? 4 / JR : 4;      // first lane step of a row; waves that share one
-    __shared__ float pc[4][JR], ps[4][JR];
+    __shared__ float pc[4][JR], ps[4][JR], pp[4][JR];
     __shared__ double sl[JR];
     const int count = g.r.count[0];
     const int tid = threadIdx.x, lr = NARROW ? tid / JS : tid % JR, slice = NARROW ? tid % JS : tid / JR;
@@ -121,7 +122,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     const float c_old = g.c_in && live ? g.c_in[row] : NEG;
     // The new reference: the largest there is; eight tiles' loads at a time.  A tile with nothing but the label has a sum of
     // zero and a reference that says nothing.
-    float c = c_old, sum = 0.0f, low = -NEG;
+    float c = c_old, sum = 0.0f, sum_p = 0.0f, low = -NEG;
     // entries of this row's tiles: ntile, and the second halves of the tiles that are cut
     const LossTiles tiles((count + LT - 1) / LT, g.ntile);
     const int cut = NARROW ? g.ntile : tiles.first_cut(row / LT), entries = 2 * g.ntile - cut;
@@ -137,7 +138,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     }
     if (live)
         for (int t0 = slice; t0 < entries; t0 += JS * 8) {
-            float f[8], s[8], most = c;
+            float f[8], s[8], sp[8], most = c;
             bool has[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -145,6 +146,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
                 has[u] = t < entries;
                 f[u] = has[u] ? g.tref[at(t)] : NEG;
                 s[u] = has[u] ? g.tsum[at(t)] : 0.0f;
+                sp[u] = g.grad && has[u] ? g.tp[at(t)] : 0.0f;
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -153,10 +155,16 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
                 low = fminf(low, has[u] ? f[u] : -NEG);
             }
             // c = most also before the first tile, where there is nothing to move (and both may be -inf)
-            sum *= most == c ? 1.0f : __builtin_amdgcn_exp2f(c - most);
+            const float move = most == c ? 1.0f : __builtin_amdgcn_exp2f(c - most);
+            sum *= move;
+            sum_p *= move;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (has[u]) sum += s[u] * __builtin_amdgcn_exp2f(f[u] - most);
+            for (int u = 0; u < 8; ++u) {
+                if (!has[u]) continue;
+                const float to = __builtin_amdgcn_exp2f(f[u] - most);
+                sum += s[u] * to;
+                sum_p += sp[u] * to;
+            }
             c = most;
         }
     float top = c;
@@ -166,10 +174,16 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < NWR; ++w) top = fmaxf(top, pc[w0 + w][lr]);
-    sum = sum == 0.0f ? 0.0f : sum * __builtin_amdgcn_exp2f(c - top);
+    const float move = sum == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(c - top);
+    sum = sum == 0.0f ? 0.0f : sum * move;
+    sum_p = sum == 0.0f ? 0.0f : sum_p * move;
 #pragma unroll
-    for (int d = W0; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    for (int d = W0; d < 64; d <<= 1) {
+        sum += __shfl_xor(sum, d);
+        sum_p += __shfl_xor(sum_p, d);
+    }
     ps[wave][lr] = sum;
+    pp[wave][lr] = sum_p;
     __syncthreads();
     // Tiles with a reference below the row's: p is brought to it (rare, and only this workgroup's rows).  Row `row` of
     // P's blocks: 128 bytes for each 64 vocabulary rows, so 512 for a whole tile.
@@ -197,10 +211,15 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
     if (slice == 0) {
         double value = 0.0;
         if (live) {
-            float S = g.c_in ? g.r.S[row] * __builtin_amdgcn_exp2f(c_old - top) : 0.0f;
+            const float moved = g.c_in ? __builtin_amdgcn_exp2f(c_old - top) : 0.0f;
+            float S = g.c_in ? g.r.S[row] * moved : 0.0f, Sp = g.c_in && g.grad ? g.r.a[row] * moved : 0.0f;
 #pragma unroll
-            for (int w = 0; w < NWR; ++w) S += ps[w0 + w][lr];
+            for (int w = 0; w < NWR; ++w) {
+                S += ps[w0 + w][lr];
+                Sp += pp[w0 + w][lr];
+            }
             g.r.S[row] = S;
+            if (g.grad && !g.last) g.r.a[row] = Sp;
             g.c_out[row] = top > NEG ? top : 0.0f;
             if (g.last) {
                 // ln S + (c - zl) ln 2; a label out of the vocabulary has no logit
@@ -210,8 +229,9 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
                 g.loss[m] = loss;
                 value = (double)loss;
                 if (g.grad) {
-                    // (p_v's own factor, 1 / (S + 2^(zl - top)), leaves float32 where the label lies 2^128 above the reference)
-                    g.r.a[row] = S == 0.0f ? 0.0f : 1.0f / S;
+                    // The sum of P as it was rounded, not S: see loss_logits.hip.  (p_v's own factor, 1 / (S + 2^(zl - top)), leaves
+                    // float32 where the label lies 2^128 above the reference.)
+                    g.r.a[row] = Sp == 0.0f ? 0.0f : 1.0f / Sp;
                     g.r.b[row] = weight / (1.0f + expf(-d));
                 }
             }

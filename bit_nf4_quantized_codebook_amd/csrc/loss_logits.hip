@@ -12,7 +12,12 @@
 // step as one contiguous run.  The label's own p is left out (0): its coefficient in dX is
 // -(1 - p_label), which a rounded p_label near 1 would lose; the sum leaves it out for the same reason.
 //
-// p is rounded to bf16 because it is an operand of the next product; the sum takes the unrounded values.
+// p is rounded to bf16 because it is an operand of the next product.  The loss takes the sum of the unrounded values, dX
+// that of the rounded ones: the weights that its rows of W enter with then add up to 1, and what all rows have in common
+// cancels against the label's row as it does in the formula.  (Divided by the unrounded sum, p's rounding errors met that
+// common part: with one four times the rows' own and a largest p of 0.5 a token's dX was off by up to 6.5e-3 of itself,
+// now 1.95e-3, of which its own rounding is 1.8e-3.  The second sum costs 1 us of 117 at 129 x 32000 x 4096 with 39
+// labelled and 5 of 1650 at 4096.)
 //
 // 256 x 256 tiles: both operands of a step are then 64 KB for 2048 cycles of MFMAs, two stages fill the LDS.  Bound by
 // the MFMAs at the clock that their power allows: a step of 64 takes 1.57 us (1.37 PFLOP/s over the chip), a tile's
@@ -33,6 +38,7 @@ struct LossStages {
     float *refs;              // [LT]
     int *labs;                // [LT] labels, counted from the tile's first vocabulary row; -1: not in the tile
     float (*sums)[LT];        // [2] by the waves along the vocabulary
+    float (*psums)[LT];       // the same of p
     float (*tops)[LT];
 };
 
@@ -186,7 +192,8 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
             constexpr int B = 4;
 #pragma unroll 1
             for (int it = 0; it < 32 / TI; it += B) {
-                float x[B][8], c[B], s[B];
+                float x[B][8], c[B], s[B], sp[B];
+                u32x4 p[B];
                 int lab[B];
                 const int tl0 = wn * 128 + 32 * decltype(jc)::value + TI * it + tt;
                 bool any = ragged;
@@ -223,19 +230,25 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
                     for (int k = 0; k < 8; ++k) x[b][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][k], kLog2e, -c[b]));
                     const float *e = x[b];
                     s[b] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+                    if (GRAD) {
+                        p[b] = u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
+                        sp[b] = add_bf16x2(add_bf16x2(0.0f, p[b][0]), p[b][1]) + add_bf16x2(add_bf16x2(0.0f, p[b][2]), p[b][3]);
+                    }
                 }
+                const auto plus = [](float a, float b) { return a + b; };
 #pragma unroll
-                for (int b = 0; b < B; ++b) s[b] = over_lanes<NQ>(s[b], [](float a, float b) { return a + b; });
+                for (int b = 0; b < B; ++b) {
+                    s[b] = over_lanes<NQ>(s[b], plus);
+                    if (GRAD) sp[b] = over_lanes<NQ>(sp[b], plus);
+                }
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
                     const int row = tl0 + TI * b;
                     st.sums[wm][row] = s[b];      // the same from all of a token's lanes
                     if (GRAD) {      // nontemporal: 1647 us for the whole call at 4096 x 32000 x 4096, 1659 without
-                        const float *e = x[b];
+                        st.psums[wm][row] = sp[b];
                         __builtin_amdgcn_raw_buffer_store_b128(
-                            u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]),
-                                  pack_bf16x2(e[6], e[7])}, rP,
-                            (uint32_t)((q >> 3) * (int)(LBLOCK * 2) + row * 128 + (((q & 7) ^ ((row >> 1) & 7)) * 16)), 0, 2);
+                            p[b], rP, (uint32_t)((q >> 3) * (int)(LBLOCK * 2) + row * 128 + (((q & 7) ^ ((row >> 1) & 7)) * 16)), 0, 2);
                     }
                 }
             }
@@ -286,6 +299,7 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
             const int64_t o = (int64_t)cur.entry * g.Mp + m0 + tid;
             g.tref[o] = st.refs[tid];
             g.tsum[o] = sum;
+            if (GRAD) g.tp[o] = st.psums[0][tid] + st.psums[1][tid];
         }
         if (!more) break;
         __syncthreads();       // sums and refs are read
@@ -299,9 +313,9 @@ __global__ __launch_bounds__(256, 1) void loss_logits_kernel(LogitsArgs g) {
     // direct-to-LDS loads in flight into the other
     __shared__ __align__(16) uint8_t S0[2 * LOPB];
     __shared__ __align__(16) uint8_t S1[2 * LOPB];
-    __shared__ float refs[LT], sums[2][LT], tops[2][LT];
+    __shared__ float refs[LT], sums[2][LT], psums[GRAD ? 2 : 1][LT], tops[2][LT];
     __shared__ int labs[LT];
-    const LossStages st{S0, S1, refs, labs, sums, tops};
+    const LossStages st{S0, S1, refs, labs, sums, psums, tops};
 
     const int count = __builtin_amdgcn_readfirstlane(g.r.count[0]);
     const LossTiles tiles((count + LT - 1) / LT, g.ntile);

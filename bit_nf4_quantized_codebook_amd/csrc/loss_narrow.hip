@@ -34,7 +34,7 @@ __device__ __forceinline__ void step_barrier() {
 template <int MT>
 struct NarrowLds {
     uint8_t *S[6];                                   // LDS objects (a stage is one, or two of them)
-    float (*refs)[MT], (*sums)[MT], (*tops)[MT];
+    float (*refs)[MT], (*sums)[MT], (*psums)[MT], (*tops)[MT];      // psums: of p
     int *labs, *rows;
 };
 
@@ -55,7 +55,7 @@ struct NarrowLogits {
             w[i] = lds_.S[MT == 256 && TT == 128 ? 3 + i : i];
             x[i] = APART ? lds_.S[3 + i] : w[i] + VB;
         }
-        float (*const refs)[MT] = lds_.refs, (*const sums)[MT] = lds_.sums, (*const tops)[MT] = lds_.tops;
+        float (*const refs)[MT] = lds_.refs, (*const sums)[MT] = lds_.sums, (*const psums)[MT] = lds_.psums, (*const tops)[MT] = lds_.tops;
         int *const labs = lds_.labs, *const rows = lds_.rows;
 
         const int tid = threadIdx.x;
@@ -188,7 +188,7 @@ struct NarrowLogits {
             for (int b = 0; b < B; ++b) {
                 const int tl = 32 * JN * wn + 16 * b + tt;
                 const float c = refs[half][tl];
-                float s = 0.0f;
+                float s = 0.0f, sp = 0.0f;
 #pragma unroll
                 for (int i = 0; i < VI; ++i) {
                     const int lab = labs[tl] < 0 ? -1 : labs[tl] - 32 * (VI * wm + i) - 8 * q;
@@ -199,12 +199,17 @@ struct NarrowLogits {
                         e[k] = lab == k || k >= end[i] ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(z[i][b][k], kLog2e, -c));
                         s += e[k];
                     }
-                    if (GRAD) __builtin_amdgcn_raw_buffer_store_b128(
-                        u32x4{pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])}, rP,
-                        (uint32_t)(tl * 128 + (((4 * (VI == 2 ? i : wm) + q) ^ ((tl >> 1) & 7)) * 16)), 0, 0);
+                    if (GRAD) {
+                        const u32x4 p = {pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]), pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7])};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) sp = add_bf16x2(sp, p[k]);
+                        __builtin_amdgcn_raw_buffer_store_b128(
+                            p, rP, (uint32_t)(tl * 128 + (((4 * (VI == 2 ? i : wm) + q) ^ ((tl >> 1) & 7)) * 16)), 0, 0);
+                    }
                 }
-                s = over_lanes<4>(s, [](float a, float b) { return a + b; });
-                sums[wm][tl] = s;                        // the same from all of a token's lanes
+                const auto plus = [](float a, float b) { return a + b; };
+                sums[wm][tl] = over_lanes<4>(s, plus);   // the same from all of a token's lanes
+                if (GRAD) psums[wm][tl] = over_lanes<4>(sp, plus);
             }
             __syncthreads();
         };
@@ -243,6 +248,7 @@ struct NarrowLogits {
                 const int64_t o = (int64_t)tid * g.steps + (int)blockIdx.x * VI + h;
                 g.tref[o] = refs[h][tid];
                 g.tsum[o] = sum[h];
+                if (GRAD) g.tp[o] = VI == 2 ? psums[h][tid] : psums[0][tid] + psums[1][tid];
             }
     }
 };
@@ -356,7 +362,7 @@ __device__ __forceinline__ void narrow_logits_any(const LossNarrow &g) {
     __shared__ __align__(16) uint8_t S3[MT == 256 ? D : C];
     __shared__ __align__(16) uint8_t S4[D];
     __shared__ __align__(16) uint8_t S5[D];
-    __shared__ float refs[2][MT], sums[2][MT], tops[2][MT];
+    __shared__ float refs[2][MT], sums[2][MT], psums[GRAD ? 2 : 1][MT], tops[2][MT];
     __shared__ int labs[MT], rows[MT], waves[4];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -398,7 +404,7 @@ __device__ __forceinline__ void narrow_logits_any(const LossNarrow &g) {
     }
     __syncthreads();
     count = __builtin_amdgcn_readfirstlane(count);
-    const NarrowLds<MT> l{{S0, S1, S2, S3, S4, S5}, refs, sums, tops, labs, rows};
+    const NarrowLds<MT> l{{S0, S1, S2, S3, S4, S5}, refs, sums, psums, tops, labs, rows};
     if constexpr (MT > 128)
         if (count > 128) {
             if (!narrow_pairs(g.steps)) NarrowLogits<256, MT, 3, 1, GRAD>::run(g, l, count);

@@ -35,7 +35,13 @@ __device__ __forceinline__ float over_lanes(float x, Op op) {
     return x;
 }
 
-// A token's last step: dX = b (a sum P W - W[label]), a = 1 / S, rounded once.
+// s + the two bf16 values of v
+__device__ __forceinline__ float add_bf16x2(float s, uint32_t v) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, v), bf16x2{(__bf16)1.0f, (__bf16)1.0f}, s, false);
+}
+
+// A token's last step: dX = b (a sum P W - W[label]), a = 1 / sum P, rounded once.
 struct LossFinal {
     float a, b;
     __device__ __forceinline__ uint2 value(const f32x4 &x, const uint2 &v) const {

@@ -394,3 +394,43 @@ def test_graph_replays_match_eager(M):
         torch.cuda.synchronize()
         for a, b in zip((loss, mean, dX), ref):
             assert same(a, b), rep
+
+
+@pytest.mark.parametrize("M,V,chain", [(1, 1500, 1500), (20, 1500, 1500), (100, 1500, 1500), (200, 1500, 1500),
+                                       (200, 16500, 512), (300, 1500, 1500)])
+def test_what_all_rows_have_in_common_cancels(M, V, chain):
+    """A head whose rows share a part 40 times their own size in some columns, and tokens with one strong entry that is not
+    the label.  With q the softmax without the label, w' = sum q W and 1 - p_y in front of it all, dX = sum q W - W_y.  P and
+    the logits' errors are factors 1 + e on each q, |e| <= H + D, in the sum and in what divides it: that moves sum q W by
+    sum q e (W - w') at most, without the common part.  Sums of at most `chain` terms are off by chain U of the sizes that go
+    in (200 x 16500 x 128: parts of 5 steps of 64, 52 of them), the divisor by (104 + tiles) U."""
+    K = 128
+    X, W, labels = make(M, V, K, seed=51 + M + V, none=0.2 if M > 1 else 0.0)
+    rng = np.random.default_rng(52)
+    W = W.float()
+    W[:, :32] += 2.0
+    W = W.bfloat16()
+    other = rng.integers(0, V, M)
+    w16 = f64(W)
+    own = w16[other].copy()
+    own[:, :32] = 0.0                        # along the row's own part, to a share of about a half
+    lift = (np.log(V) + 0.2 + rng.normal(0, 0.5, (M, 1))) * own / (own ** 2).sum(1, keepdims=True)
+    x = f64(X)
+    x[:, :32] /= 64.0
+    X = bf16(x + lift)
+    _, _, got = check(X, W, labels, torch.ones(M, device=DEV), fwd=False)[0]
+    x, y, tiles = f64(X), labels.cpu().numpy(), -(-V // 256)
+    _, _, ref = oracle.loss(x, w16, y, np.ones(M))
+    D = 2 * (K * U * (np.abs(x) @ np.abs(w16).T).max(1) + 8 * U * (np.abs(x @ w16.T).max(1) + 64)) + (96 + tiles) * U
+    for m in np.flatnonzero(y >= 0):
+        z = w16 @ x[m]
+        q = np.exp(z - np.delete(z, y[m]).max())
+        miss = (q.sum() - q[y[m]]) / q.sum()
+        q[y[m]] = 0.0
+        q /= q.sum()
+        mid = q @ w16
+        size = (H * (1 + 2 * H) + 2 * D[m]) * (q @ np.abs(w16 - mid)) + chain * U * (q @ np.abs(w16)) \
+            + (104 + tiles) * U * np.abs(mid) + 4 * U * np.abs(w16[y[m]])
+        tol = miss * size * (1 + H) + (2 * D[m] + H) * np.abs(ref[m]) + TINY
+        err = np.abs(f64(got[m]) - ref[m])
+        assert (err <= tol).all(), (m, int((err > tol).sum()), float((err / tol).max()))
