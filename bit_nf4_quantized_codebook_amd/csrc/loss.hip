@@ -222,8 +222,9 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
             if (g.grad && !g.last) g.r.a[row] = Sp;
             g.c_out[row] = top > NEG ? top : 0.0f;
             if (g.last) {
-                // ln S + (c - zl) ln 2; a label out of the vocabulary has no logit
-                if (label < 0) zl = __builtin_nanf("");
+                // ln S + (c - zl) ln 2; a label out of the vocabulary has no logit, and one that is not finite gives NaN (as it
+                // stands, d would be infinite: a loss of 0 or infinity)
+                if (label < 0 || !(fabsf(zl) < __builtin_inff())) zl = __builtin_nanf("");
                 const float d = (log2f(S) + (top - zl)) * kLn2;
                 const float loss = fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d)));
                 g.loss[m] = loss;

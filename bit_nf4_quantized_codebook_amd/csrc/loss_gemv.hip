@@ -202,8 +202,10 @@ __global__ __launch_bounds__(256) void loss_gemv_join_kernel(LossGemv g, int nti
             join(pc[w], ps[w]);
         }
     }
-    const float d = (log2f(sum) + (c - g.zl[t])) * kLn2;
-    const float loss = lab < 0 ? 0.0f : (lab < g.V ? fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))) : __builtin_nanf(""));
+    // (a label's logit that is not finite: NaN; d would be infinite)
+    const float zl = g.zl[t];
+    const float d = (log2f(sum) + (c - zl)) * kLn2;
+    const float loss = lab < 0 ? 0.0f : (lab < g.V && fabsf(zl) < __builtin_inff() ? fmaxf(d, 0.0f) + log1pf(expf(-fabsf(d))) : __builtin_nanf(""));
     if (tid == 0) g.loss[t] = loss;
     if (g.M == 1) {
         if (tid == 0) g.mean[0] = loss;

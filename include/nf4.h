@@ -442,8 +442,10 @@ int qlora_norm_bwd(const qlora_norm *p, const void *R_out, const uint16_t *B, co
  *   1 <= M <= 2^20, 1 <= V <= 2^24, K a multiple of 64 up to 16384, X below 2 GiB (W may be larger).
  * The logits are formed in pieces of the vocabulary and never kept; sums are float32 and the mean's float64.
  * A loss keeps its relative accuracy down to tokens that are predicted almost surely (it is computed from the
- * other entries' sum, not as a difference).  Values of X or W that are not finite give NaN to the tokens that
- * meet them and leave the others as they are.
+ * other entries' sum, not as a difference).  Values of X that are not finite give NaN to their token, loss and
+ * dX, and leave the others as they are.  A row of W that is not finite meets every token: where its logit is NaN or
+ * +infinity, or not finite and the label's own, the token's loss and dX are NaN; where it is -infinity its probability
+ * is zero, the loss is that of the other rows, and dX is NaN in the columns where the row is not finite.
  *   workspace: >= qlora_loss_workspace_size(M, V, K, 0) bytes, 16-byte aligned; calls that may overlap need
  *      a workspace each.
  */

@@ -434,3 +434,35 @@ def test_what_all_rows_have_in_common_cancels(M, V, chain):
         tol = miss * size * (1 + H) + (2 * D[m] + H) * np.abs(ref[m]) + TINY
         err = np.abs(f64(got[m]) - ref[m])
         assert (err <= tol).all(), (m, int((err > tol).sum()), float((err / tol).max()))
+
+
+@pytest.mark.parametrize("M", [1, 3, 12, 40, 100, 200, 300])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_weight_rows_that_are_not_finite(value, M):
+    """One value of W: every token meets its row.  A logit that is NaN or +inf, or the label's own if it is not finite, gives
+    NaN; another row's -inf is a probability of zero, which leaves the loss finite and dX NaN in that value's column alone.
+    The finite ones against the oracle: D as at the top, of the other rows, which are as they were."""
+    V, K, row, col = 700, 128, 333, 5
+    X, W, labels = make(M, V, K, seed=61 + M, none=0.2 if M > 20 else 0.0)
+    labels[::3] = row
+    x, y, g = f64(X), labels.cpu().numpy(), torch.ones(M, device=DEV)
+    w = f64(W)
+    D = 2 * (K * U * (np.abs(x) @ np.abs(w).T).max(1) + 8 * U * (np.abs(x @ w.T).max(1) + 64)) + (96 + 3) * U
+    W[row, col] = w[row, col] = value
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, rmean, rdX = oracle.loss(x, w, y, np.ones(M))
+    down = (y >= 0) & (y != row) & (value * x[:, col] == -np.inf)
+    assert (np.isfinite(ref) == (down | (y < 0))).all()
+    loss, mean, dX = nf4.qlora_loss_grad(W, X, labels, g)
+    for each, m in ((loss, mean), nf4.qlora_loss_fwd(W, X, labels)):
+        got = f64(each)
+        assert (np.isnan(got) == np.isnan(ref)).all()
+        ok = np.isfinite(ref)
+        assert (np.abs(got - ref)[ok] <= (D + 8 * U * ref + TINY)[ok]).all()
+        assert np.isnan(float(m)) == np.isnan(rmean)
+    got = f64(dX)
+    assert np.isnan(got[np.isnan(ref)]).all() and not got[y < 0].any()
+    assert np.isnan(got[down, col]).all() and np.isfinite(np.delete(got[down], col, 1)).all()
+    keep = np.arange(K) != col
+    size = 2 * np.abs(w[np.arange(V) != row]).max()          # of |sum q W - W_y|, of which 1 + e on each q moves H + 2 D
+    assert (np.abs(got - rdX)[down][:, keep] <= ((H + 2 * D)[down, None] + V * U) * size + H * np.abs(rdX[down][:, keep])).all()
