@@ -587,13 +587,18 @@ def _scratch(nbytes, dev, workspace):
     return _workspace(nbytes, dev, workspace)
 
 
+def _raw_stream(index):
+    """The device's current stream, its handle alone: torch.cuda.current_stream builds a Python object around it (1.9 us)."""
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(fn, name, dev, *args):
     """fn(*args, stream) on the device's current stream, with that device current."""
     torch = _torch()
     index = dev.index
-    # the stream's handle alone: torch.cuda.current_stream builds a Python object around it (1.9 us)
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    stream = raw(index) if raw else torch.cuda.current_stream(index).cuda_stream
+    stream = _raw_stream(index)
     if torch.cuda.current_device() == index:
         status = fn(*args, stream)
     else:
@@ -893,8 +898,9 @@ def qlora_loss_grad(W, X, labels, dloss=None, loss=None, mean=None, dX=None, wor
 class QLoRAGrads:
     """A list of gradient tensors (bf16 or float32, contiguous, on one device) for qlora_clip_grads, with where the
     scaled ones go: the tensors themselves, or outs, of the same shapes and types, in memory that overlaps no gradient
-    and no other of outs (so a gradient scaled in place is in the list once).  Checked and laid out once (a small table on the device); it keeps the tensors, whose contents may change between
-    calls."""
+    and no other of outs (so a gradient scaled in place is in the list once).  Checked and laid out once (a small table of
+    their addresses on the device); it keeps the tensors, whose contents may change between calls, but not their memory
+    (resize_, set_, an assignment to .data).  A graph that captured a call needs the list for as long as it is replayed."""
 
     def __init__(self, grads, outs=None):
         torch = _torch()
@@ -918,7 +924,7 @@ class QLoRAGrads:
         _check(lib.qlora_grad_table(ctypes.addressof(desc), n, host.ctypes.data, host.nbytes, ctypes.addressof(chunks)),
                "qlora_grad_table")
         # a copy from pageable memory has arrived when it returns: any stream may read the table
-        self._table = torch.from_numpy(host).to(dev)
+        self._table, self._stream = torch.from_numpy(host).to(dev), _raw_stream(dev.index)
         self._chunks = chunks.value
         self._grads, self._outs = grads, outs
 
@@ -938,6 +944,9 @@ def qlora_clip_grads(grads: QLoRAGrads, max_norm: float, norm=None, workspace=No
     """Scales all gradients by max_norm / norm where their global norm exceeds max_norm (a norm that is not finite
     leaves them as they are).  Returns the norm before, float32 [1] on the device."""
     dev = grads._table.device
+    # the table is nobody's but the list's, which may be gone before another stream than the table's has read it
+    if _raw_stream(dev.index) != grads._stream:
+        grads._table.record_stream(_torch().cuda.current_stream(dev))
     norm = _out(norm, _torch().float32, (1,), dev, "norm")
     wsb = lib.qlora_clip_workspace_size()
     ws = _scratch(wsb, dev, workspace)

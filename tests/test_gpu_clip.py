@@ -199,3 +199,30 @@ def test_end_of_a_finetuning_step():
     assert all(g.any() for g in grads)
     norm = check(grads, 1e-3)
     assert norm > 1e-3
+
+
+def test_a_list_may_be_dropped_while_another_stream_still_reads_it():
+    """The table's memory is not given out again before a call on another stream has ended (nothing is written to what is
+    given out here)."""
+    grads = tensors([5000, 70001, 9], "bf", seed=7, std=1.0)
+    outs = [torch.empty_like(g) for g in grads]
+    norm, ref = nf4.qlora_clip_grads(nf4.QLoRAGrads(grads, outs), 1.0), [o.clone() for o in outs]
+    busy = torch.ones((8192, 8192), dtype=torch.bfloat16, device=DEV)
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    lst = nf4.QLoRAGrads(grads, outs)
+    at, size = lst._table.data_ptr(), lst._table.numel()
+    with torch.cuda.stream(s):
+        for _ in range(40):
+            busy = busy @ busy
+        ended = torch.cuda.Event()
+        got = nf4.qlora_clip_grads(lst, 1.0)
+        ended.record()
+    del lst
+    new = [torch.empty(size, dtype=torch.int64, device=DEV) for _ in range(64)]
+    waiting = not ended.query()
+    assert waiting and at not in [t.data_ptr() for t in new]
+    torch.cuda.synchronize()
+    assert same(got, norm) and all(same(a, b) for a, b in zip(outs, ref))

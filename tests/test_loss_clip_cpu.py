@@ -204,3 +204,28 @@ def test_binding_refuses_host_tensors_and_empty_lists():
     for call in (lambda: nf4.QLoRAGrads([]), lambda: nf4.QLoRAGrads([x], [x, x])):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_list_on_another_stream_keeps_its_table(monkeypatch):
+    """qlora_clip_grads tells the allocator of a stream that reads the list's table and is not the table's own."""
+    torch = pytest.importorskip("torch")
+    seen = []
+
+    class Table:
+        device = torch.device("cuda", 0)
+        record_stream = staticmethod(seen.append)
+        data_ptr = staticmethod(lambda: 0x1000)
+
+    lst = nf4.QLoRAGrads.__new__(nf4.QLoRAGrads)
+    lst._table, lst._grads, lst._outs, lst._chunks, lst._stream = Table(), (), (), 0, 11
+    now = [11]
+    monkeypatch.setattr(nf4, "_raw_stream", lambda index: now[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: ("stream", now[0]))
+    monkeypatch.setattr(nf4, "_out", lambda t, dtype, shape, dev, name: torch.empty(shape))
+    monkeypatch.setattr(nf4, "_scratch", lambda n, dev, ws: torch.empty(n, dtype=torch.uint8))
+    calls = []
+    monkeypatch.setattr(nf4, "_launch", lambda fn, name, dev, *a: calls.append(len(seen)))
+    nf4.qlora_clip_grads(lst, 1.0)
+    now[0] = 12
+    nf4.qlora_clip_grads(lst, 1.0)
+    assert seen == [("stream", 12)] and calls == [0, 1]
