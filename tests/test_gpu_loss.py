@@ -466,3 +466,111 @@ def test_weight_rows_that_are_not_finite(value, M):
     keep = np.arange(K) != col
     size = 2 * np.abs(w[np.arange(V) != row]).max()          # of |sum q W - W_y|, of which 1 + e on each q moves H + 2 D
     assert (np.abs(got - rdX)[down][:, keep] <= ((H + 2 * D)[down, None] + V * U) * size + H * np.abs(rdX[down][:, keep])).all()
+
+
+def check_sampled(X, W, labels, dloss, rows):
+    """check() for large W: the definition in float64 on the device, 4096 vocabulary rows at a time, at `rows` (with a label)."""
+    M, K = X.shape
+    V = W.shape[0]
+    at = torch.as_tensor(rows, device=DEV)
+    x, y, g = X[at].double(), labels[at], dloss[at].double()
+    assert (y >= 0).all()
+    blocks = [slice(i, min(i + 4096, V)) for i in range(0, V, 4096)]
+
+    def dots(a, f):
+        return torch.cat([a @ f(W[b].double()).t().contiguous() for b in blocks], 1)
+
+    z = dots(x, lambda w: w)
+    Ez = K * U * dots(x.abs(), torch.abs).max(1).values
+    D = (2 * (Ez + 8 * U * (z.abs().max(1).values + 64)) + (96 + -(-V // 256)) * U)[:, None]
+    rest = z - z.gather(1, y[:, None])
+    rest.scatter_(1, y[:, None], -float("inf"))
+    d = torch.logsumexp(rest, 1, keepdim=True)
+    ref = torch.clamp(d, min=0) + torch.log1p(torch.exp(-d.abs()))
+    p, miss, wy = torch.exp(rest - ref), torch.sigmoid(d), W[y].double()
+    pw, size = torch.zeros_like(wy), torch.zeros_like(wy)
+    for b in blocks:
+        w = W[b].double()
+        pw += p[:, b].contiguous() @ w
+        size += p[:, b].contiguous() @ w.abs()
+    dX = g[:, None] * (pw - miss * wy)
+    tol = miss * D + 8 * U * ref + TINY
+    tolx = g[:, None].abs() * (size * (H + 2 * D + V * U) + miss * 2 * D * wy.abs()) * (1 + H) + H * dX.abs() \
+        + TINY * (1 + 2 * float(W.abs().max()))
+    out = nf4.qlora_loss_fwd(W, X, labels), nf4.qlora_loss_grad(W, X, labels, dloss)
+    for o in out:
+        err = (o[0][at].double() - ref[:, 0]).abs() / tol[:, 0]
+        assert (err <= 1).all(), float(err.max())
+        each = o[0].double()
+        assert not o[0][labels < 0].any() and abs(float(o[1]) - float(each.sum() / (labels >= 0).sum())) <= 2 * U * abs(float(o[1]))
+    err = (out[1][2][at].double() - dX).abs() / tolx
+    assert (err <= 1).all(), (float(err.max()), torch.nonzero(~(err <= 1))[:4].tolist())
+    assert not out[1][2][labels < 0].any()
+
+
+def some(labels, n, seed=0):
+    """n of the tokens with a label, the first and the last among them."""
+    live = torch.nonzero(labels >= 0)[:, 0].cpu().numpy()
+    return np.unique(np.concatenate([live[[0, -1]], np.random.default_rng(seed).choice(live, min(n, len(live)), replace=False)]))
+
+
+def in_pieces(M, V, K, grad):
+    """The vocabulary is not taken in one piece: twice as many rows need no more workspace."""
+    assert nf4.qlora_loss_workspace_size(M, V, K, grad) == nf4.qlora_loss_workspace_size(M, 2 * V, K, grad)
+
+
+@pytest.mark.parametrize("M,V,K,none", [(300, 69888, 256, 0.0), (700, 8000, 8192, 0.0), (1200, 8000, 8192, 0.45),
+                                        (1700, 14000, 4096, 0.0)])
+def test_tails_of_parts_in_runs(M, V, K, none):
+    """Tiles of dX beyond whole rounds whose parts leave tails, shared by runs of the workgroups left over: a run inside a tile
+    (2 tiles), and runs that begin in one tile and end in another (96 and 112)."""
+    X, W, labels = make(M, V, K, seed=71, none=none, lift=9.0)
+    print(f"runs: M={M} V={V} K={K}", flush=True)
+    check_sampled(X, W, labels, torch.rand(M, device=DEV) + 0.1, some(labels, 60))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("M,none", [(8192, 0.0), (8300, 0.0), (9000, 0.08)])
+def test_pieces_added_by_the_product(M, none, order):
+    """Pieces of the vocabulary with 256 tiles of dX and more, whose sums the product itself adds to what the piece before
+    left; the largest logits move from piece to piece, and the row's reference with them."""
+    V, K = 33000, 2048
+    in_pieces(M, V, K, True)
+    X, W, labels = make(M, V, K, seed=72, none=none, lift=8.0)
+    W[:, 0] = (torch.arange(V, device=DEV) // 8192 * 9.0 * order).bfloat16()
+    X[:, 0] = torch.linspace(-8, 8, M, device=DEV).bfloat16()
+    print(f"pieces: M={M} V={V} K={K} order={order}", flush=True)
+    check_sampled(X, W, labels, torch.rand(M, device=DEV) + 0.1, some(labels, 60))
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_forward_in_pieces(order):
+    """65537 tokens: the forward's tables hold 63 tiles of 256 vocabulary rows, and there are 65."""
+    M, V, K = 65537, 16400, 64
+    in_pieces(M, V, K, False)
+    X, W, labels = make(64, V, K, seed=73, lift=8.0)
+    W[:, 0] = (torch.arange(V, device=DEV) // 4100 * 9.0 * order).bfloat16()
+    X = X[torch.arange(M, device=DEV) % 64].contiguous()
+    X[:, 0] = torch.linspace(-8, 8, M, device=DEV).bfloat16()
+    labels = labels[torch.arange(M, device=DEV) % 64].contiguous()
+    labels[::7] = NONE
+    print(f"forward pieces: M={M} V={V} K={K} order={order}", flush=True)
+    check_sampled(X, W, labels, torch.rand(M, device=DEV) + 0.1, some(labels, 100))
+
+
+@pytest.mark.parametrize("M", [8, 100])
+def test_few_tokens_where_the_weight_exceeds_2_gib(M):
+    """The gradient then takes W in two pieces, and with them the large tiles; up to 8 tokens the sums' one workgroup writes
+    the mean."""
+    V, K = 65700, 16384
+    in_pieces(M, V, K, True)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(74)
+    W = torch.randn((V, K), generator=g, device=DEV, dtype=torch.bfloat16).mul_(0.02)
+    W[:, 0] = (torch.arange(V, device=DEV) // 65280 * 6.0).bfloat16()
+    X = torch.randn((M, K), generator=g, device=DEV, dtype=torch.bfloat16)
+    X[:, 0] = torch.linspace(-3, 3, M, device=DEV).bfloat16()
+    labels = torch.randint(0, V, (M,), generator=g, device=DEV)
+    labels[0], labels[1], labels[2] = V - 1, 65279, NONE
+    print(f"W of 2 GiB: M={M} V={V} K={K}", flush=True)
+    check_sampled(X, W, labels, torch.rand(M, device=DEV) + 0.1, some(labels, 60))
