@@ -34,7 +34,7 @@ struct LossRows {
 
 // Tiles of rows and columns, numbered along the columns within groups of four tiles of rows (an XCD's concurrent
 // tiles then share both operands in its L2).
-__device__ __forceinline__ void loss_place(int ntm, int ntn, int t, int &tm, int &tn) {
+__host__ __device__ __forceinline__ void loss_place(int ntm, int ntn, int t, int &tm, int &tn) {
     const int grp = t / (4 * ntn), first = 4 * grp, size = ntm - first < 4 ? ntm - first : 4, in = t - 4 * grp * ntn;
     tm = first + in % size;
     tn = in / size;
@@ -68,16 +68,16 @@ struct LossShares {
         extra = over;
         tail = steps - ks * len;
     }
-    __device__ __forceinline__ bool partial() const { return ks > 1 || extra; }
+    __host__ __device__ __forceinline__ bool partial() const { return ks > 1 || extra; }
     // runs of the tails, in steps of all tails
-    __device__ __forceinline__ int64_t begin(int e) const { return (int64_t)rest * tail * e / extra; }
-    __device__ __forceinline__ int run_of(int64_t u) const {
+    __host__ __device__ __forceinline__ int64_t begin(int e) const { return (int64_t)rest * tail * e / extra; }
+    __host__ __device__ __forceinline__ int run_of(int64_t u) const {
         const int64_t all = (int64_t)rest * tail;
         return (int)(((u + 1) * extra + all - 1) / all) - 1;
     }
     // partials: part j of tile x; a run's part in the tile that it begins in; a tile whose tail begins inside a run
-    __device__ __forceinline__ int slot_part(int j, int x) const { return j * rest + x; }
-    __device__ __forceinline__ int slot_run(int e, int x) const {
+    __host__ __device__ __forceinline__ int slot_part(int j, int x) const { return j * rest + x; }
+    __host__ __device__ __forceinline__ int slot_run(int e, int x) const {
         return ks * rest + (begin(e) >= (int64_t)x * tail ? e : extra + x);
     }
 };
