@@ -1409,7 +1409,8 @@ constexpr size_t kLossTableBytes = (size_t)64 << 20;     // the forward's piece:
 constexpr int64_t kLossMinTiles = 32;
 
 struct LossPlan {
-    bool narrow;                       // few tokens, with the gradient
+    bool narrow;                       // narrow tiles: few tokens (forward, from 17)
+    nf4k::LossNarrowPlan tiles64;      // their numbers
     bool gemv;                         // few tokens, forward: its table lies at off_tref
     int32_t Mp, tiles, piece;          // rows padded to tiles; tiles of the vocabulary, and of a piece
     size_t off_count, off_sums, off_row, off_label, off_zl, off_S, off_a, off_b, off_c[2], off_tref, off_tsum, off_tp, off_P, off_part,
@@ -1452,11 +1453,11 @@ LossPlan make_loss_plan(int64_t M, int64_t V, int64_t K, bool grad) {
         return p;
     }
     if (p.narrow) {
-        const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
+        const nf4k::LossNarrowPlan &n = p.tiles64 = nf4k::loss_narrow_plan(M, V, K);
         p.off_tref = take((size_t)n.steps * M * 4);
         p.off_tsum = take((size_t)n.steps * M * 4);
         p.off_tp = take(grad ? (size_t)n.steps * M * 4 : 0);
-        p.off_P = take(grad ? (size_t)n.steps * nf4k::LBLOCK * 2 : 0);
+        p.off_P = take(grad ? (size_t)n.steps * n.MT * nf4k::LSTEP * 2 : 0);
         p.off_part = take(grad ? n.parts * 4 : 0);
         p.total = off;
         return p;
@@ -1522,10 +1523,9 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
     }
     float *part = ws_at<float>(workspace, p.off_part);
     if (p.narrow) {
-        const nf4k::LossNarrowPlan n = nf4k::loss_narrow_plan(M, V, K);
-        const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.Mp, n.steps, n.per, tref, tsum, tp, P, part, loss, mean, dX};
+        const nf4k::LossNarrow a{W, X, V, K, M, labels, r, p.tiles64, tref, tsum, tp, P, part, loss, mean, dX};
         NF4_CHECK_HIP(nf4k::launch_loss_narrow_logits(a, s), "loss logits of few tokens");
-        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, tp, n.steps, nullptr, c[0], P, true, grad,
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, tp, p.tiles64.steps, nullptr, c[0], P, p.tiles64.MT, true, grad,
                                                             dloss, loss, mean, !grad}, true, s), "loss sums");
         if (grad) NF4_CHECK_HIP(nf4k::launch_loss_narrow_dx(a, s), "loss dX of few tokens");
         return NF4_OK;
@@ -1539,7 +1539,7 @@ int run_loss(const uint16_t *W, int64_t V, const uint16_t *X, const int64_t *lab
         float *now = c[piece % 2];
         NF4_CHECK_HIP(nf4k::launch_loss_logits(nf4k::LogitsArgs{W, X, V, K, r, p.Mp, t0, nt, before, tref, tsum, tp, P, 4 * nt}, s),
                       "loss logits");
-        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, tp, nt, before, now, P, last, grad, dloss, loss,
+        NF4_CHECK_HIP(nf4k::launch_loss_join(nf4k::LossJoin{r, M, p.Mp, tref, tsum, tp, nt, before, now, P, nf4k::LT, last, grad, dloss, loss,
                                                             mean, false}, false, s), "loss sums");
         // one workgroup of the join writes the mean itself
         float *mean_after = last && M > nf4k::kLossJoinRows ? mean : nullptr;

@@ -150,6 +150,7 @@ struct LossJoin {
     const float *c_in;
     float *c_out;
     uint16_t *P;              // or NULL: the forward
+    int32_t prows;            // rows of one of P's blocks
     // the last join: losses, the sums for their mean, and with grad the coefficients of dX
     bool last, grad;
     const float *dloss;
@@ -181,7 +182,9 @@ __device__ __forceinline__ void loss_write_mean(const double *sums, int n, int c
 // 60 labelled 120 and 156; 8000 x 4096 85 and 107; 160 x 4000 x 1024 42 and 59.  Above: 50001 x 4096 304 and 264).
 constexpr int64_t kLossNarrowMaxM = 128, kLossNarrowMaxM2 = 256, kLossNarrowMaxTiles = 128;
 struct LossNarrowPlan {
-    int32_t MT, steps, per, splits;
+    int32_t MT;               // tokens there may be: 64, 128 or 256
+    int32_t steps, per;       // steps of 64 vocabulary rows: all, and of dX's workgroup
+    int32_t splits;           // dX's workgroups along the vocabulary
     size_t parts;             // float32 partials
 };
 LossNarrowPlan loss_narrow_plan(int64_t M, int64_t V, int64_t K);
@@ -190,9 +193,9 @@ struct LossNarrow {
     int64_t V, K, M;
     const int64_t *labels;
     LossRows r;
-    int32_t Mp, steps, per;   // steps of 64 vocabulary rows: all, and of dX's workgroup
+    LossNarrowPlan n;
     float *tref, *tsum, *tp;  // [M][steps]; tp: as in LogitsArgs
-    uint16_t *P;              // [steps] blocks; NULL: the forward
+    uint16_t *P;              // [steps] blocks of MT rows; NULL: the forward
     float *part;
     float *loss, *mean;
     uint16_t *dX;

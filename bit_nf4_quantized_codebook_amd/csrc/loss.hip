@@ -197,7 +197,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(LossJoin g) {
             const float f = __builtin_amdgcn_exp2f(from - top);
             for (int b = b0; b < b1; ++b) {
                 const int64_t block = ((int64_t)(row / LT) * g.ntile + tile) * BLOCKS + b;
-                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + block * LBLOCK + (row % LT) * LSTEP);
+                u32x4 *p = reinterpret_cast<u32x4 *>(g.P + (block * g.prows + row % LT) * LSTEP);
                 for (int i = 0; i < 8; ++i) {
                     u32x4 v = p[i];
 #pragma unroll

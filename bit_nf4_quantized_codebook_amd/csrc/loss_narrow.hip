@@ -7,7 +7,7 @@
 //   4. their sum, dX, and the mean.
 // A launch is made for the M tokens there may be (MT = 64, 128 or 256: its LDS and its grid), a tile for those that are
 // live (TT): 60 labelled of 200 cost what 60 do.
-// The layouts of p, of the LDS stages and of the fragments are those of loss_logits.hip and loss_dx.hip.
+// The layouts of p (in blocks of MT tokens), of the LDS stages and of the fragments are those of loss_logits.hip and loss_dx.hip.
 //
 // Bound by HBM: forward 37 x 50001 x 4096 101 us a call (logits 90: 4.5 TB/s), 100 x 32000 x 4096 71 (90 on tiles of 256),
 // 200 88 (101); with the gradient, which reads the weight twice, 16, 64, 100 and 200 x 32000 x 4096 108, 120, 131 and 183
@@ -181,8 +181,8 @@ struct NarrowLogits {
                 tops[wm][32 * JN * wn + 16 * b + tt] = x;
             }
         };
-        const __amdgpu_buffer_rsrc_t rP = make_rsrc(GRAD && block < g.steps ? g.P + (int64_t)block * LBLOCK : nullptr,
-                                                    GRAD && block < g.steps ? LBLOCK * 2 : 0);
+        const __amdgpu_buffer_rsrc_t rP = make_rsrc(GRAD && block < g.n.steps ? g.P + (int64_t)block * (MT * LSTEP) : nullptr,
+                                                    GRAD && block < g.n.steps ? MT * LSTEP * 2 : 0);
         auto groups = [&]() {
 #pragma unroll
             for (int b = 0; b < B; ++b) {
@@ -225,7 +225,7 @@ struct NarrowLogits {
         collect();
 #pragma unroll
         for (int h = 0; h < VI; ++h) {
-            ok[h] = t >= count || (int)blockIdx.x * VI + h >= g.steps ||
+            ok[h] = t >= count || (int)blockIdx.x * VI + h >= g.n.steps ||
                     (sum[h] <= __builtin_ldexpf(1.0f, kLossSlack) && sum[h] >= __builtin_ldexpf(1.0f, -kLossSlack));
             all &= ok[h];
         }
@@ -244,8 +244,8 @@ struct NarrowLogits {
         if (tid < count)
 #pragma unroll
             for (int h = 0; h < VI; ++h) {
-                if ((int)blockIdx.x * VI + h >= g.steps) break;
-                const int64_t o = (int64_t)tid * g.steps + (int)blockIdx.x * VI + h;
+                if ((int)blockIdx.x * VI + h >= g.n.steps) break;
+                const int64_t o = (int64_t)tid * g.n.steps + (int)blockIdx.x * VI + h;
                 g.tref[o] = refs[h][tid];
                 g.tsum[o] = sum[h];
                 if (GRAD) g.tp[o] = VI == 2 ? psums[h][tid] : psums[0][tid] + psums[1][tid];
@@ -260,16 +260,17 @@ struct NarrowDx {
         constexpr int WB = LSTEP * 128 * 2;              // bytes of W in a stage, before P's
         constexpr int JN = TT / 32;
         constexpr int QP = TT / 32;                      // a wave's loads of P a step (of W: 4)
+        constexpr int PB = MT * LSTEP * 2;               // bytes of one of P's blocks
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         const int r32 = lane & 31, hh = lane >> 5;
         const int ntn = (int)((g.K + 127) / 128);
         const int split = (int)blockIdx.x / ntn, tn = (int)blockIdx.x % ntn;
-        const int kb = split * g.per, steps = min(g.steps - kb, g.per);
+        const int kb = split * g.n.per, steps = min(g.n.steps - kb, g.n.per);
         const int64_t n0 = (int64_t)tn * 128, v0 = (int64_t)kb * LSTEP;
 
         const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.W + v0 * g.K, (g.V - v0) * g.K * 2);
-        const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.P + (int64_t)kb * LBLOCK, (int64_t)steps * LBLOCK * 2);
+        const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.P + (int64_t)kb * (PB / 2), (int64_t)steps * PB);
         const __amdgpu_buffer_rsrc_t none = make_rsrc(g.W, 0);
         // W: instruction q of wave w writes stage rows 4u .. 4u+3 (u = 4w + q) of 256 bytes; lane l takes row 4u + l/16 and
         // physical 16-byte chunk l%16, whose granule (l%16)/4 holds logical granule ((l%16)/4) ^ (row%4)
@@ -290,7 +291,7 @@ struct NarrowDx {
 #pragma unroll
             for (int q = 0; q < QP; ++q)
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(past ? none : rB, (lds_void *)(db + q * 1024), 16, boff[q],
-                                                         step * (int)(LBLOCK * 2), 0, 0);
+                                                         step * PB, 0, 0);
         };
         f32x16 acc[JN];
 #pragma unroll
@@ -386,7 +387,7 @@ __device__ __forceinline__ void narrow_logits_any(const LossNarrow &g) {
     if (lab64 >= 0) {
         const uint32_t lo = (uint32_t)live, hi = (uint32_t)(live >> 32);
         const int at = before + (int)__builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0u));
-        const int size = MT == 256 && count > 128 && narrow_pairs(g.steps) ? 128 : 64;
+        const int size = MT == 256 && count > 128 && narrow_pairs(g.n.steps) ? 128 : 64;
         const int64_t in = lab64 - (int64_t)blockIdx.x * size;
         rows[at] = tid;
         labs[at] = in >= 0 && in < size && lab64 < g.V ? (int)in : -1;
@@ -407,8 +408,8 @@ __device__ __forceinline__ void narrow_logits_any(const LossNarrow &g) {
     const NarrowLds<MT> l{{S0, S1, S2, S3, S4, S5}, refs, sums, psums, tops, labs, rows};
     if constexpr (MT > 128)
         if (count > 128) {
-            if (!narrow_pairs(g.steps)) NarrowLogits<256, MT, 3, 1, GRAD>::run(g, l, count);
-            else if (2 * (int)blockIdx.x < g.steps) NarrowLogits<256, MT, 3, 2, GRAD>::run(g, l, count);
+            if (!narrow_pairs(g.n.steps)) NarrowLogits<256, MT, 3, 1, GRAD>::run(g, l, count);
+            else if (2 * (int)blockIdx.x < g.n.steps) NarrowLogits<256, MT, 3, 2, GRAD>::run(g, l, count);
             return;
         }
     if constexpr (MT > 64)
@@ -443,7 +444,7 @@ __global__ __launch_bounds__(256, MT == 64 ? 2 : 1) void loss_narrow_dx_kernel(L
 
 // dX of the live rows from the partials, zero for the others (a workgroup for each token and 1024 columns), and by the last
 // workgroup the mean
-__global__ __launch_bounds__(256) void loss_narrow_fold_kernel(LossNarrow g, int MT) {
+__global__ __launch_bounds__(256) void loss_narrow_fold_kernel(LossNarrow g) {
     const int count = g.r.count[0];
     if (blockIdx.x == gridDim.x - 1) {
         loss_write_mean(g.r.sums, (int)((g.M + kLossJoinRowsNarrow - 1) / kLossJoinRowsNarrow), count, g.mean);
@@ -465,7 +466,7 @@ __global__ __launch_bounds__(256) void loss_narrow_fold_kernel(LossNarrow g, int
         *reinterpret_cast<uint2 *>(g.dX + (int64_t)t * g.K + k) = uint2{0, 0};
         return;
     }
-    const int ntn = (int)((g.K + 127) / 128), splits = (g.steps + g.per - 1) / g.per;
+    const int ntn = (int)((g.K + 127) / 128), MT = g.n.MT, splits = g.n.splits;
     const float *p = g.part + ((k / 128) * MT + m) * 128 + k % 128;
     const int64_t stride = (int64_t)ntn * MT * 128;
     const int32_t lab = g.r.label[m];
@@ -504,9 +505,9 @@ LossNarrowPlan loss_narrow_plan(int64_t M, int64_t V, int64_t K) {
 namespace {
 template <bool GRAD>
 void narrow_logits_of(const LossNarrow &g, hipStream_t stream) {
-    const dim3 grid((uint32_t)g.steps), block(256);
-    if (g.M <= 64) hipLaunchKernelGGL((loss_narrow_logits_kernel<64, GRAD>), grid, block, 0, stream, g);
-    else if (g.M <= 128) hipLaunchKernelGGL((loss_narrow_logits_kernel<128, GRAD>), grid, block, 0, stream, g);
+    const dim3 grid((uint32_t)g.n.steps), block(256);
+    if (g.n.MT == 64) hipLaunchKernelGGL((loss_narrow_logits_kernel<64, GRAD>), grid, block, 0, stream, g);
+    else if (g.n.MT == 128) hipLaunchKernelGGL((loss_narrow_logits_kernel<128, GRAD>), grid, block, 0, stream, g);
     else hipLaunchKernelGGL((loss_narrow_logits_kernel<256, GRAD>), grid, block, 0, stream, g);
 }
 }  // namespace
@@ -518,14 +519,13 @@ hipError_t launch_loss_narrow_logits(const LossNarrow &g, hipStream_t stream) {
 }
 
 hipError_t launch_loss_narrow_dx(const LossNarrow &g, hipStream_t stream) {
-    const int ntn = (int)((g.K + 127) / 128), splits = (g.steps + g.per - 1) / g.per, MT = g.M <= 64 ? 64 : g.M <= 128 ? 128 : 256;
-    const dim3 grid((uint32_t)(splits * ntn)), block(256);
-    if (MT == 64) hipLaunchKernelGGL(loss_narrow_dx_kernel<64>, grid, block, 0, stream, g);
-    else if (MT == 128) hipLaunchKernelGGL(loss_narrow_dx_kernel<128>, grid, block, 0, stream, g);
+    const dim3 grid((uint32_t)(g.n.splits * ((g.K + 127) / 128))), block(256);
+    if (g.n.MT == 64) hipLaunchKernelGGL(loss_narrow_dx_kernel<64>, grid, block, 0, stream, g);
+    else if (g.n.MT == 128) hipLaunchKernelGGL(loss_narrow_dx_kernel<128>, grid, block, 0, stream, g);
     else hipLaunchKernelGGL(loss_narrow_dx_kernel<256>, grid, block, 0, stream, g);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(loss_narrow_fold_kernel, dim3((uint32_t)(g.M * ((g.K + 1023) / 1024) + 1)), dim3(256), 0, stream, g, MT);
+    hipLaunchKernelGGL(loss_narrow_fold_kernel, dim3((uint32_t)(g.M * ((g.K + 1023) / 1024) + 1)), dim3(256), 0, stream, g);
     return hipGetLastError();
 }
 

@@ -229,3 +229,11 @@ def test_a_list_on_another_stream_keeps_its_table(monkeypatch):
     now[0] = 12
     nf4.qlora_clip_grads(lst, 1.0)
     assert seen == [("stream", 12)] and calls == [0, 1]
+
+
+@pytest.mark.parametrize("M,MT", [(1, 64), (8, 64), (64, 64), (65, 128), (100, 128), (128, 128)])
+def test_loss_workspace_of_few_tokens(M, MT):
+    """A step of 64 vocabulary rows takes P for the 64 or 128 tokens of a tile, not 256, and three float32 a token; beside
+    them stand dX's partials, which the vocabulary's length does not change from here on."""
+    size, V, more, K = lib.qlora_loss_workspace_size, 64 * 512 * 8, 64 * 512, 64
+    assert size(M, V + more, K, 1) - size(M, V, K, 1) <= 512 * (MT * 64 * 2 + 12 * M) + 4 * 256
