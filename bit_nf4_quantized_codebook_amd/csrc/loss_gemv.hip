@@ -13,6 +13,7 @@
 #include "common.h"
 #include "dqtile.h"
 #include "loss.h"
+#include "loss_tile.h"
 
 namespace nf4k {
 
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(NW * 64) void loss_gemv_kernel(LossGemv g) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const int64_t n = n0 + 16 * a + 4 * lg + v;
-            s += n < g.V && n != lab ? __builtin_amdgcn_exp2f(__builtin_fmaf(z[a][v], kLog2e, -top)) : 0.0f;
+            s += n < g.V && n != lab ? __builtin_amdgcn_exp2f(loss_above(z[a][v], top, true)) : 0.0f;
         }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);

@@ -186,7 +186,7 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
         const bool ragged = left < WV;
         const __amdgpu_buffer_rsrc_t rP = make_rsrc(
             GRAD ? g.P + ((int64_t)cur.tm * g.psteps + cur.p0 + wm * (IA / 2)) * LBLOCK : nullptr, GRAD ? LBLOCK * IA : 0);
-        auto group = [&](auto jc) {
+        auto group = [&](auto jc, auto far) {
             turn(jc);
             // B iterations' reads at a time: a wave is alone on its SIMD, nothing else hides their latency
             constexpr int B = 4;
@@ -227,7 +227,7 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
 #pragma unroll
                 for (int b = 0; b < B; ++b) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[b][k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b][k], kLog2e, -c[b]));
+                    for (int k = 0; k < 8; ++k) x[b][k] = __builtin_amdgcn_exp2f(loss_above(x[b][k], c[b], decltype(far)::value));
                     const float *e = x[b];
                     s[b] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
                     if (GRAD) {
@@ -253,20 +253,20 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
                 }
             }
         };
-        auto groups = [&]() {
-            group(std::integral_constant<int, 0>{});
-            group(std::integral_constant<int, 1>{});
-            group(std::integral_constant<int, 2>{});
-            group(std::integral_constant<int, 3>{});
+        auto groups = [&](auto far) {
+            group(std::integral_constant<int, 0>{}, far);
+            group(std::integral_constant<int, 1>{}, far);
+            group(std::integral_constant<int, 2>{}, far);
+            group(std::integral_constant<int, 3>{}, far);
             __syncthreads();
         };
-        groups();
+        groups(std::false_type{});
         float sum = st.sums[0][tid] + st.sums[1][tid];
         // Is every token's sum where it should be?  Above 2^kLossSlack a logit lies too far above the reference; below
         // 2^-kLossSlack all lie too far below it, or there are none but the label (a reference of an earlier piece may lie
-        // above all of this tile); NaN fails too.
+        // above all of this tile, but needs the other pass from kLossFar on); NaN fails too.
         const bool ok = m0 + tid >= count || (sum <= __builtin_ldexpf(1.0f, kLossSlack) &&
-                                              (g.ref || sum >= __builtin_ldexpf(1.0f, -kLossSlack)));
+                                              (g.ref ? fabsf(st.refs[tid]) < kLossFar : sum >= __builtin_ldexpf(1.0f, -kLossSlack)));
         if (!__syncthreads_and(ok)) {
             // the tile once more, those tokens against their largest logit but the label's (which may lie so far above the others
             // that float32 would hold nothing of them beside it)
@@ -292,7 +292,7 @@ __device__ __forceinline__ void logits_tiles(const LogitsArgs &g, const LossStag
             const float most = fmaxf(st.tops[0][tid], st.tops[1][tid]);
             if (!ok && most > -__builtin_inff()) st.refs[tid] = ceilf(most * kLog2e);
             __syncthreads();
-            groups();
+            groups(std::true_type{});
             sum = st.sums[0][tid] + st.sums[1][tid];
         }
         if (m0 + tid < count) {

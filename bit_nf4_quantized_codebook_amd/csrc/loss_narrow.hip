@@ -183,7 +183,7 @@ struct NarrowLogits {
         };
         const __amdgpu_buffer_rsrc_t rP = make_rsrc(GRAD && block < g.n.steps ? g.P + (int64_t)block * (MT * LSTEP) : nullptr,
                                                     GRAD && block < g.n.steps ? MT * LSTEP * 2 : 0);
-        auto groups = [&]() {
+        auto groups = [&](auto far) {
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 const int tl = 32 * JN * wn + 16 * b + tt;
@@ -196,7 +196,7 @@ struct NarrowLogits {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         if (lab == k) g.r.zl[tl] = z[i][b][k] * kLog2e;
-                        e[k] = lab == k || k >= end[i] ? 0.0f : __builtin_amdgcn_exp2f(__builtin_fmaf(z[i][b][k], kLog2e, -c));
+                        e[k] = lab == k || k >= end[i] ? 0.0f : __builtin_amdgcn_exp2f(loss_above(z[i][b][k], c, decltype(far)::value));
                         s += e[k];
                     }
                     if (GRAD) {
@@ -213,7 +213,7 @@ struct NarrowLogits {
             }
             __syncthreads();
         };
-        groups();
+        groups(std::false_type{});
         // thread: a token's one or two blocks
         const int t = tid < TT ? tid : 0;
         float sum[VI];
@@ -238,7 +238,7 @@ struct NarrowLogits {
                 if (tid < TT && !ok[h] && most > -__builtin_inff()) refs[h][t] = ceilf(most * kLog2e);
             }
             __syncthreads();
-            groups();
+            groups(std::true_type{});
             collect();
         }
         if (tid < count)

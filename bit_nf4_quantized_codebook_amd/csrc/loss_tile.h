@@ -22,6 +22,17 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 // was slower.)
 constexpr int kLossSlack = 48;
 
+// l - c for a logit z: one fma, which keeps the product l = z log2(e) whole.  c is such a product rounded to float32: from
+// |c| = 2^28 on that moves it by 16 and more, and soon by more than 2^x takes (2^32: 256).  There the product is rounded as c was,
+// so that the largest logit stands within 1 of its reference again.  A tile's first pass, against references below that, needs
+// no such choice (far false).
+constexpr float kLossFar = 0x1p28f;
+__device__ __forceinline__ float loss_above(float z, float c, bool far) {
+#pragma clang fp contract(off)
+    const float l = z * kLog2e;
+    return far && !(fabsf(c) < kLossFar) ? l - c : __builtin_fmaf(z, kLog2e, -c);
+}
+
 // the sum or maximum over groups of N lanes (4, 8 or 16), in all of them
 template <int N, class Op>
 __device__ __forceinline__ float over_lanes(float x, Op op) {

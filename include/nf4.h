@@ -457,9 +457,10 @@ int qlora_loss_fwd(const uint16_t *W, int64_t V, const uint16_t *X, const int64_
  * The same with the gradient for X, in one pass over the vocabulary:
  *   dX[m] = dloss[m] sum_v (softmax(z[m])_v - [v == labels[m]]) W[v]
  *   dloss: float32 [M], the gradient of each token's loss, or NULL: of the mean (1 / tokens with a label).
- *   dX: [M, K] bf16, rounded once; zero for a token without a label, whatever its X.  Probabilities enter
- *      their product with W in bf16, divided by the sum of what enters (the label's own in float32).  dX must not overlap X or W
- *      (NF4_ERR_ARG).
+ *   dX: [M, K] bf16, rounded once; zero for a token without a label, whatever its X. 
+ *      Probabilities enter their product with W in bf16, divided by the sum of what enters (the label's own in
+ *      float32).  That product is summed in float32 before the division, by sums between 2^-48 and 2^64: W's largest
+ *      values should lie between 2^-64 and 2^64.  dX must not overlap X or W (NF4_ERR_ARG).
  *   loss and mean as qlora_loss_fwd's, up to the rounding of float32.
  *   workspace: >= qlora_loss_workspace_size(M, V, K, 1) bytes.
  */

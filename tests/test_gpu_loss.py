@@ -574,3 +574,40 @@ def test_few_tokens_where_the_weight_exceeds_2_gib(M):
     labels[0], labels[1], labels[2] = V - 1, 65279, NONE
     print(f"W of 2 GiB: M={M} V={V} K={K}", flush=True)
     check_sampled(X, W, labels, torch.rand(M, device=DEV) + 0.1, some(labels, 60))
+
+
+def far_logits(M, V, K, seed, size):
+    """Logits of about 8 `size`; returns also float64 logits, and D's logit part: how far off one may be (natural units)."""
+    X, W, labels = make(M, V, K, seed=seed, none=0.2 if M > 4 else 0.0)
+    X, W = (X.float() * size).bfloat16(), (W.float() * 20.0).bfloat16()
+    x, w = X.double(), W.double().t().contiguous()
+    z = x @ w
+    off = K * U * (x.abs() @ w.abs()).max(1).values + 8 * U * (z.abs().max(1).values + 64)
+    return X, W, labels, z, off
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 700, 64), (3, 20, 64), (12, 700, 64), (40, 700, 128), (100, 700, 64), (200, 700, 64), (200, 17000, 64),
+                                   (300, 700, 64), (32768, 20001, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 20, 1e9, 1e14, 1e30])
+def test_logits_beyond_what_a_reference_resolves(M, V, K, size):
+    """Logits so large that neighbouring float32 values are hundreds apart and more: a token's softmax then is its largest
+    logit alone, wherever that exceeds the next by far more than the logits' own error (their error E, twice and 100 more)."""
+    X, W, labels, z, off = far_logits(M, V, K, 81 + M + V, size)
+    g = torch.ones(M, device=DEV)
+    out = nf4.qlora_loss_fwd(W, X, labels), nf4.qlora_loss_grad(W, X, labels, g)
+    y = labels.clamp(min=0)
+    zl = z.gather(1, y[:, None])[:, 0]
+    z.scatter_(1, y[:, None], -float("inf"))
+    top, at = z.topk(2, 1)
+    d = top[:, 0] - zl
+    clear = (labels >= 0) & (top[:, 0] - top[:, 1] > 2 * off + 100) & (d.abs() > 2 * off + 100)
+    assert clear.any()
+    ref = torch.clamp(d, min=0)
+    for o in out:
+        assert not o[0][labels < 0].any()
+        err = (o[0].double() - ref).abs()[clear]
+        assert (err <= (2 * off + 8 * U * ref)[clear]).all(), (int((err > (2 * off + 8 * U * ref)[clear]).sum()), float(err.max()))
+    # its probability is 1 but for e^-100, and so is 1 - p_y, or e^-100 at most where the label is ahead
+    want = torch.where(d[:, None] > 0, W[at[:, 0]].double() - W[y].double(), 0.0)
+    most = W.double().abs().max()
+    assert ((out[1][2].double() - want).abs()[clear] <= (H * want.abs() + 4 * U * most + TINY)[clear]).all()
