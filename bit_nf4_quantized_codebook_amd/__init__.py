@@ -899,7 +899,7 @@ class QLoRAGrads:
     """A list of gradient tensors (bf16 or float32, contiguous, on one device) for qlora_clip_grads, with where the
     scaled ones go: the tensors themselves, or outs, of the same shapes and types, in memory that overlaps no gradient
     and no other of outs (so a gradient scaled in place is in the list once).  Checked and laid out once (a small table of
-    their addresses on the device); it keeps the tensors, whose contents may change between calls, but not their memory
+    their addresses on the device; some 2 us a tensor, and a copy that is waited for); it keeps the tensors, whose contents may change between calls, but not their memory
     (resize_, set_, an assignment to .data).  A graph that captured a call needs the list for as long as it is replayed."""
 
     def __init__(self, grads, outs=None):

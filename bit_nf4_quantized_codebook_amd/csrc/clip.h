@@ -13,7 +13,7 @@ struct ClipEntry {
     int64_t chunk;       // chunks of the tensors before it, times two; + 1: float32
 };
 constexpr int kClipChunk = 4096;     // elements
-constexpr int kClipParts = 2048;     // workgroups of a pass at most, eight on each CU (224 pairs: 163 us, 176 with 1024, 168 with 4096)
+constexpr int kClipParts = 2048;     // workgroups of a pass at most, eight on each CU (224 pairs: 160 us, 173 with 1024, 163 with 4096)
 
 // table: device [n]; part: device [kClipParts]
 hipError_t launch_clip(const ClipEntry *table, int32_t n, int64_t chunks, float max_norm, float *norm, double *part,

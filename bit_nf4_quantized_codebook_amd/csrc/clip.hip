@@ -16,7 +16,8 @@
 // with the first tensor found by bisection and each chunk's entry read again.  One pair takes 8 us of kernels, 11 as a
 // call.
 //
-// The list (pointers, sizes, first chunks) is a table in device memory that the caller keeps with the gradients.
+// The list (pointers, sizes, first chunks) is a table in device memory that the caller keeps with the gradients: made from 448
+// tensors by the Python binding it costs 1.0 ms of the host, six calls' time.
 
 #include "common.h"
 #include "clip.h"

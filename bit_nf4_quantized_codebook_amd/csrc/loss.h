@@ -83,12 +83,13 @@ struct LossShares {
 };
 
 // Tiles of the logits of a piece, for ntm tiles of rows and ntn of the vocabulary.  Where they fill the chip's last round
-// at most half, that round's tiles are cut in two along the vocabulary (129 x 32000 x 4096 170 us, 188 uncut): their second
-// halves' statistics stand ntn entries further in the tables.
+// at most half, that round's tiles are cut in two along the vocabulary (777 x 50001 x 8192 with about 700
+// labelled 1183 us, 1219 uncut): their second halves' statistics stand ntn entries further in the tables.
 //
 // The last tile of rows is a whole one however few of them are live.  Tiles of 128 tokens there took 923 us against 796 at
 // 1639 x 32000 x 4096 (a step of half the MFMAs does not hide its loads with two stages), and 128 x 512 ones 1343 against
-// 1335 at 777 x 50001 x 8192: rows of zeros cost the MFMAs little power, and the wide tiles read W once more.
+// 1335 at 777 x 50001 x 8192, all labelled (both with the gradient): rows of zeros cost the MFMAs little power, and the wide
+// tiles read W once more.
 struct LossTiles {
     int ntm, ntn, whole;      // whole: tiles that are not cut, the first ones
     __host__ __device__ LossTiles(int m, int n) : ntm(m), ntn(n) {
@@ -179,7 +180,9 @@ __device__ __forceinline__ void loss_write_mean(const double *sums, int n, int c
 
 // Up to kLossNarrowMaxM tokens, in one piece; up to kLossNarrowMaxM2 where the vocabulary is at most kLossNarrowMaxTiles
 // tiles of 256, half a round of the chip (with the gradient, 200 tokens: 32000 x 4096 183 us, tiles of 256 189, of those
-// 60 labelled 120 and 156; 8000 x 4096 85 and 107; 160 x 4000 x 1024 42 and 59.  Above: 50001 x 4096 304 and 264).
+// 60 labelled 120 and 156; 8000 x 4096 85 and 107; 160 x 4000 x 1024 42 and 59.  Above: 32769 x 4096 250 and 210, of 200
+// labelled 60 143 and 182; 50001 x 4096 298 and 263, 120 labelled 247 and 241, 60 203 and 225: few labels would want the narrow
+// tiles there too, but how many there are is known on the device only).
 constexpr int64_t kLossNarrowMaxM = 128, kLossNarrowMaxM2 = 256, kLossNarrowMaxTiles = 128;
 struct LossNarrowPlan {
     int32_t MT;               // tokens there may be: 64, 128 or 256

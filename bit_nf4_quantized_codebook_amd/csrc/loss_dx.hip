@@ -13,8 +13,7 @@
 // device), with float32 partials that loss_fold_kernel sums in a fixed order.
 //
 // Bound by the MFMAs as the logits are: 4096 x 32000 x 4096 798 us of kernel, 1.35 PFLOP/s (a library product of these
-// sizes 1.29); 777 x 50001 x 8192 with 700 labelled 523 us and the fold 20; 129 x 32000 x 4096 with 39 labelled, where W's
-// stream is the bound, 51 and 8.
+// sizes 1.29); 777 x 50001 x 8192 with 700 labelled 503 to 523 us and the fold 20.
 
 #include "common.h"
 #include "dqtile.h"
