@@ -611,3 +611,19 @@ def test_logits_beyond_what_a_reference_resolves(M, V, K, size):
     want = torch.where(d[:, None] > 0, W[at[:, 0]].double() - W[y].double(), 0.0)
     most = W.double().abs().max()
     assert ((out[1][2].double() - want).abs()[clear] <= (H * want.abs() + 4 * U * most + TINY)[clear]).all()
+
+
+@pytest.mark.parametrize("M,V,K", [(1 << 20, 300, 64), (65535, 300, 16384), (1, 1 << 24, 64), (16, 1 << 24, 64), (24, 1 << 24, 64)])
+def test_largest_sizes(M, V, K):
+    """The most tokens, an X just below 2 GiB, and the most vocabulary rows (W of 2 GiB)."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(91)
+    X = torch.randn((M, K), generator=g, device=DEV, dtype=torch.bfloat16)
+    W = torch.randn((V, K), generator=g, device=DEV, dtype=torch.bfloat16).mul_(0.05)
+    labels = torch.randint(0, V, (M,), generator=g, device=DEV)
+    labels[-1] = V - 1
+    if M > 16:
+        labels[::5] = NONE
+        labels[0] = 0
+    print(f"largest: M={M} V={V} K={K}", flush=True)
+    check_sampled(X, W, labels, torch.rand(M, device=DEV) + 0.1, some(labels, 40))
